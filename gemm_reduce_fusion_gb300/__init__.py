@@ -48,6 +48,20 @@ TP_OP_AG_MM = 5
 TP_OP_ROW_AR_UNFUSED = 6
 TP_OP_AG_MM_BWD = 7
 TP_OP_ROW_RS_BWD = 8
+TP_OP_BLOCK_NORM_BWD = 9
+TP_OP_COL_BWD_CKPT = 10
+TP_OP_ROW_BWD_CKPT = 11
+TP_OP_AG_MM_BWD_CKPT = 12
+TP_OP_ROW_RS_BWD_CKPT = 13
+TP_OP_COL_W4 = 14
+TP_OP_ROW_W4 = 15
+# tp_norm
+TP_NORM_NONE = 0
+TP_NORM_RMS = 1
+TP_NORM_LAYER = 2
+# largest hidden size of the block norms, and most tokens of the 4-bit forward calls
+TP_BLOCK_NORM_MAX_H = 16384
+TP_W4_MAX_M = 64
 # tp_debug_key
 TP_DEBUG_TIMEOUT_MS = 0
 TP_DEBUG_DROP_LOAD = 1
@@ -66,6 +80,18 @@ class TPError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
         super().__init__(f"{where}: {tp_status_string(status)} (status {status})")
+
+
+class _NormDesc(ctypes.Structure):
+    """tp_block_norm_desc"""
+    _fields_ = [("post", ctypes.c_int), ("pre", ctypes.c_int), ("w_post", ctypes.c_void_p), ("b_post", ctypes.c_void_p),
+                ("w_pre", ctypes.c_void_p), ("b_pre", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("gate_rows", ctypes.c_int64), ("alpha", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class _NormGrads(ctypes.Structure):
+    """tp_block_norm_grads"""
+    _fields_ = [(k, ctypes.c_void_p) for k in ("dw_post", "db_post", "dw_pre", "db_pre", "dgate")]
 
 
 def _load() -> ctypes.CDLL:
@@ -90,6 +116,18 @@ def _load() -> ctypes.CDLL:
         "tp_row_linear_fwd_unfused": (I, [PP, PP, P, I, L, L, L, L, I, I, I, P, S, P]),
         "tp_ag_matmul_bwd": (I, [PP, PP, PP, PP, PP, PP, I, L, L, L, L, I, P, S, P]),
         "tp_row_linear_bwd_reducescatter": (I, [PP, PP, PP, PP, PP, P, PP, I, L, L, L, L, I, P, S, P]),
+        "tp_block_norm_fwd": (I, [PP, PP, PP, PP, P, I, L, L, I, P]),
+        "tp_block_norm_bwd": (I, [PP, PP, PP, PP, PP, PP, P, P, I, L, L, I, I, P, S, P]),
+        "tp_ckpt_pack": (I, [PP, PP, PP, I, L, L, P]),
+        "tp_ckpt_unpack": (I, [PP, PP, PP, I, I, L, L, P]),
+        "tp_col_linear_bwd_ckpt": (I, [P, P, PP, PP, P, PP, PP, I, L, L, L, L, I, P, S, P]),
+        "tp_row_linear_bwd_ckpt": (I, [PP, PP, PP, P, PP, PP, P, I, I, L, L, L, L, I, P, S, P]),
+        "tp_ag_matmul_bwd_ckpt": (I, [PP, PP, PP, PP, PP, PP, PP, I, L, L, L, L, I, P, S, P]),
+        "tp_row_linear_bwd_reducescatter_ckpt": (I, [PP, PP, PP, PP, PP, PP, P, I, I, L, L, L, L, I, P, S, P]),
+        "tp_col_linear_fwd_w4": (I, [P, PP, PP, PP, PP, I, I, L, L, L, L, I, P, S, P]),
+        "tp_row_linear_fwd_w4": (I, [PP, PP, PP, P, P, I, L, L, L, L, I, P, S, P]),
+        "tp_w4_pack": (I, [PP, PP, PP, I, L, L, L, P]),
+        "tp_w4_unpack": (I, [PP, PP, PP, I, L, L, L, P]),
         "tp_pipeline_time": (ctypes.c_double, [ctypes.c_double, ctypes.c_double, L]),
         "tp_num_chunks": (L, [L, L]),
         "tp_choose_chunk_m": (L, [I, I, L, L, L]),
@@ -467,3 +505,270 @@ def tp_noalloc_device_status(stream=None) -> int:
     fn.restype = ctypes.c_int
     fn.argtypes = [ctypes.c_void_p]
     return fn(_stream(stream))
+
+
+# ------------------------------------------------------------------ around the sharded Linear
+#
+# The calls below take few microseconds on the device when they serve single
+# tokens, so their checks go through one loop per list and read each property
+# of a tensor once.
+
+def _list(where: str, name: str, ts, count: int, shape, dtype, dev: int):
+    """The C array of `count` tensors of one shape and dtype (None: NULL)."""
+    if ts is None:
+        return None
+    if len(ts) != count:
+        raise ValueError(f"{where}: {name} holds {len(ts)} tensors, expected {count}")
+    for i, t in enumerate(ts):
+        if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+            _refuse(where, f"{name}[{i}]", t, shape, dtype, dev)
+    return (ctypes.c_void_p * count)(*[t.data_ptr() for t in ts])
+
+
+def _one(where: str, name: str, t, shape, dtype, dev: int):
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _refuse(where, name, t, shape, dtype, dev)
+    return t.data_ptr()
+
+
+def _refuse(where: str, name: str, t, shape, dtype, dev: int) -> None:
+    _need(where, name, t, shape, False, dev)
+    raise TypeError(f"{where}: {name} must be {str(dtype).replace('torch.', '')}, got {t.dtype}")
+
+
+def _norm_args(where, h, post, w_post, b_post, pre, w_pre, b_pre, gate, alpha, eps, dev):
+    import torch
+    bf = torch.bfloat16
+    rows = 0
+    if gate is not None:
+        if gate.dim() != 2:
+            raise ValueError(f"{where}: gate is [rows, h], got {tuple(gate.shape)}")
+        rows = gate.shape[0]
+    return _NormDesc(post, pre, _one(where, "w_post", w_post, (h,), bf, dev), _one(where, "b_post", b_post, (h,), bf, dev),
+                     _one(where, "w_pre", w_pre, (h,), bf, dev), _one(where, "b_pre", b_pre, (h,), bf, dev),
+                     _one(where, "gate", gate, (rows, h), bf, dev), rows, alpha, eps)
+
+
+def _residual(where, t):
+    import torch
+    if t.dim() != 2:
+        raise ValueError(f"{where}: a token shard is [tokens, h], got {tuple(t.shape)}")
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{where}: the residual stream is bfloat16 or float32, got {t.dtype}")
+    return t.shape[0], t.shape[1], t.dtype, TP_FP32 if t.dtype is torch.float32 else TP_BF16
+
+
+def tp_block_norm_fwd(x: Sequence, z, y, n, *, post: int = TP_NORM_NONE, w_post=None, b_post=None,
+                      pre: int = TP_NORM_NONE, w_pre=None, b_pre=None, gate=None, alpha: float = 1.0,
+                      eps: float = 1e-5, stream=None) -> None:
+    """y[s] = x[s] + alpha gate N_post(z[s]); n[s] = N_pre(y[s]), over p row shards.
+
+    z None (then y None): n[s] = N_pre(x[s]).  n None: y alone.  x and y are
+    bfloat16 or float32, z and n bfloat16; gate is [rows, h], its row i / (M / rows)
+    for token i of the M = p * len(x[0]) tokens.  y[s] may be x[s]."""
+    import torch
+    W, dev, p = "tp_block_norm_fwd", _current_device(), len(x)
+    m, h, dtype, code = _residual(W, x[0])
+    d = _norm_args(W, h, post, w_post, b_post, pre, w_pre, b_pre, gate, alpha, eps, dev)
+    shape, bf = (m, h), torch.bfloat16
+    _check(_lib.tp_block_norm_fwd(_list(W, "x", x, p, shape, dtype, dev), _list(W, "z", z, p, shape, bf, dev),
+                                  _list(W, "y", y, p, shape, dtype, dev), _list(W, "n", n, p, shape, bf, dev),
+                                  ctypes.byref(d), p, p * m, h, code, _stream(stream)), W)
+
+
+def tp_block_norm_bwd(z, y, dn, dy, dx, dz, ws, *, post: int = TP_NORM_NONE, w_post=None, b_post=None,
+                      pre: int = TP_NORM_NONE, w_pre=None, b_pre=None, gate=None, alpha: float = 1.0,
+                      eps: float = 1e-5, dw_post=None, db_post=None, dw_pre=None, db_pre=None, dgate=None,
+                      stream=None) -> None:
+    """Gradients of tp_block_norm_fwd: dx[s], dz[s] and those of the vectors.
+
+    y: the stream after the boundary (the forward x when z is None), needed
+    with dn; dn, dy: gradients of n and (from its later uses) of y, either may
+    be None; dx, dz and each vector's gradient may be None.  dy, y, dx share
+    one dtype; the vectors' gradients share one (bfloat16 or float32).
+    dx[s] may be dy[s].  ws: workspace(TP_OP_BLOCK_NORM_BWD, p, M, h, 0)."""
+    import torch
+    W, dev = "tp_block_norm_bwd", _current_device()
+    first = next((t for t in (y, dy, dx) if t), None)
+    if first is None:
+        raise ValueError(f"{W}: one of y, dy and dx is given")
+    p = len(first)
+    m, h, dtype, code = _residual(W, first[0])
+    d = _norm_args(W, h, post, w_post, b_post, pre, w_pre, b_pre, gate, alpha, eps, dev)
+    vectors = (dw_post, db_post, dw_pre, db_pre, dgate)
+    out = next((t.dtype for t in vectors if t is not None), torch.float32)
+    names = ("dw_post", "db_post", "dw_pre", "db_pre")
+    g = _NormGrads(*[_one(W, k, t, (h,), out, dev) for k, t in zip(names, vectors)],
+                   _one(W, "dgate", dgate, gate.shape if gate is not None else (0, h), out, dev))
+    _need_ws(W, ws, dev)
+    wp, wb = _ws(ws)
+    shape, bf = (m, h), torch.bfloat16
+    _check(_lib.tp_block_norm_bwd(_list(W, "z", z, p, shape, bf, dev), _list(W, "y", y, p, shape, dtype, dev),
+                                  _list(W, "dn", dn, p, shape, bf, dev), _list(W, "dy", dy, p, shape, dtype, dev),
+                                  _list(W, "dx", dx, p, shape, dtype, dev), _list(W, "dz", dz, p, shape, bf, dev),
+                                  ctypes.byref(d), ctypes.byref(g), p, p * m, h, code, _grad_code(W, out), wp, wb,
+                                  _stream(stream)), W)
+
+
+def _grad_code(where, dtype) -> int:
+    import torch
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{where}: gradients are bfloat16 or float32, got {dtype}")
+    return TP_FP32 if dtype is torch.float32 else TP_BF16
+
+
+def ckpt_shapes(M: int, N: int) -> tuple:
+    """Shapes of a checkpoint of an [M, N] activation: (q int8, e uint8)."""
+    return (M, N), (M, (N + 31) // 32)
+
+
+def tp_ckpt_pack(x: Sequence, q: Sequence, e: Sequence, stream=None) -> None:
+    """(q[i], e[i]) = x[i] in 8 bits: int8 [M, N] and a power of two per 32 columns, uint8 [M, ceil(N/32)]."""
+    import torch
+    W, dev, p = "tp_ckpt_pack", _current_device(), len(x)
+    M, N = x[0].shape
+    qs, es = ckpt_shapes(M, N)
+    _check(_lib.tp_ckpt_pack(_list(W, "x", x, p, (M, N), torch.bfloat16, dev), _list(W, "q", q, p, qs, torch.int8, dev),
+                             _list(W, "e", e, p, es, torch.uint8, dev), p, M, N, _stream(stream)), W)
+
+
+def tp_ckpt_unpack(q: Sequence, e: Sequence, y: Sequence, epi: int = TP_EPI_NONE, stream=None) -> None:
+    """y[i] = the value of (q[i], e[i]), or its GeLU (epi=TP_EPI_GELU), in bfloat16."""
+    import torch
+    W, dev, p = "tp_ckpt_unpack", _current_device(), len(q)
+    M, N = q[0].shape
+    qs, es = ckpt_shapes(M, N)
+    _check(_lib.tp_ckpt_unpack(_list(W, "q", q, p, qs, torch.int8, dev), _list(W, "e", e, p, es, torch.uint8, dev),
+                               _list(W, "y", y, p, (M, N), torch.bfloat16, dev), epi, p, M, N, _stream(stream)), W)
+
+
+def tp_col_linear_bwd_ckpt(q, e, w: Sequence, dy: Sequence, dx, dw, ws, chunk_m: int = 0, stream=None, db=None) -> None:
+    """tp_col_linear_bwd with X given as a checkpoint (q, e) (both None without dw)."""
+    import torch
+    W, dev, p, bf = "tp_col_linear_bwd_ckpt", _current_device(), len(w), torch.bfloat16
+    (K, N), M = w[0].shape, dy[0].shape[0]
+    qs, es = ckpt_shapes(M, K)
+    out = _out_dtype(dx, dw, db)
+    od = torch.float32 if out == TP_FP32 else bf
+    _need_ws(W, ws, dev)
+    wp, wb = _ws(ws)
+    _check(_lib.tp_col_linear_bwd_ckpt(
+        _one(W, "q", q, qs, torch.int8, dev), _one(W, "e", e, es, torch.uint8, dev), _list(W, "w", w, p, (K, N), bf, dev),
+        _list(W, "dy", dy, p, (M, N), bf, dev), _one(W, "dx", dx, (M, K), od, dev), _list(W, "dw", dw, p, (K, N), od, dev),
+        _list(W, "db", db, p, (N,), od, dev), p, M, N, K, chunk_m, out, wp, wb, _stream(stream)), W)
+
+
+def tp_row_linear_bwd_ckpt(q, e, w: Sequence, dy, dx, dw, ws, epi: int = TP_EPI_DGELU, chunk_m: int = 0, stream=None,
+                           db=None) -> None:
+    """tp_row_linear_bwd from checkpoints: of the pre-activations H_k (epi=TP_EPI_DGELU: dx[k] = dY A_k^T * GeLU'(H_k),
+    dw[k] = GeLU(H_k)^T dY) or of the layer's inputs X_k (epi=TP_EPI_NONE)."""
+    import torch
+    W, dev, p, bf = "tp_row_linear_bwd_ckpt", _current_device(), len(w), torch.bfloat16
+    (K, N), M = w[0].shape, dy.shape[0]
+    qs, es = ckpt_shapes(M, K)
+    out = _out_dtype(dx, dw, db)
+    od = torch.float32 if out == TP_FP32 else bf
+    _need_ws(W, ws, dev)
+    wp, wb = _ws(ws)
+    _check(_lib.tp_row_linear_bwd_ckpt(
+        _list(W, "q", q, p, qs, torch.int8, dev), _list(W, "e", e, p, es, torch.uint8, dev),
+        _list(W, "w", w, p, (K, N), bf, dev), _one(W, "dy", dy, (M, N), bf, dev), _list(W, "dx", dx, p, (M, K), od, dev),
+        _list(W, "dw", dw, p, (K, N), od, dev), _one(W, "db", db, (N,), od, dev), epi, p, M, N, K, chunk_m, out, wp, wb,
+        _stream(stream)), W)
+
+
+def tp_ag_matmul_bwd_ckpt(q, e, w: Sequence, dy: Sequence, dx, dw, ws, chunk_m: int = 0, stream=None, db=None) -> None:
+    """tp_ag_matmul_bwd with the token shards X_s given as checkpoints (None without dw)."""
+    import torch
+    W, dev, p, bf = "tp_ag_matmul_bwd_ckpt", _current_device(), len(w), torch.bfloat16
+    (K, N), M = w[0].shape, dy[0].shape[0]
+    qs, es = ckpt_shapes(M // p, K)
+    out = _out_dtype(dx, dw, db)
+    od = torch.float32 if out == TP_FP32 else bf
+    _need_ws(W, ws, dev)
+    wp, wb = _ws(ws)
+    _check(_lib.tp_ag_matmul_bwd_ckpt(
+        _list(W, "q", q, p, qs, torch.int8, dev), _list(W, "e", e, p, es, torch.uint8, dev),
+        _list(W, "w", w, p, (K, N), bf, dev), _list(W, "dy", dy, p, (M, N), bf, dev),
+        _list(W, "dx", dx, p, (M // p, K), od, dev), _list(W, "dw", dw, p, (K, N), od, dev),
+        _list(W, "db", db, p, (N,), od, dev), p, M, N, K, chunk_m, out, wp, wb, _stream(stream)), W)
+
+
+def tp_row_linear_bwd_reducescatter_ckpt(q, e, w: Sequence, dy: Sequence, dx, dw, ws, epi: int = TP_EPI_DGELU,
+                                         chunk_m: int = 0, stream=None, db=None) -> None:
+    """tp_row_linear_bwd_reducescatter from checkpoints, as tp_row_linear_bwd_ckpt; dy[s] are row shards."""
+    import torch
+    W, dev, p, bf = "tp_row_linear_bwd_reducescatter_ckpt", _current_device(), len(w), torch.bfloat16
+    (K, N), M = w[0].shape, dy[0].shape[0] * len(w)
+    qs, es = ckpt_shapes(M, K)
+    out = _out_dtype(dx, dw, db)
+    od = torch.float32 if out == TP_FP32 else bf
+    _need_ws(W, ws, dev)
+    wp, wb = _ws(ws)
+    _check(_lib.tp_row_linear_bwd_reducescatter_ckpt(
+        _list(W, "q", q, p, qs, torch.int8, dev), _list(W, "e", e, p, es, torch.uint8, dev),
+        _list(W, "w", w, p, (K, N), bf, dev), _list(W, "dy", dy, p, (M // p, N), bf, dev),
+        _list(W, "dx", dx, p, (M, K), od, dev), _list(W, "dw", dw, p, (K, N), od, dev),
+        _one(W, "db", db, (N,), od, dev), epi, p, M, N, K, chunk_m, out, wp, wb, _stream(stream)), W)
+
+
+def w4_shapes(K: int, N: int, group: int) -> tuple:
+    """Shapes of a 4-bit weight [K, N]: (q uint8, s bfloat16)."""
+    return ((N + 31) // 32, (K + 63) // 64, 1024), ((N + 31) // 32, (K + group - 1) // group, 32)
+
+
+def _group(where: str, group: int) -> int:
+    if group not in (32, 64, 128):
+        raise ValueError(f"{where}: group is 32, 64 or 128 rows, got {group}")
+    return group
+
+
+def tp_col_linear_fwd_w4(x, q: Sequence, s: Sequence, y: Sequence, ws, group: int = 128, epi: int = TP_EPI_NONE,
+                         stream=None, bias=None) -> None:
+    """y[k] = X W_k + b_k (or its GeLU) with 4-bit weights (q[k], s[k]); up to TP_W4_MAX_M tokens."""
+    import torch
+    W, dev, p, bf = "tp_col_linear_fwd_w4", _current_device(), len(q), torch.bfloat16
+    (M, K), N, dtype = x.shape, y[0].shape[1], y[0].dtype
+    qs, ss = w4_shapes(K, N, _group(W, group))
+    _need_ws(W, ws, dev)
+    wp, wb = _ws(ws)
+    _check(_lib.tp_col_linear_fwd_w4(
+        _one(W, "x", x, (M, K), bf, dev), _list(W, "q", q, p, qs, torch.uint8, dev), _list(W, "s", s, p, ss, bf, dev),
+        _list(W, "bias", bias, p, (N,), bf, dev), _list(W, "y", y, p, (M, N), dtype, dev), epi, p, M, N, K, group,
+        _dtype_code(y[0]), wp, wb, _stream(stream)), W)
+
+
+def tp_row_linear_fwd_w4(x: Sequence, q: Sequence, s: Sequence, y, ws, group: int = 128, stream=None, bias=None) -> None:
+    """y = sum_r X_r W_r (+ bias) with 4-bit weights (q[r], s[r]); up to TP_W4_MAX_M tokens."""
+    import torch
+    W, dev, p, bf = "tp_row_linear_fwd_w4", _current_device(), len(q), torch.bfloat16
+    (M, K), N, dtype = x[0].shape, y.shape[1], y.dtype
+    qs, ss = w4_shapes(K, N, _group(W, group))
+    _need_ws(W, ws, dev)
+    wp, wb = _ws(ws)
+    _check(_lib.tp_row_linear_fwd_w4(
+        _list(W, "x", x, p, (M, K), bf, dev), _list(W, "q", q, p, qs, torch.uint8, dev), _list(W, "s", s, p, ss, bf, dev),
+        _one(W, "bias", bias, (N,), bf, dev), _one(W, "y", y, (M, N), dtype, dev), p, M, N, K, group, _dtype_code(y), wp, wb,
+        _stream(stream)), W)
+
+
+def tp_w4_pack(w: Sequence, q: Sequence, s: Sequence, group: int = 128, stream=None) -> None:
+    """(q[r], s[r]) = w[r] [K, N] in 4 bits, a scale max|w| / 7 for each column and group of rows."""
+    import torch
+    W, dev, p, bf = "tp_w4_pack", _current_device(), len(w), torch.bfloat16
+    K, N = w[0].shape
+    qs, ss = w4_shapes(K, N, _group(W, group))
+    _check(_lib.tp_w4_pack(_list(W, "w", w, p, (K, N), bf, dev), _list(W, "q", q, p, qs, torch.uint8, dev),
+                           _list(W, "s", s, p, ss, bf, dev), p, N, K, group, _stream(stream)), W)
+
+
+def tp_w4_unpack(q: Sequence, s: Sequence, w: Sequence, group: int = 128, stream=None) -> None:
+    """w[r] [K, N] in bfloat16 of the 4-bit weights (q[r], s[r])."""
+    import torch
+    W, dev, p, bf = "tp_w4_unpack", _current_device(), len(w), torch.bfloat16
+    K, N = w[0].shape
+    qs, ss = w4_shapes(K, N, _group(W, group))
+    _check(_lib.tp_w4_unpack(_list(W, "q", q, p, qs, torch.uint8, dev), _list(W, "s", s, p, ss, bf, dev),
+                             _list(W, "w", w, p, (K, N), bf, dev), p, N, K, group, _stream(stream)), W)

@@ -24,7 +24,8 @@ BUILD = os.path.join(ROOT, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include")]
-SOURCES = ["tp_fused.cu"]
+SOURCES = ["tp_fused.cu", "block_norm.cu", "block_norm_bwd_bf16_rms.cu", "block_norm_bwd_bf16_ln.cu",
+           "block_norm_bwd_f32_rms.cu", "block_norm_bwd_f32_ln.cu", "ckpt.cu", "w4.cu"]
 
 
 def nvcc() -> str:

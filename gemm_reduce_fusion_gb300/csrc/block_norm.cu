@@ -1,0 +1,388 @@
+// C ABI of the block boundary (norms, gate, residual) and its gradients:
+// argument checks and launches of the kernels in block_norm.cuh.
+#include "block_norm.cuh"
+
+#include <cmath>
+#include <cstring>
+
+#include "block_norm.h"
+#include "host_util.h"
+
+using namespace tpf;
+
+namespace {
+
+struct NormGradParams {
+  const float* part;    // [4][ctas][h]: C, A, D, B
+  const float* gpart;   // [2][workers][h]
+  const __nv_bfloat16 *gate, *w_post, *b_post;  // gate: its only row, or null
+  void *dw_pre, *db_pre, *dw_post, *db_post, *dgate;
+  uint32_t h, ctas, workers, M, rows_per_gate, groups;  // groups: gate rows; 0 or 1: by A and B
+  int32_t out_f32;
+};
+
+__device__ __forceinline__ void put_grad(void* out, int64_t i, float v, int f32) {
+  if (out == nullptr) return;
+  if (f32) static_cast<float*>(out)[i] = v;
+  else static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
+}
+
+// Adds the CTAs' column sums in CTA order: 32 columns a block, 32 lanes of
+// partial sums a column, joined in lane order.  blockIdx.y: 0 the weights'
+// and biases' gradients (and the gate's, with one gate row), g + 1 gate row g
+// where several workers hold parts of it.
+__global__ void __launch_bounds__(1024) block_norm_grad_kernel(const __grid_constant__ NormGradParams P) {
+  __shared__ float sh[32][33];
+  griddep_wait();
+  griddep_launch_dependents();
+  const uint32_t c = blockIdx.x * 32 + (threadIdx.x & 31), lane = threadIdx.x >> 5;
+  auto column = [&](const float* src, uint32_t n) {
+    float t = 0.f;
+    if (c < P.h)
+      for (uint32_t i = lane; i < n; i += 32) t += src[static_cast<int64_t>(i) * P.h + c];
+    sh[lane][threadIdx.x & 31] = t;
+    __syncthreads();
+    t = 0.f;
+    if (lane == 0)
+      for (int i = 0; i < 32; ++i) t += sh[i][threadIdx.x & 31];
+    __syncthreads();
+    return t;  // in the threads of lane 0
+  };
+  const int64_t plane = static_cast<int64_t>(P.ctas) * P.h;
+  const bool mine = lane == 0 && c < P.h;
+  if (blockIdx.y == 0) {
+    if (P.dw_pre) {
+      const float t = column(P.part, P.ctas);
+      if (mine) put_grad(P.dw_pre, c, t, P.out_f32);
+    }
+    if (P.db_pre) {
+      const float t = column(P.part + 2 * plane, P.ctas);
+      if (mine) put_grad(P.db_pre, c, t, P.out_f32);
+    }
+    const bool one = P.dgate != nullptr && P.groups == 1;
+    if (P.dw_post || P.db_post || one) {
+      const float A = column(P.part + plane, P.ctas);
+      const float B = P.db_post || P.b_post ? column(P.part + 3 * plane, P.ctas) : 0.f;
+      if (mine) {
+        const float g = P.groups == 1 ? __bfloat162float(P.gate[c]) : 1.f;
+        put_grad(P.dw_post, c, g * A, P.out_f32);
+        put_grad(P.db_post, c, g * B, P.out_f32);
+        if (one) {
+          const float w = P.w_post ? __bfloat162float(P.w_post[c]) : 1.f, b = P.b_post ? __bfloat162float(P.b_post[c]) : 0.f;
+          put_grad(P.dgate, c, fmaf(w, A, b * B), P.out_f32);
+        }
+      }
+    }
+  }
+  for (uint32_t g = blockIdx.y; g < P.groups && P.groups > 1 && P.dgate; g += gridDim.y) {
+    // workers w with rows [w M / W, (w + 1) M / W) that meet the group's rows
+    const uint64_t g0 = static_cast<uint64_t>(g) * P.rows_per_gate, g1 = g0 + P.rows_per_gate;
+    const uint32_t w0 = static_cast<uint32_t>(((g0 + 1) * P.workers - 1) / P.M);
+    const uint32_t w1 = static_cast<uint32_t>((g1 * P.workers - 1) / P.M);
+    if (w0 == w1) continue;  // written whole by its worker
+    // the first worker holds the group in its second plane unless its rows
+    // begin with it; the others' rows begin inside the group
+    const bool starts = static_cast<uint64_t>(w0) * P.M / P.workers >= g0;
+    const int64_t gplane = static_cast<int64_t>(P.workers) * P.h;
+    float t = 0.f;
+    if (c < P.h)
+      for (uint32_t w = w0 + lane; w <= w1; w += 32)
+        t += P.gpart[(w == w0 && !starts ? gplane : 0) + static_cast<int64_t>(w) * P.h + c];
+    sh[lane][threadIdx.x & 31] = t;
+    __syncthreads();
+    if (mine) {
+      t = 0.f;
+      for (int i = 0; i < 32; ++i) t += sh[i][threadIdx.x & 31];
+      put_grad(P.dgate, static_cast<int64_t>(g) * P.h + c, t, P.out_f32);
+    }
+    __syncthreads();
+  }
+}
+
+// ----------------------------------------------------------------- host
+
+// How a row of nvec 8-column vectors is spread over threads.
+struct Shape {
+  bool warp;    // one worker per warp, 8 workers per CTA; else one CTA per row
+  int nv;       // vectors per thread
+  int threads;  // of the CTA
+};
+
+// Rows of up to 1024 columns go to a warp, which needs no barrier for its
+// sums; longer ones to a CTA with two vectors a thread.
+Shape shape_for(int64_t nvec) {
+  if (nvec <= 64) return {true, 2, 256};
+  if (nvec <= 128) return {true, 4, 256};
+  return {false, 2, static_cast<int>(cdiv(cdiv(nvec, 2), 32) * 32)};
+}
+
+// CTAs per SM the backward pass is planned for; fixes its workspace.
+int bwd_ctas_per_sm(const Shape& s) { return s.threads <= 256 ? 3 : s.threads <= 512 ? 2 : 1; }
+
+constexpr int kSMs = 152;
+
+using Kernel = void (*)(NormParams);
+
+template <int NV, bool RES32, bool WARP, int MAXT>
+tp_status run_fwd(const NormParams& P0, const Shape& sh, const DevInfo& di, cudaStream_t stream) {
+  static KernelInfo info;
+  Kernel k = block_norm_fwd_kernel<NV, RES32, WARP, MAXT>;
+  int regs = 0;
+  TP_TRY(kernel_regs(reinterpret_cast<const void*>(k), &info, &regs));
+  NormParams P = P0;
+  const size_t stage = static_cast<size_t>(sh.threads) * NV * ((RES32 ? 2 : 1) + 1) * 16;
+  P.stages = 2;
+  const int per_sm = blocks_per_sm(sh.threads, regs, P.stages * stage + 3072);
+  const int workers = WARP ? sh.threads / 32 : 1;
+  const int64_t grid = std::min<int64_t>(cdiv(P.M, workers), static_cast<int64_t>(di.sms) * per_sm);
+  return launch_dependent(k, dim3(static_cast<unsigned>(grid)), static_cast<unsigned>(sh.threads), P.stages * stage, stream, P);
+}
+
+template <bool RES32>
+tp_status dispatch_fwd(const NormParams& P, const DevInfo& di, cudaStream_t stream) {
+  const Shape sh = shape_for(P.nvec);
+  if (sh.warp) return sh.nv == 2 ? run_fwd<2, RES32, true, 256>(P, sh, di, stream) : run_fwd<4, RES32, true, 256>(P, sh, di, stream);
+  if (sh.threads <= 256) return run_fwd<2, RES32, false, 256>(P, sh, di, stream);
+  if (sh.threads <= 512) return run_fwd<2, RES32, false, 512>(P, sh, di, stream);
+  return run_fwd<2, RES32, false, 1024>(P, sh, di, stream);
+}
+
+// The backward pass's shape: every worker gets a row at least, since the
+// owner of a row is found by dividing the rows evenly among the workers.
+Shape bwd_shape(int64_t nvec, int64_t M) {
+  Shape s = shape_for(nvec);
+  if (s.warp) s.threads = static_cast<int>(32 * std::max<int64_t>(1, std::min<int64_t>(M, s.threads / 32)));
+  return s;
+}
+
+int64_t bwd_workers(const Shape& sh) { return sh.warp ? sh.threads / 32 : 1; }
+
+int64_t bwd_ctas(const Shape& sh, int64_t M) {
+  return std::max<int64_t>(1, std::min<int64_t>(M / bwd_workers(sh), static_cast<int64_t>(kSMs) * bwd_ctas_per_sm(sh)));
+}
+
+tp_status check_norm(const tp_block_norm_desc* d, bool has_z, int64_t M, bool need_pre) {
+  if (d == nullptr) return TP_ERR_INVALID_ARG;
+  for (tp_norm k : {d->post, d->pre})
+    if (k != TP_NORM_NONE && k != TP_NORM_RMS && k != TP_NORM_LAYER) return TP_ERR_INVALID_ARG;
+  if (!(d->eps >= 0.f) || !std::isfinite(d->eps) || !std::isfinite(d->alpha)) return TP_ERR_INVALID_ARG;
+  if (!has_z && (d->post != TP_NORM_NONE || d->gate != nullptr)) return TP_ERR_INVALID_ARG;
+  if (need_pre != (d->pre != TP_NORM_NONE)) return TP_ERR_INVALID_ARG;
+  if (d->post == TP_NORM_NONE && d->w_post != nullptr) return TP_ERR_INVALID_ARG;
+  if (d->pre == TP_NORM_NONE && d->w_pre != nullptr) return TP_ERR_INVALID_ARG;
+  if (d->post != TP_NORM_LAYER && d->b_post != nullptr) return TP_ERR_INVALID_ARG;
+  if (d->pre != TP_NORM_LAYER && d->b_pre != nullptr) return TP_ERR_INVALID_ARG;
+  for (const void* v : {d->w_post, d->b_post, d->w_pre, d->b_pre, d->gate})
+    if (!aligned16(v)) return TP_ERR_ALIGNMENT;
+  if (d->gate != nullptr) {
+    if (d->gate_rows < 1) return TP_ERR_INVALID_ARG;
+    if (M % d->gate_rows != 0) return TP_ERR_UNSUPPORTED_SHAPE;
+  }
+  return TP_OK;
+}
+
+tp_status check_extent(int p, int64_t M, int64_t h, tp_dtype res) {
+  TP_TRY(check_sizes(p, M, h, 0, 0, res));
+  if (h > TP_BLOCK_NORM_MAX_H || M % p != 0) return TP_ERR_UNSUPPORTED_SHAPE;
+  return TP_OK;
+}
+
+void fill(NormParams* P, const tp_block_norm_desc* d, int p, int64_t M, int64_t h) {
+  std::memset(P, 0, sizeof(*P));
+  P->gate = static_cast<const uint4*>(d->gate);
+  P->w_post = static_cast<const uint4*>(d->w_post);
+  P->b_post = static_cast<const uint4*>(d->b_post);
+  P->w_pre = static_cast<const uint4*>(d->w_pre);
+  P->b_pre = static_cast<const uint4*>(d->b_pre);
+  P->alpha = d->alpha;
+  P->eps = d->eps;
+  P->inv_h = 1.f / static_cast<float>(h);
+  P->M = static_cast<uint32_t>(M);
+  P->m = static_cast<uint32_t>(M / p);
+  P->nvec = static_cast<uint32_t>(h / 8);
+  P->rows_per_gate = static_cast<uint32_t>(d->gate != nullptr ? M / d->gate_rows : M);
+  P->post = d->post;
+  P->pre = d->pre;
+}
+
+// Ranges of the descriptor's vectors, which are inputs.
+void add_desc(std::vector<Range>* in, const tp_block_norm_desc* d, int64_t h) {
+  for (const void* v : {d->w_post, d->b_post, d->w_pre, d->b_pre}) in->push_back({v, v ? static_cast<size_t>(h) * 2 : 0});
+  in->push_back({d->gate, d->gate ? static_cast<size_t>(d->gate_rows * h) * 2 : 0});
+}
+
+// Refuses overlaps, save that out[s] may be in[s] itself where `same` is
+// given: a row of it is written only after it has been read by the same
+// thread block.
+bool clash(const std::vector<Range>& outs, const std::vector<Range>& ins, const void* const* out, const void* const* same, int p,
+           size_t bytes) {
+  std::vector<Range> rest;
+  for (const Range& r : ins) {
+    bool skip = false;
+    for (int s = 0; s < p && same != nullptr && out != nullptr; ++s)
+      skip |= r.p == same[s] && r.bytes == bytes && out[s] == same[s];
+    if (!skip) rest.push_back(r);
+  }
+  return any_overlap(outs, rest);
+}
+
+}  // namespace
+
+namespace tpf {
+
+size_t block_norm_bwd_workspace(int64_t M, int64_t h) {
+  const Shape sh = bwd_shape(cdiv(h, 8), M);
+  const int64_t ctas = bwd_ctas(sh, M), workers = ctas * bwd_workers(sh);
+  return kStatusBytes + static_cast<size_t>(4 * ctas + 2 * workers) * h * sizeof(float);
+}
+
+}  // namespace tpf
+
+extern "C" tp_status tp_block_norm_fwd(const void* const* x, const void* const* z, void* const* y, void* const* n,
+                                       const tp_block_norm_desc* d, int p, int64_t M, int64_t h, tp_dtype res_dtype,
+                                       cudaStream_t stream) {
+  TP_TRY(check_extent(p, M, h, res_dtype));
+  TP_TRY(check_norm(d, z != nullptr, M, n != nullptr));
+  if ((z != nullptr) != (y != nullptr) || (z == nullptr && n == nullptr)) return TP_ERR_INVALID_ARG;
+  const bool work = M > 0 && h > 0;
+  const auto in = [](void* const* a) { return const_cast<const void* const*>(a); };
+  TP_TRY(check_ptrs(x, p, work));
+  TP_TRY(check_ptrs(z, p, work && z != nullptr));
+  TP_TRY(check_ptrs(in(y), p, work && y != nullptr));
+  TP_TRY(check_ptrs(in(n), p, work && n != nullptr));
+  if (!work) return TP_OK;
+  {
+    const size_t one = static_cast<size_t>(M / p * h);
+    std::vector<Range> ins, outs;
+    ins.reserve(24);
+    outs.reserve(16);
+    add_ranges(&ins, x, p, one * esize(res_dtype));
+    add_ranges(&ins, z, p, one * 2);
+    add_desc(&ins, d, h);
+    add_ranges(&outs, in(y), p, one * esize(res_dtype));
+    add_ranges(&outs, in(n), p, one * 2);
+    if (clash(outs, ins, in(y), x, p, one * esize(res_dtype))) return TP_ERR_INVALID_ARG;
+  }
+  DevInfo di;
+  TP_TRY(device_info(&di));
+  NormParams P;
+  fill(&P, d, p, M, h);
+  P.has_z = z != nullptr;
+  for (int s = 0; s < p; ++s) {
+    P.x[s] = x[s];
+    P.z[s] = z ? z[s] : nullptr;
+    P.y[s] = y ? y[s] : nullptr;
+    P.n[s] = n ? n[s] : nullptr;
+  }
+  return res_dtype == TP_FP32 ? dispatch_fwd<true>(P, di, stream) : dispatch_fwd<false>(P, di, stream);
+}
+
+extern "C" tp_status tp_block_norm_bwd(const void* const* z, const void* const* y, const void* const* dn, const void* const* dy,
+                                       void* const* dx, void* const* dz, const tp_block_norm_desc* d,
+                                       const tp_block_norm_grads* grads, int p, int64_t M, int64_t h, tp_dtype res_dtype,
+                                       tp_dtype out_dtype, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  TP_TRY(check_extent(p, M, h, res_dtype));
+  if (out_dtype != TP_BF16 && out_dtype != TP_FP32) return TP_ERR_INVALID_ARG;
+  TP_TRY(check_norm(d, z != nullptr, M, dn != nullptr));
+  const tp_block_norm_grads none = {};
+  const tp_block_norm_grads g = grads != nullptr ? *grads : none;
+  if (dn == nullptr && dy == nullptr) return TP_ERR_INVALID_ARG;
+  if (dx == nullptr && dz == nullptr && !g.dw_post && !g.db_post && !g.dw_pre && !g.db_pre && !g.dgate) return TP_ERR_INVALID_ARG;
+  if (z == nullptr && dz != nullptr) return TP_ERR_INVALID_ARG;
+  // a gradient is asked for of a vector that the forward pass can have had
+  // (a bias, and a weight of ones, need not be given for it)
+  if ((g.dw_post && d->post == TP_NORM_NONE) || (g.db_post && d->post != TP_NORM_LAYER) ||
+      (g.dw_pre && d->pre == TP_NORM_NONE) || (g.db_pre && d->pre != TP_NORM_LAYER) || (g.dgate && !d->gate))
+    return TP_ERR_INVALID_ARG;
+  for (const void* v : {g.dw_post, g.db_post, g.dw_pre, g.db_pre, g.dgate})
+    if (!aligned16(v)) return TP_ERR_ALIGNMENT;
+  const bool rows = M > 0 && h > 0;
+  const auto in = [](void* const* a) { return const_cast<const void* const*>(a); };
+  TP_TRY(check_ptrs(y, p, rows && dn != nullptr));
+  TP_TRY(check_ptrs(z, p, rows && z != nullptr));
+  TP_TRY(check_ptrs(dn, p, rows && dn != nullptr));
+  TP_TRY(check_ptrs(dy, p, rows && dy != nullptr));
+  TP_TRY(check_ptrs(in(dx), p, rows && dx != nullptr));
+  TP_TRY(check_ptrs(in(dz), p, rows && dz != nullptr));
+  TP_TRY(check_ws(ws, ws_bytes, block_norm_bwd_workspace(M, h)));
+  if (h == 0) return TP_OK;
+  {
+    const size_t one = static_cast<size_t>(M / p * h), r = esize(res_dtype), o = esize(out_dtype);
+    std::vector<Range> ins, outs;
+    ins.reserve(48);
+    outs.reserve(24);
+    add_ranges(&ins, z, p, one * 2);
+    if (dn != nullptr) add_ranges(&ins, y, p, one * r);
+    add_ranges(&ins, dn, p, one * 2);
+    add_ranges(&ins, dy, p, one * r);
+    add_desc(&ins, d, h);
+    add_ranges(&outs, in(dx), p, one * r);
+    add_ranges(&outs, in(dz), p, one * 2);
+    for (void* v : {g.dw_post, g.db_post, g.dw_pre, g.db_pre}) outs.push_back({v, v ? static_cast<size_t>(h) * o : 0});
+    outs.push_back({g.dgate, g.dgate ? static_cast<size_t>(d->gate_rows * h) * o : 0});
+    outs.push_back({ws, ws_bytes});
+    if (clash(outs, ins, in(dx), dy, p, one * r)) return TP_ERR_INVALID_ARG;
+  }
+  DevInfo di;
+  TP_TRY(device_info(&di));
+  if (M == 0) {  // sums over no rows
+    for (void* v : {g.dw_post, g.db_post, g.dw_pre, g.db_pre})
+      if (v != nullptr && cudaMemsetAsync(v, 0, static_cast<size_t>(h) * esize(out_dtype), stream) != cudaSuccess)
+        return TP_ERR_CUDA;
+    if (g.dgate != nullptr &&
+        cudaMemsetAsync(g.dgate, 0, static_cast<size_t>(d->gate_rows * h) * esize(out_dtype), stream) != cudaSuccess)
+      return TP_ERR_CUDA;
+    return TP_OK;
+  }
+  NormParams P;
+  fill(&P, d, p, M, h);
+  P.has_z = z != nullptr;
+  P.has_dn = dn != nullptr;
+  P.has_dy = dy != nullptr;
+  P.out_f32 = out_dtype == TP_FP32;
+  for (int s = 0; s < p; ++s) {
+    P.x[s] = dn ? y[s] : nullptr;
+    P.z[s] = z ? z[s] : nullptr;
+    P.dn[s] = dn ? dn[s] : nullptr;
+    P.dy[s] = dy ? dy[s] : nullptr;
+    P.y[s] = dx ? dx[s] : nullptr;
+    P.n[s] = dz ? dz[s] : nullptr;
+  }
+  const Shape sh = bwd_shape(P.nvec, M);
+  const int64_t ctas = bwd_ctas(sh, M), workers = ctas * bwd_workers(sh);
+  const bool groups = d->gate != nullptr && d->gate_rows > 1;
+  float* area = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kStatusBytes);
+  const bool sums = g.dw_post || g.db_post || g.dw_pre || g.db_pre || (g.dgate && !groups);
+  P.part = sums ? area : nullptr;
+  P.gpart = g.dgate && groups ? area + 4 * ctas * h : nullptr;
+  P.dgate = g.dgate;
+  const bool ln = d->post == TP_NORM_LAYER || d->pre == TP_NORM_LAYER;
+  NormBwdLaunch L = {sh.warp, sh.nv, sh.threads, static_cast<int>(ctas), groups, ln};
+  if (res_dtype == TP_FP32) TP_TRY(ln ? block_norm_bwd_run_f32_ln(P, L, stream) : block_norm_bwd_run_f32_rms(P, L, stream));
+  else TP_TRY(ln ? block_norm_bwd_run_bf16_ln(P, L, stream) : block_norm_bwd_run_bf16_rms(P, L, stream));
+  // gate rows that one worker holds whole are written already: with a row
+  // per token that is all of them
+  const bool joins = P.gpart != nullptr && P.rows_per_gate > 1;
+  if (!sums && !joins) return TP_OK;
+  NormGradParams G;
+  std::memset(&G, 0, sizeof(G));
+  G.part = P.part;
+  G.gpart = P.gpart;
+  G.gate = static_cast<const __nv_bfloat16*>(groups ? nullptr : d->gate);
+  G.w_post = static_cast<const __nv_bfloat16*>(d->w_post);
+  G.b_post = static_cast<const __nv_bfloat16*>(d->b_post);
+  G.dw_pre = g.dw_pre;
+  G.db_pre = g.db_pre;
+  G.dw_post = g.dw_post;
+  G.db_post = g.db_post;
+  G.dgate = groups && !joins ? nullptr : g.dgate;
+  G.h = static_cast<uint32_t>(h);
+  G.ctas = static_cast<uint32_t>(ctas);
+  G.workers = static_cast<uint32_t>(workers);
+  G.M = static_cast<uint32_t>(M);
+  G.rows_per_gate = P.rows_per_gate;
+  G.groups = static_cast<uint32_t>(d->gate != nullptr ? d->gate_rows : 0);
+  G.out_f32 = P.out_f32;
+  const unsigned ny = joins ? static_cast<unsigned>(std::min<int64_t>(d->gate_rows, 64)) : 1u;
+  return launch_dependent(block_norm_grad_kernel, dim3(static_cast<unsigned>(cdiv(h, 32)), ny), 1024u, 0, stream, G);
+}

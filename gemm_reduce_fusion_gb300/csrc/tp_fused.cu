@@ -14,7 +14,11 @@
 #include <vector>
 
 #include "../../include/tp_fused.h"
+#include "block_norm.h"
+#include "ckpt.h"
 #include "gemm_kernel.cuh"
+#include "host_util.h"
+#include "w4.h"
 
 using namespace tpf;
 
@@ -22,9 +26,7 @@ namespace {
 
 // ------------------------------------------------------------------ constants
 
-constexpr int kMaxP = 8;
 constexpr int kPlanSMs = 152;            // SM count the split-K plan assumes (GB300)
-constexpr size_t kStatusBytes = 256;     // workspace head: status word, padded
 constexpr int kStagesWide = 4;           // 128x256 tiles: 48 KiB per stage
 constexpr int kPairKChunks = PAIR_BK / 64;  // 64-wide K chunks per pair k-block (K-major operand maps)
 constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
@@ -55,10 +57,6 @@ constexpr int64_t kKAlternateDepth = 8192;
 
 // ------------------------------------------------------------------ small helpers
 
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // Device wait limit: TP_DEVICE_TIMEOUT_MS from the environment (read once),
 // else 2 s; tp_debug_set(TP_DEBUG_TIMEOUT_MS, ...) overrides it.
 std::atomic<uint64_t> g_timeout_override_ns{0};
@@ -68,7 +66,6 @@ std::atomic<int64_t> g_debug_no_tail{0};    // 1: no k-slices in the last wave o
 std::atomic<int64_t> g_debug_split_k{0};    // n > 0: split-K factor of launches below one wave
 std::atomic<unsigned long long*> g_trace{nullptr};  // timeline trace buffer of the next launches
 std::atomic<int64_t> g_trace_cap{0};
-std::atomic<unsigned long long> g_launch_epoch{0};  // numbers every launch (slice counters)
 std::atomic<int64_t> g_l2_hints{1};         // 1: L2 cache policies on operand loads and output stores
 std::atomic<int64_t> g_tma_store{1};        // 1: staged epilogues leave shared memory by TMA store
 std::atomic<int64_t> g_debug_no_fuse{0};    // 1: backward dX and dW always as two launches
@@ -100,53 +97,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
       fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
   });
   return fn;
-}
-
-struct DevInfo {
-  int sms = 0;
-  bool ok = false;
-};
-
-// The calling thread's current device, with that device's primary context
-// made current on the thread.  A thread that has not yet made a CUDA call of
-// its own (an autograd worker thread, a user's thread) may have no current
-// context, and tensor-map encoding and launches from it then fail;
-// cudaSetDevice binds the primary context.
-tp_status bind_device(int* dev) {
-  int d = 0;
-  if (cudaGetDevice(&d) != cudaSuccess) return TP_ERR_CUDA;
-  if (cudaSetDevice(d) != cudaSuccess) return TP_ERR_CUDA;
-  *dev = d;
-  return TP_OK;
-}
-
-tp_status device_info(DevInfo* out) {
-  int dev = 0;
-  if (bind_device(&dev) != TP_OK) return TP_ERR_CUDA;
-  // SM count of each device seen (0: not yet queried; -1: not an sm_103 device)
-  static std::atomic<int> sm_count[64] = {};
-  if (dev >= 0 && dev < 64) {
-    const int c = sm_count[dev].load(std::memory_order_relaxed);
-    if (c > 0) {
-      out->sms = c;
-      out->ok = true;
-      return TP_OK;
-    }
-    if (c < 0) return TP_ERR_ARCH;
-  }
-  int major = 0, minor = 0, sms = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return TP_ERR_CUDA;
-  if (major != 10 || minor != 3) {
-    if (dev >= 0 && dev < 64) sm_count[dev].store(-1, std::memory_order_relaxed);
-    return TP_ERR_ARCH;
-  }
-  if (dev >= 0 && dev < 64 && sms > 0) sm_count[dev].store(sms, std::memory_order_relaxed);
-  out->sms = sms;
-  out->ok = true;
-  return TP_OK;
 }
 
 // bf16 tensor map with 128-byte swizzle over a row-major matrix with
@@ -671,8 +621,6 @@ void fill_common(GemmParams* P, const Shape& s) {
   P->trace_cap = static_cast<int32_t>(std::min<int64_t>(g_trace_cap.load(), INT32_MAX));
 }
 
-size_t esize(tp_dtype d) { return d == TP_FP32 ? 4 : 2; }
-
 // Output maps of the TMA-store epilogue for the group outputs `ptrs` (pitch
 // `ld`): one map per group output (and replica) when there are at most
 // MAX_MAPS of them, each clipped to the group's rows and columns; otherwise,
@@ -949,72 +897,22 @@ void prepare_gemm(Launch& L, tp_dtype out_dtype, void* ws) {
   }
 }
 
-// ------------------------------------------------------------------ validation
-
-struct Range {
-  const void* p;
-  size_t bytes;
+// Workspace of a backward call on checkpoints: the products' own workspace,
+// then the restored tensors (values and, for row layouts, their GeLU).
+struct CkptArea {
+  size_t gemm, tensor, end;  // bytes of the products' part, of one restored tensor, of all
+  int n;                     // restored tensors of each kind
 };
 
-bool overlap(const Range& a, const Range& b) {
-  if (a.bytes == 0 || b.bytes == 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-  return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
-
-bool any_overlap(const std::vector<Range>& outs, const std::vector<Range>& ins) {
-  for (size_t i = 0; i < outs.size(); ++i) {
-    for (const Range& r : ins)
-      if (overlap(outs[i], r)) return true;
-    for (size_t j = i + 1; j < outs.size(); ++j)
-      if (overlap(outs[i], outs[j])) return true;
-  }
-  return false;
-}
-
-tp_status check_sizes(int p, int64_t M, int64_t N, int64_t K, int64_t chunk_m, tp_dtype dt) {
-  if (p < 1 || p > kMaxP) return TP_ERR_INVALID_ARG;
-  if (M < 0 || N < 0 || K < 0 || chunk_m < 0) return TP_ERR_INVALID_ARG;
-  if (dt != TP_BF16 && dt != TP_FP32) return TP_ERR_INVALID_ARG;
-  const int64_t lim = (int64_t(1) << 31) - 1;
-  if (M > lim || N > lim || K > lim || static_cast<int64_t>(p) * K > lim) return TP_ERR_UNSUPPORTED_SHAPE;
-  if (N % 8 != 0 || K % 8 != 0) return TP_ERR_ALIGNMENT;
-  return TP_OK;
-}
-
-tp_status check_ptrs(const void* const* a, int n, bool need) {
-  if (!need) return TP_OK;
-  if (a == nullptr) return TP_ERR_INVALID_ARG;
-  for (int i = 0; i < n; ++i) {
-    if (a[i] == nullptr) return TP_ERR_INVALID_ARG;
-    if (!aligned16(a[i])) return TP_ERR_ALIGNMENT;
-  }
-  return TP_OK;
-}
-
-tp_status check_ptr(const void* a, bool need) {
-  if (!need) return TP_OK;
-  if (a == nullptr) return TP_ERR_INVALID_ARG;
-  return aligned16(a) ? TP_OK : TP_ERR_ALIGNMENT;
-}
-
-tp_status check_ws(void* ws, size_t ws_bytes, size_t need) {
-  if (ws == nullptr) return TP_ERR_INVALID_ARG;
-  if (!aligned16(ws)) return TP_ERR_ALIGNMENT;
-  if (ws_bytes < need) return TP_ERR_WORKSPACE_TOO_SMALL;
-  return TP_OK;
-}
-
-#define TP_TRY(expr)                     \
-  do {                                   \
-    tp_status _st = (expr);              \
-    if (_st != TP_OK) return _st;        \
-  } while (0)
-
-void add_ranges(std::vector<Range>* v, const void* const* a, int n, size_t bytes) {
-  if (a == nullptr) return;
-  for (int i = 0; i < n; ++i)
-    if (a[i] != nullptr) v->push_back({a[i], bytes});
+CkptArea ckpt_area(tp_op op, int p, int64_t M, int64_t N, int64_t K, int64_t chunk_m, tp_dtype dt) {
+  const bool col = op == TP_OP_COL_BWD_CKPT, ag = op == TP_OP_AG_MM_BWD_CKPT;
+  const tp_op base = col ? TP_OP_COL_BWD : ag ? TP_OP_AG_MM_BWD : op == TP_OP_ROW_BWD_CKPT ? TP_OP_ROW_BWD : TP_OP_ROW_RS_BWD;
+  CkptArea a;
+  a.gemm = (workspace_for(op_shapes(base, p, M, N, K, chunk_m, dt)) + 255) / 256 * 256;
+  a.tensor = (static_cast<size_t>((ag ? M / p : M) * K) * 2 + 255) / 256 * 256;
+  a.n = col ? 1 : p;
+  a.end = a.gemm + a.tensor * a.n * (col || ag ? 1 : 2);
+  return a;
 }
 
 int sw_variant_mk(int bn) { return bn == 16 ? V_SW_MK16 : bn == 32 ? V_SW_MK32 : V_SW_MK64; }
@@ -1173,6 +1071,16 @@ int64_t tp_choose_chunk_m_measured(int64_t M, const int64_t* chunk, const double
 size_t tp_workspace_size(tp_op op, int p, int64_t M, int64_t N, int64_t K, int64_t chunk_m,
                          tp_dtype out_dtype) {
   if (p < 1 || p > kMaxP || M < 0 || N < 0 || K < 0 || chunk_m < 0) return kStatusBytes;
+  switch (op) {
+    case TP_OP_BLOCK_NORM_BWD: return block_norm_bwd_workspace(M, N);
+    case TP_OP_COL_W4: return w4_workspace(false, p, M, N, K);
+    case TP_OP_ROW_W4: return w4_workspace(true, p, M, N, K);
+    case TP_OP_COL_BWD_CKPT:
+    case TP_OP_ROW_BWD_CKPT:
+    case TP_OP_AG_MM_BWD_CKPT:
+    case TP_OP_ROW_RS_BWD_CKPT: return ckpt_area(op, p, M, N, K, chunk_m, out_dtype).end;
+    default: break;
+  }
   if ((op == TP_OP_ROW_RS || op == TP_OP_AG_MM) && M % p != 0) return kStatusBytes;
   return workspace_for(op_shapes(op, p, M, N, K, chunk_m, out_dtype));
 }
@@ -1434,10 +1342,11 @@ static tp_status weight_grad(Launch& L, const Shape& s, const void* const* xk, c
   return TP_OK;
 }
 
-tp_status tp_col_linear_bwd(const void* x, const void* const* w, const void* const* dy, void* dx,
+static tp_status col_bwd(const void* x, const void* const* w, const void* const* dy, void* dx,
                             void* const* dw, void* const* db, int p, int64_t M, int64_t N, int64_t K,
                             int64_t chunk_m, tp_dtype out_dtype, void* ws, size_t ws_bytes,
-                            cudaStream_t stream) {
+                            cudaStream_t stream,
+                         const CkptRestore* restore) {
   TP_TRY(check_sizes(p, M, N, K, chunk_m, out_dtype));
   if (dx == nullptr && dw == nullptr && db == nullptr) return TP_ERR_INVALID_ARG;
   const bool dx_work = dx != nullptr && M > 0 && K > 0;
@@ -1464,6 +1373,7 @@ tp_status tp_col_linear_bwd(const void* x, const void* const* w, const void* con
   if (!dx_work && !dw_work && !db_work) return TP_OK;
   DevInfo di;
   TP_TRY(device_info(&di));
+  if (restore != nullptr) TP_TRY(ckpt_restore(*restore, stream));
   Launch LX, LW;
   if (dx_work) {
     Launch& L = LX;
@@ -1500,10 +1410,18 @@ tp_status tp_col_linear_bwd(const void* x, const void* const* w, const void* con
   return TP_OK;
 }
 
-tp_status tp_row_linear_bwd(const void* const* x, const void* const* w, const void* dy,
+tp_status tp_col_linear_bwd(const void* x, const void* const* w, const void* const* dy, void* dx,
+                            void* const* dw, void* const* db, int p, int64_t M, int64_t N, int64_t K,
+                            int64_t chunk_m, tp_dtype out_dtype, void* ws, size_t ws_bytes,
+                            cudaStream_t stream) {
+  return col_bwd(x, w, dy, dx, dw, db, p, M, N, K, chunk_m, out_dtype, ws, ws_bytes, stream, nullptr);
+}
+
+static tp_status row_bwd(const void* const* x, const void* const* w, const void* dy,
                             void* const* dx, void* const* dw, void* db, const void* const* preact,
                             int p, int64_t M, int64_t N, int64_t K, int64_t chunk_m,
-                            tp_dtype out_dtype, void* ws, size_t ws_bytes, cudaStream_t stream) {
+                            tp_dtype out_dtype, void* ws, size_t ws_bytes, cudaStream_t stream,
+                         const CkptRestore* restore) {
   TP_TRY(check_sizes(p, M, N, K, chunk_m, out_dtype));
   const bool dx_work = dx != nullptr && M > 0 && K > 0;
   const bool dw_work = dw != nullptr && K > 0 && N > 0;
@@ -1532,6 +1450,7 @@ tp_status tp_row_linear_bwd(const void* const* x, const void* const* w, const vo
   if (!dx_work && !dw_work && !db_work) return TP_OK;
   DevInfo di;
   TP_TRY(device_info(&di));
+  if (restore != nullptr) TP_TRY(ckpt_restore(*restore, stream));
   Launch LX, LW;
   if (dx_work) {
     Launch& L = LX;
@@ -1573,16 +1492,24 @@ tp_status tp_row_linear_bwd(const void* const* x, const void* const* w, const vo
   return TP_OK;
 }
 
+tp_status tp_row_linear_bwd(const void* const* x, const void* const* w, const void* dy,
+                            void* const* dx, void* const* dw, void* db, const void* const* preact,
+                            int p, int64_t M, int64_t N, int64_t K, int64_t chunk_m,
+                            tp_dtype out_dtype, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  return row_bwd(x, w, dy, dx, dw, db, preact, p, M, N, K, chunk_m, out_dtype, ws, ws_bytes, stream, nullptr);
+}
+
 }  // extern "C"
 
 
 // ---------------------------------------------------------------- sequence-parallel backward
 
-extern "C" tp_status tp_ag_matmul_bwd(const void* const* x, const void* const* w, const void* const* dy,
+static tp_status ag_bwd(const void* const* x, const void* const* w, const void* const* dy,
                                       void* const* dx, void* const* dw, void* const* db, int p,
                                       int64_t M, int64_t N, int64_t K, int64_t chunk_m,
                                       tp_dtype out_dtype, void* ws, size_t ws_bytes,
-                                      cudaStream_t stream) {
+                                      cudaStream_t stream,
+                        const CkptRestore* restore) {
   TP_TRY(check_sizes(p, M, N, K, chunk_m, out_dtype));
   if (M % p != 0) return TP_ERR_UNSUPPORTED_SHAPE;
   if (dx == nullptr && dw == nullptr && db == nullptr) return TP_ERR_INVALID_ARG;
@@ -1611,6 +1538,7 @@ extern "C" tp_status tp_ag_matmul_bwd(const void* const* x, const void* const* w
   if (!dx_work && !dw_work && !db_work) return TP_OK;
   DevInfo di;
   TP_TRY(device_info(&di));
+  if (restore != nullptr) TP_TRY(ckpt_restore(*restore, stream));
   Launch LX, LW;
   if (dx_work) {
     Launch& L = LX;
@@ -1672,13 +1600,22 @@ extern "C" tp_status tp_ag_matmul_bwd(const void* const* x, const void* const* w
   return TP_OK;
 }
 
-extern "C" tp_status tp_row_linear_bwd_reducescatter(const void* const* x, const void* const* w,
+extern "C" tp_status tp_ag_matmul_bwd(const void* const* x, const void* const* w, const void* const* dy,
+                                      void* const* dx, void* const* dw, void* const* db, int p,
+                                      int64_t M, int64_t N, int64_t K, int64_t chunk_m,
+                                      tp_dtype out_dtype, void* ws, size_t ws_bytes,
+                                      cudaStream_t stream) {
+  return ag_bwd(x, w, dy, dx, dw, db, p, M, N, K, chunk_m, out_dtype, ws, ws_bytes, stream, nullptr);
+}
+
+static tp_status row_rs_bwd(const void* const* x, const void* const* w,
                                                      const void* const* dy, void* const* dx,
                                                      void* const* dw, void* db,
                                                      const void* const* preact, int p, int64_t M,
                                                      int64_t N, int64_t K, int64_t chunk_m,
                                                      tp_dtype out_dtype, void* ws, size_t ws_bytes,
-                                                     cudaStream_t stream) {
+                                                     cudaStream_t stream,
+                            const CkptRestore* restore) {
   TP_TRY(check_sizes(p, M, N, K, chunk_m, out_dtype));
   if (M % p != 0) return TP_ERR_UNSUPPORTED_SHAPE;
   if (dx == nullptr && dw == nullptr && db == nullptr) return TP_ERR_INVALID_ARG;
@@ -1709,6 +1646,7 @@ extern "C" tp_status tp_row_linear_bwd_reducescatter(const void* const* x, const
   if (!dx_work && !dw_work && !db_work) return TP_OK;
   DevInfo di;
   TP_TRY(device_info(&di));
+  if (restore != nullptr) TP_TRY(ckpt_restore(*restore, stream));
   const size_t es = esize(out_dtype);
   Launch LX, LW;
   if (dx_work) {
@@ -1781,6 +1719,16 @@ extern "C" tp_status tp_row_linear_bwd_reducescatter(const void* const* x, const
   // db = sum over the p token shards of dY, in shard order, of their rows
   if (db_work) TP_TRY(bias_grad(dy, p, p, &db, Mp, N, out_dtype, stream));
   return TP_OK;
+}
+
+extern "C" tp_status tp_row_linear_bwd_reducescatter(const void* const* x, const void* const* w,
+                                                     const void* const* dy, void* const* dx,
+                                                     void* const* dw, void* db,
+                                                     const void* const* preact, int p, int64_t M,
+                                                     int64_t N, int64_t K, int64_t chunk_m,
+                                                     tp_dtype out_dtype, void* ws, size_t ws_bytes,
+                                                     cudaStream_t stream) {
+  return row_rs_bwd(x, w, dy, dx, dw, db, preact, p, M, N, K, chunk_m, out_dtype, ws, ws_bytes, stream, nullptr);
 }
 
 // ====================================================================== unfused baseline
@@ -1925,4 +1873,120 @@ extern "C" tp_status tp_noalloc_device_status(cudaStream_t stream) {
   void* scratch = nullptr;
   TP_TRY(noalloc_scratch(&scratch));
   return tp_get_device_status(scratch, stream);
+}
+
+// ---------------------------------------------------------------- backward from 8-bit checkpoints
+
+namespace {
+
+// What the four calls share: the checks of the packed tensors and of the
+// workspace, and the places of the restored ones in it.
+struct CkptCall {
+  CkptArea area;
+  void* plain[kMaxP];
+  void* gelu[kMaxP];
+};
+
+tp_status ckpt_call(tp_op op, const void* const* q, const void* const* e, bool need, const std::vector<Range>& outs, int p, int64_t M,
+                    int64_t N, int64_t K, int64_t chunk_m, tp_dtype dt, void* ws, size_t ws_bytes, CkptCall* c) {
+  TP_TRY(check_sizes(p, M, N, K, chunk_m, dt));
+  if ((op == TP_OP_AG_MM_BWD_CKPT || op == TP_OP_ROW_RS_BWD_CKPT) && M % p != 0) return TP_ERR_UNSUPPORTED_SHAPE;
+  c->area = ckpt_area(op, p, M, N, K, chunk_m, dt);
+  const int n = c->area.n;
+  const int64_t rows = op == TP_OP_AG_MM_BWD_CKPT ? M / p : M;
+  need = need && M > 0 && K > 0;
+  TP_TRY(check_ptrs(q, n, need));
+  if (need) {
+    if (e == nullptr) return TP_ERR_INVALID_ARG;
+    for (int i = 0; i < n; ++i)
+      if (e[i] == nullptr) return TP_ERR_INVALID_ARG;
+  }
+  TP_TRY(check_ws(ws, ws_bytes, c->area.end));
+  std::vector<Range> ins, written = outs;
+  if (need) {
+    add_ranges(&ins, q, n, static_cast<size_t>(rows * K));
+    add_ranges(&ins, e, n, static_cast<size_t>(rows * cdiv(K, 32)));
+  }
+  written.push_back({ws, ws_bytes});
+  if (any_overlap(written, ins)) return TP_ERR_INVALID_ARG;
+  uint8_t* at = static_cast<uint8_t*>(ws) + c->area.gemm;
+  for (int i = 0; i < n; ++i) {
+    c->plain[i] = at + c->area.tensor * i;
+    c->gelu[i] = at + c->area.tensor * (n + i);
+  }
+  return TP_OK;
+}
+
+const void* const* in(void* const* a) { return const_cast<const void* const*>(a); }
+
+// Row layouts: the packed tensors are H (epi == TP_EPI_DGELU) or the layer's
+// inputs themselves.
+tp_status row_ckpt(bool rs, const void* const* q, const void* const* e, const void* const* w, const void* const* dy, void* const* dx,
+                   void* const* dw, void* db, tp_epilogue epi, int p, int64_t M, int64_t N, int64_t K, int64_t chunk_m,
+                   tp_dtype dt, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (epi != TP_EPI_NONE && epi != TP_EPI_DGELU) return TP_ERR_INVALID_ARG;
+  const bool act = epi == TP_EPI_DGELU;
+  TP_TRY(check_sizes(p, M, N, K, chunk_m, dt));
+  std::vector<Range> outs;
+  add_ranges(&outs, in(dx), p, static_cast<size_t>(M * K) * esize(dt));
+  add_ranges(&outs, in(dw), p, static_cast<size_t>(K * N) * esize(dt));
+  outs.push_back({db, db ? static_cast<size_t>(N) * esize(dt) : 0});
+  CkptCall c;
+  const bool need_h = act && dx != nullptr, need_x = dw != nullptr;
+  TP_TRY(ckpt_call(rs ? TP_OP_ROW_RS_BWD_CKPT : TP_OP_ROW_BWD_CKPT, q, e, need_h || need_x, outs, p, M, N, K, chunk_m, dt, ws, ws_bytes,
+                   &c));
+  const bool plain = need_h || (need_x && !act), gelu = need_x && act;
+  const CkptRestore r = {q, e, plain ? c.plain : nullptr, gelu ? c.gelu : nullptr, p, M, K};
+  const void* const* x = in(act ? c.gelu : c.plain);
+  const void* const* h = need_h ? in(c.plain) : nullptr;
+  const CkptRestore* restore = need_h || need_x ? &r : nullptr;
+  if (rs) return row_rs_bwd(x, w, dy, dx, dw, db, h, p, M, N, K, chunk_m, dt, ws, c.area.gemm, stream, restore);
+  return row_bwd(x, w, dy ? dy[0] : nullptr, dx, dw, db, h, p, M, N, K, chunk_m, dt, ws, c.area.gemm, stream, restore);
+}
+
+}  // namespace
+
+extern "C" tp_status tp_col_linear_bwd_ckpt(const void* q, const void* e, const void* const* w, const void* const* dy, void* dx,
+                                            void* const* dw, void* const* db, int p, int64_t M, int64_t N, int64_t K,
+                                            int64_t chunk_m, tp_dtype out_dtype, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  TP_TRY(check_sizes(p, M, N, K, chunk_m, out_dtype));
+  std::vector<Range> outs;
+  outs.push_back({dx, dx ? static_cast<size_t>(M * K) * esize(out_dtype) : 0});
+  add_ranges(&outs, in(dw), p, static_cast<size_t>(K * N) * esize(out_dtype));
+  add_ranges(&outs, in(db), p, static_cast<size_t>(N) * esize(out_dtype));
+  CkptCall c;
+  TP_TRY(ckpt_call(TP_OP_COL_BWD_CKPT, &q, &e, dw != nullptr, outs, p, M, N, K, chunk_m, out_dtype, ws, ws_bytes, &c));
+  const CkptRestore r = {&q, &e, c.plain, nullptr, 1, M, K};
+  return col_bwd(dw ? c.plain[0] : nullptr, w, dy, dx, dw, db, p, M, N, K, chunk_m, out_dtype, ws, c.area.gemm, stream,
+                 dw ? &r : nullptr);
+}
+
+extern "C" tp_status tp_row_linear_bwd_ckpt(const void* const* q, const void* const* e, const void* const* w, const void* dy,
+                                            void* const* dx, void* const* dw, void* db, tp_epilogue epi, int p, int64_t M,
+                                            int64_t N, int64_t K, int64_t chunk_m, tp_dtype out_dtype, void* ws, size_t ws_bytes,
+                                            cudaStream_t stream) {
+  return row_ckpt(false, q, e, w, &dy, dx, dw, db, epi, p, M, N, K, chunk_m, out_dtype, ws, ws_bytes, stream);
+}
+
+extern "C" tp_status tp_ag_matmul_bwd_ckpt(const void* const* q, const void* const* e, const void* const* w, const void* const* dy,
+                                           void* const* dx, void* const* dw, void* const* db, int p, int64_t M, int64_t N,
+                                           int64_t K, int64_t chunk_m, tp_dtype out_dtype, void* ws, size_t ws_bytes,
+                                           cudaStream_t stream) {
+  TP_TRY(check_sizes(p, M, N, K, chunk_m, out_dtype));
+  std::vector<Range> outs;
+  add_ranges(&outs, in(dx), p, static_cast<size_t>(M / p * K) * esize(out_dtype));
+  add_ranges(&outs, in(dw), p, static_cast<size_t>(K * N) * esize(out_dtype));
+  add_ranges(&outs, in(db), p, static_cast<size_t>(N) * esize(out_dtype));
+  CkptCall c;
+  TP_TRY(ckpt_call(TP_OP_AG_MM_BWD_CKPT, q, e, dw != nullptr, outs, p, M, N, K, chunk_m, out_dtype, ws, ws_bytes, &c));
+  const CkptRestore r = {q, e, c.plain, nullptr, p, M / p, K};
+  return ag_bwd(in(c.plain), w, dy, dx, dw, db, p, M, N, K, chunk_m, out_dtype, ws, c.area.gemm, stream, dw ? &r : nullptr);
+}
+
+extern "C" tp_status tp_row_linear_bwd_reducescatter_ckpt(const void* const* q, const void* const* e, const void* const* w,
+                                                          const void* const* dy, void* const* dx, void* const* dw, void* db,
+                                                          tp_epilogue epi, int p, int64_t M, int64_t N, int64_t K,
+                                                          int64_t chunk_m, tp_dtype out_dtype, void* ws, size_t ws_bytes,
+                                                          cudaStream_t stream) {
+  return row_ckpt(true, q, e, w, dy, dx, dw, db, epi, p, M, N, K, chunk_m, out_dtype, ws, ws_bytes, stream);
 }

@@ -111,8 +111,21 @@ typedef enum {
   TP_OP_AG_MM = 5,   /* tp_ag_matmul */
   TP_OP_ROW_AR_UNFUSED = 6, /* tp_row_linear_fwd_unfused */
   TP_OP_AG_MM_BWD = 7,      /* tp_ag_matmul_bwd */
-  TP_OP_ROW_RS_BWD = 8      /* tp_row_linear_bwd_reducescatter */
+  TP_OP_ROW_RS_BWD = 8,     /* tp_row_linear_bwd_reducescatter */
+  TP_OP_BLOCK_NORM_BWD = 9, /* tp_block_norm_bwd (N = h, K not used) */
+  TP_OP_COL_BWD_CKPT = 10,  /* tp_col_linear_bwd_ckpt */
+  TP_OP_ROW_BWD_CKPT = 11,  /* tp_row_linear_bwd_ckpt */
+  TP_OP_AG_MM_BWD_CKPT = 12,   /* tp_ag_matmul_bwd_ckpt */
+  TP_OP_ROW_RS_BWD_CKPT = 13,  /* tp_row_linear_bwd_reducescatter_ckpt */
+  TP_OP_COL_W4 = 14,        /* tp_col_linear_fwd_w4 */
+  TP_OP_ROW_W4 = 15         /* tp_row_linear_fwd_w4 */
 } tp_op;
+
+typedef enum {
+  TP_NORM_NONE = 0,
+  TP_NORM_RMS = 1,   /* v / sqrt(mean(v^2) + eps) */
+  TP_NORM_LAYER = 2  /* (v - mean v) / sqrt(var v + eps) */
+} tp_norm;
 
 /* Bytes of device workspace the call (op, p, M, N, K, chunk_m, out_dtype)
  * needs, with M, N, K meant as in that call.  Always >= 256 (the status
@@ -235,6 +248,145 @@ tp_status tp_row_linear_bwd_reducescatter(const void* const* x, const void* cons
                                           int64_t N,
                                           int64_t K, int64_t chunk_m, tp_dtype out_dtype, void* ws,
                                           size_t ws_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The boundary between two blocks: the norm after a block with its gate and
+ * residual scale, the residual addition, and the norm before the next block.
+ *   y = x + alpha * gate * N_post(z),   n = N_pre(y)
+ *   N(v) = hat(v) * w + b, hat by the kind of norm; TP_NORM_NONE: N(v) = v.
+ * Statistics and sums are fp32; n is formed from the unrounded y; every
+ * output is rounded once.  The tensors are p row shards of M/p tokens (the
+ * token shards of the ReduceScatter layouts; p = 1 for a full tensor), all
+ * served by one launch.  M % p == 0, h % 8 == 0, h <= TP_BLOCK_NORM_MAX_H.
+ * The residual stream (x, y, dy, dx) is bf16 or fp32 (`res_dtype`); z, n and
+ * their gradients are bf16, the types of the products around them.
+ *   w_post, b_post, w_pre, b_pre: [h] bf16, or NULL (ones, zeros); weights
+ *     only with a norm, biases only with TP_NORM_LAYER.
+ *   gate: [gate_rows, h] bf16, or NULL (ones).  Token i of the M uses row
+ *     i / (M / gate_rows): 1 row is a gate per channel, one row per sequence
+ *     an adaptive gate, M rows a gate per token.  M % gate_rows == 0.       */
+#define TP_BLOCK_NORM_MAX_H 16384
+typedef struct {
+  tp_norm post, pre;
+  const void *w_post, *b_post, *w_pre, *b_pre, *gate;
+  int64_t gate_rows;
+  float alpha, eps;
+} tp_block_norm_desc;
+
+/* Gradients of the descriptor's vectors, in out_dtype; each may be NULL. */
+typedef struct {
+  void *dw_post, *db_post, *dw_pre, *db_pre, *dgate;
+} tp_block_norm_grads;
+
+/*   x[s], y[s]: [M/p, h] in res_dtype; z[s], n[s]: [M/p, h] bf16.
+ *   z == NULL (then y == NULL, post == TP_NORM_NONE, no gate): n = N_pre(x).
+ *   n == NULL (then pre == TP_NORM_NONE): y alone, after the last block.
+ *   y[s] == x[s] updates the stream in place; no other overlap.            */
+tp_status tp_block_norm_fwd(const void* const* x, const void* const* z, void* const* y, void* const* n,
+                            const tp_block_norm_desc* d, int p, int64_t M, int64_t h, tp_dtype res_dtype,
+                            cudaStream_t stream);
+
+/* Gradients, from the tensors the forward pass leaves anyway (statistics are
+ * formed again: the rows are read for the gradients in any case).
+ *   y[s]: the stream after the boundary (x of the forward pass when z is
+ *         NULL), read when dn is given; z[s]: as in the forward pass;
+ *   dn[s]: gradient of n, or NULL (then pre == TP_NORM_NONE);
+ *   dy[s]: gradient of y from its later uses, or NULL; dn or dy is given.
+ *   dx[s] = dy[s] + N_pre'(dn[s]) -> gradient of x (dx[s] == dy[s] allowed);
+ *   dz[s] -> gradient of z; each of dx, dz and the grads may be NULL, not
+ *   all.  The descriptor is the forward pass's; b_pre is not read and may be
+ *   NULL.  Column sums run in a fixed order (ws of TP_OP_BLOCK_NORM_BWD, which
+ *   need not be zero-filled).                                              */
+tp_status tp_block_norm_bwd(const void* const* z, const void* const* y, const void* const* dn,
+                            const void* const* dy, void* const* dx, void* const* dz,
+                            const tp_block_norm_desc* d, const tp_block_norm_grads* grads, int p, int64_t M,
+                            int64_t h, tp_dtype res_dtype, tp_dtype out_dtype, void* ws, size_t ws_bytes,
+                            cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Activation checkpoints in 8 bits.  Groups of 32 columns of a row share a
+ * power of two:
+ *   value = q * 2^(e - 126),  q int8 [M, N], e uint8 [M, ceil(N/32)];
+ *   2^(e - 126) is the smallest power of two whose 127-fold reaches the
+ *   group's largest magnitude, and at least 2^-126; q is rounded to nearest
+ *   even.  e == 255 marks a group that held an infinity or NaN and is
+ *   restored as NaN.  A restored value is exactly a bf16.
+ * q is 16-byte aligned; e has no alignment.  1 <= p <= 8 tensors a call.    */
+tp_status tp_ckpt_pack(const void* const* x, void* const* q, void* const* e, int p, int64_t M, int64_t N,
+                       cudaStream_t stream);
+
+/* y[i] = value (TP_EPI_NONE) or GeLU(value) (TP_EPI_GELU), [M, N] bf16. */
+tp_status tp_ckpt_unpack(const void* const* q, const void* const* e, void* const* y, tp_epilogue epi, int p,
+                         int64_t M, int64_t N, cudaStream_t stream);
+
+/* The backward calls on checkpoints.  As tp_col_linear_bwd, tp_ag_matmul_bwd,
+ * tp_row_linear_bwd and tp_row_linear_bwd_reducescatter, with the saved
+ * activations given packed:
+ *   column layouts: (q, e) hold x: X [M, K], or the shards X_s [M/p, K];
+ *   row layouts, TP_EPI_DGELU: (q[r], e[r]) hold the pre-activation H_r
+ *     [M, K], which serves both products:
+ *       dx[r] = dY . A_r^T * GeLU'(H_r),  dw[r] = GeLU(H_r)^T . dY;
+ *   row layouts, TP_EPI_NONE: (q[r], e[r]) hold the layer's input X_r.
+ * GeLU(H_r) is rounded to bf16, as the forward pass's own activation was.
+ * The workspace (TP_OP_..._CKPT) holds the restored tensors as well.        */
+tp_status tp_col_linear_bwd_ckpt(const void* q, const void* e, const void* const* w, const void* const* dy,
+                                 void* dx, void* const* dw, void* const* db, int p, int64_t M, int64_t N,
+                                 int64_t K, int64_t chunk_m, tp_dtype out_dtype, void* ws, size_t ws_bytes,
+                                 cudaStream_t stream);
+tp_status tp_row_linear_bwd_ckpt(const void* const* q, const void* const* e, const void* const* w,
+                                 const void* dy, void* const* dx, void* const* dw, void* db,
+                                 tp_epilogue epi, int p, int64_t M, int64_t N, int64_t K, int64_t chunk_m,
+                                 tp_dtype out_dtype, void* ws, size_t ws_bytes, cudaStream_t stream);
+tp_status tp_ag_matmul_bwd_ckpt(const void* const* q, const void* const* e, const void* const* w,
+                                const void* const* dy, void* const* dx, void* const* dw, void* const* db,
+                                int p, int64_t M, int64_t N, int64_t K, int64_t chunk_m, tp_dtype out_dtype,
+                                void* ws, size_t ws_bytes, cudaStream_t stream);
+tp_status tp_row_linear_bwd_reducescatter_ckpt(const void* const* q, const void* const* e,
+                                               const void* const* w, const void* const* dy,
+                                               void* const* dx, void* const* dw, void* db, tp_epilogue epi,
+                                               int p, int64_t M, int64_t N, int64_t K, int64_t chunk_m,
+                                               tp_dtype out_dtype, void* ws, size_t ws_bytes,
+                                               cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The sharded Linear with 4-bit weights, for a few tokens.  A shard W [K, N]
+ * is kept as (q, s) with groups of G = 32, 64 or 128 rows of a column:
+ *   W[k, n] = (nibble - 8) * scale(n, k / G)
+ *   q: uint8 [ceil(N/32), ceil(K/64), 1024].  Tile (a, b) holds the columns
+ *      32 a.. and rows 64 b.. as 256 little-endian 32-bit words in the order
+ *      (f, i, t, d, j); nibble 4 v + 2 u + r (0 the lowest) of a word is
+ *        k = 64 b + 32 d + 8 t + 4 j + 2 u + v,  n = 32 a + 16 f + 8 r + i
+ *      with f, r, d, j, u, v in 0..1, i in 0..7, t in 0..3.
+ *   s: bf16 [ceil(N/32), ceil(K/G), 32]; column n = 32 a + 16 f + 8 r + i at
+ *      16 f + 2 i + r.
+ * Past K and N any nibble and scale is allowed.  Both are 16-byte aligned.
+ * The sums are fp32; a scale multiplies its group's fp32 sum.               */
+
+/* Y_k = X . W_k (+ b_k), optionally GeLU (TP_EPI_GELU); arguments as in
+ * tp_col_linear_fwd.  M <= 64 (TP_ERR_UNSUPPORTED_SHAPE above: unpack the
+ * weights and call tp_col_linear_fwd).                                     */
+tp_status tp_col_linear_fwd_w4(const void* x, const void* const* q, const void* const* s,
+                               const void* const* bias, void* const* y, tp_epilogue epi, int p, int64_t M,
+                               int64_t N, int64_t K, int64_t group, tp_dtype out_dtype, void* ws,
+                               size_t ws_bytes, cudaStream_t stream);
+
+/* Y = sum_r X_r . W_r (+ b), written once; arguments as in
+ * tp_row_linear_fwd_allreduce with n_out = 1.  M <= 64.                    */
+tp_status tp_row_linear_fwd_w4(const void* const* x, const void* const* q, const void* const* s,
+                               const void* bias, void* y, int p, int64_t M, int64_t N, int64_t K,
+                               int64_t group, tp_dtype out_dtype, void* ws, size_t ws_bytes,
+                               cudaStream_t stream);
+
+/* (q, s) of bf16 weights w[r] [K, N]: scale = max|w| / 7 of the group,
+ * rounded to bf16, and nibble - 8 = w / scale rounded to nearest even, in
+ * -7..7.  A group with an infinity or NaN gets a NaN scale.                */
+tp_status tp_w4_pack(const void* const* w, void* const* q, void* const* s, int p, int64_t N, int64_t K,
+                     int64_t group, cudaStream_t stream);
+
+/* w[r] [K, N] bf16 of (q[r], s[r]), each product rounded once: for prompts
+ * of many tokens, whose products run on the tensor cores in bf16.          */
+tp_status tp_w4_unpack(const void* const* q, const void* const* s, void* const* w, int p, int64_t N,
+                       int64_t K, int64_t group, cudaStream_t stream);
 
 /* Unfused baseline of the row-parallel MatMul+AllReduce, for measurement
  * and for the output-error comparison against it.
