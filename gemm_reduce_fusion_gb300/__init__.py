@@ -169,7 +169,8 @@ def _arr(ts) -> ctypes.Array | None:
 def _stream(stream) -> int:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # as below, without a Stream object
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -510,8 +511,8 @@ def tp_noalloc_device_status(stream=None) -> int:
 # ------------------------------------------------------------------ around the sharded Linear
 #
 # The calls below take few microseconds on the device when they serve single
-# tokens, so their checks go through one loop per list and read each property
-# of a tensor once.
+# tokens, so their checks read each property of a tensor once and go through
+# _refuse, which finds the words, only when something is wrong.
 
 def _list(where: str, name: str, ts, count: int, shape, dtype, dev: int):
     """The C array of `count` tensors of one shape and dtype (None: NULL)."""
@@ -519,10 +520,12 @@ def _list(where: str, name: str, ts, count: int, shape, dtype, dev: int):
         return None
     if len(ts) != count:
         raise ValueError(f"{where}: {name} holds {len(ts)} tensors, expected {count}")
+    arr = (ctypes.c_void_p * count)()
     for i, t in enumerate(ts):
         if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
             _refuse(where, f"{name}[{i}]", t, shape, dtype, dev)
-    return (ctypes.c_void_p * count)(*[t.data_ptr() for t in ts])
+        arr[i] = t.data_ptr()
+    return arr
 
 
 def _one(where: str, name: str, t, shape, dtype, dev: int):
@@ -538,26 +541,27 @@ def _refuse(where: str, name: str, t, shape, dtype, dev: int) -> None:
     raise TypeError(f"{where}: {name} must be {str(dtype).replace('torch.', '')}, got {t.dtype}")
 
 
-def _norm_args(where, h, post, w_post, b_post, pre, w_pre, b_pre, gate, alpha, eps, dev):
-    import torch
-    bf = torch.bfloat16
-    rows = 0
+def _norm_args(where, h, post, w_post, b_post, pre, w_pre, b_pre, gate, alpha, eps, bf, dev):
+    rows, v = 0, (h,)
     if gate is not None:
         if gate.dim() != 2:
             raise ValueError(f"{where}: gate is [rows, h], got {tuple(gate.shape)}")
         rows = gate.shape[0]
-    return _NormDesc(post, pre, _one(where, "w_post", w_post, (h,), bf, dev), _one(where, "b_post", b_post, (h,), bf, dev),
-                     _one(where, "w_pre", w_pre, (h,), bf, dev), _one(where, "b_pre", b_pre, (h,), bf, dev),
-                     _one(where, "gate", gate, (rows, h), bf, dev), rows, alpha, eps)
+        gate = _one(where, "gate", gate, (rows, h), bf, dev)
+    return _NormDesc(post, pre, w_post if w_post is None else _one(where, "w_post", w_post, v, bf, dev),
+                     b_post if b_post is None else _one(where, "b_post", b_post, v, bf, dev),
+                     w_pre if w_pre is None else _one(where, "w_pre", w_pre, v, bf, dev),
+                     b_pre if b_pre is None else _one(where, "b_pre", b_pre, v, bf, dev), gate, rows, alpha, eps)
 
 
-def _residual(where, t):
-    import torch
+def _residual(where, t, torch):
     if t.dim() != 2:
         raise ValueError(f"{where}: a token shard is [tokens, h], got {tuple(t.shape)}")
-    if t.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"{where}: the residual stream is bfloat16 or float32, got {t.dtype}")
-    return t.shape[0], t.shape[1], t.dtype, TP_FP32 if t.dtype is torch.float32 else TP_BF16
+    if t.dtype is torch.bfloat16:
+        return *t.shape, torch.bfloat16, TP_BF16
+    if t.dtype is torch.float32:
+        return *t.shape, torch.float32, TP_FP32
+    raise TypeError(f"{where}: the residual stream is bfloat16 or float32, got {t.dtype}")
 
 
 def tp_block_norm_fwd(x: Sequence, z, y, n, *, post: int = TP_NORM_NONE, w_post=None, b_post=None,
@@ -570,9 +574,9 @@ def tp_block_norm_fwd(x: Sequence, z, y, n, *, post: int = TP_NORM_NONE, w_post=
     for token i of the M = p * len(x[0]) tokens.  y[s] may be x[s]."""
     import torch
     W, dev, p = "tp_block_norm_fwd", _current_device(), len(x)
-    m, h, dtype, code = _residual(W, x[0])
-    d = _norm_args(W, h, post, w_post, b_post, pre, w_pre, b_pre, gate, alpha, eps, dev)
+    m, h, dtype, code = _residual(W, x[0], torch)
     shape, bf = (m, h), torch.bfloat16
+    d = _norm_args(W, h, post, w_post, b_post, pre, w_pre, b_pre, gate, alpha, eps, bf, dev)
     _check(_lib.tp_block_norm_fwd(_list(W, "x", x, p, shape, dtype, dev), _list(W, "z", z, p, shape, bf, dev),
                                   _list(W, "y", y, p, shape, dtype, dev), _list(W, "n", n, p, shape, bf, dev),
                                   ctypes.byref(d), p, p * m, h, code, _stream(stream)), W)
@@ -595,8 +599,9 @@ def tp_block_norm_bwd(z, y, dn, dy, dx, dz, ws, *, post: int = TP_NORM_NONE, w_p
     if first is None:
         raise ValueError(f"{W}: one of y, dy and dx is given")
     p = len(first)
-    m, h, dtype, code = _residual(W, first[0])
-    d = _norm_args(W, h, post, w_post, b_post, pre, w_pre, b_pre, gate, alpha, eps, dev)
+    m, h, dtype, code = _residual(W, first[0], torch)
+    shape, bf = (m, h), torch.bfloat16
+    d = _norm_args(W, h, post, w_post, b_post, pre, w_pre, b_pre, gate, alpha, eps, bf, dev)
     vectors = (dw_post, db_post, dw_pre, db_pre, dgate)
     out = next((t.dtype for t in vectors if t is not None), torch.float32)
     names = ("dw_post", "db_post", "dw_pre", "db_pre")
@@ -604,7 +609,6 @@ def tp_block_norm_bwd(z, y, dn, dy, dx, dz, ws, *, post: int = TP_NORM_NONE, w_p
                    _one(W, "dgate", dgate, gate.shape if gate is not None else (0, h), out, dev))
     _need_ws(W, ws, dev)
     wp, wb = _ws(ws)
-    shape, bf = (m, h), torch.bfloat16
     _check(_lib.tp_block_norm_bwd(_list(W, "z", z, p, shape, bf, dev), _list(W, "y", y, p, shape, dtype, dev),
                                   _list(W, "dn", dn, p, shape, bf, dev), _list(W, "dy", dy, p, shape, dtype, dev),
                                   _list(W, "dx", dx, p, shape, dtype, dev), _list(W, "dz", dz, p, shape, bf, dev),

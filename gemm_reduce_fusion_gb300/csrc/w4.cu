@@ -13,16 +13,32 @@
 // Layout (32 columns x 64 rows a tile of 1024 bytes): a lane's 16 bytes are
 // its A fragments of four mma, so that weights go from memory to registers
 // without a shuffle or a transposition.  A word holds the rows 8 t + 4 j ..
-// + 3 (of 32) of the columns i and i + 8, in the order that makes
-//   ((word >> 4 r) & 0x000F000F) | 0x43004300
-// the bf16 pair 128 + q of fragment register r; subtracting 136 leaves q - 8
-// exactly.  The scale is applied to the group's fp32 sum (once in G rows
-// instead of once a weight), so no product is rounded before it is added.
+// + 3 (of 32) of the columns i and i + 8, two rows of one column to a
+// fragment register.  The bits of a bf16 below 256 are its value in units of
+// 2^-133 (subnormals and the first binade), so that a masked nibble is the
+// bf16 q * 2^-133 (column i) or 16 q * 2^-133 (column i + 8) as it stands.
+// The logic instructions that take, two issue cycles each, are what bounds
+// the kernel beside HBM, and there are two ways to go on from there:
+//   few tokens (NS = 4): the masked nibbles are the operands, and the tokens
+//     are multiplied by 2^64 instead, which keeps the products normal; the
+//     8 that a nibble stands above its value comes off as 8 sum(x), from one
+//     more mma for all strips.  (A token's element of 2^64 or more becomes
+//     infinite here, one below 2^-56 loses its last bits.)
+//   more tokens: one fused multiply-add of a pair,
+//       2^127 * (word & 0x000F000F) - 2^-3 = (q - 8) / 64
+//       2^127 * (word & 0x00F000F0) - 2    = (q - 8) / 4,
+//     exact, gives operands that need nothing of the tokens.
+// The scale, with the power of two that is left over, is applied to the
+// group's fp32 sum (once in G rows instead of once a weight), so no product
+// is rounded before it is added.
 //
-// The work, blocks of 256 columns x stages of 128 rows (of every rank), is
-// cut into equal runs of stages, one for each thread block, whatever the
-// shapes: a block of columns that several thread blocks share is summed by
-// the last of them to finish, in a fixed order.
+// The work, blocks of columns x stages of rows (of every rank), is cut into
+// equal runs of stages, one for each thread block, whatever the shapes.  A
+// column block that several runs share is added up by a second kernel, in
+// the order of the runs.  (Several shorter runs to a thread block, taken
+// from a counter, would even out the SMs' unequal shares of HBM's bandwidth,
+// up to 20 %; the sums at their ends cost as much: 66 to 69 us at 1 token,
+// 97 to 101 us at 16, p = 8, 12288 -> 49152.)
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -38,11 +54,36 @@ using namespace tpf;
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kCols = 32 * kWarps;  // columns of a thread block
-constexpr int kStageK = 128;        // rows of a stage
-constexpr int kXPitch = kStageK * 2 + 64;  // bytes of a token's row in shared memory (lanes of two tokens hit different banks)
 constexpr int kMaxTokens = 64;
 constexpr int kSMs = 152;
+
+// How a thread block is divided for NT tiles of 8 tokens and scale groups of
+// 32 GB rows.  A warp owns NS strips of 16 columns (as many as the sums of NT
+// tiles leave registers for) and, with few tokens, half of a stage's rows.
+// It streams its weights in pieces of 64 rows; a lane fills and empties its
+// own part of the PIECES buffers, and refills each for the next stage as soon
+// as it has been used.  Only the tokens, shared by all warps, need a barrier,
+// one a stage.
+template <int NT, int GB>
+struct Shape {
+  static constexpr int NS = NT <= 2 ? 4 : NT <= 4 ? 2 : 1;
+  static constexpr int KH = NT <= 2 ? 2 : 1;               // row halves
+  static constexpr int PIECES = NT <= 2 && GB == 1 ? 2 : 4;
+  static constexpr int NO = NS / KH;                       // strips a warp finishes
+  static constexpr bool RAW = NS == 4;                     // nibbles as operands, tokens times 2^64
+  static constexpr int kStrips = kWarps / KH * NS;         // strips of a block
+  static constexpr int kStageK = 64 * PIECES * KH;         // rows of a stage
+  static constexpr int kXPitch = kStageK * 2 + 64;         // bytes of a token's row: lanes of two tokens hit different banks
+  static constexpr int kGroups = 2 * PIECES / GB;          // scale groups of a warp's stage
+  // shared memory: the pieces, then two stages of scales and tokens
+  static constexpr int kPiece = kWarps * NS * 512, kS = kWarps * NS * kGroups * 32, kX = NT * 8 * kXPitch;
+  static constexpr int kBytes = PIECES * kPiece + 2 * (kS + kX);
+  static_assert(NS * kGroups * 2 <= 32, "a lane copies 16 bytes of the warp's scales");
+  static_assert(2 * (kBytes + 2048) <= 227 * 1024, "two thread blocks share an SM");
+  // token tiles whose sums the row halves exchange at a time, in a stage's buffer
+  static constexpr int kSwap = (kS + kX) / (kWarps * NO * 512) < NT ? 1 : NT;
+  static_assert(KH == 1 || kSwap * kWarps * NO * 512 <= kS + kX, "the row halves meet in a stage's buffer");
+};
 
 struct W4Params {
   const void* x[8];
@@ -50,11 +91,10 @@ struct W4Params {
   const void* s[8];
   const __nv_bfloat16* bias[8];
   void* y[8];
-  unsigned long long* count;  // [blocks]
-  float* part;                // [2 * gridDim.x][kCols * 8 NT]
-  unsigned long long epoch;
+  float* part;                // [2 * runs][kStrips x 8 NT]: sums of a column block's part
+  uint32_t run_stages;        // run r: stages r * run_stages ... (the last run may be shorter)
   uint32_t M, N, K;
-  uint32_t ktiles, groups, pairs;  // 64-row tiles, scale groups, 32-column pairs of strips of a shard
+  uint32_t ktiles, groups, pairs;  // 64-row tiles, scale groups, 32-column pairs of 16-column strips of a shard
   uint32_t nblocks;                // column blocks of a shard
   uint32_t kstages;                // stages of a shard
   uint32_t spb;                    // stages of a column block: row layout p * kstages, column layout kstages
@@ -67,144 +107,254 @@ __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, 
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
-  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
 }
 
-// D += A . B, 16 x 8 x 16, bf16 in, fp32 accumulator.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// The four fragment registers of a word (see the top), for the columns i and
+// i + 8 in turn: RAW the nibbles times 2^-133 and 2^-129, else q - 8 times
+// 2^-6 and 2^-2.
+template <bool RAW>
+__device__ __forceinline__ void dequant(uint32_t w, uint32_t (&a)[4]) {
+  const uint32_t v = w >> 8;
+  a[0] = w & 0x000F000Fu;
+  a[1] = w & 0x00F000F0u;
+  a[2] = v & 0x000F000Fu;
+  a[3] = v & 0x00F000F0u;
+  if constexpr (!RAW) {
+    constexpr uint32_t kUp = 0x7F007F00u, kOff0 = 0xBE00BE00u, kOff1 = 0xC000C000u;  // 2^127, -2^-3, -2
+    a[0] = fma_bf16x2(a[0], kUp, kOff0);
+    a[1] = fma_bf16x2(a[1], kUp, kOff1);
+    a[2] = fma_bf16x2(a[2], kUp, kOff0);
+    a[3] = fma_bf16x2(a[3], kUp, kOff1);
+  }
+}
+
+// D += A . B, 16 x 8 x 16, bf16 in, fp32 accumulator; the other form starts from zero.
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 
-// Bytes of one stage in shared memory: weights, scales, tokens.
-template <int NT, int GB>
-struct StageLayout {
-  static constexpr int kScales = 4 / GB;  // scale groups of a stage
-  static constexpr int kW = kThreads * 64, kS = kWarps * kScales * 64, kX = NT * 8 * kXPitch;
-  static constexpr int kBytes = kW + kS + kX;
+// The runs that hold stages of a column block.
+struct Parts {
+  uint32_t first, last;
 };
+__device__ __forceinline__ Parts parts_of(const W4Params& P, uint32_t block) {
+  const uint32_t b0 = block * P.spb;
+  return {b0 / P.run_stages, (b0 + P.spb - 1) / P.run_stages};
+}
+
+// Where run r keeps its sums of a column block that it shares: its first
+// slab for the block it begins in, its second for a later one (the block it
+// ends in: those between are its own).
+template <int NT, int GB>
+__device__ __forceinline__ float4* slab_of(const W4Params& P, uint32_t r, uint32_t block) {
+  constexpr int kSlab = kThreads * Shape<NT, GB>::NO * NT;
+  const bool begins = r * P.run_stages >= block * P.spb;
+  return reinterpret_cast<float4*>(P.part) + static_cast<int64_t>(2 * r + (begins ? 0 : 1)) * kSlab;
+}
+
+// Epilogue of the four sums that thread `tid` of a thread block has of its
+// strip o and token tile n: rows (columns of Y) g and g + 8, tokens 2 t and
+// 2 t + 1.
+template <int NT, int GB>
+__device__ __forceinline__ void write_out(const W4Params& P, uint32_t block, uint32_t tid, uint32_t o, uint32_t n, const float4& v) {
+  using S = Shape<NT, GB>;
+  const uint32_t warp = tid >> 5, g = (tid & 31) >> 2, t = tid & 3;
+  const uint32_t cg = warp % (kWarps / S::KH), kh = warp / (kWarps / S::KH);
+  const uint32_t shard = P.row ? 0 : block / P.nblocks;
+  const uint32_t strip = (P.row ? block : block % P.nblocks) * S::kStrips + cg * S::NS + kh * S::NO + o;
+  const float vals[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const uint32_t col = strip * 16 + r * 8 + g;
+    if (col >= P.N) continue;
+    const float bias = P.bias[shard] ? __bfloat162float(P.bias[shard][col]) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t tok = n * 8 + 2 * t + i;
+      if (tok >= P.M) continue;
+      float y = vals[2 * r + i] + bias;
+      if (P.epi == TP_EPI_GELU) y = gelu_f(y);
+      const int64_t at = static_cast<int64_t>(tok) * P.N + col;
+      if (P.out_f32) static_cast<float*>(P.y[shard])[at] = y;
+      else static_cast<__nv_bfloat16*>(P.y[shard])[at] = __float2bfloat16_rn(y);
+    }
+  }
+}
 
 // NT: tiles of 8 tokens; GB: rows of a scale group / 32.
-template <int NT, int GB, int STAGES>
-__global__ void __launch_bounds__(kThreads, NT <= 4 ? 2 : 1) w4_linear_kernel(const __grid_constant__ W4Params P) {
-  using L = StageLayout<NT, GB>;
+template <int NT, int GB>
+__global__ void __launch_bounds__(kThreads, 2) w4_linear_kernel(const __grid_constant__ W4Params P) {
+  using S = Shape<NT, GB>;
+  constexpr int NS = S::NS, KH = S::KH, PIECES = S::PIECES, GROUPS = S::kGroups, NO = S::NO;
+  constexpr uint32_t kShared = S::kS + S::kX;
+  constexpr bool RAW = S::RAW;
+  constexpr float kUp0 = RAW ? 0x1p69f : 64.f, kUp1 = RAW ? 0x1p65f : 4.f;  // what the sums of columns i, i + 8 lack
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ uint32_t is_last;
-  const uint32_t base = smem_u32(smem);
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const uint32_t cg = warp % (kWarps / KH), kh = warp / (kWarps / KH);
+  const uint32_t cell = smem_u32(smem) + warp * (NS * 512) + lane * 16;  // this lane's part of piece 0
+  const uint32_t shared = smem_u32(smem) + PIECES * S::kPiece;           // scales and tokens, two stages in turn
   griddep_wait();
   griddep_launch_dependents();
-  const uint32_t u0 = static_cast<uint32_t>(static_cast<uint64_t>(blockIdx.x) * P.stages / gridDim.x);
-  const uint32_t u1 = static_cast<uint32_t>(static_cast<uint64_t>(blockIdx.x + 1) * P.stages / gridDim.x);
+  // The run: stages u .. u1 - 1.
+  uint32_t u = blockIdx.x * P.run_stages;
+  const uint32_t u1 = min(u + P.run_stages, P.stages);
 
-  // load cursor: column block, and stage in it as (rank, stage of the rank)
-  uint32_t lblock = u0 / P.spb, lrank = (u0 % P.spb) / P.kstages, lk = (u0 % P.spb) % P.kstages, lu = u0;
-  auto fetch = [&](uint32_t slot) {
-    if (lu < u1) {
-      const uint32_t shard = P.row ? lrank : lblock / P.nblocks;
-      const uint32_t pair = (P.row ? lblock : lblock % P.nblocks) * kWarps + warp;
-      const uint32_t dst = base + slot * L::kBytes;
-      if (pair < P.pairs) {
-        const uint8_t* q = static_cast<const uint8_t*>(P.q[shard]) +
-                           (static_cast<int64_t>(pair) * P.ktiles + lk * (kStageK / 64)) * 1024 + lane * 16;
+  // The stage to load, one ahead of the one worked on: column block, rank and
+  // stage of the rank, and pointers of the thread's own, which move on by a
+  // constant until the rank or block ends.
+  constexpr int XC = S::kStageK / 8, XT = kThreads / XC;  // 16-byte pieces of a token's stage; tokens of one sweep
+  const uint32_t xtok = threadIdx.x / XC, xcol = threadIdx.x % XC * 8;
+  const uint32_t sn = lane / (2 * GROUPS), sg = lane / 2 % GROUPS;  // strip and group of this lane's 16 bytes of scales
+  uint32_t lu = u, lblock = u / P.spb, lrank = (u % P.spb) / P.kstages, lk = (u % P.spb) % P.kstages;
+  const uint8_t *wq = nullptr, *sp = nullptr;
+  const __nv_bfloat16* xp = nullptr;
+  uint32_t strips = 0;  // of the warp's that exist
+  const int64_t pair_bytes = static_cast<int64_t>(P.ktiles) * 1024;
+  auto aim = [&] {
+    const uint32_t shard = P.row ? lrank : lblock / P.nblocks;
+    const uint32_t strip = (P.row ? lblock : lblock % P.nblocks) * S::kStrips + cg * NS;
+    strips = min(static_cast<uint32_t>(NS), max(P.pairs * 2, strip) - strip);
+    wq = static_cast<const uint8_t*>(P.q[shard]) + (strip / 2) * pair_bytes + (lk * KH + kh) * (PIECES * 1024ll) + strip % 2 * 512 + lane * 16;
+    sp = static_cast<const uint8_t*>(P.s[shard]) +
+         (static_cast<int64_t>((strip + sn) / 2) * P.groups + (lk * KH + kh) * GROUPS + sg) * 64 + (strip + sn) % 2 * 32 + lane % 2 * 16;
+    xp = static_cast<const __nv_bfloat16*>(P.x[P.row ? lrank : 0]) + static_cast<int64_t>(xtok) * P.K + lk * S::kStageK + xcol;
+  };
+  aim();
+  auto fetch_weights = [&](int h) {
+    if (lu >= u1) return;
+    const uint32_t tile = (lk * KH + kh) * PIECES + h, dst = cell + h * S::kPiece;
+    if (strips == NS && tile < P.ktiles) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool ok = lk * 2 + i / 2 < P.ktiles;
-          cp_async16_zfill(dst + (warp * 4 + i) * 512 + lane * 16, ok ? q + i * 512 : q, ok);
-        }
-        if (lane < L::kScales * 4) {
-          const uint32_t first = lk * L::kScales;
-          const bool ok = first + lane / 4 < P.groups;
-          const uint8_t* s = static_cast<const uint8_t*>(P.s[shard]) + (static_cast<int64_t>(pair) * P.groups + first) * 64;
-          cp_async16_zfill(dst + L::kW + warp * (L::kScales * 64) + lane * 16, ok ? s + lane * 16 : s, ok);
-        }
-      }
-      const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(P.x[P.row ? lrank : 0]) + lk * kStageK;
-      const uint32_t left = P.K - lk * kStageK;  // columns of x from here on
-      for (uint32_t c = threadIdx.x; c < P.M * (kStageK / 8); c += kThreads) {
-        const uint32_t tok = c / (kStageK / 8), col = c % (kStageK / 8) * 8;
-        const bool ok = col < left;
-        cp_async16_zfill(dst + L::kW + L::kS + tok * kXPitch + col * 2, x + static_cast<int64_t>(tok) * P.K + (ok ? col : 0), ok);
-      }
-      ++lu;
-      if (++lk == P.kstages) {
-        lk = 0;
-        if (!P.row || ++lrank == P.spb / P.kstages) {
-          lrank = 0;
-          ++lblock;
-        }
+      for (int n = 0; n < NS; ++n) cp_async16(dst + n * 512, wq + (n / 2) * pair_bytes + (h * 1024 + n % 2 * 512));
+    } else {  // past the shard's columns or rows: zero nibbles, which meet zero scales or zero tokens
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
+        const bool ok = static_cast<uint32_t>(n) < strips && tile < P.ktiles;
+        cp_async16_zfill(dst + n * 512, ok ? wq + (n / 2) * pair_bytes + (h * 1024 + n % 2 * 512) : static_cast<const uint8_t*>(P.q[0]), ok);
       }
     }
-    cp_async_commit();
   };
+  auto fetch_shared = [&](uint32_t dst) {
+    if (lu >= u1) return;
+    if (lane < NS * GROUPS * 2) {
+      const bool ok = sn < strips && (lk * KH + kh) * GROUPS + sg < P.groups;
+      cp_async16_zfill(dst + warp * (NS * GROUPS * 32) + lane * 16, ok ? sp : static_cast<const uint8_t*>(P.s[0]), ok);
+    }
+    const bool ok = lk * S::kStageK + xcol < P.K;
 #pragma unroll
-  for (int i = 0; i < STAGES - 1; ++i) fetch(i);
+    for (int i = 0; i < (NT * 8 + XT - 1) / XT; ++i)
+      if (xtok + i * XT < P.M)
+        cp_async16_zfill(dst + S::kS + (xtok + i * XT) * S::kXPitch + xcol * 2,
+                         ok ? xp + static_cast<int64_t>(i) * XT * P.K : static_cast<const __nv_bfloat16*>(P.x[0]), ok);
+  };
+  auto advance = [&] {
+    if (++lu >= u1) return;
+    wq += KH * PIECES * 1024;
+    sp += KH * GROUPS * 64;
+    xp += S::kStageK;
+    if (++lk == P.kstages) {
+      lk = 0;
+      if (++lrank * P.kstages == P.spb) {
+        lrank = 0;
+        ++lblock;
+      }
+      aim();
+    }
+  };
+  fetch_shared(shared);
+#pragma unroll
+  for (int h = 0; h < PIECES; ++h) {
+    fetch_weights(h);
+    cp_async_commit();
+  }
+  advance();
 
-  float acc[2][NT][4];
+  float acc[NS][NT][4];
+  auto clear = [&] {
 #pragma unroll
-  for (int f = 0; f < 2; ++f)
+    for (int f = 0; f < NS; ++f)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[f][n][i] = 0.f;
+        for (int i = 0; i < 4; ++i) acc[f][n][i] = 0.f;
+  };
+  clear();
 
-  uint32_t block = u0 / P.spb, left = P.spb - u0 % P.spb;  // stages to the end of the column block
-  uint32_t slot = 0;
-  for (uint32_t u = u0; u < u1; ++u) {
-    cp_async_wait<STAGES - 2>();
-    __syncthreads();  // stage u is here for everybody, and everybody is done with stage u - 1
-    fetch(slot == 0 ? STAGES - 1 : slot - 1);
-    const uint32_t src = base + slot * L::kBytes;
-    slot = slot + 1 == STAGES ? 0 : slot + 1;
-    const uint32_t pair = (P.row ? block : block % P.nblocks) * kWarps + warp;
-    if (pair < P.pairs) {
-      const uint32_t wsrc = src + warp * 2048 + lane * 16, xsrc = src + L::kW + L::kS + g * kXPitch + t * 16;
-      const uint32_t ssrc = src + L::kW + warp * (L::kScales * 64) + g * 4;
-      float part[2][NT][4];
-      uint4 w[2];
+  uint32_t block = u / P.spb, left = P.spb - u % P.spb;  // stages to the end of the column block
+  uint32_t here = shared, ahead = shared + kShared;
+  while (u < u1) {
+    const uint32_t ssrc = here + warp * (NS * GROUPS * 32) + g * 4;
+    const uint32_t xsrc = here + S::kS + g * S::kXPitch + kh * (PIECES * 128) + t * 16;
+    float part[NS][NT][4], eight[RAW ? NT : 1][4];  // eight: 8 sum(x), in the units of the rows' columns
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {  // 32 rows each
-        if (b % 2 == 0) {
+    for (int h = 0; h < PIECES; ++h) {
+      cp_async_wait<PIECES - 1>();
+      if (h == 0) {
+        __syncthreads();  // this stage's tokens are here, and everybody is done with the last stage's
+        fetch_shared(ahead);
+      }
+      uint4 w[NS];
 #pragma unroll
-          for (int f = 0; f < 2; ++f) w[f] = ld_shared_v4(wsrc + ((b / 2) * 2 + f) * 512);
-        }
-        if (b % GB == 0) {
+      for (int f = 0; f < NS; ++f) w[f] = ld_shared_v4(cell + h * S::kPiece + f * 512);
 #pragma unroll
-          for (int f = 0; f < 2; ++f)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) part[f][n][i] = 0.f;
-        }
-        uint32_t a[2][2][4];
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t word = b % 2 == 0 ? (j == 0 ? w[f].x : w[f].y) : (j == 0 ? w[f].z : w[f].w);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) a[f][j][r] = sub_bf16x2(((word >> (4 * r)) & 0x000F000Fu) | 0x43004300u, 0x43084308u);
-          }
+      for (int hb = 0; hb < 2; ++hb) {  // 32 rows each
+        const int b = h * 2 + hb;
+        uint4 xv[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const uint4 xv = ld_shared_v4(xsrc + n * (8 * kXPitch) + b * 64);
-#pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            mma16816(part[f][n], a[f][0], xv.x, xv.y);
-            mma16816(part[f][n], a[f][1], xv.z, xv.w);
+          xv[n] = ld_shared_v4(xsrc + n * (8 * S::kXPitch) + b * 64);
+          if constexpr (RAW) {
+            constexpr uint32_t k64 = 0x5F805F80u;  // 2^64
+            xv[n] = make_uint4(mul_bf16x2(xv[n].x, k64), mul_bf16x2(xv[n].y, k64), mul_bf16x2(xv[n].z, k64), mul_bf16x2(xv[n].w, k64));
+            const uint32_t e[4] = {0x00080008u, 0x00800080u, 0x00080008u, 0x00800080u};
+            if (b % GB == 0) mma16816_first(eight[n], e, xv[n].x, xv[n].y);
+            else mma16816(eight[n], e, xv[n].x, xv[n].y);
+            mma16816(eight[n], e, xv[n].z, xv[n].w);
           }
+        }
+#pragma unroll
+        for (int f = 0; f < NS; ++f) {
+          uint32_t a[4];
+          dequant<RAW>(hb == 0 ? w[f].x : w[f].z, a);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if (b % GB == 0) mma16816_first(part[f][n], a, xv[n].x, xv[n].y);
+            else mma16816(part[f][n], a, xv[n].x, xv[n].y);
+          }
+          dequant<RAW>(hb == 0 ? w[f].y : w[f].w, a);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma16816(part[f][n], a, xv[n].z, xv[n].w);
         }
         if (b % GB == GB - 1) {
 #pragma unroll
-          for (int f = 0; f < 2; ++f) {
+          for (int f = 0; f < NS; ++f) {
             uint32_t sc;
-            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sc) : "r"(ssrc + (b / GB) * 64 + f * 32));
-            const float s0 = bf_lo(sc), s1 = bf_hi(sc);
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sc) : "r"(ssrc + (f * GROUPS + b / GB) * 32));
+            const float s0 = bf_lo(sc) * kUp0, s1 = bf_hi(sc) * kUp1;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
+              if constexpr (RAW) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) part[f][n][i] -= eight[n][i];
+              }
               acc[f][n][0] = fmaf(s0, part[f][n][0], acc[f][n][0]);
               acc[f][n][1] = fmaf(s0, part[f][n][1], acc[f][n][1]);
               acc[f][n][2] = fmaf(s1, part[f][n][2], acc[f][n][2]);
@@ -213,106 +363,97 @@ __global__ void __launch_bounds__(kThreads, NT <= 4 ? 2 : 1) w4_linear_kernel(co
           }
         }
       }
+      // the lane's part of this piece is used up: the next stage's goes there
+      fetch_weights(h);
+      cp_async_commit();
     }
-    if (--left != 0 && u + 1 != u1) continue;
+    advance();
+    const uint32_t done = here;
+    here = ahead;
+    ahead = done;
+    ++u;
+    if (--left != 0 && u != u1) continue;
 
-    // the run of this column block ends here
-    const uint32_t b0 = block * P.spb, b1 = b0 + P.spb;
-    const uint32_t c0 = static_cast<uint32_t>(((static_cast<uint64_t>(b0) + 1) * gridDim.x - 1) / P.stages);
-    const uint32_t c1 = static_cast<uint32_t>((static_cast<uint64_t>(b1) * gridDim.x - 1) / P.stages);
-    constexpr int kSlab = kThreads * 2 * NT * 4;  // floats of a block's sums, in the threads' own order
-    bool write = true;
-    if (c0 != c1) {
-      // slab 0 of a thread block is for the column block its run begins in,
-      // slab 1 for the one it ends in
-      auto slab = [&](uint32_t c) {
-        const bool begins = static_cast<uint64_t>(c) * P.stages / gridDim.x >= b0;
-        return P.part + static_cast<int64_t>(2 * c + (begins ? 0 : 1)) * kSlab;
-      };
-      // (the run of c begins at or after b0 for all but c0, whose run may
-      // have begun in an earlier column block)
-      float4* mine = reinterpret_cast<float4*>(slab(blockIdx.x)) + threadIdx.x;
+    // the run of this column block ends here: the row halves first give each
+    // other half of their strips, after which a warp finishes NO of them
+    if constexpr (KH > 1) {
+      float4* swap = reinterpret_cast<float4*>(smem + (done - smem_u32(smem)));  // the stage just used
 #pragma unroll
-      for (int f = 0; f < 2; ++f)
+      for (int n0 = 0; n0 < NT; n0 += S::kSwap) {
+        __syncthreads();
+#pragma unroll
+        for (int n = n0; n < n0 + S::kSwap; ++n)
+#pragma unroll
+          for (int o = 0; o < NO; ++o) {
+            const float(&v)[4] = kh == 0 ? acc[NO + o][n] : acc[o][n];
+            swap[((warp * NO + o) * S::kSwap + n - n0) * 32 + lane] = make_float4(v[0], v[1], v[2], v[3]);
+          }
+        __syncthreads();
+#pragma unroll
+        for (int n = n0; n < n0 + S::kSwap; ++n)
+#pragma unroll
+          for (int o = 0; o < NO; ++o) {
+            const float4 v = swap[(((warp ^ (kWarps / 2)) * NO + o) * S::kSwap + n - n0) * 32 + lane];
+            float(&d)[4] = kh == 0 ? acc[o][n] : acc[NO + o][n];
+            // a sum of two: the same whichever half comes first
+            d[0] += v.x;
+            d[1] += v.y;
+            d[2] += v.z;
+            d[3] += v.w;
+          }
+      }
+      if (kh == 1) {
+#pragma unroll
+        for (int o = 0; o < NO; ++o)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[o][n][i] = acc[NO + o][n][i];
+      }
+    }
+    const Parts parts = parts_of(P, block);
+    if (parts.first != parts.last) {
+      float4* mine = slab_of<NT, GB>(P, blockIdx.x, block) + threadIdx.x;
+#pragma unroll
+      for (int o = 0; o < NO; ++o)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-          __stcg(mine + (f * NT + n) * kThreads, make_float4(acc[f][n][0], acc[f][n][1], acc[f][n][2], acc[f][n][3]));
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        // (launch number << 16 | arrivals); a counter left by another launch
-        // counts as zero.  Each failed exchange is another block's success.
-        unsigned long long* cnt = P.count + block;
-        const uint32_t n = c1 - c0 + 1;
-        unsigned long long cur = *reinterpret_cast<volatile unsigned long long*>(cnt), next = 0;
-        bool done = false;
-        for (uint32_t i = 0; i <= n + 4 && !done; ++i) {
-          next = (cur >> 16) == P.epoch ? cur + 1 : ((P.epoch << 16) | 1ull);
-          const unsigned long long prev = atomicCAS(cnt, cur, next);
-          done = prev == cur;
-          cur = prev;
-        }
-        is_last = done && (next & 0xFFFFull) == n;
-        if (is_last) atomicExch(cnt, 0ull);
-        __threadfence();
-      }
-      __syncthreads();
-      write = is_last != 0;
-      if (write) {
+          if (n * 8 + 2 * t < P.M)
+            __stcg(mine + (o * NT + n) * kThreads, make_float4(acc[o][n][0], acc[o][n][1], acc[o][n][2], acc[o][n][3]));
+    } else {
 #pragma unroll
-        for (int f = 0; f < 2; ++f)
+      for (int o = 0; o < NO; ++o)
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (uint32_t c = c0; c <= c1; ++c) {
-              const float4 o = __ldcg(reinterpret_cast<const float4*>(slab(c)) + threadIdx.x + (f * NT + n) * kThreads);
-              v.x += o.x;
-              v.y += o.y;
-              v.z += o.z;
-              v.w += o.w;
-            }
-            acc[f][n][0] = v.x;
-            acc[f][n][1] = v.y;
-            acc[f][n][2] = v.z;
-            acc[f][n][3] = v.w;
-          }
-      }
+        for (int n = 0; n < NT; ++n)
+          write_out<NT, GB>(P, block, threadIdx.x, o, n, make_float4(acc[o][n][0], acc[o][n][1], acc[o][n][2], acc[o][n][3]));
     }
-    if (write && pair < P.pairs) {
-      const uint32_t shard = P.row ? 0 : block / P.nblocks;
-#pragma unroll
-      for (int f = 0; f < 2; ++f)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const uint32_t n = pair * 32 + f * 16 + r * 8 + g;
-          if (n < P.N) {
-            const float bias = P.bias[shard] ? __bfloat162float(P.bias[shard][n]) : 0.f;
-#pragma unroll
-            for (int k = 0; k < NT; ++k)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const uint32_t tok = k * 8 + 2 * t + i;
-                if (tok < P.M) {
-                  float v = acc[f][k][2 * r + i] + bias;
-                  if (P.epi == TP_EPI_GELU) v = gelu_f(v);
-                  const int64_t o = static_cast<int64_t>(tok) * P.N + n;
-                  if (P.out_f32) static_cast<float*>(P.y[shard])[o] = v;
-                  else static_cast<__nv_bfloat16*>(P.y[shard])[o] = __float2bfloat16_rn(v);
-                }
-              }
-          }
-        }
-    }
-#pragma unroll
-    for (int f = 0; f < 2; ++f)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[f][n][i] = 0.f;
+    clear();
     ++block;
     left = P.spb;
   }
   cp_async_wait<0>();
+}
+
+// Adds up the column blocks that several runs share: blockIdx.x the column
+// block, blockIdx.y one of its (strip, token tile) pairs.
+template <int NT, int GB>
+__global__ void __launch_bounds__(kThreads) w4_join_kernel(const __grid_constant__ W4Params P) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const uint32_t block = blockIdx.x, o = blockIdx.y / NT, n = blockIdx.y % NT;
+  if (n * 8 + 2 * (threadIdx.x & 3) >= P.M) return;
+  const Parts parts = parts_of(P, block);
+  if (parts.first == parts.last) return;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (uint32_t r = parts.first; r <= parts.last; ++r) {
+    const float4 a = __ldcg(slab_of<NT, GB>(P, r, block) + blockIdx.y * kThreads + threadIdx.x);
+    v.x += a.x;
+    v.y += a.y;
+    v.z += a.z;
+    v.w += a.w;
+  }
+  write_out<NT, GB>(P, block, threadIdx.x, o, n, v);
 }
 
 // ----------------------------------------------------------------- packing
@@ -418,7 +559,8 @@ __global__ void __launch_bounds__(256) w4_unpack_kernel(const __grid_constant__ 
 // ----------------------------------------------------------------- host
 
 struct Plan {
-  uint32_t ktiles, pairs, nblocks, kstages, spb, stages, grid, nt;
+  uint32_t ktiles, pairs, nblocks, kstages, spb, stages, runs, run_stages, blocks, nt;
+  size_t slab;  // bytes of a thread block's sums of one column block
 };
 
 int tiles_for(int64_t M) {
@@ -426,42 +568,61 @@ int tiles_for(int64_t M) {
   return n <= 2 ? n : n <= 4 ? 4 : n <= 6 ? 6 : 8;
 }
 
-bool make_plan(bool row, int p, int64_t M, int64_t N, int64_t K, Plan* out) {
+template <int NT, int GB>
+void shape_of(Plan* P, int64_t N, int64_t K) {
+  using S = Shape<NT, GB>;
+  P->nblocks = static_cast<uint32_t>(cdiv(N, 16 * S::kStrips));
+  P->kstages = static_cast<uint32_t>(cdiv(K, S::kStageK));
+  P->slab = static_cast<size_t>(kThreads) * S::NO * NT * 4 * sizeof(float);
+}
+
+template <int NT>
+void shape_of(Plan* P, int64_t N, int64_t K, int64_t G) {
+  if (G == 32) shape_of<NT, 1>(P, N, K);
+  else if (G == 64) shape_of<NT, 2>(P, N, K);
+  else shape_of<NT, 4>(P, N, K);
+}
+
+bool make_plan(bool row, int p, int64_t M, int64_t N, int64_t K, int64_t G, Plan* out) {
   Plan P;
   P.nt = static_cast<uint32_t>(tiles_for(M));
   P.ktiles = static_cast<uint32_t>(cdiv(K, 64));
   P.pairs = static_cast<uint32_t>(cdiv(N, 32));
-  P.nblocks = static_cast<uint32_t>(cdiv(N, kCols));
-  P.kstages = static_cast<uint32_t>(cdiv(K, kStageK));
+  switch (P.nt) {
+    case 1: shape_of<1>(&P, N, K, G); break;
+    case 2: shape_of<2>(&P, N, K, G); break;
+    case 4: shape_of<4>(&P, N, K, G); break;
+    case 6: shape_of<6>(&P, N, K, G); break;
+    default: shape_of<8>(&P, N, K, G); break;
+  }
   const int64_t spb = row ? static_cast<int64_t>(p) * P.kstages : P.kstages;
   const int64_t stages = spb * P.nblocks * (row ? 1 : p);
   if (stages > 0x7FFFFFFFll) return false;
   P.spb = static_cast<uint32_t>(spb);
   P.stages = static_cast<uint32_t>(stages);
-  P.grid = static_cast<uint32_t>(std::min<int64_t>(stages, static_cast<int64_t>(kSMs) * (P.nt <= 4 ? 2 : 1)));
+  P.blocks = static_cast<uint32_t>(P.nblocks * (row ? 1 : p));
+  P.run_stages = static_cast<uint32_t>(cdiv(stages, std::min<int64_t>(stages, static_cast<int64_t>(kSMs) * 2)));
+  P.runs = static_cast<uint32_t>(cdiv(stages, P.run_stages));
   *out = P;
   return true;
 }
 
-size_t counter_bytes(const Plan& L, bool row, int p) {
-  return static_cast<size_t>(cdiv(static_cast<int64_t>(L.nblocks) * (row ? 1 : p) * 8, 256)) * 256;
-}
-
-template <int NT, int GB, int STAGES>
-tp_status run_w4(const W4Params& P, uint32_t grid, cudaStream_t stream) {
+template <int NT, int GB>
+tp_status run_w4(const W4Params& P, const Plan& L, cudaStream_t stream) {
   static KernelInfo info;
-  void (*k)(W4Params) = w4_linear_kernel<NT, GB, STAGES>;
+  void (*k)(W4Params) = w4_linear_kernel<NT, GB>;
   int regs = 0;
   TP_TRY(kernel_regs(reinterpret_cast<const void*>(k), &info, &regs));
-  return launch_dependent(k, dim3(grid), static_cast<unsigned>(kThreads), static_cast<size_t>(STAGES) * StageLayout<NT, GB>::kBytes,
-                          stream, P);
+  TP_TRY(launch_dependent(k, dim3(L.runs), static_cast<unsigned>(kThreads), static_cast<size_t>(Shape<NT, GB>::kBytes), stream, P));
+  if (L.run_stages == L.spb) return TP_OK;  // every column block is one run's
+  return launch_dependent(w4_join_kernel<NT, GB>, dim3(L.blocks, NT * Shape<NT, GB>::NO), static_cast<unsigned>(kThreads), 0, stream, P);
 }
 
-template <int NT, int STAGES>
-tp_status run_group(const W4Params& P, int G, uint32_t grid, cudaStream_t stream) {
-  if (G == 32) return run_w4<NT, 1, STAGES>(P, grid, stream);
-  if (G == 64) return run_w4<NT, 2, STAGES>(P, grid, stream);
-  return run_w4<NT, 4, STAGES>(P, grid, stream);
+template <int NT>
+tp_status run_group(const W4Params& P, int G, const Plan& L, cudaStream_t stream) {
+  if (G == 32) return run_w4<NT, 1>(P, L, stream);
+  if (G == 64) return run_w4<NT, 2>(P, L, stream);
+  return run_w4<NT, 4>(P, L, stream);
 }
 
 tp_status check_group(int64_t G) { return G == 32 || G == 64 || G == 128 ? TP_OK : TP_ERR_INVALID_ARG; }
@@ -487,7 +648,7 @@ tp_status w4_forward(bool row, const void* const* x, const void* const* q, const
   if (bias != nullptr && row) TP_TRY(check_ptr(bias[0], bias[0] != nullptr && work));
   Plan L;
   // an empty contraction still has its epilogue: one stage of zero rows
-  if (!make_plan(row, p, M, N, std::max<int64_t>(K, 1), &L)) return TP_ERR_UNSUPPORTED_SHAPE;
+  if (!make_plan(row, p, M, N, std::max<int64_t>(K, 1), G, &L)) return TP_ERR_UNSUPPORTED_SHAPE;
   TP_TRY(check_ws(ws, ws_bytes, w4_workspace(row, p, M, N, K)));
   if (!work) return TP_OK;
   {
@@ -515,9 +676,8 @@ tp_status w4_forward(bool row, const void* const* x, const void* const* q, const
     P.y[r] = y[r];
     P.bias[r] = static_cast<const __nv_bfloat16*>(bias ? bias[r] : nullptr);
   }
-  P.count = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(ws) + kStatusBytes);
-  P.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kStatusBytes + counter_bytes(L, row, p));
-  P.epoch = g_launch_epoch.fetch_add(1) + 1;
+  P.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kStatusBytes);
+  P.run_stages = L.run_stages;
   P.M = static_cast<uint32_t>(M);
   P.N = static_cast<uint32_t>(N);
   P.K = static_cast<uint32_t>(K);
@@ -532,11 +692,11 @@ tp_status w4_forward(bool row, const void* const* x, const void* const* q, const
   P.epi = epi;
   P.out_f32 = out_dtype == TP_FP32;
   switch (L.nt) {
-    case 1: return run_group<1, 4>(P, static_cast<int>(G), L.grid, stream);
-    case 2: return run_group<2, 4>(P, static_cast<int>(G), L.grid, stream);
-    case 4: return run_group<4, 4>(P, static_cast<int>(G), L.grid, stream);
-    case 6: return run_group<6, 5>(P, static_cast<int>(G), L.grid, stream);
-    default: return run_group<8, 5>(P, static_cast<int>(G), L.grid, stream);
+    case 1: return run_group<1>(P, static_cast<int>(G), L, stream);
+    case 2: return run_group<2>(P, static_cast<int>(G), L, stream);
+    case 4: return run_group<4>(P, static_cast<int>(G), L, stream);
+    case 6: return run_group<6>(P, static_cast<int>(G), L, stream);
+    default: return run_group<8>(P, static_cast<int>(G), L, stream);
   }
 }
 
@@ -563,9 +723,14 @@ tp_status pack_params(W4PackParams* P, const void* const* w, const void* const* 
 namespace tpf {
 
 size_t w4_workspace(bool row, int p, int64_t M, int64_t N, int64_t K) {
-  Plan L;
-  if (M <= 0 || N <= 0 || M > kMaxTokens || !make_plan(row, p, M, N, std::max<int64_t>(K, 1), &L)) return kStatusBytes;
-  return kStatusBytes + counter_bytes(L, row, p) + static_cast<size_t>(L.grid) * 2 * kThreads * 2 * L.nt * 4 * sizeof(float);
+  size_t most = kStatusBytes;
+  if (M <= 0 || N <= 0 || M > kMaxTokens) return most;
+  for (int64_t G : {32, 64, 128}) {  // the size does not ask for the group
+    Plan L;
+    if (make_plan(row, p, M, N, std::max<int64_t>(K, 1), G, &L))
+      most = std::max(most, kStatusBytes + static_cast<size_t>(L.runs) * 2 * L.slab);
+  }
+  return most;
 }
 
 }  // namespace tpf
