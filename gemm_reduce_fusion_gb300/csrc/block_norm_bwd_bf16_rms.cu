@@ -2,7 +2,7 @@
 
 namespace tpf {
 
-tp_status block_norm_bwd_run_bf16_rms(const NormParams& P, const NormBwdLaunch& L, cudaStream_t stream) {
+tp_status block_norm_bwd_run_bf16_rms(const NormParams& P, NormBwdLaunch& L, cudaStream_t stream) {
   return dispatch_bwd_groups<false, false>(P, L, stream);
 }
 

@@ -2,7 +2,7 @@
 
 namespace tpf {
 
-tp_status block_norm_bwd_run_f32_ln(const NormParams& P, const NormBwdLaunch& L, cudaStream_t stream) {
+tp_status block_norm_bwd_run_f32_ln(const NormParams& P, NormBwdLaunch& L, cudaStream_t stream) {
   return dispatch_bwd_groups<true, true>(P, L, stream);
 }
 

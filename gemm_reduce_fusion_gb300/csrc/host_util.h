@@ -145,17 +145,20 @@ inline void add_ranges(std::vector<Range>* v, const void* const* a, int n, size_
 // (griddepcontrol.wait) for its completion before they touch memory.
 template <typename Params>
 inline tp_status launch_dependent(void (*k)(Params), dim3 grid, unsigned block, size_t smem, cudaStream_t stream,
-                                  const Params& params) {
+                                  const Params& params, int cluster = 1) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k, params) == cudaSuccess ? TP_OK : TP_ERR_CUDA;
 }
 
