@@ -169,8 +169,7 @@ def _arr(ts) -> ctypes.Array | None:
 def _stream(stream) -> int:
     if stream is None:
         import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # as below, without a Stream object
-        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -514,17 +513,39 @@ def tp_noalloc_device_status(stream=None) -> int:
 # tokens, so their checks read each property of a tensor once and go through
 # _refuse, which finds the words, only when something is wrong.
 
+_ARRAY = tuple(ctypes.c_void_p * n for n in range(65))  # the C array types, looked up once
+_BF16 = _FP32 = _INT8 = _UINT8 = _RAW_STREAM = None
+
+
+def _begin() -> int:
+    """The current device; the first call fetches torch's dtypes and stream getter."""
+    global _BF16, _FP32, _INT8, _UINT8, _RAW_STREAM
+    if _BF16 is None:
+        import torch
+        _FP32, _INT8, _UINT8 = torch.float32, torch.int8, torch.uint8
+        # the current stream's handle without a Stream object around it, where torch has it
+        _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        _BF16 = torch.bfloat16
+    return _current_device()
+
+
+def _on(stream, dev: int) -> int:
+    return _RAW_STREAM(dev) if stream is None else _stream(stream)
+
+
 def _list(where: str, name: str, ts, count: int, shape, dtype, dev: int):
     """The C array of `count` tensors of one shape and dtype (None: NULL)."""
     if ts is None:
         return None
     if len(ts) != count:
         raise ValueError(f"{where}: {name} holds {len(ts)} tensors, expected {count}")
-    arr = (ctypes.c_void_p * count)()
-    for i, t in enumerate(ts):
+    arr = _ARRAY[count]()
+    i = 0
+    for t in ts:
         if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
             _refuse(where, f"{name}[{i}]", t, shape, dtype, dev)
         arr[i] = t.data_ptr()
+        i += 1
     return arr
 
 
@@ -541,8 +562,8 @@ def _refuse(where: str, name: str, t, shape, dtype, dev: int) -> None:
     raise TypeError(f"{where}: {name} must be {str(dtype).replace('torch.', '')}, got {t.dtype}")
 
 
-def _norm_args(where, h, post, w_post, b_post, pre, w_pre, b_pre, gate, alpha, eps, bf, dev):
-    rows, v = 0, (h,)
+def _norm_args(where, h, post, w_post, b_post, pre, w_pre, b_pre, gate, alpha, eps, dev):
+    rows, v, bf = 0, (h,), _BF16
     if gate is not None:
         if gate.dim() != 2:
             raise ValueError(f"{where}: gate is [rows, h], got {tuple(gate.shape)}")
@@ -554,14 +575,16 @@ def _norm_args(where, h, post, w_post, b_post, pre, w_pre, b_pre, gate, alpha, e
                      b_pre if b_pre is None else _one(where, "b_pre", b_pre, v, bf, dev), gate, rows, alpha, eps)
 
 
-def _residual(where, t, torch):
+def _residual(where, t):
     if t.dim() != 2:
         raise ValueError(f"{where}: a token shard is [tokens, h], got {tuple(t.shape)}")
-    if t.dtype is torch.bfloat16:
-        return *t.shape, torch.bfloat16, TP_BF16
-    if t.dtype is torch.float32:
-        return *t.shape, torch.float32, TP_FP32
-    raise TypeError(f"{where}: the residual stream is bfloat16 or float32, got {t.dtype}")
+    m, h = t.shape
+    dtype = t.dtype
+    if dtype is _BF16:
+        return m, h, dtype, TP_BF16
+    if dtype is _FP32:
+        return m, h, dtype, TP_FP32
+    raise TypeError(f"{where}: the residual stream is bfloat16 or float32, got {dtype}")
 
 
 def tp_block_norm_fwd(x: Sequence, z, y, n, *, post: int = TP_NORM_NONE, w_post=None, b_post=None,
@@ -572,14 +595,13 @@ def tp_block_norm_fwd(x: Sequence, z, y, n, *, post: int = TP_NORM_NONE, w_post=
     z None (then y None): n[s] = N_pre(x[s]).  n None: y alone.  x and y are
     bfloat16 or float32, z and n bfloat16; gate is [rows, h], its row i / (M / rows)
     for token i of the M = p * len(x[0]) tokens.  y[s] may be x[s]."""
-    import torch
-    W, dev, p = "tp_block_norm_fwd", _current_device(), len(x)
-    m, h, dtype, code = _residual(W, x[0], torch)
-    shape, bf = (m, h), torch.bfloat16
-    d = _norm_args(W, h, post, w_post, b_post, pre, w_pre, b_pre, gate, alpha, eps, bf, dev)
+    W, dev, p = "tp_block_norm_fwd", _begin(), len(x)
+    m, h, dtype, code = _residual(W, x[0])
+    shape, bf = (m, h), _BF16
+    d = _norm_args(W, h, post, w_post, b_post, pre, w_pre, b_pre, gate, alpha, eps, dev)
     _check(_lib.tp_block_norm_fwd(_list(W, "x", x, p, shape, dtype, dev), _list(W, "z", z, p, shape, bf, dev),
                                   _list(W, "y", y, p, shape, dtype, dev), _list(W, "n", n, p, shape, bf, dev),
-                                  ctypes.byref(d), p, p * m, h, code, _stream(stream)), W)
+                                  ctypes.byref(d), p, p * m, h, code, _on(stream, dev)), W)
 
 
 def tp_block_norm_bwd(z, y, dn, dy, dx, dz, ws, *, post: int = TP_NORM_NONE, w_post=None, b_post=None,
@@ -593,34 +615,30 @@ def tp_block_norm_bwd(z, y, dn, dy, dx, dz, ws, *, post: int = TP_NORM_NONE, w_p
     be None; dx, dz and each vector's gradient may be None.  dy, y, dx share
     one dtype; the vectors' gradients share one (bfloat16 or float32).
     dx[s] may be dy[s].  ws: workspace(TP_OP_BLOCK_NORM_BWD, p, M, h, 0)."""
-    import torch
-    W, dev = "tp_block_norm_bwd", _current_device()
-    first = next((t for t in (y, dy, dx) if t), None)
-    if first is None:
+    W, dev = "tp_block_norm_bwd", _begin()
+    first = y or dy or dx
+    if not first:
         raise ValueError(f"{W}: one of y, dy and dx is given")
     p = len(first)
-    m, h, dtype, code = _residual(W, first[0], torch)
-    shape, bf = (m, h), torch.bfloat16
-    d = _norm_args(W, h, post, w_post, b_post, pre, w_pre, b_pre, gate, alpha, eps, bf, dev)
-    vectors = (dw_post, db_post, dw_pre, db_pre, dgate)
-    out = next((t.dtype for t in vectors if t is not None), torch.float32)
-    names = ("dw_post", "db_post", "dw_pre", "db_pre")
-    g = _NormGrads(*[_one(W, k, t, (h,), out, dev) for k, t in zip(names, vectors)],
-                   _one(W, "dgate", dgate, gate.shape if gate is not None else (0, h), out, dev))
+    m, h, dtype, code = _residual(W, first[0])
+    shape, v, bf = (m, h), (h,), _BF16
+    d = _norm_args(W, h, post, w_post, b_post, pre, w_pre, b_pre, gate, alpha, eps, dev)
+    out = _FP32
+    for t in (dw_post, db_post, dw_pre, db_pre, dgate):
+        if t is not None:
+            out = t.dtype
+            break
+    if out is not _BF16 and out is not _FP32:
+        raise TypeError(f"{W}: gradients are bfloat16 or float32, got {out}")
+    g = _NormGrads(_one(W, "dw_post", dw_post, v, out, dev), _one(W, "db_post", db_post, v, out, dev),
+                   _one(W, "dw_pre", dw_pre, v, out, dev), _one(W, "db_pre", db_pre, v, out, dev),
+                   dgate if dgate is None else _one(W, "dgate", dgate, gate.shape if gate is not None else (0, h), out, dev))
     _need_ws(W, ws, dev)
-    wp, wb = _ws(ws)
     _check(_lib.tp_block_norm_bwd(_list(W, "z", z, p, shape, bf, dev), _list(W, "y", y, p, shape, dtype, dev),
                                   _list(W, "dn", dn, p, shape, bf, dev), _list(W, "dy", dy, p, shape, dtype, dev),
                                   _list(W, "dx", dx, p, shape, dtype, dev), _list(W, "dz", dz, p, shape, bf, dev),
-                                  ctypes.byref(d), ctypes.byref(g), p, p * m, h, code, _grad_code(W, out), wp, wb,
-                                  _stream(stream)), W)
-
-
-def _grad_code(where, dtype) -> int:
-    import torch
-    if dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"{where}: gradients are bfloat16 or float32, got {dtype}")
-    return TP_FP32 if dtype is torch.float32 else TP_BF16
+                                  ctypes.byref(d), ctypes.byref(g), p, p * m, h, code, TP_FP32 if out is _FP32 else TP_BF16,
+                                  *_ws(ws), _on(stream, dev)), W)
 
 
 def ckpt_shapes(M: int, N: int) -> tuple:
@@ -630,92 +648,86 @@ def ckpt_shapes(M: int, N: int) -> tuple:
 
 def tp_ckpt_pack(x: Sequence, q: Sequence, e: Sequence, stream=None) -> None:
     """(q[i], e[i]) = x[i] in 8 bits: int8 [M, N] and a power of two per 32 columns, uint8 [M, ceil(N/32)]."""
-    import torch
-    W, dev, p = "tp_ckpt_pack", _current_device(), len(x)
+    W, dev, p = "tp_ckpt_pack", _begin(), len(x)
     M, N = x[0].shape
     qs, es = ckpt_shapes(M, N)
-    _check(_lib.tp_ckpt_pack(_list(W, "x", x, p, (M, N), torch.bfloat16, dev), _list(W, "q", q, p, qs, torch.int8, dev),
-                             _list(W, "e", e, p, es, torch.uint8, dev), p, M, N, _stream(stream)), W)
+    _check(_lib.tp_ckpt_pack(_list(W, "x", x, p, (M, N), _BF16, dev), _list(W, "q", q, p, qs, _INT8, dev),
+                             _list(W, "e", e, p, es, _UINT8, dev), p, M, N, _on(stream, dev)), W)
 
 
 def tp_ckpt_unpack(q: Sequence, e: Sequence, y: Sequence, epi: int = TP_EPI_NONE, stream=None) -> None:
     """y[i] = the value of (q[i], e[i]), or its GeLU (epi=TP_EPI_GELU), in bfloat16."""
-    import torch
-    W, dev, p = "tp_ckpt_unpack", _current_device(), len(q)
+    W, dev, p = "tp_ckpt_unpack", _begin(), len(q)
     M, N = q[0].shape
     qs, es = ckpt_shapes(M, N)
-    _check(_lib.tp_ckpt_unpack(_list(W, "q", q, p, qs, torch.int8, dev), _list(W, "e", e, p, es, torch.uint8, dev),
-                               _list(W, "y", y, p, (M, N), torch.bfloat16, dev), epi, p, M, N, _stream(stream)), W)
+    _check(_lib.tp_ckpt_unpack(_list(W, "q", q, p, qs, _INT8, dev), _list(W, "e", e, p, es, _UINT8, dev),
+                               _list(W, "y", y, p, (M, N), _BF16, dev), epi, p, M, N, _on(stream, dev)), W)
 
 
 def tp_col_linear_bwd_ckpt(q, e, w: Sequence, dy: Sequence, dx, dw, ws, chunk_m: int = 0, stream=None, db=None) -> None:
     """tp_col_linear_bwd with X given as a checkpoint (q, e) (both None without dw)."""
-    import torch
-    W, dev, p, bf = "tp_col_linear_bwd_ckpt", _current_device(), len(w), torch.bfloat16
+    W, dev, p, bf = "tp_col_linear_bwd_ckpt", _begin(), len(w), _BF16
     (K, N), M = w[0].shape, dy[0].shape[0]
     qs, es = ckpt_shapes(M, K)
     out = _out_dtype(dx, dw, db)
-    od = torch.float32 if out == TP_FP32 else bf
+    od = _FP32 if out == TP_FP32 else bf
     _need_ws(W, ws, dev)
     wp, wb = _ws(ws)
     _check(_lib.tp_col_linear_bwd_ckpt(
-        _one(W, "q", q, qs, torch.int8, dev), _one(W, "e", e, es, torch.uint8, dev), _list(W, "w", w, p, (K, N), bf, dev),
+        _one(W, "q", q, qs, _INT8, dev), _one(W, "e", e, es, _UINT8, dev), _list(W, "w", w, p, (K, N), bf, dev),
         _list(W, "dy", dy, p, (M, N), bf, dev), _one(W, "dx", dx, (M, K), od, dev), _list(W, "dw", dw, p, (K, N), od, dev),
-        _list(W, "db", db, p, (N,), od, dev), p, M, N, K, chunk_m, out, wp, wb, _stream(stream)), W)
+        _list(W, "db", db, p, (N,), od, dev), p, M, N, K, chunk_m, out, wp, wb, _on(stream, dev)), W)
 
 
 def tp_row_linear_bwd_ckpt(q, e, w: Sequence, dy, dx, dw, ws, epi: int = TP_EPI_DGELU, chunk_m: int = 0, stream=None,
                            db=None) -> None:
     """tp_row_linear_bwd from checkpoints: of the pre-activations H_k (epi=TP_EPI_DGELU: dx[k] = dY A_k^T * GeLU'(H_k),
     dw[k] = GeLU(H_k)^T dY) or of the layer's inputs X_k (epi=TP_EPI_NONE)."""
-    import torch
-    W, dev, p, bf = "tp_row_linear_bwd_ckpt", _current_device(), len(w), torch.bfloat16
+    W, dev, p, bf = "tp_row_linear_bwd_ckpt", _begin(), len(w), _BF16
     (K, N), M = w[0].shape, dy.shape[0]
     qs, es = ckpt_shapes(M, K)
     out = _out_dtype(dx, dw, db)
-    od = torch.float32 if out == TP_FP32 else bf
+    od = _FP32 if out == TP_FP32 else bf
     _need_ws(W, ws, dev)
     wp, wb = _ws(ws)
     _check(_lib.tp_row_linear_bwd_ckpt(
-        _list(W, "q", q, p, qs, torch.int8, dev), _list(W, "e", e, p, es, torch.uint8, dev),
+        _list(W, "q", q, p, qs, _INT8, dev), _list(W, "e", e, p, es, _UINT8, dev),
         _list(W, "w", w, p, (K, N), bf, dev), _one(W, "dy", dy, (M, N), bf, dev), _list(W, "dx", dx, p, (M, K), od, dev),
         _list(W, "dw", dw, p, (K, N), od, dev), _one(W, "db", db, (N,), od, dev), epi, p, M, N, K, chunk_m, out, wp, wb,
-        _stream(stream)), W)
+        _on(stream, dev)), W)
 
 
 def tp_ag_matmul_bwd_ckpt(q, e, w: Sequence, dy: Sequence, dx, dw, ws, chunk_m: int = 0, stream=None, db=None) -> None:
     """tp_ag_matmul_bwd with the token shards X_s given as checkpoints (None without dw)."""
-    import torch
-    W, dev, p, bf = "tp_ag_matmul_bwd_ckpt", _current_device(), len(w), torch.bfloat16
+    W, dev, p, bf = "tp_ag_matmul_bwd_ckpt", _begin(), len(w), _BF16
     (K, N), M = w[0].shape, dy[0].shape[0]
     qs, es = ckpt_shapes(M // p, K)
     out = _out_dtype(dx, dw, db)
-    od = torch.float32 if out == TP_FP32 else bf
+    od = _FP32 if out == TP_FP32 else bf
     _need_ws(W, ws, dev)
     wp, wb = _ws(ws)
     _check(_lib.tp_ag_matmul_bwd_ckpt(
-        _list(W, "q", q, p, qs, torch.int8, dev), _list(W, "e", e, p, es, torch.uint8, dev),
+        _list(W, "q", q, p, qs, _INT8, dev), _list(W, "e", e, p, es, _UINT8, dev),
         _list(W, "w", w, p, (K, N), bf, dev), _list(W, "dy", dy, p, (M, N), bf, dev),
         _list(W, "dx", dx, p, (M // p, K), od, dev), _list(W, "dw", dw, p, (K, N), od, dev),
-        _list(W, "db", db, p, (N,), od, dev), p, M, N, K, chunk_m, out, wp, wb, _stream(stream)), W)
+        _list(W, "db", db, p, (N,), od, dev), p, M, N, K, chunk_m, out, wp, wb, _on(stream, dev)), W)
 
 
 def tp_row_linear_bwd_reducescatter_ckpt(q, e, w: Sequence, dy: Sequence, dx, dw, ws, epi: int = TP_EPI_DGELU,
                                          chunk_m: int = 0, stream=None, db=None) -> None:
     """tp_row_linear_bwd_reducescatter from checkpoints, as tp_row_linear_bwd_ckpt; dy[s] are row shards."""
-    import torch
-    W, dev, p, bf = "tp_row_linear_bwd_reducescatter_ckpt", _current_device(), len(w), torch.bfloat16
+    W, dev, p, bf = "tp_row_linear_bwd_reducescatter_ckpt", _begin(), len(w), _BF16
     (K, N), M = w[0].shape, dy[0].shape[0] * len(w)
     qs, es = ckpt_shapes(M, K)
     out = _out_dtype(dx, dw, db)
-    od = torch.float32 if out == TP_FP32 else bf
+    od = _FP32 if out == TP_FP32 else bf
     _need_ws(W, ws, dev)
     wp, wb = _ws(ws)
     _check(_lib.tp_row_linear_bwd_reducescatter_ckpt(
-        _list(W, "q", q, p, qs, torch.int8, dev), _list(W, "e", e, p, es, torch.uint8, dev),
+        _list(W, "q", q, p, qs, _INT8, dev), _list(W, "e", e, p, es, _UINT8, dev),
         _list(W, "w", w, p, (K, N), bf, dev), _list(W, "dy", dy, p, (M // p, N), bf, dev),
         _list(W, "dx", dx, p, (M, K), od, dev), _list(W, "dw", dw, p, (K, N), od, dev),
-        _one(W, "db", db, (N,), od, dev), epi, p, M, N, K, chunk_m, out, wp, wb, _stream(stream)), W)
+        _one(W, "db", db, (N,), od, dev), epi, p, M, N, K, chunk_m, out, wp, wb, _on(stream, dev)), W)
 
 
 def w4_shapes(K: int, N: int, group: int) -> tuple:
@@ -732,47 +744,43 @@ def _group(where: str, group: int) -> int:
 def tp_col_linear_fwd_w4(x, q: Sequence, s: Sequence, y: Sequence, ws, group: int = 128, epi: int = TP_EPI_NONE,
                          stream=None, bias=None) -> None:
     """y[k] = X W_k + b_k (or its GeLU) with 4-bit weights (q[k], s[k]); up to TP_W4_MAX_M tokens."""
-    import torch
-    W, dev, p, bf = "tp_col_linear_fwd_w4", _current_device(), len(q), torch.bfloat16
+    W, dev, p, bf = "tp_col_linear_fwd_w4", _begin(), len(q), _BF16
     (M, K), N, dtype = x.shape, y[0].shape[1], y[0].dtype
     qs, ss = w4_shapes(K, N, _group(W, group))
     _need_ws(W, ws, dev)
     wp, wb = _ws(ws)
     _check(_lib.tp_col_linear_fwd_w4(
-        _one(W, "x", x, (M, K), bf, dev), _list(W, "q", q, p, qs, torch.uint8, dev), _list(W, "s", s, p, ss, bf, dev),
+        _one(W, "x", x, (M, K), bf, dev), _list(W, "q", q, p, qs, _UINT8, dev), _list(W, "s", s, p, ss, bf, dev),
         _list(W, "bias", bias, p, (N,), bf, dev), _list(W, "y", y, p, (M, N), dtype, dev), epi, p, M, N, K, group,
-        _dtype_code(y[0]), wp, wb, _stream(stream)), W)
+        _dtype_code(y[0]), wp, wb, _on(stream, dev)), W)
 
 
 def tp_row_linear_fwd_w4(x: Sequence, q: Sequence, s: Sequence, y, ws, group: int = 128, stream=None, bias=None) -> None:
     """y = sum_r X_r W_r (+ bias) with 4-bit weights (q[r], s[r]); up to TP_W4_MAX_M tokens."""
-    import torch
-    W, dev, p, bf = "tp_row_linear_fwd_w4", _current_device(), len(q), torch.bfloat16
+    W, dev, p, bf = "tp_row_linear_fwd_w4", _begin(), len(q), _BF16
     (M, K), N, dtype = x[0].shape, y.shape[1], y.dtype
     qs, ss = w4_shapes(K, N, _group(W, group))
     _need_ws(W, ws, dev)
     wp, wb = _ws(ws)
     _check(_lib.tp_row_linear_fwd_w4(
-        _list(W, "x", x, p, (M, K), bf, dev), _list(W, "q", q, p, qs, torch.uint8, dev), _list(W, "s", s, p, ss, bf, dev),
+        _list(W, "x", x, p, (M, K), bf, dev), _list(W, "q", q, p, qs, _UINT8, dev), _list(W, "s", s, p, ss, bf, dev),
         _one(W, "bias", bias, (N,), bf, dev), _one(W, "y", y, (M, N), dtype, dev), p, M, N, K, group, _dtype_code(y), wp, wb,
-        _stream(stream)), W)
+        _on(stream, dev)), W)
 
 
 def tp_w4_pack(w: Sequence, q: Sequence, s: Sequence, group: int = 128, stream=None) -> None:
     """(q[r], s[r]) = w[r] [K, N] in 4 bits, a scale max|w| / 7 for each column and group of rows."""
-    import torch
-    W, dev, p, bf = "tp_w4_pack", _current_device(), len(w), torch.bfloat16
+    W, dev, p, bf = "tp_w4_pack", _begin(), len(w), _BF16
     K, N = w[0].shape
     qs, ss = w4_shapes(K, N, _group(W, group))
-    _check(_lib.tp_w4_pack(_list(W, "w", w, p, (K, N), bf, dev), _list(W, "q", q, p, qs, torch.uint8, dev),
-                           _list(W, "s", s, p, ss, bf, dev), p, N, K, group, _stream(stream)), W)
+    _check(_lib.tp_w4_pack(_list(W, "w", w, p, (K, N), bf, dev), _list(W, "q", q, p, qs, _UINT8, dev),
+                           _list(W, "s", s, p, ss, bf, dev), p, N, K, group, _on(stream, dev)), W)
 
 
 def tp_w4_unpack(q: Sequence, s: Sequence, w: Sequence, group: int = 128, stream=None) -> None:
     """w[r] [K, N] in bfloat16 of the 4-bit weights (q[r], s[r])."""
-    import torch
-    W, dev, p, bf = "tp_w4_unpack", _current_device(), len(w), torch.bfloat16
+    W, dev, p, bf = "tp_w4_unpack", _begin(), len(w), _BF16
     K, N = w[0].shape
     qs, ss = w4_shapes(K, N, _group(W, group))
-    _check(_lib.tp_w4_unpack(_list(W, "q", q, p, qs, torch.uint8, dev), _list(W, "s", s, p, ss, bf, dev),
-                             _list(W, "w", w, p, (K, N), bf, dev), p, N, K, group, _stream(stream)), W)
+    _check(_lib.tp_w4_unpack(_list(W, "q", q, p, qs, _UINT8, dev), _list(W, "s", s, p, ss, bf, dev),
+                             _list(W, "w", w, p, (K, N), bf, dev), p, N, K, group, _on(stream, dev)), W)

@@ -250,7 +250,7 @@ void fill(NormParams* P, const tp_block_norm_desc* d, int p, int64_t M, int64_t 
 }
 
 // Ranges of the descriptor's vectors, which are inputs.
-void add_desc(std::vector<Range>* in, const tp_block_norm_desc* d, int64_t h) {
+void add_desc(RangeList* in, const tp_block_norm_desc* d, int64_t h) {
   for (const void* v : {d->w_post, d->b_post, d->w_pre, d->b_pre}) in->push_back({v, v ? static_cast<size_t>(h) * 2 : 0});
   in->push_back({d->gate, d->gate ? static_cast<size_t>(d->gate_rows * h) * 2 : 0});
 }
@@ -258,9 +258,9 @@ void add_desc(std::vector<Range>* in, const tp_block_norm_desc* d, int64_t h) {
 // Refuses overlaps, save that out[s] may be in[s] itself where `same` is
 // given: a row of it is written only after it has been read by the same
 // thread block.
-bool clash(const std::vector<Range>& outs, const std::vector<Range>& ins, const void* const* out, const void* const* same, int p,
+bool clash(const RangeList& outs, const RangeList& ins, const void* const* out, const void* const* same, int p,
            size_t bytes) {
-  std::vector<Range> rest;
+  RangeList rest;
   for (const Range& r : ins) {
     bool skip = false;
     for (int s = 0; s < p && same != nullptr && out != nullptr; ++s)
@@ -326,9 +326,7 @@ extern "C" tp_status tp_block_norm_fwd(const void* const* x, const void* const* 
   if (!work) return TP_OK;
   {
     const size_t one = static_cast<size_t>(M / p * h);
-    std::vector<Range> ins, outs;
-    ins.reserve(24);
-    outs.reserve(16);
+    RangeList ins, outs;
     add_ranges(&ins, x, p, one * esize(res_dtype));
     add_ranges(&ins, z, p, one * 2);
     add_desc(&ins, d, h);
@@ -382,9 +380,7 @@ extern "C" tp_status tp_block_norm_bwd(const void* const* z, const void* const* 
   if (h == 0) return TP_OK;
   {
     const size_t one = static_cast<size_t>(M / p * h), r = esize(res_dtype), o = esize(out_dtype);
-    std::vector<Range> ins, outs;
-    ins.reserve(48);
-    outs.reserve(24);
+    RangeList ins, outs;
     add_ranges(&ins, z, p, one * 2);
     if (dn != nullptr) add_ranges(&ins, y, p, one * r);
     add_ranges(&ins, dn, p, one * 2);

@@ -195,7 +195,7 @@ extern "C" tp_status tp_ckpt_pack(const void* const* x, void* const* q, void* co
   TP_TRY(check_ptrs(x, p, work));
   TP_TRY(check_packed(in(q), in(e), p, work));
   if (!work) return TP_OK;
-  std::vector<Range> ins, outs;
+  RangeList ins, outs;
   add_ranges(&ins, x, p, static_cast<size_t>(M * N) * 2);
   add_ranges(&outs, in(q), p, static_cast<size_t>(M * N));
   add_ranges(&outs, in(e), p, static_cast<size_t>(M * cdiv(N, 32)));
@@ -223,7 +223,7 @@ extern "C" tp_status tp_ckpt_unpack(const void* const* q, const void* const* e, 
   TP_TRY(check_packed(q, e, p, work));
   TP_TRY(check_ptrs(in(y), p, work));
   if (!work) return TP_OK;
-  std::vector<Range> ins, outs;
+  RangeList ins, outs;
   add_ranges(&ins, q, p, static_cast<size_t>(M * N));
   add_ranges(&ins, e, p, static_cast<size_t>(M * cdiv(N, 32)));
   add_ranges(&outs, in(y), p, static_cast<size_t>(M * N) * 2);

@@ -85,7 +85,26 @@ inline bool overlap(const Range& a, const Range& b) {
   return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
 }
 
-inline bool any_overlap(const std::vector<Range>& outs, const std::vector<Range>& ins) {
+// A call's ranges without a heap allocation (calls that serve single tokens
+// take a few microseconds): at most 8 shards of a few tensors each.
+class RangeList {
+ public:
+  void push_back(const Range& r) {
+    if (r.bytes != 0 && n_ < kMost) r_[n_++] = r;
+  }
+  size_t size() const { return n_; }
+  const Range& operator[](size_t i) const { return r_[i]; }
+  const Range* begin() const { return r_; }
+  const Range* end() const { return r_ + n_; }
+
+ private:
+  static constexpr size_t kMost = 64;
+  size_t n_ = 0;
+  Range r_[kMost];
+};
+
+template <typename Outs, typename Ins>
+bool any_overlap(const Outs& outs, const Ins& ins) {
   for (size_t i = 0; i < outs.size(); ++i) {
     for (const Range& r : ins)
       if (overlap(outs[i], r)) return true;
@@ -134,7 +153,8 @@ inline tp_status check_ws(void* ws, size_t ws_bytes, size_t need) {
     if (_st != TP_OK) return _st;        \
   } while (0)
 
-inline void add_ranges(std::vector<Range>* v, const void* const* a, int n, size_t bytes) {
+template <typename List>
+void add_ranges(List* v, const void* const* a, int n, size_t bytes) {
   if (a == nullptr) return;
   for (int i = 0; i < n; ++i)
     if (a[i] != nullptr) v->push_back({a[i], bytes});

@@ -652,9 +652,7 @@ tp_status w4_forward(bool row, const void* const* x, const void* const* q, const
   TP_TRY(check_ws(ws, ws_bytes, w4_workspace(row, p, M, N, K)));
   if (!work) return TP_OK;
   {
-    std::vector<Range> ins, outs;
-    ins.reserve(40);
-    outs.reserve(10);
+    RangeList ins, outs;
     add_ranges(&ins, x, nx, static_cast<size_t>(M * K) * 2);
     add_ranges(&ins, q, p, q_bytes(N, K));
     add_ranges(&ins, s, p, s_bytes(N, K, G));
@@ -759,7 +757,7 @@ extern "C" tp_status tp_w4_pack(const void* const* w, void* const* q, void* cons
   if (!work) return TP_OK;
   W4PackParams P;
   TP_TRY(pack_params(&P, w, in(q), in(s), p, N, K, group));
-  std::vector<Range> ins, outs;
+  RangeList ins, outs;
   add_ranges(&ins, w, p, static_cast<size_t>(N * K) * 2);
   add_ranges(&outs, in(q), p, q_bytes(N, K));
   add_ranges(&outs, in(s), p, s_bytes(N, K, group));
@@ -783,7 +781,7 @@ extern "C" tp_status tp_w4_unpack(const void* const* q, const void* const* s, vo
   if (!work) return TP_OK;
   W4PackParams P;
   TP_TRY(pack_params(&P, in(w), q, s, p, N, K, group));
-  std::vector<Range> ins, outs;
+  RangeList ins, outs;
   add_ranges(&ins, q, p, q_bytes(N, K));
   add_ranges(&ins, s, p, s_bytes(N, K, group));
   add_ranges(&outs, in(w), p, static_cast<size_t>(N * K) * 2);
