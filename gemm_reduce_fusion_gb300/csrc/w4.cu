@@ -17,17 +17,14 @@
 // fragment register.  The bits of a bf16 below 256 are its value in units of
 // 2^-133 (subnormals and the first binade), so that a masked nibble is the
 // bf16 q * 2^-133 (column i) or 16 q * 2^-133 (column i + 8) as it stands.
-// The logic instructions that take, two issue cycles each, are what bounds
-// the kernel beside HBM, and there are two ways to go on from there:
-//   few tokens (NS = 4): the masked nibbles are the operands, and the tokens
-//     are multiplied by 2^64 instead, which keeps the products normal; the
-//     8 that a nibble stands above its value comes off as 8 sum(x), from one
-//     more mma for all strips.  (A token's element of 2^64 or more becomes
-//     infinite here, one below 2^-56 loses its last bits.)
-//   more tokens: one fused multiply-add of a pair,
-//       2^127 * (word & 0x000F000F) - 2^-3 = (q - 8) / 64
-//       2^127 * (word & 0x00F000F0) - 2    = (q - 8) / 4,
-//     exact, gives operands that need nothing of the tokens.
+// One fused multiply-add of a pair makes it an exact operand:
+//   2^127 * (word & 0x000F000F) - 2^-3 = (q - 8) / 64     (column i)
+//   2^127 * (word & 0x00F000F0) - 2    = (q - 8) / 4      (column i + 8)
+// Five logic instructions and four multiply-adds for eight weights, each at
+// half the rate of the others, and the mma (eight cycles of the tensor pipe
+// each) bound the kernel beside HBM.  (Masked nibbles as operands as they
+// are, against tokens times 2^64 and less 8 sum(x), gain 2 us of 54 at 1
+// token, lose 8 at 16, and turn infinite tokens into NaN.)
 // The scale, with the power of two that is left over, is applied to the
 // group's fp32 sum (once in G rows instead of once a weight), so no product
 // is rounded before it is added.
@@ -70,7 +67,6 @@ struct Shape {
   static constexpr int KH = NT <= 2 ? 2 : 1;               // row halves
   static constexpr int PIECES = NT <= 2 && GB == 1 ? 2 : 4;
   static constexpr int NO = NS / KH;                       // strips a warp finishes
-  static constexpr bool RAW = NS == 4;                     // nibbles as operands, tokens times 2^64
   static constexpr int kStrips = kWarps / KH * NS;         // strips of a block
   static constexpr int kStageK = 64 * PIECES * KH;         // rows of a stage
   static constexpr int kXPitch = kStageK * 2 + 64;         // bytes of a token's row: lanes of two tokens hit different banks
@@ -113,29 +109,15 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
   return d;
 }
 
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
-// The four fragment registers of a word (see the top), for the columns i and
-// i + 8 in turn: RAW the nibbles times 2^-133 and 2^-129, else q - 8 times
-// 2^-6 and 2^-2.
-template <bool RAW>
+// The four fragment registers of a word (see the top), for the columns i
+// (q - 8, times 2^-6) and i + 8 (times 2^-2) in turn.
 __device__ __forceinline__ void dequant(uint32_t w, uint32_t (&a)[4]) {
+  constexpr uint32_t kUp = 0x7F007F00u, kOff0 = 0xBE00BE00u, kOff1 = 0xC000C000u;  // 2^127, -2^-3, -2
   const uint32_t v = w >> 8;
-  a[0] = w & 0x000F000Fu;
-  a[1] = w & 0x00F000F0u;
-  a[2] = v & 0x000F000Fu;
-  a[3] = v & 0x00F000F0u;
-  if constexpr (!RAW) {
-    constexpr uint32_t kUp = 0x7F007F00u, kOff0 = 0xBE00BE00u, kOff1 = 0xC000C000u;  // 2^127, -2^-3, -2
-    a[0] = fma_bf16x2(a[0], kUp, kOff0);
-    a[1] = fma_bf16x2(a[1], kUp, kOff1);
-    a[2] = fma_bf16x2(a[2], kUp, kOff0);
-    a[3] = fma_bf16x2(a[3], kUp, kOff1);
-  }
+  a[0] = fma_bf16x2(w & 0x000F000Fu, kUp, kOff0);
+  a[1] = fma_bf16x2(w & 0x00F000F0u, kUp, kOff1);
+  a[2] = fma_bf16x2(v & 0x000F000Fu, kUp, kOff0);
+  a[3] = fma_bf16x2(v & 0x00F000F0u, kUp, kOff1);
 }
 
 // D += A . B, 16 x 8 x 16, bf16 in, fp32 accumulator; the other form starts from zero.
@@ -204,8 +186,6 @@ __global__ void __launch_bounds__(kThreads, 2) w4_linear_kernel(const __grid_con
   using S = Shape<NT, GB>;
   constexpr int NS = S::NS, KH = S::KH, PIECES = S::PIECES, GROUPS = S::kGroups, NO = S::NO;
   constexpr uint32_t kShared = S::kS + S::kX;
-  constexpr bool RAW = S::RAW;
-  constexpr float kUp0 = RAW ? 0x1p69f : 64.f, kUp1 = RAW ? 0x1p65f : 4.f;  // what the sums of columns i, i + 8 lack
   extern __shared__ __align__(16) uint8_t smem[];
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const uint32_t cg = warp % (kWarps / KH), kh = warp / (kWarps / KH);
@@ -303,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_linear_kernel(const __grid_con
   while (u < u1) {
     const uint32_t ssrc = here + warp * (NS * GROUPS * 32) + g * 4;
     const uint32_t xsrc = here + S::kS + g * S::kXPitch + kh * (PIECES * 128) + t * 16;
-    float part[NS][NT][4], eight[RAW ? NT : 1][4];  // eight: 8 sum(x), in the units of the rows' columns
+    float part[NS][NT][4];
 #pragma unroll
     for (int h = 0; h < PIECES; ++h) {
       cp_async_wait<PIECES - 1>();
@@ -319,27 +299,17 @@ __global__ void __launch_bounds__(kThreads, 2) w4_linear_kernel(const __grid_con
         const int b = h * 2 + hb;
         uint4 xv[NT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          xv[n] = ld_shared_v4(xsrc + n * (8 * S::kXPitch) + b * 64);
-          if constexpr (RAW) {
-            constexpr uint32_t k64 = 0x5F805F80u;  // 2^64
-            xv[n] = make_uint4(mul_bf16x2(xv[n].x, k64), mul_bf16x2(xv[n].y, k64), mul_bf16x2(xv[n].z, k64), mul_bf16x2(xv[n].w, k64));
-            const uint32_t e[4] = {0x00080008u, 0x00800080u, 0x00080008u, 0x00800080u};
-            if (b % GB == 0) mma16816_first(eight[n], e, xv[n].x, xv[n].y);
-            else mma16816(eight[n], e, xv[n].x, xv[n].y);
-            mma16816(eight[n], e, xv[n].z, xv[n].w);
-          }
-        }
+        for (int n = 0; n < NT; ++n) xv[n] = ld_shared_v4(xsrc + n * (8 * S::kXPitch) + b * 64);
 #pragma unroll
         for (int f = 0; f < NS; ++f) {
           uint32_t a[4];
-          dequant<RAW>(hb == 0 ? w[f].x : w[f].z, a);
+          dequant(hb == 0 ? w[f].x : w[f].z, a);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             if (b % GB == 0) mma16816_first(part[f][n], a, xv[n].x, xv[n].y);
             else mma16816(part[f][n], a, xv[n].x, xv[n].y);
           }
-          dequant<RAW>(hb == 0 ? w[f].y : w[f].w, a);
+          dequant(hb == 0 ? w[f].y : w[f].w, a);
 #pragma unroll
           for (int n = 0; n < NT; ++n) mma16816(part[f][n], a, xv[n].z, xv[n].w);
         }
@@ -348,13 +318,9 @@ __global__ void __launch_bounds__(kThreads, 2) w4_linear_kernel(const __grid_con
           for (int f = 0; f < NS; ++f) {
             uint32_t sc;
             asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sc) : "r"(ssrc + (f * GROUPS + b / GB) * 32));
-            const float s0 = bf_lo(sc) * kUp0, s1 = bf_hi(sc) * kUp1;
+            const float s0 = bf_lo(sc) * 64.f, s1 = bf_hi(sc) * 4.f;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              if constexpr (RAW) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) part[f][n][i] -= eight[n][i];
-              }
               acc[f][n][0] = fmaf(s0, part[f][n][0], acc[f][n][0]);
               acc[f][n][1] = fmaf(s0, part[f][n][1], acc[f][n][1]);
               acc[f][n][2] = fmaf(s1, part[f][n][2], acc[f][n][2]);

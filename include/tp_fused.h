@@ -360,8 +360,7 @@ tp_status tp_row_linear_bwd_reducescatter_ckpt(const void* const* q, const void*
  *   s: bf16 [ceil(N/32), ceil(K/G), 32]; column n = 32 a + 16 f + 8 r + i at
  *      16 f + 2 i + r.
  * Past K and N any nibble and scale is allowed.  Both are 16-byte aligned.
- * The sums are fp32; a scale multiplies its group's fp32 sum.  Magnitudes of
- * x from 2^64 on count as infinite.                                        */
+ * The sums are fp32; a scale multiplies its group's fp32 sum.               */
 
 /* Y_k = X . W_k (+ b_k), optionally GeLU (TP_EPI_GELU); arguments as in
  * tp_col_linear_fwd.  M <= 64 (TP_ERR_UNSUPPORTED_SHAPE above: unpack the
