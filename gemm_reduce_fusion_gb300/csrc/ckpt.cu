@@ -138,13 +138,21 @@ __global__ void __launch_bounds__(kThreads) ckpt_restore_kernel(const __grid_con
     float f[8];
     bytes_to_f(v[i].x, f);
     bytes_to_f(v[i].y, f + 4);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] *= s;
-    if (plain) plain[at[i]] = pack8(f);
     if (gelu) {
+      const uint64_t s2 = pk2(s, s), scaled = pk2(s * kTailRoot, s * kTailRoot);
+      uint32_t w[4];
 #pragma unroll
-      for (int j = 0; j < 8; j += 2) gelu2(f[j], f[j + 1]);
-      gelu[at[i]] = pack8(f);
+      for (int j = 0; j < 4; ++j) {
+        float lo, hi;
+        upk2(gelu_scaled2(f[2 * j], f[2 * j + 1], s2, scaled), lo, hi);
+        w[j] = pack_bf16(lo, hi);
+      }
+      gelu[at[i]] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    if (plain) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] *= s;
+      plain[at[i]] = pack8(f);
     }
   }
 }

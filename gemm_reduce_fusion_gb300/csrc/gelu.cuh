@@ -83,4 +83,27 @@ __device__ __forceinline__ void times_gelu_prime2(float& v0, float& v1, float h0
   upk2(mul2(pk2(v0, v1), gp), v0, v1);
 }
 
+// GeLU(s r0), GeLU(s r1) of finite r, with the scale applied where it costs
+// least: h Phi(h) = s (max(r, 0) - |r| Phi(-|h|)), the tail at
+// |h| sqrt(log2(e) / 2) = |r| scaled, scaled = s kTailRoot, whose square is
+// the exponent of 2.  Four packed instructions and four selections fewer a
+// pair than scaling first.
+constexpr float kTailRoot = 0.84932180028801905f;  // sqrt(log2(e) / 2)
+__device__ __forceinline__ uint64_t gelu_scaled2(float r0, float r1, uint64_t s, uint64_t scaled) {
+  const uint64_t mag = pk2(fabsf(r0), fabsf(r1)), a = mul2(mag, scaled);
+  constexpr float kP = kTailP / kTailRoot;
+  float d0, d1, g0, g1;
+  upk2(fma2(pk2(kP, kP), a, pk2(1.0f, 1.0f)), d0, d1);
+  const uint64_t t = pk2(rcp_approx(d0), rcp_approx(d1));
+  // the polynomial with its sign turned: c = -Phi(-|h|)
+  uint64_t q = fma2(t, pk2(-kTailA5, -kTailA5), pk2(-kTailA4, -kTailA4));
+  q = fma2(t, q, pk2(-kTailA3, -kTailA3));
+  q = fma2(t, q, pk2(-kTailA2, -kTailA2));
+  q = fma2(t, q, pk2(-kTailA1, -kTailA1));
+  q = mul2(t, q);
+  upk2(mul2(a, a), g0, g1);
+  const uint64_t c = mul2(q, pk2(ex2_approx(-g0), ex2_approx(-g1)));
+  return mul2(s, fma2(mag, c, pk2(fmaxf(r0, 0.0f), fmaxf(r1, 0.0f))));
+}
+
 }  // namespace tpf
