@@ -180,7 +180,10 @@ tp_status dispatch_fwd(const NormParams& P, bool gate, const DevInfo& di, cudaSt
 // registers for two or three CTAs on an SM: the rows under way hide each
 // other's reductions.  Measured at 12288 columns and 2048 rows, bf16 (302 MB,
 // 45 us at the copy rate): one CTA a row with four vectors a thread, whose
-// column sums spill, 91 us for both kernels; clusters of four, 74 us.
+// column sums spill, 91 us for both kernels; clusters of four, 73 us.  What is
+// left over is the latency of a row's two barriers, with half of HBM's rate
+// and 43 % of the issue slots in use.  (One vector a thread, tried at 1160
+// columns: 31 us against 33, for twice the kernels.)
 int bwd_cluster(int64_t nvec) { return nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4; }
 
 // Every worker gets a row at least, since the owner of a row is found by

@@ -394,7 +394,9 @@ struct Coefs {
 
 // NV vectors of 8 columns per thread; RES32: the residual stream is fp32;
 // LN: one of the norms is a layer norm; GATE: the gate has several rows,
-// streamed like the other inputs.
+// streamed like the other inputs.  Measured, RMS norms and a gate per channel,
+// bf16: 8192 x 8192 (537 MB) 93 us, 5.8 TB/s, against 79 us at the copy rate;
+// HBM bounds it, with 40 % of the issue slots in use.
 template <int NV, bool RES32, bool LN, bool GATE, int KIND, int MAXT>
 __global__ void __launch_bounds__(MAXT) block_norm_fwd_kernel(const __grid_constant__ NormParams P) {
   extern __shared__ __align__(16) uint8_t ring[];

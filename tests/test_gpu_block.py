@@ -5,7 +5,7 @@ same values.
 Each bf16 tensor that passes from one call to the next is rounded once (2^-9
 of its size) and a sum over it keeps that relative error; about eight such
 roundings lie between the inputs and the gradients of the first block, and the
-checkpoints add an error of at most 2^-7 of their group's largest value, 1 % of
+checkpoints add an error of at most 1/127 of their group's largest value, 1 % of
 a product's size when it is random.  Outputs are held to 1 % and gradients to
 3 % in the 2-norm."""
 import pytest
