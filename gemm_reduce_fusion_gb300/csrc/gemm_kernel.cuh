@@ -40,6 +40,7 @@
 #include <cuda_bf16.h>
 #include <cstdint>
 
+#include "device_wait.cuh"
 #include "gelu.cuh"
 #include "ptx.cuh"
 
@@ -54,9 +55,6 @@ constexpr int NUM_EPI_WARPS = 8;
 constexpr int NUM_THREADS = 64 + 32 * NUM_EPI_WARPS;
 
 enum Epi : int32_t { EPI_NONE = 0, EPI_GELU = 1, EPI_DGELU = 2 };
-
-// Status word bits (workspace word 0).
-constexpr uint32_t ST_TIMEOUT = 1u;
 
 struct GemmParams {
   CUtensorMap tmA[MAX_MAPS];
@@ -200,31 +198,9 @@ __device__ __forceinline__ Unit decode_pair_unit(const GemmParams& P, int32_t t,
   return decode_unit(P, t);
 }
 
-// Bounded wait; false on timeout (latched) or when another role aborted.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const GemmParams& P,
                                          volatile int32_t* abort_flag, uint32_t role) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  uint32_t n = 0;
-  while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((++n & 127u) == 0) {
-      if (*abort_flag) return false;
-      if (globaltimer_ns() - t0 > P.timeout_ns) {
-        *abort_flag = 1;
-        atomicOr(P.status, ST_TIMEOUT | (role << 4));
-        return false;
-      }
-    }
-  }
-}
-
-// Bounded wait used while shutting down: never latches, never aborts others.
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (globaltimer_ns() - t0 > limit_ns) return;
-  }
+  return wait_bar(bar, parity, P.timeout_ns, P.status, abort_flag, role);
 }
 
 __device__ __forceinline__ float bf16_bits_to_f(uint16_t b) {

@@ -15,6 +15,11 @@ namespace tpf {
 constexpr int kMaxP = 8;
 constexpr size_t kStatusBytes = 256;     // workspace head: status word, padded
 
+// Limit of a kernel's wait on an mbarrier (tp_fused.cu).
+uint64_t device_timeout_ns();
+// Stage that a kernel is told never to hand over, or -1 (TP_DEBUG_DROP_LOAD).
+int64_t debug_drop();
+
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

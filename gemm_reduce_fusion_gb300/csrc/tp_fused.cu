@@ -71,6 +71,10 @@ std::atomic<int64_t> g_tma_store{1};        // 1: staged epilogues leave shared 
 std::atomic<int64_t> g_debug_no_fuse{0};    // 1: backward dX and dW always as two launches
 std::atomic<int64_t> g_k_alternate{1};      // 1: deep contractions alternate their direction by wave
 
+}  // namespace
+
+namespace tpf {
+
 uint64_t device_timeout_ns() {
   const uint64_t o = g_timeout_override_ns.load();
   if (o != 0) return o;
@@ -84,6 +88,12 @@ uint64_t device_timeout_ns() {
   }();
   return v;
 }
+
+int64_t debug_drop() { return g_debug_drop_q.load(); }
+
+}  // namespace tpf
+
+namespace {
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;

@@ -6,9 +6,9 @@
 // the weights (K N (1/2 + 2/G)), so that the kernel streams each of them once
 // and has to spend few instructions on it.  The tokens' dot products run on
 // mma.sync m16n8k16 with the weights' columns as its 16 rows and the tokens
-// as its 8 columns: 8 tokens cost what one does, where the 128-row tiles of
-// tcgen05 would need the dequantised weights written to tensor memory or
-// shared memory first, which costs more than the product at these sizes.
+// as its 8 columns: 8 tokens cost what one does, and a weight goes from
+// memory to its product through registers alone.  More tokens on large
+// weights are the work of w4_wide_kernel (w4_wide.cuh), on tcgen05.
 //
 // Layout (32 columns x 64 rows a tile of 1024 bytes): a lane's 16 bytes are
 // its A fragments of four mma, so that weights go from memory to registers
@@ -52,6 +52,8 @@
 #include "host_util.h"
 #include "vec_util.cuh"
 #include "w4.h"
+#include "w4_device.cuh"
+#include "w4_wide.cuh"
 
 using namespace tpf;
 
@@ -88,45 +90,6 @@ struct Shape {
   static_assert(KH == 1 || kSwap * kWarps * NO * 512 <= kS + kX, "the row halves meet in a stage's buffer");
 };
 
-struct W4Params {
-  const void* x[8];
-  const void* q[8];
-  const void* s[8];
-  const __nv_bfloat16* bias[8];
-  void* y[8];
-  float* part;                // [2 * runs][kStrips x 8 NT]: sums of a column block's part
-  uint32_t run_stages;        // run r: stages r * run_stages ... (the last run may be shorter)
-  uint32_t M, N, K;
-  uint32_t ktiles, groups, pairs;  // 64-row tiles, scale groups, 32-column pairs of 16-column strips of a shard
-  uint32_t nblocks;                // column blocks of a shard
-  uint32_t kstages;                // stages of a shard
-  uint32_t spb;                    // stages of a column block: row layout p * kstages, column layout kstages
-  uint32_t stages;                 // all
-  int32_t row, epi, out_f32;
-};
-
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool valid) {
-  const uint32_t n = valid ? 16u : 0u;
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-
-__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-
-// The four fragment registers of a word (see the top), for the columns i
-// (q - 8, times 2^-6) and i + 8 (times 2^-2) in turn.
-__device__ __forceinline__ void dequant(uint32_t w, uint32_t (&a)[4]) {
-  constexpr uint32_t kUp = 0x7F007F00u, kOff0 = 0xBE00BE00u, kOff1 = 0xC000C000u;  // 2^127, -2^-3, -2
-  const uint32_t v = w >> 8;
-  a[0] = fma_bf16x2(w & 0x000F000Fu, kUp, kOff0);
-  a[1] = fma_bf16x2(w & 0x00F000F0u, kUp, kOff1);
-  a[2] = fma_bf16x2(v & 0x000F000Fu, kUp, kOff0);
-  a[3] = fma_bf16x2(v & 0x00F000F0u, kUp, kOff1);
-}
-
 // D += A . B, 16 x 8 x 16, bf16 in, fp32 accumulator; the other form starts from zero.
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -137,15 +100,6 @@ __device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
                : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
-}
-
-// The runs that hold stages of a column block.
-struct Parts {
-  uint32_t first, last;
-};
-__device__ __forceinline__ Parts parts_of(const W4Params& P, uint32_t block) {
-  const uint32_t b0 = block * P.spb;
-  return {b0 / P.run_stages, (b0 + P.spb - 1) / P.run_stages};
 }
 
 // Where run r keeps its sums of a column block that it shares: its first
@@ -178,11 +132,7 @@ __device__ __forceinline__ void write_out(const W4Params& P, uint32_t block, uin
     for (int i = 0; i < 2; ++i) {
       const uint32_t tok = n * 8 + 2 * t + i;
       if (tok >= P.M) continue;
-      float y = vals[2 * r + i] + bias;
-      if (P.epi == TP_EPI_GELU) y = gelu_f(y);
-      const int64_t at = static_cast<int64_t>(tok) * P.N + col;
-      if (P.out_f32) static_cast<float*>(P.y[shard])[at] = y;
-      else static_cast<__nv_bfloat16*>(P.y[shard])[at] = __float2bfloat16_rn(y);
+      write_one(P, shard, tok, col, bias, vals[2 * r + i]);
     }
   }
 }
@@ -533,12 +483,30 @@ __global__ void __launch_bounds__(256) w4_unpack_kernel(const __grid_constant__ 
 
 struct Plan {
   uint32_t ktiles, pairs, nblocks, kstages, spb, stages, runs, run_stages, blocks, nt;
+  bool wide;    // w4_wide_kernel
   size_t slab;  // bytes of a thread block's sums of one column block
 };
 
+// Token tiles of 8 of w4_linear_kernel.
 int tiles_for(int64_t M) {
   const int n = static_cast<int>(cdiv(M, 8));
   return n <= 2 ? n : n <= 4 ? 4 : n <= 6 ? 6 : 8;
+}
+
+// Whether w4_wide_kernel takes the call.  It has more to set up and a longer
+// way from a weight to its sum, so that it wants more than 16 tokens, eight
+// stages for each SM (of 256 columns x 128 rows), and scale groups of 64 rows
+// or more, unless there are so many tokens that mma.sync is slower still.
+// Measured, w4_linear_kernel against w4_wide_kernel, us:
+//   p = 8, 49152 -> 12288, groups of 128: 24 tokens 117 / 105, 48 177 / 117,
+//     64 250 / 125; groups of 64: 32 tokens 129 / 125, 64 238 / 162; groups
+//     of 32: 32 tokens 140 / 166, 48 199 / 202, 64 246 / 220;
+//   p = 4, 4096 -> 16384, groups of 128 (13 stages an SM): 20 tokens 25 / 25,
+//     48 33 / 27, 64 41 / 31;
+//   4096 -> 4096, groups of 128 (3 stages): 20 tokens 17 / 15, 64 21 / 23.
+// At 16 tokens w4_linear_kernel takes 75 in the first of these.
+bool is_wide(int p, int64_t M, int64_t N, int64_t K, int64_t G) {
+  return M > 16 && p * cdiv(N, kWideCols) * cdiv(K, kWideRows) >= 8 * kSMs && (G > 32 || M > 48);
 }
 
 template <int NT, int GB>
@@ -558,7 +526,8 @@ void shape_of(Plan* P, int64_t N, int64_t K, int64_t G) {
 
 bool make_plan(bool row, int p, int64_t M, int64_t N, int64_t K, int64_t G, Plan* out) {
   Plan P;
-  P.nt = static_cast<uint32_t>(tiles_for(M));
+  P.wide = is_wide(p, M, N, K, G);
+  P.nt = static_cast<uint32_t>(P.wide ? cdiv(M, 16) * 16 : tiles_for(M));
   P.ktiles = static_cast<uint32_t>(cdiv(K, 64));
   P.pairs = static_cast<uint32_t>(cdiv(N, 32));
   switch (P.nt) {
@@ -566,7 +535,12 @@ bool make_plan(bool row, int p, int64_t M, int64_t N, int64_t K, int64_t G, Plan
     case 2: shape_of<2>(&P, N, K, G); break;
     case 4: shape_of<4>(&P, N, K, G); break;
     case 6: shape_of<6>(&P, N, K, G); break;
-    default: shape_of<8>(&P, N, K, G); break;
+    case 8: shape_of<8>(&P, N, K, G); break;
+    default:  // wide
+      P.nblocks = static_cast<uint32_t>(cdiv(N, kWideCols));
+      P.kstages = static_cast<uint32_t>(cdiv(K, kWideRows));
+      P.slab = static_cast<size_t>(kWideCols) * P.nt * sizeof(float);
+      break;
   }
   const int64_t spb = row ? static_cast<int64_t>(p) * P.kstages : P.kstages;
   const int64_t stages = spb * P.nblocks * (row ? 1 : p);
@@ -574,7 +548,7 @@ bool make_plan(bool row, int p, int64_t M, int64_t N, int64_t K, int64_t G, Plan
   P.spb = static_cast<uint32_t>(spb);
   P.stages = static_cast<uint32_t>(stages);
   P.blocks = static_cast<uint32_t>(P.nblocks * (row ? 1 : p));
-  P.run_stages = static_cast<uint32_t>(cdiv(stages, std::min<int64_t>(stages, static_cast<int64_t>(kSMs) * 2)));
+  P.run_stages = static_cast<uint32_t>(cdiv(stages, std::min<int64_t>(stages, static_cast<int64_t>(kSMs) * (P.wide ? 1 : 2))));
   P.runs = static_cast<uint32_t>(cdiv(stages, P.run_stages));
   *out = P;
   return true;
@@ -589,6 +563,25 @@ tp_status run_w4(const W4Params& P, const Plan& L, cudaStream_t stream) {
   TP_TRY(launch_dependent(k, dim3(L.runs), static_cast<unsigned>(kThreads), static_cast<size_t>(Shape<NT, GB>::kBytes), stream, P));
   if (L.run_stages == L.spb) return TP_OK;  // every column block is one run's
   return launch_dependent(w4_join_kernel<NT, GB>, dim3(L.blocks, NT * Shape<NT, GB>::NO), static_cast<unsigned>(kThreads), 0, stream, P);
+}
+
+template <int NB, int GB>
+tp_status run_wide(const W4Params& P, const Plan& L, cudaStream_t stream) {
+  static KernelInfo info;
+  void (*k)(W4Params) = w4_wide_kernel<NB, GB>;
+  int regs = 0;
+  TP_TRY(kernel_regs(reinterpret_cast<const void*>(k), &info, &regs));
+  TP_TRY(launch_dependent(k, dim3(L.runs), static_cast<unsigned>(kWideThreads), static_cast<size_t>(WideShape<NB, GB>::kBytes), stream, P));
+  if (L.run_stages == L.spb) return TP_OK;
+  return launch_dependent(w4_wide_join_kernel<NB>, dim3(L.blocks, static_cast<unsigned>(cdiv(P.M, 4))), static_cast<unsigned>(kWideCols), 0,
+                          stream, P);
+}
+
+template <int NB>
+tp_status run_wide_group(const W4Params& P, int G, const Plan& L, cudaStream_t stream) {
+  if (G == 32) return run_wide<NB, 1>(P, L, stream);
+  if (G == 64) return run_wide<NB, 2>(P, L, stream);
+  return run_wide<NB, 4>(P, L, stream);
 }
 
 template <int NT>
@@ -662,12 +655,18 @@ tp_status w4_forward(bool row, const void* const* x, const void* const* q, const
   P.row = row;
   P.epi = epi;
   P.out_f32 = out_dtype == TP_FP32;
+  P.status = static_cast<uint32_t*>(ws);
+  P.timeout_ns = device_timeout_ns();
+  P.drop = static_cast<int32_t>(debug_drop());
   switch (L.nt) {
     case 1: return run_group<1>(P, static_cast<int>(G), L, stream);
     case 2: return run_group<2>(P, static_cast<int>(G), L, stream);
     case 4: return run_group<4>(P, static_cast<int>(G), L, stream);
     case 6: return run_group<6>(P, static_cast<int>(G), L, stream);
-    default: return run_group<8>(P, static_cast<int>(G), L, stream);
+    case 8: return run_group<8>(P, static_cast<int>(G), L, stream);
+    case 32: return run_wide_group<32>(P, static_cast<int>(G), L, stream);
+    case 48: return run_wide_group<48>(P, static_cast<int>(G), L, stream);
+    default: return run_wide_group<64>(P, static_cast<int>(G), L, stream);
   }
 }
 
