@@ -40,8 +40,7 @@
 // Measured with scale groups of 128 (of 64 at 16 tokens), both kernels:
 //   p = 8, 12288 -> 49152, 1 token    (312 MB)  54 us, 5.8 TB/s
 //   p = 8, 49152 -> 12288, 16 tokens  (323 MB)  75 us, 4.3 TB/s
-//   p = 4, 4096 -> 16384, 48 tokens   (37 MB)   28 us; the mma alone 11 us
-// against 46, 48 and 5.4 us at the copy rate.  The second kernel takes 5 to 7
+// against 46 and 48 us at the copy rate.  The second kernel takes 5 to 7
 // us of it, most of them the latency of its few reads.
 #include <cuda_bf16.h>
 

@@ -497,6 +497,7 @@ tp_status tp_noalloc_device_status(cudaStream_t stream);
  *     the kernel latches TP_ERR_DEVICE_TIMEOUT, stops its other roles, waits
  *     (bounded) for its own copies and MMAs in flight, frees its tensor
  *     memory and returns; -1 turns the hook off.  No fault or trap is used.
+ *     (The 4-bit tcgen05 kernel's CTA 0 never hands over stage n of the tokens.)
  *   TP_DEBUG_TILE_MODE: 0 (default) lets the planner choose 128x256 tiles on
  *     one CTA or 256x256 tiles on a CTA pair; 1 forces single-CTA tiles; 2
  *     uses CTA pairs for every non-swapped launch (parity testing of both
