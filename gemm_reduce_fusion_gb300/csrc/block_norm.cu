@@ -309,7 +309,7 @@ tp_status resident_clusters(const void* kernel, int cluster, int threads, size_t
 size_t block_norm_bwd_workspace(int64_t M, int64_t h) {
   const Shape sh = bwd_shape(cdiv(h, 8), M);
   const int64_t ctas = bwd_ctas(sh, cdiv(h, 8), M), workers = ctas * bwd_workers(sh);
-  return kStatusBytes + static_cast<size_t>(4 * ctas + 2 * workers) * h * sizeof(float);
+  return kDataOffset + static_cast<size_t>(4 * ctas + 2 * workers) * h * sizeof(float);
 }
 
 }  // namespace tpf
@@ -425,7 +425,7 @@ extern "C" tp_status tp_block_norm_bwd(const void* const* z, const void* const* 
   const bool groups = d->gate != nullptr && d->gate_rows > 1;
   const bool ln = d->post == TP_NORM_LAYER || d->pre == TP_NORM_LAYER;
   const int64_t ctas = bwd_ctas(sh, P.nvec, M);
-  float* area = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kStatusBytes);
+  float* area = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kDataOffset);
   const bool sums = g.dw_post || g.db_post || g.dw_pre || g.db_pre || (g.dgate && !groups);
   P.part = sums ? area : nullptr;
   P.gpart = g.dgate && groups ? area + 4 * ctas * h : nullptr;

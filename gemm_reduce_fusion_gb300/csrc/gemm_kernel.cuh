@@ -54,6 +54,8 @@ constexpr int MAX_GROUPS = 64;
 constexpr int NUM_EPI_WARPS = 8;
 constexpr int NUM_THREADS = 64 + 32 * NUM_EPI_WARPS;
 
+constexpr int kSliceBits = 3;  // of a slice counter: slices finished, at most 4
+
 enum Epi : int32_t { EPI_NONE = 0, EPI_GELU = 1, EPI_DGELU = 2 };
 
 struct GemmParams {
@@ -467,10 +469,12 @@ __device__ __forceinline__ void drain_half_from_parts(const GemmParams& P, int32
 }
 
 // Counts this warp's slice of a (tile, warp) region as finished; true for
-// the warp whose slice is the last of n.  A counter holds (launch epoch <<
-// 16 | slices finished); one left by another launch counts as zero, so a
+// the warp whose slice is the last of n <= 4.  A counter holds (launch tag <<
+// 3 | slices finished); one left by another launch counts as zero, so a
 // launch stopped part-way (a device timeout) leaves nothing the next launch
-// could miscount.  The last warp also sets the counter back to zero, so
+// could miscount.  The tags are 61 scattered bits (slice_tag), so that other
+// calls' partials, which may lie where this launch counts, are not a count
+// either.  The last warp also sets the counter back to zero, so
 // that a launch replayed with the same number (a CUDA graph) starts from
 // zero too.  Each compare-and-swap that fails means another of the region's
 // n warps succeeded, so at most n attempts are needed; past that bound the
@@ -484,13 +488,13 @@ __device__ __forceinline__ bool finish_slice(const GemmParams& P, unsigned long 
     unsigned long long next = 0;
     bool done = false;
     for (int i = 0; i <= n + 4 && !done; ++i) {
-      next = (cur >> 16) == P.epoch ? cur + 1 : ((P.epoch << 16) | 1ull);
+      next = (cur >> kSliceBits) == P.epoch ? cur + 1 : ((P.epoch << kSliceBits) | 1ull);
       const unsigned long long prev = atomicCAS(cnt, cur, next);
       done = prev == cur;
       cur = prev;
     }
     if (!done) atomicOr(P.status, ST_TIMEOUT | (5u << 4));
-    last = done && (next & 0xFFFFull) == static_cast<unsigned long long>(n);
+    last = done && (next & ((1ull << kSliceBits) - 1)) == static_cast<unsigned long long>(n);
     if (last) atomicExch(cnt, 0ull);  // every slice of the region has arrived: no other writer is left
   }
   last = __shfl_sync(0xFFFFFFFFu, last, 0);

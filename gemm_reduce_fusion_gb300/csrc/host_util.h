@@ -14,6 +14,10 @@ namespace tpf {
 
 constexpr int kMaxP = 8;
 constexpr size_t kStatusBytes = 256;     // workspace head: status word, padded
+// Behind it the counters of a sliced last wave (tp_fused.cu), at most.  What
+// the calls around the sharded Linear keep in a workspace begins after them.
+constexpr size_t kSliceCounterBytes = 9728;
+constexpr size_t kDataOffset = kStatusBytes + kSliceCounterBytes;
 
 // Limit of a kernel's wait on an mbarrier (tp_fused.cu).
 uint64_t device_timeout_ns();
@@ -25,10 +29,6 @@ inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 inline size_t esize(tp_dtype d) { return d == TP_FP32 ? 4 : 2; }
-
-// Numbers every launch that counts arrivals in its workspace, so that a
-// counter left by another launch reads as zero (never 0 itself).
-inline std::atomic<unsigned long long> g_launch_epoch{0};
 
 struct DevInfo {
   int sms = 0;

@@ -66,6 +66,7 @@ std::atomic<int64_t> g_debug_no_tail{0};    // 1: no k-slices in the last wave o
 std::atomic<int64_t> g_debug_split_k{0};    // n > 0: split-K factor of launches below one wave
 std::atomic<unsigned long long*> g_trace{nullptr};  // timeline trace buffer of the next launches
 std::atomic<int64_t> g_trace_cap{0};
+std::atomic<unsigned long long> g_launch_number{0};  // numbers every launch (slice counters)
 std::atomic<int64_t> g_l2_hints{1};         // 1: L2 cache policies on operand loads and output stores
 std::atomic<int64_t> g_tma_store{1};        // 1: staged epilogues leave shared memory by TMA store
 std::atomic<int64_t> g_debug_no_fuse{0};    // 1: backward dX and dW always as two launches
@@ -353,6 +354,8 @@ struct Shape {
   size_t tail_cnt_bytes() const {
     return static_cast<size_t>((tail_tiles() * 2 * NUM_EPI_WARPS * 8 + 255) / 256 * 256);
   }
+  // (a tail has less than a wave of tiles)
+  static_assert((kPlanSMs / 2 - 1) * 2 * NUM_EPI_WARPS * 8 <= kSliceCounterBytes, "room for every counter");
   size_t partial_bytes() const {
     if (tail_split > 1)  // counters, then one fp32 256 x 256 tile per slice
       return tail_cnt_bytes() + static_cast<size_t>(tail_tiles()) * tail_split * 256 * 256 * 4u;
@@ -840,6 +843,21 @@ tp_status run_launch_phases(Launch& L, tp_dtype out_dtype, void* ws, cudaStream_
   return TP_OK;
 }
 
+// Tag of the slice counters of launch n >= 1.  A bijection of 61 bits (odd
+// products and shifts to the right), so that no two launches share a tag and
+// none is zero; its bits are scattered, so that data which another call left
+// in the workspace is not a tag (the chance is 2^-61 a word), as a small number
+// may be: 16256 is also a bfloat16 one, followed by zeros.
+unsigned long long slice_tag(unsigned long long n) {
+  constexpr unsigned long long kMask = (1ull << (64 - kSliceBits)) - 1;
+  unsigned long long t = n & kMask;
+  for (unsigned long long odd : {0x1E3779B97F4A7C15ull, 0x17A3C5D99B4F6E8Bull, 0x0D6E8FEB86659FD9ull}) {
+    t ^= t >> 30;
+    t = (t * odd) & kMask;
+  }
+  return t ^ (t >> 31);
+}
+
 // The launch-time fields of a GEMM launch with work to do (K > 0): workspace
 // regions, the launch number, L2 policies and the TMA-store output maps.
 void prepare_gemm(Launch& L, tp_dtype out_dtype, void* ws) {
@@ -848,8 +866,7 @@ void prepare_gemm(Launch& L, tp_dtype out_dtype, void* ws) {
   P.status = static_cast<uint32_t*>(ws);
   P.out_f32 = out_dtype == TP_FP32 ? 1 : 0;
   if (s.n_split > 1) P.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kStatusBytes);
-  // slice counters tagged with another launch's number read as zero
-  P.epoch = g_launch_epoch.fetch_add(1) + 1;
+  P.epoch = slice_tag(g_launch_number.fetch_add(1) + 1);
   if (s.tail_split > 1) {
     uint8_t* base = static_cast<uint8_t*>(ws) + kStatusBytes;
     P.tail_cnt = reinterpret_cast<unsigned long long*>(base);
@@ -908,7 +925,8 @@ void prepare_gemm(Launch& L, tp_dtype out_dtype, void* ws) {
 }
 
 // Workspace of a backward call on checkpoints: the products' own workspace,
-// then the restored tensors (values and, for row layouts, their GeLU).
+// then, behind any launch's counters, the restored tensors (values and, for
+// row layouts, their GeLU).
 struct CkptArea {
   size_t gemm, tensor, end;  // bytes of the products' part, of one restored tensor, of all
   int n;                     // restored tensors of each kind
@@ -918,7 +936,7 @@ CkptArea ckpt_area(tp_op op, int p, int64_t M, int64_t N, int64_t K, int64_t chu
   const bool col = op == TP_OP_COL_BWD_CKPT, ag = op == TP_OP_AG_MM_BWD_CKPT;
   const tp_op base = col ? TP_OP_COL_BWD : ag ? TP_OP_AG_MM_BWD : op == TP_OP_ROW_BWD_CKPT ? TP_OP_ROW_BWD : TP_OP_ROW_RS_BWD;
   CkptArea a;
-  a.gemm = (workspace_for(op_shapes(base, p, M, N, K, chunk_m, dt)) + 255) / 256 * 256;
+  a.gemm = (std::max(kDataOffset, workspace_for(op_shapes(base, p, M, N, K, chunk_m, dt))) + 255) / 256 * 256;
   a.tensor = (static_cast<size_t>((ag ? M / p : M) * K) * 2 + 255) / 256 * 256;
   a.n = col ? 1 : p;
   a.end = a.gemm + a.tensor * a.n * (col || ag ? 1 : 2);

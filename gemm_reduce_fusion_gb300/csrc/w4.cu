@@ -639,7 +639,7 @@ tp_status w4_forward(bool row, const void* const* x, const void* const* q, const
     P.y[r] = y[r];
     P.bias[r] = static_cast<const __nv_bfloat16*>(bias ? bias[r] : nullptr);
   }
-  P.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kStatusBytes);
+  P.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kDataOffset);
   P.run_stages = L.run_stages;
   P.M = static_cast<uint32_t>(M);
   P.N = static_cast<uint32_t>(N);
@@ -697,7 +697,7 @@ size_t w4_workspace(bool row, int p, int64_t M, int64_t N, int64_t K) {
   for (int64_t G : {32, 64, 128}) {  // the size does not ask for the group
     Plan L;
     if (make_plan(row, p, M, N, std::max<int64_t>(K, 1), G, &L))
-      most = std::max(most, kStatusBytes + static_cast<size_t>(L.runs) * 2 * L.slab);
+      most = std::max(most, kDataOffset + static_cast<size_t>(L.runs) * 2 * L.slab);
   }
   return most;
 }

@@ -45,8 +45,10 @@
  *    device status word (which stays zero unless a device wait times out)
  *    and, when a launch needs them, fp32 partials: split-K partials, or the
  *    k-slices of the last partial wave of a CTA-pair launch together with
- *    their counters (tagged with a per-launch number, so a counter left
- *    by any earlier launch, finished or stopped, reads as zero).
+ *    their counters (tagged with 61 scattered bits of the launch's own, so
+ *    that a counter left by any earlier launch, finished or stopped, reads
+ *    as zero, and so does other calls' data).  The calls around the sharded
+ *    Linear keep theirs behind the largest launch's counters.
  *    tp_workspace_size() is the size of the fastest plan; a smaller
  *    workspace that still holds the plan without last-wave slices is
  *    accepted, and the call then runs without them.
@@ -465,8 +467,8 @@ tp_status tp_get_device_status(void* ws, cudaStream_t stream);
  *    the GPU (different streams without ordering between them) race on it;
  *    order them on one stream.  Nothing in the array has to start at zero:
  *    every partial a call reads was written earlier by that same call, and
- *    slice counters carry the number of the launch that wrote them, so
- *    stale ones read as zero.
+ *    slice counters carry the tag of the launch that wrote them, so stale
+ *    ones read as zero.
  *  - A device-side wait that runs out of time latches
  *    TP_ERR_DEVICE_TIMEOUT into the array's status word, as it would into a
  *    workspace; tp_noalloc_device_status() reads and clears it.
