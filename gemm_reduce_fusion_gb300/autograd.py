@@ -40,24 +40,37 @@ from typing import Sequence
 
 import torch
 
-from . import (TP_EPI_GELU, TP_OP_AG_MM, TP_OP_AG_MM_BWD, TP_OP_COL_BWD, TP_OP_COL_FWD, TP_OP_ROW_AR,
-               TP_OP_ROW_BWD, TP_OP_ROW_RS, TP_OP_ROW_RS_BWD, tp_ag_matmul, tp_ag_matmul_bwd,
+from . import (TP_EPI_GELU, TP_OP_AG_MM, TP_OP_AG_MM_BWD, TP_OP_BLOCK_NORM_BWD, TP_OP_COL_BWD, TP_OP_COL_FWD, TP_OP_COL_W4,
+               TP_OP_ROW_AR, TP_OP_ROW_BWD, TP_OP_ROW_RS, TP_OP_ROW_RS_BWD, TP_OP_ROW_W4, tp_ag_matmul, tp_ag_matmul_bwd,
                tp_col_linear_bwd, tp_col_linear_fwd, tp_row_linear_bwd, tp_row_linear_bwd_reducescatter,
                tp_row_linear_fwd_allreduce, tp_row_linear_fwd_reducescatter, tp_workspace_size)
 
-_WS: dict[int, torch.Tensor] = {}
+_WS: dict[tuple[int, int], torch.Tensor] = {}  # by device and stream
+_HEAD = 16384  # a workspace's status word and slice counters lie in its first bytes
+_COUNT_NOTHING = {TP_OP_BLOCK_NORM_BWD, TP_OP_COL_W4, TP_OP_ROW_W4}
 
 
 def _workspace(device: torch.device, calls) -> torch.Tensor:
-    """The device's shared workspace, grown (zero-filled) to fit every call
-    in ``calls`` (tuples of tp_workspace_size arguments).  Calls that share
-    it are ordered on the current stream."""
-    need = max(tp_workspace_size(*c) for c in calls)
+    """A workspace for every call in ``calls`` (tuples of tp_workspace_size
+    arguments): the current stream's, whose calls are ordered, grown
+    (zero-filled) where it is too small.
+
+    A call that is captured into a CUDA graph gets one of the graph's own,
+    from the graph's memory: the stream's may be outgrown and freed while the
+    graph still points to it, and graphs may be replayed side by side.  What
+    has to start at zero is cleared in the graph."""
+    need = (max(tp_workspace_size(*c) for c in calls) + 255) // 256 * 256
     idx = device.index if device.index is not None else torch.cuda.current_device()
-    ws = _WS.get(idx)
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        if any(c[0] not in _COUNT_NOTHING for c in calls):
+            ws[:_HEAD].zero_()
+        return ws
+    key = idx, torch.cuda.current_stream(idx).cuda_stream
+    ws = _WS.get(key)
     if ws is None or ws.numel() < need:
-        ws = torch.zeros((need + 255) // 256 * 256, dtype=torch.uint8, device=device)
-        _WS[idx] = ws
+        ws = torch.zeros(need, dtype=torch.uint8, device=device)
+        _WS[key] = ws
     return ws
 
 
