@@ -258,19 +258,19 @@ void add_desc(RangeList* in, const tp_block_norm_desc* d, int64_t h) {
   in->push_back({d->gate, d->gate ? static_cast<size_t>(d->gate_rows * h) * 2 : 0});
 }
 
-// Refuses overlaps, save that out[s] may be in[s] itself where `same` is
-// given: a row of it is written only after it has been read by the same
-// thread block.
+// Refuses overlaps, save that the shard out[s] may be the input shard same[s]
+// itself, of `bytes` bytes: a row of it is written only after the same thread
+// block has read it.  Other shards' rows, and the other inputs (`ins`), are
+// read by blocks that do not wait for one another.
 bool clash(const RangeList& outs, const RangeList& ins, const void* const* out, const void* const* same, int p,
            size_t bytes) {
-  RangeList rest;
-  for (const Range& r : ins) {
-    bool skip = false;
-    for (int s = 0; s < p && same != nullptr && out != nullptr; ++s)
-      skip |= r.p == same[s] && r.bytes == bytes && out[s] == same[s];
-    if (!skip) rest.push_back(r);
-  }
-  return any_overlap(outs, rest);
+  if (any_overlap(outs, ins)) return true;
+  for (int s = 0; s < p && same != nullptr; ++s)
+    for (const Range& o : outs) {
+      const bool itself = out != nullptr && out[s] == same[s] && o.p == out[s];  // (outputs do not overlap)
+      if (!itself && overlap(o, {same[s], bytes})) return true;
+    }
+  return false;
 }
 
 }  // namespace
@@ -330,7 +330,6 @@ extern "C" tp_status tp_block_norm_fwd(const void* const* x, const void* const* 
   {
     const size_t one = static_cast<size_t>(M / p * h);
     RangeList ins, outs;
-    add_ranges(&ins, x, p, one * esize(res_dtype));
     add_ranges(&ins, z, p, one * 2);
     add_desc(&ins, d, h);
     add_ranges(&outs, in(y), p, one * esize(res_dtype));
@@ -387,7 +386,6 @@ extern "C" tp_status tp_block_norm_bwd(const void* const* z, const void* const* 
     add_ranges(&ins, z, p, one * 2);
     if (dn != nullptr) add_ranges(&ins, y, p, one * r);
     add_ranges(&ins, dn, p, one * 2);
-    add_ranges(&ins, dy, p, one * r);
     add_desc(&ins, d, h);
     add_ranges(&outs, in(dx), p, one * r);
     add_ranges(&outs, in(dz), p, one * 2);
