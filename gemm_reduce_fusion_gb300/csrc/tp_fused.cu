@@ -1915,8 +1915,9 @@ struct CkptCall {
   void* gelu[kMaxP];
 };
 
-tp_status ckpt_call(tp_op op, const void* const* q, const void* const* e, bool need, const std::vector<Range>& outs, int p, int64_t M,
-                    int64_t N, int64_t K, int64_t chunk_m, tp_dtype dt, void* ws, size_t ws_bytes, CkptCall* c) {
+tp_status ckpt_call(tp_op op, const void* const* q, const void* const* e, bool need, const void* const* w, const void* const* dy,
+                    const std::vector<Range>& outs, int p, int64_t M, int64_t N, int64_t K, int64_t chunk_m, tp_dtype dt, void* ws,
+                    size_t ws_bytes, CkptCall* c) {
   TP_TRY(check_sizes(p, M, N, K, chunk_m, dt));
   if ((op == TP_OP_AG_MM_BWD_CKPT || op == TP_OP_ROW_RS_BWD_CKPT) && M % p != 0) return TP_ERR_UNSUPPORTED_SHAPE;
   c->area = ckpt_area(op, p, M, N, K, chunk_m, dt);
@@ -1937,6 +1938,14 @@ tp_status ckpt_call(tp_op op, const void* const* q, const void* const* e, bool n
   }
   written.push_back({ws, ws_bytes});
   if (any_overlap(written, ins)) return TP_ERR_INVALID_ARG;
+  // the products' operands: the restore writes to ws before they are read
+  // (the products check them against the outputs)
+  std::vector<Range> operands;
+  const bool row = op == TP_OP_ROW_BWD_CKPT, rs = op == TP_OP_ROW_RS_BWD_CKPT;
+  add_ranges(&operands, w, p, static_cast<size_t>(K * N) * 2);
+  add_ranges(&operands, dy, row ? 1 : p, static_cast<size_t>((rs ? M / p : M) * N) * 2);
+  for (const Range& r : operands)
+    if (overlap(r, {ws, ws_bytes})) return TP_ERR_INVALID_ARG;
   uint8_t* at = static_cast<uint8_t*>(ws) + c->area.gemm;
   for (int i = 0; i < n; ++i) {
     c->plain[i] = at + c->area.tensor * i;
@@ -1961,8 +1970,8 @@ tp_status row_ckpt(bool rs, const void* const* q, const void* const* e, const vo
   outs.push_back({db, db ? static_cast<size_t>(N) * esize(dt) : 0});
   CkptCall c;
   const bool need_h = act && dx != nullptr, need_x = dw != nullptr;
-  TP_TRY(ckpt_call(rs ? TP_OP_ROW_RS_BWD_CKPT : TP_OP_ROW_BWD_CKPT, q, e, need_h || need_x, outs, p, M, N, K, chunk_m, dt, ws, ws_bytes,
-                   &c));
+  TP_TRY(ckpt_call(rs ? TP_OP_ROW_RS_BWD_CKPT : TP_OP_ROW_BWD_CKPT, q, e, need_h || need_x, w, dy, outs, p, M, N, K, chunk_m, dt, ws,
+                   ws_bytes, &c));
   const bool plain = need_h || (need_x && !act), gelu = need_x && act;
   const CkptRestore r = {q, e, plain ? c.plain : nullptr, gelu ? c.gelu : nullptr, p, M, K};
   const void* const* x = in(act ? c.gelu : c.plain);
@@ -1983,7 +1992,7 @@ extern "C" tp_status tp_col_linear_bwd_ckpt(const void* q, const void* e, const 
   add_ranges(&outs, in(dw), p, static_cast<size_t>(K * N) * esize(out_dtype));
   add_ranges(&outs, in(db), p, static_cast<size_t>(N) * esize(out_dtype));
   CkptCall c;
-  TP_TRY(ckpt_call(TP_OP_COL_BWD_CKPT, &q, &e, dw != nullptr, outs, p, M, N, K, chunk_m, out_dtype, ws, ws_bytes, &c));
+  TP_TRY(ckpt_call(TP_OP_COL_BWD_CKPT, &q, &e, dw != nullptr, w, dy, outs, p, M, N, K, chunk_m, out_dtype, ws, ws_bytes, &c));
   const CkptRestore r = {&q, &e, c.plain, nullptr, 1, M, K};
   return col_bwd(dw ? c.plain[0] : nullptr, w, dy, dx, dw, db, p, M, N, K, chunk_m, out_dtype, ws, c.area.gemm, stream,
                  dw ? &r : nullptr);
@@ -2006,7 +2015,7 @@ extern "C" tp_status tp_ag_matmul_bwd_ckpt(const void* const* q, const void* con
   add_ranges(&outs, in(dw), p, static_cast<size_t>(K * N) * esize(out_dtype));
   add_ranges(&outs, in(db), p, static_cast<size_t>(N) * esize(out_dtype));
   CkptCall c;
-  TP_TRY(ckpt_call(TP_OP_AG_MM_BWD_CKPT, q, e, dw != nullptr, outs, p, M, N, K, chunk_m, out_dtype, ws, ws_bytes, &c));
+  TP_TRY(ckpt_call(TP_OP_AG_MM_BWD_CKPT, q, e, dw != nullptr, w, dy, outs, p, M, N, K, chunk_m, out_dtype, ws, ws_bytes, &c));
   const CkptRestore r = {q, e, c.plain, nullptr, p, M / p, K};
   return ag_bwd(in(c.plain), w, dy, dx, dw, db, p, M, N, K, chunk_m, out_dtype, ws, c.area.gemm, stream, dw ? &r : nullptr);
 }

@@ -57,3 +57,32 @@ def test_in_place_in_the_backward_pass():
     assert call([dy[0], other[1]], dy=[dy[0], dy[0]]) == BAD
     assert call([dy[1], dy[0]]) == BAD
     assert call(dy, y=dy) == BAD and call(dy, dn=dy) == BAD and call(dy, y=[y[0], dy[0]]) == BAD
+
+
+def test_the_restored_part_of_a_workspace_overlaps_no_operand():
+    P, M, N, K = 2, 8, 64, 32
+    q, e, w, dy, dx, dw = ([at(2 * i), at(2 * i + 1)] for i in range(6))
+    ws = at(20)
+
+    def need(op):
+        return tp.tp_workspace_size(op, P, M, N, K)
+
+    def col(w=w, dy=dy):
+        return L.tp_col_linear_bwd_ckpt(q[0], e[0], arr(*w), arr(*dy), dx[0], arr(*dw), None, P, M, N, K, 0, 0, ws, need(10), None)
+
+    def row(w=w, dy=dy):
+        return L.tp_row_linear_bwd_ckpt(arr(*q), arr(*e), arr(*w), dy[0], arr(*dx), arr(*dw), None, 2, P, M, N, K, 0, 0, ws, need(11), None)
+
+    def ag(w=w, dy=dy):
+        return L.tp_ag_matmul_bwd_ckpt(arr(*q), arr(*e), arr(*w), arr(*dy), arr(*dx), arr(*dw), None, P, M, N, K, 0, 0, ws, need(12), None)
+
+    def rs(w=w, dy=dy):
+        return L.tp_row_linear_bwd_reducescatter_ckpt(arr(*q), arr(*e), arr(*w), arr(*dy), arr(*dx), arr(*dw), None, 2, P, M, N, K, 0, 0,
+                                                      ws, need(13), None)
+    for call, op in ((col, 10), (row, 11), (ag, 12), (rs, 13)):
+        assert call() not in (tp.TP_OK, BAD)
+        last = ws + need(op) - 16  # the last restored tensor's end
+        assert call(w=[w[0], last]) == BAD and call(w=[ws + 256, w[1]]) == BAD, op
+        assert call(dy=[last, dy[1]]) == BAD, op
+        if call is not row:
+            assert call(dy=[dy[0], last]) == BAD, op
