@@ -91,12 +91,16 @@ inline bool overlap(const Range& a, const Range& b) {
 }
 
 // A call's ranges without a heap allocation (calls that serve single tokens
-// take a few microseconds): at most 8 shards of a few tensors each.
+// take a few microseconds): at most 8 shards of a few tensors each.  A list
+// that was given more overlaps everything.
 class RangeList {
  public:
   void push_back(const Range& r) {
-    if (r.bytes != 0 && n_ < kMost) r_[n_++] = r;
+    if (r.bytes == 0) return;
+    if (n_ < kMost) r_[n_++] = r;
+    else full_ = true;
   }
+  bool full() const { return full_; }
   size_t size() const { return n_; }
   const Range& operator[](size_t i) const { return r_[i]; }
   const Range* begin() const { return r_; }
@@ -105,11 +109,16 @@ class RangeList {
  private:
   static constexpr size_t kMost = 64;
   size_t n_ = 0;
+  bool full_ = false;
   Range r_[kMost];
 };
 
+inline bool holds_all(const RangeList& r) { return !r.full(); }
+inline bool holds_all(const std::vector<Range>&) { return true; }
+
 template <typename Outs, typename Ins>
 bool any_overlap(const Outs& outs, const Ins& ins) {
+  if (!holds_all(outs) || !holds_all(ins)) return true;
   for (size_t i = 0; i < outs.size(); ++i) {
     for (const Range& r : ins)
       if (overlap(outs[i], r)) return true;

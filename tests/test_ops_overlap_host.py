@@ -2,6 +2,8 @@
 made-up pointers, nothing is launched.  A call that passes these checks goes
 on to the device query, which fails without a GPU."""
 import ctypes
+import os
+import subprocess
 
 import pytest
 
@@ -9,6 +11,7 @@ import gemm_reduce_fusion_gb300 as tp
 from test_block_ops_host import BAD, arr, at
 
 L = tp._lib
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(autouse=True)
@@ -86,3 +89,26 @@ def test_the_restored_part_of_a_workspace_overlaps_no_operand():
         assert call(dy=[last, dy[1]]) == BAD, op
         if call is not row:
             assert call(dy=[dy[0], last]) == BAD, op
+
+
+def test_a_full_list_of_ranges_refuses(tmp_path):
+    """What a list of ranges has no room for counts as an overlap."""
+    src = tmp_path / "ranges.cpp"
+    src.write_text('''
+#include "host_util.h"
+int main() {
+  tpf::RangeList outs, few, many;
+  outs.push_back({reinterpret_cast<void*>(1 << 20), 16});
+  for (int i = 0; i < 64; ++i) few.push_back({reinterpret_cast<void*>((2 << 20) + 32 * i), 16});
+  for (int i = 0; i < 65; ++i) many.push_back({reinterpret_cast<void*>((2 << 20) + 32 * i), 16});
+  if (tpf::any_overlap(outs, few)) return 1;
+  if (!tpf::any_overlap(outs, many) || !tpf::any_overlap(many, outs)) return 2;
+  return 0;
+}
+''')
+    from gemm_reduce_fusion_gb300.build import nvcc
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    csrc = os.path.join(ROOT, "gemm_reduce_fusion_gb300", "csrc")
+    exe = tmp_path / "ranges"
+    subprocess.run(["g++", "-std=c++17", "-O1", "-I", csrc, "-I", cuda, str(src), "-o", str(exe)], check=True, capture_output=True)
+    assert subprocess.run([str(exe)]).returncode == 0
