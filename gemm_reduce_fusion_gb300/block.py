@@ -219,15 +219,19 @@ class MLPBlock(torch.nn.Module):
 
 
 class W4MLPBlock:
-    """A block that serves: ``y, n = block(x, n)`` on [tokens, h] tensors.
+    """A block that serves: ``y, n = block(x, n)`` on [tokens, h] tensors,
+    also where the trained block takes token shards.
 
-    Up to TP_W4_MAX_M tokens take their products from the 4-bit weights, more
-    from weights unpacked for the call.  The stream is updated in place."""
+    It keeps copies of what the block holds when it is made.  Up to
+    TP_W4_MAX_M tokens take their products from the 4-bit weights, more from
+    weights unpacked for the call (rounded to bfloat16, so that 64 and 65
+    tokens differ by that rounding).  The stream x is updated in place.  A
+    gate of several rows serves multiples of them only."""
 
     def __init__(self, block: MLPBlock, group: int = 128):
         self.p, self.group = block.p, group
         with torch.no_grad():
-            self.how = {k: v.detach() if torch.is_tensor(v) else v for k, v in block.boundary().items()}
+            self.how = {k: v.detach().clone() if torch.is_tensor(v) else v for k, v in block.boundary().items()}
             self.fc1, self.fc2 = self._pack(block.w1), self._pack(block.w2)
         self.how.update(post=_kind(self.how["post"]), pre=_kind(self.how["pre"]))
 

@@ -21,6 +21,18 @@ def make(blk, h=264, f=528, p=2, seed=1, kind="layer"):
     return b, rnd
 
 
+def test_training_on_leaves_a_served_block_as_it_was(blk):
+    b, rnd = make(blk)
+    served = b.serve(group=64)
+    x, n = rnd(3, 264), rnd(3, 264)
+    first = [t.clone() for t in served(x.clone(), n)]
+    with torch.no_grad():
+        for t in b.parameters():
+            t.add_(1.0)
+    again = served(x.clone(), n)
+    assert all(torch.equal(s, t) for s, t in zip(first, again))
+
+
 def test_streams_and_graphs_have_workspaces_of_their_own(blk):
     from gemm_reduce_fusion_gb300.autograd import _workspace
     dev, call = torch.device("cuda", torch.cuda.current_device()), [(blk.TP_OP_ROW_W4, 2, 4, 264, 528)]
