@@ -26,6 +26,7 @@ from __future__ import annotations
 from typing import Sequence
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (TP_EPI_GELU, TP_NORM_LAYER, TP_NORM_NONE, TP_NORM_RMS, TP_OP_AG_MM, TP_OP_AG_MM_BWD_CKPT,
                TP_OP_BLOCK_NORM_BWD, TP_OP_COL_BWD_CKPT, TP_OP_COL_FWD, TP_OP_COL_W4, TP_OP_ROW_AR, TP_OP_ROW_BWD_CKPT,
@@ -71,6 +72,7 @@ class _BoundaryFn(torch.autograd.Function):
         return tuple((y or []) + (n or []))
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, *grads):
         p, how = ctx.p, ctx.how
         s = ctx.saved_tensors
@@ -146,6 +148,7 @@ class _CkptMLPFn(torch.autograd.Function):
         return tuple(y)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, *dy):
         p, sp = ctx.p, ctx.sp
         nx = p if sp else 1

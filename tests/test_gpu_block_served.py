@@ -33,6 +33,18 @@ def test_training_on_leaves_a_served_block_as_it_was(blk):
     assert all(torch.equal(s, t) for s, t in zip(first, again))
 
 
+def test_second_derivatives_are_refused(blk):
+    """The gradients come from kernels that autograd cannot differentiate
+    again: a penalty on them is refused, not taken for a constant."""
+    b, rnd = make(blk)
+    for apply in (lambda t: blk.parallel_mlp_ckpt(t, list(b.w1), list(b.w2)), lambda t: blk.pre_norm([t])[0],
+                  lambda t: blk.block_boundary([t], [t])[0][0]):
+        t = rnd(16, 264).requires_grad_()
+        (g,) = torch.autograd.grad(apply(t).float().square().sum(), t, create_graph=True)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            (g.float().square().sum() + t.float().sum()).backward()
+
+
 def test_streams_and_graphs_have_workspaces_of_their_own(blk):
     from gemm_reduce_fusion_gb300.autograd import _workspace
     dev, call = torch.device("cuda", torch.cuda.current_device()), [(blk.TP_OP_ROW_W4, 2, 4, 264, 528)]
