@@ -342,8 +342,11 @@ struct Coefs {
   uint32_t v0, nvec;
   float scale;
 
-  // v: of the CTA's vectors; past the last one, that one
+  // v: of the CTA's vectors.  Past the last one make_post gives zeros, so that
+  // the zeros of z there stay zeros whatever the last weights are (times an
+  // infinity they would be NaN in the row's sums); make_pre gives the last one.
   __device__ __forceinline__ Vec make_post(const NormParams& P, uint32_t v) const {
+    const bool past = v >= nvec;
     v = v0 + min(v, max(nvec, 1u) - 1);
     Vec c;
 #pragma unroll
@@ -357,6 +360,10 @@ struct Coefs {
       const Vec g = widen(__ldg(P.gate + v));
 #pragma unroll
       for (int i = 0; i < 4; ++i) c.p[i] = mul2(c.p[i], g.p[i]);
+    }
+    if (past) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c.p[i] = 0;
     }
     return c;
   }
