@@ -25,9 +25,9 @@
 // each) bound the kernel beside HBM.  (Masked nibbles as operands as they
 // are, against tokens times 2^64 and less 8 sum(x), gain 2 us of 54 at 1
 // token, lose 8 at 16, and turn infinite tokens into NaN.)
-// The scale, with the power of two that is left over, is applied to the
-// group's fp32 sum (once in G rows instead of once a weight), so no product
-// is rounded before it is added.
+// The scale is applied to the group's fp32 sum (once in G rows instead of
+// once a weight), so no product is rounded before it is added; the power of
+// two that is left over comes with the bias.
 //
 // The work, blocks of columns x stages of rows (of every rank), is cut into
 // equal runs of stages, one for each thread block, whatever the shapes.  A
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_linear_kernel(const __grid_con
           for (int f = 0; f < NS; ++f) {
             uint32_t sc;
             asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sc) : "r"(ssrc + (f * GROUPS + b / GB) * 32));
-            const float s0 = bf_lo(sc) * 64.f, s1 = bf_hi(sc) * 4.f;
+            const float s0 = bf_lo(sc), s1 = bf_hi(sc) * kEven;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               acc[f][n][0] = fmaf(s0, part[f][n][0], acc[f][n][0]);

@@ -53,6 +53,12 @@ __device__ __forceinline__ void dequant(uint32_t w, uint32_t (&a)[4]) {
   a[3] = fma_bf16x2(v & 0x00F000F0u, kUp, kOff1);
 }
 
+// The operands lack 2^6 (columns i) and 2^2 (columns i + 8).  The scales of
+// the latter are multiplied by 2^-4, which is exact for the smallest of them
+// too, and the sums by 2^6 at the end: a scale times 2^6 would be infinite
+// from 2^122.
+constexpr float kLift = 64.f, kEven = 0.0625f;
+
 // The runs that hold stages of a column block.
 struct Parts {
   uint32_t first, last;
@@ -62,10 +68,10 @@ __device__ __forceinline__ Parts parts_of(const W4Params& P, uint32_t block) {
   return {b0 / P.run_stages, (b0 + P.spb - 1) / P.run_stages};
 }
 
-// Bias, activation and rounding of one sum: token `tok`, column `col` of an
-// output shard.
+// Bias, activation and rounding of one sum, which lacks a factor of 2^6
+// (kLift): token `tok`, column `col` of an output shard.
 __device__ __forceinline__ void write_one(const W4Params& P, uint32_t shard, uint32_t tok, uint32_t col, float bias, float v) {
-  float y = v + bias;
+  float y = fmaf(v, kLift, bias);
   if (P.epi == TP_EPI_GELU) y = gelu_f(y);
   const int64_t at = static_cast<int64_t>(tok) * P.N + col;
   if (P.out_f32) static_cast<float*>(P.y[shard])[at] = y;

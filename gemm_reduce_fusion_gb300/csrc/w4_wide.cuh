@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) w4_wide_kernel(const __grid_c
     // The thread's column is its lane of tensor memory: 16 f + 8 r + i of the
     // pair, whose scale stands at 16 f + 2 i + r.
     const uint32_t scale_at = (lane & 16) + 2 * (lane & 7) + (lane >> 3 & 1);
-    const float lift = (lane & 8) ? 4.f : 64.f;  // what the operands lack
+    const float even = (lane & 8) ? kEven : 1.f;
     const uint32_t at = tmem + ((quarter * 32) << 16);
     uint64_t acc[TOK / 2];  // tokens in pairs
     float scale[GROUPS] = {};
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) w4_wide_kernel(const __grid_c
       for (int g = 0; g < GROUPS; ++g) {
         uint16_t b;
         asm volatile("ld.shared.b16 %0, [%1];" : "=h"(b) : "r"(ssm + slot * S::kS + (warp * GROUPS + g) * 64 + scale_at * 2));
-        next[g] = __uint_as_float(static_cast<uint32_t>(b) << 16) * lift;
+        next[g] = __uint_as_float(static_cast<uint32_t>(b) << 16) * even;
       }
       tmem_wait_st();
       tc_fence_before();
