@@ -5,7 +5,9 @@
 // even, kept with the byte E + 126.  Scaling by a power of two is exact, so
 // q is the correctly rounded quotient, and q * 2^E, with seven significant
 // bits, is exactly a bf16: a restored activation enters the tensor cores
-// without a second rounding.  The price against a quantum of max|x| / 127 is
+// without a second rounding.  (One exception, at the end of the range: beside
+// the largest finite magnitude, 255/128 * 2^127, it and the next one round to
+// 64 * 2^122 and come back as infinity.)  The price against a quantum of max|x| / 127 is
 // at most one bit.  The byte 255 marks a group that held an infinity or NaN;
 // it is restored as NaN throughout, so that an overflow stays visible.
 //

@@ -502,8 +502,19 @@ int tiles_for(int64_t M) {
 //     of 32: 32 tokens 140 / 166, 48 199 / 202, 64 246 / 220;
 //   p = 4, 4096 -> 16384, groups of 128 (13 stages an SM): 20 tokens 25 / 25,
 //     48 33 / 27, 64 41 / 31;
+//   p = 2, 4096 -> 12288 (10 stages), groups of 64: 20 and 32 tokens 27 / 25,
+//     48 33 / 27, 64 41 / 31; groups of 128: 25 / 23, 31 / 25, 39 / 27;
+//   p = 4, 4096 -> 10240 (8.4 stages): 25 / 24, 29 / 26, 35 / 27; 25 / 23,
+//     27 / 25, 35 / 25;
+//   p = 2, 4096 -> 7680 (6.3 stages): 20 / 22, 26 / 24, 30 / 26; 20 / 22,
+//     24 / 24, 30 / 24;
+//   p = 4, 4096 -> 6144 (5.1 stages): 20 / 21, 24 / 24, 28 / 26; 20 / 19,
+//     24 / 22, 28 / 24;
 //   4096 -> 4096, groups of 128 (3 stages): 20 tokens 17 / 15, 64 21 / 23.
-// At 16 tokens w4_linear_kernel takes 75 in the first of these.
+// From eight stages on w4_wide_kernel is ahead at every count; below, each
+// side is ahead by up to 2 us at 20 to 48 tokens, and w4_wide_kernel by 2 to
+// 6 at 64 from five stages on.  At 16 tokens w4_linear_kernel takes 75 in the
+// first of these.  It spills 12 to 200 bytes from 17 tokens on.
 bool is_wide(int p, int64_t M, int64_t N, int64_t K, int64_t G) {
   return M > 16 && p * cdiv(N, kWideCols) * cdiv(K, kWideRows) >= 8 * kSMs && (G > 32 || M > 48);
 }

@@ -10,9 +10,9 @@
 // rows are put in that order as they are copied to shared memory, in pieces
 // of 8 bytes.
 //
-// A scale group's products (q - 8) x are exact in fp32 sums of at most 128
-// terms on the tensor cores; its sum leaves tensor memory once, is multiplied
-// by the scale and added in registers.
+// A scale group's products (q - 8) x are exact; the tensor cores add at most
+// 128 of them in fp32.  The sum leaves tensor memory once, is multiplied by
+// the scale and added in registers.
 //
 // Roles: 16 warps dequantise and add up the finished groups of the stage
 // before; two threads issue the MMAs, one for each half of the columns (one

@@ -312,7 +312,10 @@ tp_status tp_block_norm_bwd(const void* const* z, const void* const* y, const vo
  *   2^(e - 126) is the smallest power of two whose 127-fold reaches the
  *   group's largest magnitude, and at least 2^-126; q is rounded to nearest
  *   even.  e == 255 marks a group that held an infinity or NaN and is
- *   restored as NaN.  A restored value is exactly a bf16.
+ *   restored as NaN.  A restored value is exactly a bf16, and differs by at
+ *   most half a quantum, except in a group that holds the largest finite
+ *   magnitude (bits 0x7F7F): its two largest magnitudes (0x7F7E, 0x7F7F)
+ *   round to q = +-64, which stands for 2^128 and is restored as infinity.
  * q is 16-byte aligned; e has no alignment.  1 <= p <= 8 tensors a call.    */
 tp_status tp_ckpt_pack(const void* const* x, void* const* q, void* const* e, int p, int64_t M, int64_t N,
                        cudaStream_t stream);
@@ -362,7 +365,7 @@ tp_status tp_row_linear_bwd_reducescatter_ckpt(const void* const* q, const void*
  *   s: bf16 [ceil(N/32), ceil(K/G), 32]; column n = 32 a + 16 f + 8 r + i at
  *      16 f + 2 i + r.
  * Past K and N any nibble and scale is allowed.  Both are 16-byte aligned.
- * The sums are fp32; a scale multiplies its group's fp32 sum.               */
+ * The sums are fp32; a scale, any finite bf16, multiplies its group's sum.  */
 
 /* Y_k = X . W_k (+ b_k), optionally GeLU (TP_EPI_GELU); arguments as in
  * tp_col_linear_fwd.  M <= 64 (TP_ERR_UNSUPPORTED_SHAPE above: unpack the
