@@ -17,7 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Sequence
+from typing import NamedTuple, Sequence
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libtpfused.so")
@@ -55,6 +55,10 @@ TP_OP_AG_MM_BWD_CKPT = 12
 TP_OP_ROW_RS_BWD_CKPT = 13
 TP_OP_COL_W4 = 14
 TP_OP_ROW_W4 = 15
+TP_OP_COL_FP8 = 16
+TP_OP_ROW_FP8 = 17
+TP_OP_COL_BWD_FP8 = 18
+TP_OP_ROW_BWD_FP8 = 19
 # tp_norm
 TP_NORM_NONE = 0
 TP_NORM_RMS = 1
@@ -128,6 +132,12 @@ def _load() -> ctypes.CDLL:
         "tp_row_linear_fwd_w4": (I, [PP, PP, PP, P, P, I, L, L, L, L, I, P, S, P]),
         "tp_w4_pack": (I, [PP, PP, PP, I, L, L, L, P]),
         "tp_w4_unpack": (I, [PP, PP, PP, I, L, L, L, P]),
+        "tp_fp8_pack": (I, [PP, PP, PP, I, I, I, L, L, L, P]),
+        "tp_fp8_unpack": (I, [PP, PP, I, L, L, L, P]),
+        "tp_col_linear_fwd_fp8": (I, [PP, PP, PP, PP, PP, PP, I, I, L, L, L, P, S, P]),
+        "tp_row_linear_fwd_fp8": (I, [PP, PP, P, P, I, L, L, L, P, S, P]),
+        "tp_col_linear_bwd_fp8": (I, [PP, PP, PP, PP, P, PP, I, L, L, L, P, S, P]),
+        "tp_row_linear_bwd_fp8": (I, [PP, PP, PP, PP, PP, PP, PP, I, L, L, L, P, S, P]),
         "tp_pipeline_time": (ctypes.c_double, [ctypes.c_double, ctypes.c_double, L]),
         "tp_num_chunks": (L, [L, L]),
         "tp_choose_chunk_m": (L, [I, I, L, L, L]),
@@ -514,15 +524,15 @@ def tp_noalloc_device_status(stream=None) -> int:
 # _refuse, which finds the words, only when something is wrong.
 
 _ARRAY = tuple(ctypes.c_void_p * n for n in range(65))  # the C array types, looked up once
-_BF16 = _FP32 = _INT8 = _UINT8 = _RAW_STREAM = None
+_BF16 = _FP32 = _INT8 = _UINT8 = _E4M3 = _RAW_STREAM = None
 
 
 def _begin() -> int:
     """The current device; the first call fetches torch's dtypes and stream getter."""
-    global _BF16, _FP32, _INT8, _UINT8, _RAW_STREAM
+    global _BF16, _FP32, _INT8, _UINT8, _E4M3, _RAW_STREAM
     if _BF16 is None:
         import torch
-        _FP32, _INT8, _UINT8 = torch.float32, torch.int8, torch.uint8
+        _FP32, _INT8, _UINT8, _E4M3 = torch.float32, torch.int8, torch.uint8, torch.float8_e4m3fn
         # the current stream's handle without a Stream object around it, where torch has it
         _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
         _BF16 = torch.bfloat16
@@ -784,3 +794,153 @@ def tp_w4_unpack(q: Sequence, s: Sequence, w: Sequence, group: int = 128, stream
     qs, ss = w4_shapes(K, N, _group(W, group))
     _check(_lib.tp_w4_unpack(_list(W, "q", q, p, qs, _UINT8, dev), _list(W, "s", s, p, ss, bf, dev),
                              _list(W, "w", w, p, (K, N), bf, dev), p, N, K, group, _on(stream, dev)), W)
+
+
+# ------------------------------------------------------------------ 8-bit operands
+
+class Fp8(NamedTuple):
+    """An operand in 8 bits: a matrix [rows, cols] whose products sum over its columns.
+
+    q: float8_e4m3fn [rows, cols rounded up to 128], zeros past cols; e: uint8 [ceil(rows/128), ceil(cols/512), 512],
+    the exponents of a power of two for each row and 128 columns.  Both may have a leading dimension of matrices."""
+    q: object
+    e: object
+
+
+def fp8_shapes(rows: int, cols: int) -> tuple:
+    """Shapes of the operand of a matrix [rows, cols]: (q float8_e4m3fn, e uint8)."""
+    return (rows, (cols + 127) // 128 * 128), ((rows + 127) // 128, (cols + 511) // 512, 512)
+
+
+def fp8_empty(rows: int, cols: int, batch: int | None = None, device="cuda") -> Fp8:
+    """An operand (or `batch` of them, one after the other) to be packed into."""
+    import torch
+    qs, es = fp8_shapes(rows, cols)
+    lead = () if batch is None else (batch,)
+    return Fp8(torch.empty(lead + qs, dtype=torch.float8_e4m3fn, device=device),
+               torch.empty(lead + es, dtype=torch.uint8, device=device))
+
+
+def _fp8s(where: str, name: str, ts, count: int, rows: int, cols: int, dev: int, lead: tuple = ()):
+    """The C array of `count` operands of [rows, cols] (None: NULL)."""
+    if ts is None:
+        return None
+    if len(ts) != count:
+        raise ValueError(f"{where}: {name} holds {len(ts)} operands, expected {count}")
+    qs, es = fp8_shapes(rows, cols)
+    qs, es, arr, i = lead + qs, lead + es, _ARRAY[2 * count](), 0
+    for q, e in ts:
+        if q.shape != qs or q.dtype is not _E4M3 or q.get_device() != dev or not q.is_contiguous():
+            _refuse(where, f"{name}[{i // 2}].q", q, qs, _E4M3, dev)
+        if e.shape != es or e.dtype is not _UINT8 or e.get_device() != dev or not e.is_contiguous():
+            _refuse(where, f"{name}[{i // 2}].e", e, es, _UINT8, dev)
+        arr[i] = q.data_ptr()
+        arr[i + 1] = e.data_ptr()
+        i += 2
+    return arr
+
+
+def _matrices(where: str, t) -> tuple:
+    """(leading shape, matrices, rows, cols) of a tensor [M, N] or [batch, M, N]."""
+    if t.dim() == 2:
+        return (), 1, t.shape[0], t.shape[1]
+    if t.dim() == 3:
+        return (t.shape[0],), t.shape[0], t.shape[1], t.shape[2]
+    raise ValueError(f"{where}: a matrix [M, N] or matrices [batch, M, N], got {tuple(t.shape)}")
+
+
+def tp_fp8_pack(x: Sequence, q=None, qt=None, tiles: bool = False, epi: int = TP_EPI_NONE, stream=None) -> None:
+    """q[i] = the operand of x[i] ([M, N] or [batch, M, N]), qt[i] = that of its transpose; either may be None.
+
+    An exponent for each 128 columns of a row (of the operand), or with `tiles` for each 128 x 128, as weights have it;
+    epi=TP_EPI_GELU packs GeLU(x[i])."""
+    W, dev, p = "tp_fp8_pack", _begin(), len(x)
+    lead, batch, M, N = _matrices(W, x[0])
+    _check(_lib.tp_fp8_pack(_list(W, "x", x, p, lead + (M, N), _BF16, dev), _fp8s(W, "q", q, p, M, N, dev, lead),
+                            _fp8s(W, "qt", qt, p, N, M, dev, lead), int(tiles), epi, p, batch, M, N, _on(stream, dev)), W)
+
+
+def tp_fp8_unpack(q: Sequence, y: Sequence, stream=None) -> None:
+    """y[i] = the values of the operand q[i], in bfloat16."""
+    W, dev, p = "tp_fp8_unpack", _begin(), len(q)
+    lead, batch, M, N = _matrices(W, y[0])
+    _check(_lib.tp_fp8_unpack(_fp8s(W, "q", q, p, M, N, dev, lead), _list(W, "y", y, p, lead + (M, N), _BF16, dev), p, batch, M, N,
+                              _on(stream, dev)), W)
+
+
+def tp_col_linear_fwd_fp8(x: Fp8, w: Sequence, y, ws, epi: int = TP_EPI_NONE, preact=None, z=None, stream=None, bias=None) -> None:
+    """y[k] = X A_k + b_k (or its GeLU, with H_k into preact[k]) on 8-bit operands: x [M, K], w[k] [N, K], the packed
+    transpose of A_k.  With y None the results go to the operands z[k] [M, N]."""
+    W, dev, p, bf = "tp_col_linear_fwd_fp8", _begin(), len(w), _BF16
+    if (y is None) == (z is None):
+        raise ValueError(f"{W}: one of y and z is given")
+    (M, K), N = x.q.shape, w[0].q.shape[0]
+    if y is not None and y[0].shape[1] != N:
+        raise ValueError(f"{W}: y[0] has {y[0].shape[1]} columns, w[0] has {N} rows")
+    _need_ws(W, ws, dev)
+    wp, wb = _ws(ws)
+    _check(_lib.tp_col_linear_fwd_fp8(
+        _fp8s(W, "x", (x,), 1, M, K, dev), _fp8s(W, "w", w, p, N, K, dev), _list(W, "bias", bias, p, (N,), bf, dev),
+        _list(W, "y", y, p, (M, N), bf, dev), _fp8s(W, "z", z, p, M, N, dev), _list(W, "preact", preact, p, (M, N), bf, dev), epi, p, M,
+        N, K, wp, wb, _on(stream, dev)), W)
+
+
+def tp_row_linear_fwd_fp8(x: Sequence, w: Sequence, y, ws, stream=None, bias=None) -> None:
+    """y = sum_r X_r A_r (+ bias) on 8-bit operands: x[r] [M, K], w[r] [N, K], the packed transpose of A_r."""
+    W, dev, p, bf = "tp_row_linear_fwd_fp8", _begin(), len(w), _BF16
+    (M, K), N = x[0].q.shape, w[0].q.shape[0]
+    _need_ws(W, ws, dev)
+    wp, wb = _ws(ws)
+    _check(_lib.tp_row_linear_fwd_fp8(
+        _fp8s(W, "x", x, p, M, K, dev), _fp8s(W, "w", w, p, N, K, dev), _one(W, "bias", bias, (N,), bf, dev),
+        _one(W, "y", y, (M, N), bf, dev), p, M, N, K, wp, wb, _on(stream, dev)), W)
+
+
+def _bwd_sizes(where: str, dx, dw, dy, dyt, w, xt, p=None) -> tuple:
+    """(M, N, K, p) of a backward call.  An operand's rows are exact, its columns rounded up to 128: with dw alone, M
+    is what the operands hold, a multiple of 128."""
+    if dx is not None:
+        if w is None or dy is None or dy[0] is None:
+            raise ValueError(f"{where}: dx needs w and dy")
+        (M, K), N = dx.shape, dw[0].shape[1] if dw is not None else w[0].q.shape[1]
+    elif dw is not None:
+        if xt is None or dyt is None or dyt[0] is None:
+            raise ValueError(f"{where}: dw needs xt and dyt")
+        (K, N), M = dw[0].shape, dyt[0].q.shape[1]
+    else:
+        raise ValueError(f"{where}: dx or dw is given")
+    if dw is not None and (xt is None or dyt is None or dyt[0] is None):
+        raise ValueError(f"{where}: dw needs xt and dyt")
+    return M, N, K, len(dw if dw is not None else w) if p is None else p
+
+
+def tp_col_linear_bwd_fp8(xt, w, dy, dyt, dx, dw, ws, stream=None) -> None:
+    """dx = sum_k dY_k A_k^T from w[k] [K, N] (packed A_k) and dy[k] [M, N]; dw[k] = X^T dY_k from xt [K, M] and dyt[k] [N, M].
+
+    dx (with w, dy) or dw (with xt, dyt) may be None."""
+    W, dev, bf = "tp_col_linear_bwd_fp8", _begin(), _BF16
+    M, N, K, p = _bwd_sizes(W, dx, dw, dy, dyt, w, xt)
+    _need_ws(W, ws, dev)
+    wp, wb = _ws(ws)
+    need_x, need_w = dx is not None, dw is not None
+    _check(_lib.tp_col_linear_bwd_fp8(
+        _fp8s(W, "xt", (xt,) if need_w else None, 1, K, M, dev), _fp8s(W, "w", w if need_x else None, p, K, N, dev),
+        _fp8s(W, "dy", dy if need_x else None, p, M, N, dev), _fp8s(W, "dyt", dyt if need_w else None, p, N, M, dev),
+        _one(W, "dx", dx, (M, K), bf, dev), _list(W, "dw", dw, p, (K, N), bf, dev), p, M, N, K, wp, wb, _on(stream, dev)), W)
+
+
+def tp_row_linear_bwd_fp8(xt, w, dy, dyt, dx, dw, ws, preact=None, stream=None) -> None:
+    """dx[k] = dY A_k^T (times GeLU'(preact[k])) from w[k] [K, N] (packed A_k) and dy [M, N]; dw[k] = X_k^T dY from xt[k] [K, M]
+    and dyt [N, M].
+
+    dx (with w, dy) or dw (with xt, dyt) may be None."""
+    W, dev, bf = "tp_row_linear_bwd_fp8", _begin(), _BF16
+    M, N, K, p = _bwd_sizes(W, dx and dx[0], dw, (dy,), (dyt,), w, xt and xt[0], len(dx or dw or ()))
+    _need_ws(W, ws, dev)
+    wp, wb = _ws(ws)
+    need_x, need_w = dx is not None, dw is not None
+    _check(_lib.tp_row_linear_bwd_fp8(
+        _fp8s(W, "xt", xt if need_w else None, p, K, M, dev), _fp8s(W, "w", w if need_x else None, p, K, N, dev),
+        _fp8s(W, "dy", (dy,) if need_x else None, 1, M, N, dev), _fp8s(W, "dyt", (dyt,) if need_w else None, 1, N, M, dev),
+        _list(W, "dx", dx, p, (M, K), bf, dev), _list(W, "dw", dw, p, (K, N), bf, dev),
+        _list(W, "preact", preact, p, (M, K), bf, dev), p, M, N, K, wp, wb, _on(stream, dev)), W)

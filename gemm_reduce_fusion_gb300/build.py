@@ -25,7 +25,8 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include")]
 SOURCES = ["tp_fused.cu", "block_norm.cu", "block_norm_bwd_bf16_rms.cu", "block_norm_bwd_bf16_ln.cu",
-           "block_norm_bwd_f32_rms.cu", "block_norm_bwd_f32_ln.cu", "ckpt.cu", "w4.cu"]
+           "block_norm_bwd_f32_rms.cu", "block_norm_bwd_f32_ln.cu", "ckpt.cu", "w4.cu",
+           "fp8.cu", "fp8_pack.cu"]
 
 
 def nvcc() -> str:

@@ -1,0 +1,626 @@
+// Persistent tcgen05 GEMM on 8-bit operands with a power of two for each
+// block of 128 along the contraction (see tp_fused.h for the operands):
+//   D[m, n] = sum_b 2^(ea[m, b] + eb[n, b] - 254) sum_{k in block b} A[m, k] B[n, k].
+// The scales are applied by the tensor cores (kind::mxf8f6f4, one scale for
+// each row and 32 of the contraction; the four steps of a block use the same
+// byte), so that the accumulator stays in tensor memory for the whole
+// contraction and the ranks' segments, and no multiplication by a scale is
+// left for the epilogue.  An operand's exponents lie in memory as tensor
+// memory wants them: 512 bytes hold four blocks of 128 rows, which one copy
+// brings to shared memory and one tcgen05.cp to tensor memory every four
+// k-blocks; the byte is picked by the instruction descriptor.
+//
+// CTAS = 1: 128 x 128 tiles of one CTA; CTAS = 2: 256 x 256 tiles of a CTA
+// pair, each of which holds 128 rows of A and of B.  A k-block is 128 deep:
+// 32 KiB a stage and CTA in both.  A pair moves 64 bytes an SM and cycle from
+// L2 at the full MMA rate, a single CTA's tile 128.
+//
+// Roles: warp 0 loads, warp 1 issues the MMAs, the others (four for each 128
+// columns) are the epilogue, which overlaps the next tile's MMAs on the other
+// accumulator.  With 256 columns the two accumulators share 32 columns of
+// tensor memory, which the epilogue reads first: 480 of the 512 columns, the
+// rest for the scales.
+//
+// Every wait is bounded (device_wait.cuh).
+#pragma once
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "device_wait.cuh"
+#include "fp8_device.cuh"
+#include "gelu.cuh"
+#include "vec_util.cuh"
+
+namespace tpf {
+
+enum Fp8Mode : int32_t {
+  FP8_DENSE = 0,     // groups x segments of whole matrices
+  FP8_ROWS = 1,      // row tiles of the experts: tile -> expert by the plan
+  FP8_CONTRACT = 2,  // a product for each expert, contracted over its rows
+};
+
+struct Fp8GemmParams {
+  CUtensorMap a[8], b[8], ea[8], eb[8];
+  int32_t mode;
+  int32_t groups, segs;         // outputs; contraction segments (ranks reduced)
+  int32_t a_by_g, a_by_s, b_by_g, b_by_s;
+  int32_t m_tiles, n_tiles;     // of a group (FP8_ROWS: m_tiles from the plan)
+  int32_t kb;                   // k-blocks of a segment
+  int32_t splits, kb_split;     // parts of the contraction, k-blocks of a part
+  int32_t rows, cols;           // of an output (FP8_ROWS: rows not used)
+  int32_t tile_rows;            // rows of an A tile that are loaded (CTAS = 1: 16 .. 128)
+  int32_t band;                 // m-tiles that go together through the n-tiles
+  int32_t per, eb_blocks;       // experts of a shard; 128-row blocks of an expert's B
+  const int32_t* plan_tiles;    // FP8_ROWS, FP8_CONTRACT: row tiles in use
+  const int32_t* plan_expert;   // FP8_ROWS: expert of a row tile
+  const int32_t* plan_first;    // FP8_CONTRACT: first row tile of an expert, E + 1
+  const int32_t* plan_slot;     // FP8_ROWS: token and choice of a row, or -1
+  int32_t kb_tile;              // FP8_CONTRACT: k-blocks of a row tile
+  int32_t epi;                  // tp_epilogue
+  __nv_bfloat16* out[8];        // bf16 results, or null
+  __nv_bfloat16* aux[8];        // GELU: H out, or null; DGELU: H in
+  uint8_t* zq[8];               // 8-bit results, or null
+  uint8_t* ze[8];
+  const __nv_bfloat16* bias[8];
+  int64_t zq_ld, ze_ld;         // bytes of a row of zq, of 128 rows of ze
+  float* part;                  // splits > 1: fp32 sums [split][group][row][cols]
+  int64_t part_rows;            // rows of a group's sums
+  uint32_t* status;
+  uint64_t timeout_ns;
+  int32_t drop;                 // test hook (TP_DEBUG_DROP_LOAD)
+};
+
+template <int CTAS>
+struct Fp8Cfg {
+  static constexpr int BN = 128 * CTAS;
+  static constexpr uint32_t A_BYTES = 128 * 128, B_BYTES = 128 * 128;
+  static constexpr uint32_t EA_BYTES = 512, EB_BYTES = 512 * CTAS;
+  static constexpr uint32_t E_BYTES = 2048;  // of a stage, padded
+  static constexpr int STAGES = CTAS == 1 ? 6 : 5;
+  static constexpr int EPI_WARPS = 4 * CTAS;
+  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr uint32_t STG_BYTES = 4096;  // staging of an epilogue warp
+  static constexpr uint32_t A_OFF = 0, B_OFF = STAGES * A_BYTES, E_OFF = B_OFF + STAGES * B_BYTES,
+                            STG_OFF = E_OFF + STAGES * E_BYTES, BAR_OFF = STG_OFF + EPI_WARPS * STG_BYTES;
+  static constexpr uint32_t SMEM = 1024 + BAR_OFF + 256;
+  // tensor memory: accumulators of BN columns at 0 and ACC1, scales from SF
+  // on (A 4 columns, B 4 CTAS), two of them by turns
+  static constexpr uint32_t SHARED = CTAS == 1 ? 0 : 32;  // columns of both accumulators
+  static constexpr uint32_t ACC1 = BN - SHARED, SF = 480;
+  static_assert(ACC1 + BN <= SF, "accumulators before the scales");
+  static_assert(SMEM <= 227 * 1024, "shared memory of a CTA");
+};
+
+struct Fp8Unit {
+  int32_t g, mt, nt, split;
+  int32_t q0, q1;     // k-blocks
+  int32_t a_row, ea;  // first row of A's tile (CTA 0), its block of exponents
+  int32_t b_row, eb;
+  int32_t bi;         // map of B (FP8_ROWS: the expert's shard)
+  int64_t out_off;    // FP8_CONTRACT: the expert's place in its shard
+};
+
+__device__ __forceinline__ int32_t fp8_units(const Fp8GemmParams& P) {
+  if (P.mode == FP8_ROWS) return __ldcg(P.plan_tiles) * P.n_tiles * P.splits;
+  return P.groups * P.m_tiles * P.n_tiles * P.splits;
+}
+
+template <int CTAS>
+__device__ __forceinline__ Fp8Unit fp8_unit(const Fp8GemmParams& P, int32_t t) {
+  Fp8Unit u;
+  u.split = t % P.splits;
+  int32_t v = t / P.splits;
+  u.out_off = 0;
+  const int32_t total = P.segs * P.kb;
+  u.q0 = u.split * P.kb_split;
+  u.q1 = min(u.q0 + P.kb_split, total);
+  if (P.mode == FP8_ROWS) {
+    // an expert's weights are read by its row tiles one after the other
+    u.mt = v / P.n_tiles;
+    u.nt = v % P.n_tiles;
+    const int32_t e = __ldcg(P.plan_expert + u.mt), local = e % P.per;
+    u.g = 0;
+    u.bi = e / P.per;
+    u.a_row = u.mt * P.tile_rows * CTAS;
+    u.ea = u.mt * CTAS;
+    u.b_row = local * P.cols + u.nt * Fp8Cfg<CTAS>::BN;
+    u.eb = local * P.eb_blocks + u.nt * CTAS;
+    return u;
+  }
+  const int32_t per_group = P.m_tiles * P.n_tiles;
+  u.g = v / per_group;
+  v -= u.g * per_group;
+  const int32_t strip = v / (P.band * P.n_tiles), first = strip * P.band;
+  const int32_t tall = min(P.band, P.m_tiles - first);
+  v -= first * P.n_tiles;
+  u.nt = v / tall;
+  u.mt = first + v % tall;
+  u.bi = 0;
+  u.a_row = u.mt * 128 * CTAS;
+  u.ea = u.mt * CTAS;
+  u.b_row = u.nt * Fp8Cfg<CTAS>::BN;
+  u.eb = u.nt * CTAS;
+  if (P.mode == FP8_CONTRACT) {
+    u.q0 = __ldcg(P.plan_first + u.g) * P.kb_tile;
+    u.q1 = __ldcg(P.plan_first + u.g + 1) * P.kb_tile;
+    u.bi = u.g / P.per;  // of the outputs
+    u.out_off = static_cast<int64_t>(u.g % P.per) * P.rows * P.cols;
+  }
+  return u;
+}
+
+// The maps of k-block q and its place in them.
+struct Fp8Block {
+  int32_t ai, bi, k;
+};
+__device__ __forceinline__ Fp8Block fp8_block(const Fp8GemmParams& P, const Fp8Unit& u, int32_t q) {
+  Fp8Block b;
+  if (P.mode == FP8_DENSE) {
+    const int32_t s = P.segs == 1 ? 0 : q / P.kb;
+    b.k = q - s * P.kb;
+    b.ai = P.a_by_g * u.g + P.a_by_s * s;
+    b.bi = P.b_by_g * u.g + P.b_by_s * s;
+  } else {
+    b.k = q;
+    b.ai = 0;
+    b.bi = P.mode == FP8_ROWS ? u.bi : 0;
+  }
+  return b;
+}
+
+// ------------------------------------------------------------------ epilogue
+
+// 32 rows x 128 bytes of the warp's staging buffer, 16-byte pieces swizzled.
+__device__ __forceinline__ uint32_t stg_at(uint32_t stg, uint32_t row, uint32_t piece) {
+  return stg + row * 128 + ((piece ^ (row & 7)) << 4);
+}
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// Rows of 64 bf16 (or 128 bytes): staging buffer -> memory, four rows an
+// instruction, 128 bytes each.  `bytes`: of a row that are the matrix's.
+__device__ __forceinline__ void stg_out(uint32_t stg, uint8_t* to, int64_t pitch, int32_t rows, int32_t bytes, uint32_t lane) {
+  __syncwarp();
+  const uint32_t piece = lane & 7;
+  if (static_cast<int32_t>(piece * 16) < bytes) {
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) {
+      const uint32_t r = i * 4 + (lane >> 3);
+      if (static_cast<int32_t>(r) < rows) *reinterpret_cast<uint4*>(to + r * pitch + piece * 16) = ld_shared_v4(stg_at(stg, r, piece));
+    }
+  }
+  __syncwarp();
+}
+
+__device__ __forceinline__ void stg_in(uint32_t stg, const uint8_t* from, int64_t pitch, int32_t rows, int32_t bytes, uint32_t lane) {
+  __syncwarp();
+  const uint32_t piece = lane & 7;
+  const bool some = static_cast<int32_t>(piece * 16) < bytes;
+  uint4 v[8];
+#pragma unroll
+  for (uint32_t i = 0; i < 8; ++i) {
+    const uint32_t r = i * 4 + (lane >> 3);
+    v[i] = some && static_cast<int32_t>(r) < rows ? *reinterpret_cast<const uint4*>(from + r * pitch + piece * 16) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (uint32_t i = 0; i < 8; ++i) st_shared_v4(stg_at(stg, i * 4 + (lane >> 3), piece), v[i]);
+  __syncwarp();
+}
+
+__device__ __forceinline__ void add_bias(float (&v)[32], const __nv_bfloat16* bias, int32_t c, int32_t cols) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8) {
+    if (c + i < cols) {
+      float b[8];
+      unpack8(__ldg(reinterpret_cast<const uint4*>(bias + c + i)), b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i + j] += b[j];
+    }
+  }
+}
+
+__device__ __forceinline__ void stage_bf16(const float (&v)[32], uint32_t stg, uint32_t row, uint32_t piece0) {
+#pragma unroll
+  for (uint32_t i = 0; i < 4; ++i)
+    st_shared_v4(stg_at(stg, row, piece0 + i),
+                 make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]), pack_bf16(v[8 * i + 4], v[8 * i + 5]),
+                            pack_bf16(v[8 * i + 6], v[8 * i + 7])));
+}
+
+__device__ __forceinline__ void load32(uint32_t taddr, bool empty, float (&v)[32]) {
+  uint32_t r[32];
+  if (empty) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+    return;
+  }
+  tmem_ld_32x32b_x32(taddr, r);
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// One warp's 32 rows x 128 columns of a finished tile.  `released` is called
+// once the columns that both accumulators have are in registers: they are
+// among the 64 that drain_bf16 takes first.
+struct Fp8Place {
+  int32_t row, rows;  // first row in the output, rows of the warp that are the output's
+  int32_t col;        // first column
+  int32_t o;          // which output
+  int64_t off;        // elements before the output's matrix
+  int32_t eblock, erow;  // 128 rows of exponents of an 8-bit result, first row in them
+};
+
+template <typename Released>
+__device__ __forceinline__ void drain_bf16(const Fp8GemmParams& P, const Fp8Place& w, uint32_t taddr, bool empty, bool second_first,
+                                           uint32_t stg, uint32_t lane, Released released) {
+  const int64_t pitch = static_cast<int64_t>(P.cols) * 2;
+  const __nv_bfloat16* bias = P.bias[w.o];
+#pragma unroll 1
+  for (int part = 0; part < 2; ++part) {
+    const int half = second_first ? 1 - part : part;
+    const int32_t c = w.col + half * 64, bytes = min(P.cols - c, 64) * 2;
+    const int64_t at = (w.off + static_cast<int64_t>(w.row) * P.cols + c) * 2;
+    float v[2][32];
+    load32(taddr + half * 64, empty, v[0]);
+    load32(taddr + half * 64 + 32, empty, v[1]);
+    if (part == 0) released();
+    if (bytes <= 0) continue;
+    if (bias) {
+      add_bias(v[0], bias, c, P.cols);
+      add_bias(v[1], bias, c + 32, P.cols);
+    }
+    if (P.epi == TP_EPI_DGELU) {
+      stg_in(stg, reinterpret_cast<const uint8_t*>(P.aux[w.o]) + at, pitch, w.rows, bytes, lane);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+          float h[8];
+          unpack8(ld_shared_v4(stg_at(stg, lane, j * 4 + i)), h);
+#pragma unroll
+          for (int m = 0; m < 8; m += 2) times_gelu_prime2(v[j][8 * i + m], v[j][8 * i + m + 1], h[m], h[m + 1]);
+        }
+      __syncwarp();
+    } else if (P.epi == TP_EPI_GELU) {
+      if (P.aux[w.o]) {
+        stage_bf16(v[0], stg, lane, 0);
+        stage_bf16(v[1], stg, lane, 4);
+        stg_out(stg, reinterpret_cast<uint8_t*>(P.aux[w.o]) + at, pitch, w.rows, bytes, lane);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) gelu2(v[j][i], v[j][i + 1]);
+    }
+    stage_bf16(v[0], stg, lane, 0);
+    stage_bf16(v[1], stg, lane, 4);
+    stg_out(stg, reinterpret_cast<uint8_t*>(P.out[w.o]) + at, pitch, w.rows, bytes, lane);
+  }
+}
+
+// The same with the result in 8 bits: a thread has the 128 columns of its
+// row that share an exponent.
+template <typename Released>
+__device__ __forceinline__ void drain_fp8(const Fp8GemmParams& P, const Fp8Place& w, uint32_t taddr, bool empty, uint32_t stg, uint32_t lane,
+                                          Released released) {
+  const int64_t pitch = static_cast<int64_t>(P.cols) * 2;
+  const __nv_bfloat16* bias = P.bias[w.o];
+  float v[4][32];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) load32(taddr + j * 32, empty, v[j]);
+  released();
+  if (w.col >= P.cols) return;
+  float top = 0.f;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int32_t c = w.col + half * 64, bytes = min(P.cols - c, 64) * 2;
+    const int64_t at = (w.off + static_cast<int64_t>(w.row) * P.cols + c) * 2;
+    float(&v0)[32] = v[2 * half];
+    float(&v1)[32] = v[2 * half + 1];
+    if (bias) {
+      add_bias(v0, bias, c, P.cols);
+      add_bias(v1, bias, c + 32, P.cols);
+    }
+    if (P.aux[w.o] && bytes > 0) {
+      stage_bf16(v0, stg, lane, 0);
+      stage_bf16(v1, stg, lane, 4);
+      stg_out(stg, reinterpret_cast<uint8_t*>(P.aux[w.o]) + at, pitch, w.rows, bytes, lane);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        float &x0 = v[2 * half + j][i], &x1 = v[2 * half + j][i + 1];
+        if (P.epi == TP_EPI_GELU) gelu2(x0, x1);
+        if ((i & 7) == 0 && c + 32 * j + i >= P.cols) {  // past the matrix, in eights: zeros
+#pragma unroll
+          for (int m = 0; m < 8; ++m) v[2 * half + j][i + m] = 0.f;
+        }
+      }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 32; ++i) top = fmaxf(top, finite_abs(v[2 * half + j][i]));
+  }
+  const uint32_t e = fp8_exponent(top);
+  const float inv = fp8_inverse(e);
+#pragma unroll
+  for (uint32_t j = 0; j < 8; ++j) {
+    uint32_t o[4];
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) {
+      const uint32_t n = j * 16 + i * 4;
+      o[i] = fp8_pack4(v[n / 32][n % 32], v[n / 32][n % 32 + 1], v[n / 32][n % 32 + 2], v[n / 32][n % 32 + 3], inv);
+    }
+    st_shared_v4(stg_at(stg, lane, j), make_uint4(o[0], o[1], o[2], o[3]));
+  }
+  stg_out(stg, P.zq[w.o] + w.row * P.zq_ld + w.col, P.zq_ld, w.rows, 128, lane);
+  if (static_cast<int32_t>(lane) < w.rows) {
+    const int32_t b = w.col / 128;
+    P.ze[w.o][w.eblock * P.ze_ld + (b >> 2) * 512 + fp8_e_at(static_cast<uint32_t>(w.erow) + lane, b & 3)] = static_cast<uint8_t>(e);
+  }
+}
+
+// fp32 sums of a part of the contraction.
+template <typename Released>
+__device__ __forceinline__ void drain_part(const Fp8GemmParams& P, const Fp8Place& w, float* part, uint32_t taddr, bool empty,
+                                           uint32_t lane, Released released) {
+  const bool mine = static_cast<int32_t>(lane) < w.rows;
+  float* to = part + (static_cast<int64_t>(w.row) + lane) * P.cols + w.col;
+#pragma unroll 1
+  for (int j = 0; j < 4; ++j) {
+    float v[32];
+    load32(taddr + j * 32, empty, v);
+    if (mine) {
+#pragma unroll
+      for (int i = 0; i < 32; i += 4)
+        if (w.col + j * 32 + i < P.cols) __stcg(reinterpret_cast<float4*>(to + j * 32 + i), make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+    }
+  }
+  released();
+}
+
+// ------------------------------------------------------------------ kernel
+
+template <int CTAS, bool QUANT>
+__global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(const __grid_constant__ Fp8GemmParams P) {
+  using C = Fp8Cfg<CTAS>;
+  constexpr int STAGES = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem_raw + (base - raw) + C::BAR_OFF);
+  const uint32_t bar0 = base + C::BAR_OFF;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
+  const uint32_t begun_bar = bar0 + 8u * (2 * STAGES + 2), drain_bar = begun_bar + 8u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 4);
+  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
+  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t crank = CTAS == 2 ? cluster_ctarank() : 0;
+  const bool leader = crank == 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) mbar_init(tfull_bar(b), 1);
+    mbar_init(begun_bar, CTAS * C::EPI_WARPS);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    if (CTAS == 2) {
+      tmem_alloc_pair(smem_u32(tmem_slot), 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(tmem_slot), 512);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  if (CTAS == 2) {
+    __syncwarp();
+    cluster_sync_all();  // both CTAs' barriers exist before any remote signal
+  } else {
+    __syncthreads();
+  }
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  const int32_t first = static_cast<int32_t>(blockIdx.x) / CTAS, stride = static_cast<int32_t>(gridDim.x) / CTAS;
+  const int32_t units = fp8_units(P);
+  auto wait = [&](uint32_t bar, uint32_t parity, uint32_t role) {
+    return wait_bar(bar, parity & 1u, P.timeout_ns, P.status, abort_flag, role);
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ loads (both CTAs)
+      int stage = 0;
+      uint32_t phase = 0, armed = 0, armed_parity = 0;
+      int32_t issued = 0;
+      bool ok = true;
+      const uint32_t stage_bytes = static_cast<uint32_t>(P.mode == FP8_CONTRACT ? 128 : P.tile_rows) * 128 + C::B_BYTES;
+      for (int32_t t = first; t < units && ok; t += stride) {
+        const Fp8Unit u = fp8_unit<CTAS>(P, t);
+        const int32_t a_row = u.a_row + static_cast<int32_t>(crank) * 128, b_row = u.b_row + static_cast<int32_t>(crank) * 128;
+        for (int32_t q = u.q0; q < u.q1; ++q) {
+          if (!wait(empty_bar(stage), phase ^ 1u, 1u)) {
+            ok = false;
+            break;
+          }
+          const bool drop = blockIdx.x == 0 && issued++ == P.drop;  // test hook: the consumer's wait runs out
+          if (!drop) {
+            const Fp8Block b = fp8_block(P, u, q);
+            const bool scales = q == u.q0 || (b.k & 3) == 0;
+            const uint32_t bytes = stage_bytes + (scales ? C::EA_BYTES + C::EB_BYTES : 0u);
+            const uint32_t sa = base + C::A_OFF + stage * C::A_BYTES, sb = base + C::B_OFF + stage * C::B_BYTES,
+                           se = base + C::E_OFF + stage * C::E_BYTES;
+            if (CTAS == 2) {
+              const uint32_t fb = mapa_shared(full_bar(stage), 0);
+              if (leader) mbar_arrive_expect_tx(full_bar(stage), 2 * bytes);
+              tma_load_2d_pair(sa, &P.a[b.ai], fb, b.k * 128, a_row);
+              tma_load_2d_pair(sb, &P.b[b.bi], fb, b.k * 128, b_row);
+              if (scales) {
+                tma_load_3d_pair_plain(se, &P.ea[b.ai], fb, 0, b.k >> 2, u.ea + static_cast<int32_t>(crank));
+                tma_load_3d_pair_plain(se + C::EA_BYTES, &P.eb[b.bi], fb, 0, b.k >> 2, u.eb);
+              }
+            } else {
+              const uint32_t fb = full_bar(stage);
+              mbar_arrive_expect_tx(fb, bytes);
+              tma_load_2d(sa, &P.a[b.ai], fb, b.k * 128, a_row);
+              tma_load_2d(sb, &P.b[b.bi], fb, b.k * 128, b_row);
+              if (scales) {
+                tma_load_3d_plain(se, &P.ea[b.ai], fb, 0, b.k >> 2, u.ea);
+                tma_load_3d_plain(se + C::EA_BYTES, &P.eb[b.bi], fb, 0, b.k >> 2, u.eb);
+              }
+            }
+            armed |= 1u << stage;
+            armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+          }
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // every armed stage's last bytes have landed before the CTA goes on
+      if (leader)
+        for (int s = 0; s < STAGES; ++s)
+          if (armed & (1u << s)) drain_wait(full_bar(s), (armed_parity >> s) & 1u, P.timeout_ns);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // ------------------------------------------------------------ MMAs (CTA 0)
+      int stage = 0;
+      uint32_t phase = 0, n = 0, quads = 0;
+      bool ok = true;
+      for (int32_t t = first; t < units && ok; t += stride, ++n) {
+        const Fp8Unit u = fp8_unit<CTAS>(P, t);
+        // the epilogue has begun the tile before: it is done with the one
+        // before that, and with the columns that both accumulators have
+        if (n > 0 && !wait(begun_bar, n - 1, 2u)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + ((n & 1) ? C::ACC1 : 0);
+        uint32_t sf = tmem + C::SF;
+        for (int32_t q = u.q0; q < u.q1; ++q) {
+          if (!wait(full_bar(stage), phase, 3u)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const int32_t k = fp8_block(P, u, q).k;
+          const uint32_t sa = base + C::A_OFF + stage * C::A_BYTES, sb = base + C::B_OFF + stage * C::B_BYTES,
+                         se = base + C::E_OFF + stage * C::E_BYTES;
+          if (q == u.q0 || (k & 3) == 0) {
+            // copies and MMAs of a thread run in the order in which they are issued
+            sf = tmem + C::SF + (quads++ & 1) * 16;
+#pragma unroll
+            for (int i = 0; i < 1 + CTAS; ++i) tmem_cp_scales<CTAS>(sf + 4 * i, se + 512 * i);
+          }
+          const uint32_t idesc = make_idesc_mxf8(128 * CTAS, C::BN, k & 3);
+          const uint64_t ad = make_sw128_desc(sa, 16, 1024), bd = make_sw128_desc(sb, 16, 1024);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) umma_mxf8<CTAS>(d, ad + 2 * i, bd + 2 * i, idesc, sf, sf + 4, (q > u.q0 || i > 0) ? 1u : 0u);
+          if (CTAS == 2) umma_commit_pair(empty_bar(stage), 0x3);
+          else umma_commit(empty_bar(stage));
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if (CTAS == 2) umma_commit_pair(tfull_bar(n & 1), 0x3);
+        else umma_commit(tfull_bar(n & 1));
+      }
+      if (CTAS == 2) umma_commit_pair(drain_bar, 0x1);
+      else umma_commit(drain_bar);
+      drain_wait(drain_bar, 0, P.timeout_ns);
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue (both CTAs)
+    const uint32_t quarter = warp & 3, part = (warp - 2) >> 2;  // lanes of tensor memory, 128 columns
+    const uint32_t stg = base + C::STG_OFF + (warp - 2) * C::STG_BYTES;
+    uint32_t n = 0;
+    for (int32_t t = first; t < units; t += stride, ++n) {
+      const Fp8Unit u = fp8_unit<CTAS>(P, t);
+      const bool ok = wait(tfull_bar(n & 1), n >> 1, 4u);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem + ((quarter * 32) << 16) + ((n & 1) ? C::ACC1 : 0) + part * 128;
+      const bool empty = u.q0 >= u.q1;
+      auto begun = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (CTAS == 2) mbar_arrive_cluster(mapa_shared(begun_bar, 0));
+          else mbar_arrive(begun_bar);
+        }
+      };
+      Fp8Place w;
+      w.o = P.mode == FP8_DENSE ? u.g : P.mode == FP8_CONTRACT ? u.bi : 0;
+      w.off = u.out_off;
+      w.col = u.nt * C::BN + static_cast<int32_t>(part) * 128;
+      const int32_t tile_row = static_cast<int32_t>(quarter) * 32;
+      if (P.mode == FP8_ROWS) {
+        w.row = (u.mt * CTAS + static_cast<int32_t>(crank)) * P.tile_rows + tile_row;
+        w.rows = min(max(P.tile_rows - tile_row, 0), 32);
+      } else {
+        w.row = (u.mt * CTAS + static_cast<int32_t>(crank)) * 128 + tile_row;
+        w.rows = min(max(P.rows - w.row, 0), 32);
+      }
+      w.eblock = u.mt * CTAS + static_cast<int32_t>(crank);
+      w.erow = tile_row;
+      // The shared columns are the first accumulator's last 32 and the
+      // second's first; without them the tile counts as begun at once.
+      const bool shared_mine = C::SHARED != 0 && part == ((n & 1) ? 0u : 1u);
+      const bool early = !shared_mine || w.rows == 0;
+      if (early) begun();
+      auto released = [&] {
+        if (!early) begun();
+      };
+      if (w.rows > 0) {
+        if (P.splits > 1) {
+          float* to = P.part + (static_cast<int64_t>(u.split) * P.groups + u.g) * P.part_rows * P.cols;
+          drain_part(P, w, to, taddr, empty, lane, released);
+        } else if constexpr (QUANT) {
+          drain_fp8(P, w, taddr, empty, stg, lane, released);
+        } else {
+          drain_bf16(P, w, taddr, empty, (n & 1) == 0, stg, lane, released);
+        }
+      }
+      tc_fence_before();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (CTAS == 2) {
+    __syncwarp();
+    if (*abort_flag) {
+      // after a timeout, give the peer's copies into this CTA time to land
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 100000ull) {
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();  // no CTA frees tensor memory or exits while its peer may use it
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    if (CTAS == 2) tmem_dealloc_pair(tmem, 512);
+    else tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace tpf

@@ -17,7 +17,9 @@
 #include "block_norm.h"
 #include "ckpt.h"
 #include "gemm_kernel.cuh"
+#include "fp8.h"
 #include "host_util.h"
+#include "tensor_map.h"
 #include "w4.h"
 
 using namespace tpf;
@@ -92,10 +94,6 @@ uint64_t device_timeout_ns() {
 
 int64_t debug_drop() { return g_debug_drop_q.load(); }
 
-}  // namespace tpf
-
-namespace {
-
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -109,6 +107,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   });
   return fn;
 }
+
+}  // namespace tpf
+
+namespace {
 
 // bf16 tensor map with 128-byte swizzle over a row-major matrix with
 // `inner` contiguous elements per row, `outer` rows and a row pitch of `ld`
@@ -1103,6 +1105,10 @@ size_t tp_workspace_size(tp_op op, int p, int64_t M, int64_t N, int64_t K, int64
     case TP_OP_BLOCK_NORM_BWD: return block_norm_bwd_workspace(M, N);
     case TP_OP_COL_W4: return w4_workspace(false, p, M, N, K);
     case TP_OP_ROW_W4: return w4_workspace(true, p, M, N, K);
+    case TP_OP_COL_FP8:
+    case TP_OP_ROW_FP8:
+    case TP_OP_COL_BWD_FP8:
+    case TP_OP_ROW_BWD_FP8: return fp8_linear_workspace(op, p, M, N, K);
     case TP_OP_COL_BWD_CKPT:
     case TP_OP_ROW_BWD_CKPT:
     case TP_OP_AG_MM_BWD_CKPT:

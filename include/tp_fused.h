@@ -120,7 +120,11 @@ typedef enum {
   TP_OP_AG_MM_BWD_CKPT = 12,   /* tp_ag_matmul_bwd_ckpt */
   TP_OP_ROW_RS_BWD_CKPT = 13,  /* tp_row_linear_bwd_reducescatter_ckpt */
   TP_OP_COL_W4 = 14,        /* tp_col_linear_fwd_w4 */
-  TP_OP_ROW_W4 = 15         /* tp_row_linear_fwd_w4 */
+  TP_OP_ROW_W4 = 15,        /* tp_row_linear_fwd_w4 */
+  TP_OP_COL_FP8 = 16,       /* tp_col_linear_fwd_fp8 */
+  TP_OP_ROW_FP8 = 17,       /* tp_row_linear_fwd_fp8 */
+  TP_OP_COL_BWD_FP8 = 18,   /* tp_col_linear_bwd_fp8 */
+  TP_OP_ROW_BWD_FP8 = 19    /* tp_row_linear_bwd_fp8 */
 } tp_op;
 
 typedef enum {
@@ -392,6 +396,64 @@ tp_status tp_w4_pack(const void* const* w, void* const* q, void* const* s, int p
  * of many tokens, whose products run on the tensor cores in bf16.          */
 tp_status tp_w4_unpack(const void* const* q, const void* const* s, void* const* w, int p, int64_t N,
                        int64_t K, int64_t group, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The sharded Linear on 8-bit floating-point operands with a scale for each
+ * block of 128 along the contraction, forward and backward.
+ * An operand holds a matrix [R, C] whose products sum over C:
+ *   value[r, c] = q[r, c] * 2^(e - 127),  e the exponent of row r and block c / 128
+ *   q: e4m3 [R, P], P = C rounded up to 128; the P - C bytes past C are zero.
+ *   e: uint8 [ceil(R/128), ceil(C/512), 512]: of row r and block b at
+ *      [r / 128, b / 4, r % 32 * 16 + r % 128 / 32 * 4 + b % 4].
+ *   2^(e - 127) is the smallest power of two, at least 2^-127, whose 448-fold
+ *   reaches the largest finite magnitude of its block; q is rounded to
+ *   nearest even, an infinity or NaN to NaN.  Exponents of rows past R and
+ *   blocks past C are not used.  Both pointers are 16-byte aligned.
+ * A block is 128 columns of one row (activations, gradients) or 128 x 128
+ * (weights: then W and its transpose hold the same values).
+ * The tensor cores apply the scales; the sums are fp32, outputs bf16.        */
+typedef struct {
+  void *q, *e;
+} tp_fp8;
+
+/* q[i], qt[i]: the operands of x[i] and of its transpose, from one reading;
+ * either array may be NULL.  x[i]: bf16 [batch, M, N], a matrix each.
+ *   q[i]: [batch][M, N], a contraction over N; qt[i]: [batch][N, M], over M.
+ *   tiles: 0, blocks of one row (of the operand); 1, blocks of 128 x 128.
+ *   epi: TP_EPI_NONE, or TP_EPI_GELU to pack GeLU(x).                        */
+tp_status tp_fp8_pack(const void* const* x, const tp_fp8* q, const tp_fp8* qt, int tiles, tp_epilogue epi, int p,
+                      int64_t batch, int64_t M, int64_t N, cudaStream_t stream);
+
+/* y[i] = the values of q[i], bf16 [batch, M, N] (exact where they are bf16s:
+ * unless below 2^-126). */
+tp_status tp_fp8_unpack(const tp_fp8* q, void* const* y, int p, int64_t batch, int64_t M, int64_t N,
+                        cudaStream_t stream);
+
+/* Y_k = X . A_k (+ b_k), optionally GeLU, as tp_col_linear_fwd.
+ *   x: operand [M, K]; w[k]: operand [N, K] of A_k's transpose (qt of A_k);
+ *   y[k]: [M, N] bf16, or NULL and z[k]: the result's operand [M, N], packed
+ *   from the fp32 results (the input of the row layer that follows);
+ *   preact[k] (TP_EPI_GELU, may be NULL): H_k [M, N] bf16.                   */
+tp_status tp_col_linear_fwd_fp8(const tp_fp8* x, const tp_fp8* w, const void* const* bias, void* const* y,
+                                const tp_fp8* z, void* const* preact, tp_epilogue epi, int p, int64_t M, int64_t N,
+                                int64_t K, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Y = sum_r X_r . A_r (+ b), as tp_row_linear_fwd_allreduce with n_out = 1.
+ *   x[r]: operand [M, K]; w[r]: operand [N, K] of A_r's transpose.           */
+tp_status tp_row_linear_fwd_fp8(const tp_fp8* x, const tp_fp8* w, const void* bias, void* y, int p, int64_t M,
+                                int64_t N, int64_t K, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* The backward calls, as tp_col_linear_bwd and tp_row_linear_bwd.
+ *   w[k]: operand [K, N] of A_k (q of A_k); dy: operands [M, N] and
+ *   dyt: operands [N, M] of the output gradients and their transposes;
+ *   xt: operands [K, M] of the transposed inputs.  dx (from w, dy) or dw
+ *   (from xt, dyt) may be NULL, not both; all bf16.                          */
+tp_status tp_col_linear_bwd_fp8(const tp_fp8* xt, const tp_fp8* w, const tp_fp8* dy, const tp_fp8* dyt, void* dx,
+                                void* const* dw, int p, int64_t M, int64_t N, int64_t K, void* ws, size_t ws_bytes,
+                                cudaStream_t stream);
+tp_status tp_row_linear_bwd_fp8(const tp_fp8* xt, const tp_fp8* w, const tp_fp8* dy, const tp_fp8* dyt,
+                                void* const* dx, void* const* dw, const void* const* preact, int p, int64_t M,
+                                int64_t N, int64_t K, void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /* Unfused baseline of the row-parallel MatMul+AllReduce, for measurement
  * and for the output-error comparison against it.
