@@ -66,6 +66,10 @@ TP_NORM_LAYER = 2
 # largest hidden size of the block norms, and most tokens of the 4-bit forward calls
 TP_BLOCK_NORM_MAX_H = 16384
 TP_W4_MAX_M = 64
+# tp_route_score, and the most experts of a routing call
+TP_ROUTE_SOFTMAX = 0
+TP_ROUTE_SIGMOID = 1
+TP_ROUTE_MAX_EXPERTS = 512
 # tp_debug_key
 TP_DEBUG_TIMEOUT_MS = 0
 TP_DEBUG_DROP_LOAD = 1
@@ -96,6 +100,12 @@ class _NormDesc(ctypes.Structure):
 class _NormGrads(ctypes.Structure):
     """tp_block_norm_grads"""
     _fields_ = [(k, ctypes.c_void_p) for k in ("dw_post", "db_post", "dw_pre", "db_pre", "dgate")]
+
+
+class _RouteDesc(ctypes.Structure):
+    """tp_route_desc"""
+    _fields_ = [("score", ctypes.c_int), ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32), ("group_best", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 def _load() -> ctypes.CDLL:
@@ -138,6 +148,8 @@ def _load() -> ctypes.CDLL:
         "tp_row_linear_fwd_fp8": (I, [PP, PP, P, P, I, L, L, L, P, S, P]),
         "tp_col_linear_bwd_fp8": (I, [PP, PP, PP, PP, P, PP, I, L, L, L, P, S, P]),
         "tp_row_linear_bwd_fp8": (I, [PP, PP, PP, PP, PP, PP, PP, I, L, L, L, P, S, P]),
+        "tp_route_fwd": (I, [P, P, P, P, P, P, L, L, L, I, P]),
+        "tp_route_bwd": (I, [P, P, P, P, P, L, L, L, I, P]),
         "tp_pipeline_time": (ctypes.c_double, [ctypes.c_double, ctypes.c_double, L]),
         "tp_num_chunks": (L, [L, L]),
         "tp_choose_chunk_m": (L, [I, I, L, L, L]),
@@ -524,15 +536,15 @@ def tp_noalloc_device_status(stream=None) -> int:
 # _refuse, which finds the words, only when something is wrong.
 
 _ARRAY = tuple(ctypes.c_void_p * n for n in range(65))  # the C array types, looked up once
-_BF16 = _FP32 = _INT8 = _UINT8 = _E4M3 = _RAW_STREAM = None
+_BF16 = _FP32 = _INT8 = _UINT8 = _INT32 = _E4M3 = _RAW_STREAM = None
 
 
 def _begin() -> int:
     """The current device; the first call fetches torch's dtypes and stream getter."""
-    global _BF16, _FP32, _INT8, _UINT8, _E4M3, _RAW_STREAM
+    global _BF16, _FP32, _INT8, _UINT8, _INT32, _E4M3, _RAW_STREAM
     if _BF16 is None:
         import torch
-        _FP32, _INT8, _UINT8, _E4M3 = torch.float32, torch.int8, torch.uint8, torch.float8_e4m3fn
+        _FP32, _INT8, _UINT8, _INT32, _E4M3 = torch.float32, torch.int8, torch.uint8, torch.int32, torch.float8_e4m3fn
         # the current stream's handle without a Stream object around it, where torch has it
         _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
         _BF16 = torch.bfloat16
@@ -944,3 +956,47 @@ def tp_row_linear_bwd_fp8(xt, w, dy, dyt, dx, dw, ws, preact=None, stream=None) 
         _fp8s(W, "dy", (dy,) if need_x else None, 1, M, N, dev), _fp8s(W, "dyt", (dyt,) if need_w else None, 1, N, M, dev),
         _list(W, "dx", dx, p, (M, K), bf, dev), _list(W, "dw", dw, p, (K, N), bf, dev),
         _list(W, "preact", preact, p, (M, K), bf, dev), p, M, N, K, wp, wb, _on(stream, dev)), W)
+
+
+# ------------------------------------------------------------------ routing to experts
+
+def _logits(where: str, t) -> tuple:
+    if t.dim() != 2:
+        raise ValueError(f"{where}: logits are [tokens, experts], got {tuple(t.shape)}")
+    if t.dtype is not _BF16 and t.dtype is not _FP32:
+        raise TypeError(f"{where}: logits are bfloat16 or float32, got {t.dtype}")
+    return t.shape[0], t.shape[1], TP_BF16 if t.dtype is _BF16 else TP_FP32
+
+
+def _slots(where: str, name: str, t, T: int) -> int:
+    if t.dim() != 2 or t.shape[0] != T:
+        raise ValueError(f"{where}: {name} is [{T}, k], got {tuple(t.shape)}")
+    return t.shape[1]
+
+
+def tp_route_fwd(logits, experts, weights, counts=None, *, bias=None, score: int = TP_ROUTE_SOFTMAX, groups: int = 1,
+                 top_groups: int = 1, group_best: int = 1, renorm: bool = False, scale: float = 1.0, stream=None) -> None:
+    """experts[t] (int32 [T, k]) and weights[t] (float32 [T, k]) of the k best of logits[t] ([T, E], bfloat16 or float32).
+
+    The choice is by s + bias, s the softmax or sigmoid of the logits, among the top_groups groups with the largest sums
+    of their group_best best; weights = scale * s, with renorm over the sum of the chosen.  An expert with a logit of -inf
+    or NaN is closed; a slot without an open expert gets -1 and 0.  counts (int32 [E]): how often each was chosen."""
+    W, dev = "tp_route_fwd", _begin()
+    T, E, code = _logits(W, logits)
+    k = _slots(W, "experts", experts, T)
+    d = _RouteDesc(score, groups, top_groups, group_best, int(renorm), scale)
+    _check(_lib.tp_route_fwd(_one(W, "logits", logits, (T, E), logits.dtype, dev), _one(W, "bias", bias, (E,), _FP32, dev),
+                             _one(W, "experts", experts, (T, k), _INT32, dev), _one(W, "weights", weights, (T, k), _FP32, dev),
+                             _one(W, "counts", counts, (E,), _INT32, dev), ctypes.byref(d), T, E, k, code, _on(stream, dev)), W)
+
+
+def tp_route_bwd(logits, experts, dweights, dlogits, *, score: int = TP_ROUTE_SOFTMAX, renorm: bool = False, scale: float = 1.0,
+                 stream=None) -> None:
+    """dlogits ([T, E], the logits' dtype) from dweights (float32 [T, k]) and the experts that tp_route_fwd chose."""
+    W, dev = "tp_route_bwd", _begin()
+    T, E, code = _logits(W, logits)
+    k = _slots(W, "experts", experts, T)
+    d = _RouteDesc(score, 1, 1, 1, int(renorm), scale)
+    _check(_lib.tp_route_bwd(_one(W, "logits", logits, (T, E), logits.dtype, dev), _one(W, "experts", experts, (T, k), _INT32, dev),
+                             _one(W, "dweights", dweights, (T, k), _FP32, dev), _one(W, "dlogits", dlogits, (T, E), logits.dtype, dev),
+                             ctypes.byref(d), T, E, k, code, _on(stream, dev)), W)

@@ -455,6 +455,45 @@ tp_status tp_row_linear_bwd_fp8(const tp_fp8* xt, const tp_fp8* w, const tp_fp8*
                                 void* const* dx, void* const* dw, const void* const* preact, int p, int64_t M,
                                 int64_t N, int64_t K, void* ws, size_t ws_bytes, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Routing of tokens to experts.  For each of the T rows of logits [T, E]:
+ *   s = softmax(l) or sigmoid(l);  v = s + bias
+ *   groups > 1: the experts are that many groups of neighbours; the
+ *     top_groups groups with the largest sums of their group_best (1 or 2)
+ *     largest v stay (ties to the lower number);
+ *   experts[t, 0..k-1]: the k largest v that are left, in falling order, ties
+ *     to the lower number; bias moves the choice only:
+ *   weights[t, j] = scale * s of that expert, renorm: divided by the sum of
+ *     the chosen s.
+ * The choice is that of exact arithmetic on the given logits and biases (in
+ * 64 bits where it is close), whatever E, T and the other rows are.
+ * An expert whose logit is -infinity or NaN is closed: s = 0, and it is not
+ * chosen.  A slot without an open expert has experts = -1, weights = 0; a row
+ * that is closed throughout has only those.  A logit of +infinity counts as
+ * the largest finite one.  Biases are finite.
+ *   logits: bf16 or fp32 (`dtype`); bias: fp32 [E] or NULL; experts: int32
+ *   [T, k]; weights: fp32 [T, k]; counts: int32 [E] or NULL, how often each
+ *   expert was chosen.
+ * E <= TP_ROUTE_MAX_EXPERTS, k <= 32 and <= E, groups <= 32, E % groups == 0. */
+#define TP_ROUTE_MAX_EXPERTS 512
+typedef enum { TP_ROUTE_SOFTMAX = 0, TP_ROUTE_SIGMOID = 1 } tp_route_score;
+typedef struct {
+  tp_route_score score;
+  int32_t groups, top_groups, group_best, renorm;
+  float scale;
+} tp_route_desc;
+tp_status tp_route_fwd(const void* logits, const void* bias, void* experts, void* weights, void* counts,
+                       const tp_route_desc* d, int64_t T, int64_t E, int64_t k, tp_dtype dtype,
+                       cudaStream_t stream);
+
+/* The gradient of the logits, dlogits [T, E] in their dtype, from that of the
+ * weights, dweights fp32 [T, k], and the forward pass's experts (a number
+ * outside 0..E-1 has no part in it; groups and bias have no gradient).  The
+ * descriptor is the forward pass's; its groups are not used.               */
+tp_status tp_route_bwd(const void* logits, const void* experts, const void* dweights, void* dlogits,
+                       const tp_route_desc* d, int64_t T, int64_t E, int64_t k, tp_dtype dtype,
+                       cudaStream_t stream);
+
 /* Unfused baseline of the row-parallel MatMul+AllReduce, for measurement
  * and for the output-error comparison against it.
  * [M027 §04: time the MatMul and the collective separately, compare the
