@@ -108,6 +108,11 @@ class _RouteDesc(ctypes.Structure):
                 ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+class _ExpertsSaved(ctypes.Structure):
+    """tp_experts_saved"""
+    _fields_ = [(k, ctypes.c_void_p) for k in ("plan", "preact", "out")]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -150,6 +155,11 @@ def _load() -> ctypes.CDLL:
         "tp_row_linear_bwd_fp8": (I, [PP, PP, PP, PP, PP, PP, PP, I, L, L, L, P, S, P]),
         "tp_route_fwd": (I, [P, P, P, P, P, P, L, L, L, I, P]),
         "tp_route_bwd": (I, [P, P, P, P, P, L, L, L, I, P]),
+        "tp_experts_rows": (L, [L, L, L]),
+        "tp_experts_plan_size": (S, [L, L, L]),
+        "tp_experts_workspace_size": (S, [I, L, L, L, L, L, I]),
+        "tp_experts_fwd_fp8": (I, [P, P, P, PP, PP, P, P, I, L, L, L, L, L, P, S, P]),
+        "tp_experts_bwd_fp8": (I, [P, P, P, PP, PP, P, P, PP, PP, P, I, L, L, L, L, L, P, S, P]),
         "tp_pipeline_time": (ctypes.c_double, [ctypes.c_double, ctypes.c_double, L]),
         "tp_num_chunks": (L, [L, L]),
         "tp_choose_chunk_m": (L, [I, I, L, L, L]),
@@ -1000,3 +1010,95 @@ def tp_route_bwd(logits, experts, dweights, dlogits, *, score: int = TP_ROUTE_SO
     _check(_lib.tp_route_bwd(_one(W, "logits", logits, (T, E), logits.dtype, dev), _one(W, "experts", experts, (T, k), _INT32, dev),
                              _one(W, "dweights", dweights, (T, k), _FP32, dev), _one(W, "dlogits", dlogits, (T, E), logits.dtype, dev),
                              ctypes.byref(d), T, E, k, code, _on(stream, dev)), W)
+
+
+# ------------------------------------------------------------------ routed experts
+
+class ExpertsSaved(NamedTuple):
+    """What tp_experts_fwd_fp8 leaves for tp_experts_bwd_fp8 (see experts_saved)."""
+    plan: object
+    preact: object
+    out: object
+
+
+def tp_experts_rows(E: int, T: int, k: int) -> int:
+    return int(_lib.tp_experts_rows(E, T, k))
+
+
+def tp_experts_plan_size(E: int, T: int, k: int) -> int:
+    return int(_lib.tp_experts_plan_size(E, T, k))
+
+
+def tp_experts_workspace_size(p: int, E: int, T: int, k: int, h: int, f: int, backward: bool = False) -> int:
+    return int(_lib.tp_experts_workspace_size(p, E, T, k, h, f, int(backward)))
+
+
+def experts_workspace(p: int, E: int, T: int, k: int, h: int, f: int, backward: bool = False, device="cuda"):
+    """A zero-filled workspace of the forward call, with `backward` of both."""
+    import torch
+    return torch.zeros((tp_experts_workspace_size(p, E, T, k, h, f, backward) + 15) // 16 * 16, dtype=torch.uint8, device=device)
+
+
+def experts_saved(E: int, T: int, k: int, h: int, f: int, device="cuda") -> ExpertsSaved:
+    """Memory for what a forward call leaves for its backward call."""
+    import torch
+    rows = tp_experts_rows(E, T, k)
+    bf = dict(dtype=torch.bfloat16, device=device)
+    return ExpertsSaved(torch.empty(tp_experts_plan_size(E, T, k) // 4, dtype=torch.int32, device=device),
+                        torch.empty((rows, f), **bf), torch.empty((rows, h), **bf))
+
+
+def _saved(where: str, s, E: int, T: int, k: int, h: int, f: int, dev: int):
+    rows = tp_experts_rows(E, T, k)
+    return _ExpertsSaved(_one(where, "saved.plan", s.plan, (tp_experts_plan_size(E, T, k) // 4,), _INT32, dev),
+                         _one(where, "saved.preact", s.preact, (rows, f), _BF16, dev), _one(where, "saved.out", s.out, (rows, h), _BF16, dev))
+
+
+def _expert_sizes(where: str, x, name: str, t) -> tuple:
+    if x.dim() != 2:
+        raise ValueError(f"{where}: tokens are [T, h], got {tuple(x.shape)}")
+    return x.shape[0], x.shape[1], _slots(where, name, t, x.shape[0])
+
+
+def tp_experts_fwd_fp8(x, experts, weights, w1: Sequence, w2: Sequence, y, ws, saved=None, stream=None) -> None:
+    """y[t] = sum_j weights[t, j] GeLU(x[t] W1_e) W2_e, e = experts[t, j] (int32 [T, k], weights float32 [T, k]).
+
+    w1[r], w2[r]: the E/p operands [f, h] and [h, f] of shard r, packed transposes of W1_e [h, f] and W2_e [f, h] with a
+    leading dimension.  A slot with a number outside 0..E-1 has no part in it.  saved (experts_saved) for the backward call."""
+    W, dev, p, bf = "tp_experts_fwd_fp8", _begin(), len(w1), _BF16
+    T, h, k = _expert_sizes(W, x, "experts", experts)
+    if w1[0].q.dim() != 3:
+        raise ValueError(f"{W}: w1[0] is operands [experts, f, h], got {tuple(w1[0].q.shape)}")
+    per, f = w1[0].q.shape[:2]
+    E = per * p
+    _need_ws(W, ws, dev)
+    wp, wb = _ws(ws)
+    sv = None if saved is None else ctypes.byref(_saved(W, saved, E, T, k, h, f, dev))
+    _check(_lib.tp_experts_fwd_fp8(
+        _one(W, "x", x, (T, h), bf, dev), _one(W, "experts", experts, (T, k), _INT32, dev), _one(W, "weights", weights, (T, k), _FP32, dev),
+        _fp8s(W, "w1", w1, p, f, h, dev, (per,)), _fp8s(W, "w2", w2, p, h, f, dev, (per,)), _one(W, "y", y, (T, h), bf, dev), sv, p, E, T, k,
+        h, f, wp, wb, _on(stream, dev)), W)
+
+
+def tp_experts_bwd_fp8(x, weights, dy, w1t, w2t, dx, dweights, dw1, dw2, saved, ws, stream=None) -> None:
+    """Gradients of tp_experts_fwd_fp8 from what it saved: dx [T, h], dweights (bfloat16 [T, k]), dw1[r] [E/p, h, f], dw2[r] [E/p, f, h].
+
+    w1t[r] (read for dx) and w2t[r] (for dx and dw1): operands [h, f] of W1_e and [f, h] of W2_e.  Each output may be None."""
+    W, dev, bf = "tp_experts_bwd_fp8", _begin(), _BF16
+    T, h, k = _expert_sizes(W, dy, "weights", weights)
+    first = dw1 if dw1 is not None else dw2 if dw2 is not None else w2t if w2t is not None else w1t
+    if first is None:
+        raise ValueError(f"{W}: one of dw1, dw2, w1t and w2t is given")
+    p, one = len(first), first[0]
+    per, f = (one.q.shape[0] if isinstance(one, Fp8) else one.shape[0]), saved.preact.shape[1]
+    E = per * p
+    _need_ws(W, ws, dev)
+    wp, wb = _ws(ws)
+    need_h = dx is not None or dw1 is not None
+    _check(_lib.tp_experts_bwd_fp8(
+        _one(W, "x", x if dw1 is not None else None, (T, h), bf, dev), _one(W, "weights", weights, (T, k), _FP32, dev),
+        _one(W, "dy", dy, (T, h), bf, dev), _fp8s(W, "w1t", w1t if dx is not None else None, p, h, f, dev, (per,)),
+        _fp8s(W, "w2t", w2t if need_h else None, p, f, h, dev, (per,)), _one(W, "dx", dx, (T, h), bf, dev),
+        _one(W, "dweights", dweights, (T, k), bf, dev), _list(W, "dw1", dw1, p, (per, h, f), bf, dev),
+        _list(W, "dw2", dw2, p, (per, f, h), bf, dev), ctypes.byref(_saved(W, saved, E, T, k, h, f, dev)), p, E, T, k, h, f, wp, wb,
+        _on(stream, dev)), W)

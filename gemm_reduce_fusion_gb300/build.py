@@ -26,7 +26,7 @@ FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-re
          "-I", os.path.join(ROOT, "include")]
 SOURCES = ["tp_fused.cu", "block_norm.cu", "block_norm_bwd_bf16_rms.cu", "block_norm_bwd_bf16_ln.cu",
            "block_norm_bwd_f32_rms.cu", "block_norm_bwd_f32_ln.cu", "ckpt.cu", "w4.cu",
-           "fp8.cu", "fp8_pack.cu", "route.cu"]
+           "fp8.cu", "fp8_pack.cu", "route.cu", "experts.cu"]
 
 
 def nvcc() -> str:

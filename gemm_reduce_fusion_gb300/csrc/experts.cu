@@ -1,0 +1,658 @@
+// Routed experts on 8-bit operands, forward and backward:
+//   y[t] = sum_j weights[t, j] GeLU(x[t] W1_e) W2_e,  e = experts[t, j]
+// The p shards hold E/p experts each; the sum over a token's experts is the
+// sum over the ranks.
+//
+// The slots (t, j) of an expert become rows, in the order of t, in tiles of
+// `tile_rows` rows of one expert each (dispatch_kernel).  The products walk
+// the tiles in use (fp8_gemm.cuh, FP8_ROWS), or contract over an expert's
+// rows (FP8_CONTRACT); how many tiles there are stays on the device.  What
+// belongs to a row without a slot is zero in a training step, where such rows
+// are contracted over, and otherwise not written, and never read for a token.
+//
+// The gather of the tokens' rows is part of their packing, GeLU and the
+// activation's packing of the first product's epilogue, and the weighted sum
+// one kernel (combine_kernel), which adds a token's rows in fp32 in the order
+// of its choices, so that results do not depend on the order of execution.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "fp8.h"
+#include "fp8_gemm.cuh"
+#include "vec_util.cuh"
+
+using namespace tpf;
+
+namespace {
+
+constexpr int kMaxExperts = TP_ROUTE_MAX_EXPERTS, kMaxK = 32;
+constexpr int kDispatchThreads = 512;
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+
+// ------------------------------------------------------------------ plan
+
+struct DispatchParams {
+  const int32_t* experts;  // [S]
+  int32_t *tiles, *first, *expert, *slot, *row;
+  int32_t S, E, tile_rows, max_tiles;
+};
+
+__device__ __forceinline__ int32_t tiles_of(int32_t n, int32_t tile_rows) { return (n + tile_rows - 1) / tile_rows; }
+
+// A thread block an expert.  Each counts all experts' slots, so that no
+// kernel has to run before it: 2 x 4 bytes a slot from L2.
+__global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const __grid_constant__ DispatchParams P) {
+  __shared__ int32_t count[kMaxExperts];
+  __shared__ int32_t warp_sum[kDispatchThreads / 32], begin, total;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int32_t me = static_cast<int32_t>(blockIdx.x), tid = static_cast<int32_t>(threadIdx.x);
+  const uint32_t lane = tid & 31, warp = tid >> 5;
+  for (int32_t e = tid; e < P.E; e += kDispatchThreads) count[e] = 0;
+  __syncthreads();
+  for (int32_t i = tid; i < P.S; i += kDispatchThreads) {
+    const int32_t e = P.experts[i];
+    if (e >= 0 && e < P.E) atomicAdd(count + e, 1);
+  }
+  __syncthreads();
+  // tiles before this expert's, and all of them
+  int32_t before = 0, all = 0;
+  for (int32_t e = tid; e < P.E; e += kDispatchThreads) {
+    const int32_t n = tiles_of(count[e], P.tile_rows);
+    all += n;
+    if (e < me) before += n;
+  }
+  if (tid == 0) begin = total = 0;
+  __syncthreads();
+  if (before) atomicAdd(&begin, before);
+  if (all) atomicAdd(&total, all);
+  __syncthreads();
+  const int32_t mine = tiles_of(count[me], P.tile_rows);
+  if (tid == 0) {
+    P.first[me] = begin;
+    if (me == P.E - 1) {
+      P.first[P.E] = total;
+      *P.tiles = total;
+    }
+  }
+  for (int32_t i = tid; i < mine; i += kDispatchThreads) P.expert[begin + i] = me;
+  // the slots, in their order
+  int32_t at = begin * P.tile_rows;
+  for (int32_t base = 0; base < P.S; base += kDispatchThreads * 4) {
+    const int32_t i0 = base + tid * 4;
+    int32_t e[4], n = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      e[j] = i0 + j < P.S ? P.experts[i0 + j] : -1;
+      n += e[j] == me;
+    }
+    int32_t sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t v = __shfl_up_sync(kAll, sum, o);
+      if (static_cast<int32_t>(lane) >= o) sum += v;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sum[warp] = sum;
+    __syncthreads();
+    int32_t here = at + sum - n, round = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < kDispatchThreads / 32; ++w) {
+      const int32_t v = warp_sum[w];
+      if (w < warp) here += v;
+      round += v;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (e[j] == me) {
+        P.slot[here] = i0 + j;
+        P.row[i0 + j] = here++;
+      } else if (me == 0 && i0 + j < P.S && (e[j] < 0 || e[j] >= P.E)) {
+        P.row[i0 + j] = -1;
+      }
+    }
+    at += round;
+  }
+  for (int32_t r = at + tid; r < (begin + mine) * P.tile_rows; r += kDispatchThreads) P.slot[r] = -1;
+}
+
+// ------------------------------------------------------------------ sums over a token's rows
+
+struct CombineParams {
+  const __nv_bfloat16* rows;  // [R, N], or null:
+  const float* part;          // fp32 parts of them [splits][R, N]
+  int64_t part_step;
+  int32_t splits;
+  const int32_t* row;         // [T, k]
+  const float* weights;       // [T, k] or null (ones)
+  __nv_bfloat16* y;           // [T, N]
+  int64_t T, N;
+  int32_t k;
+};
+
+// Eight columns of a token a thread.
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ CombineParams P) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t per_row = P.N / 8, unit = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, t = unit / per_row;
+  if (t >= P.T) return;
+  const int64_t c = (unit - t * per_row) * 8;
+  float sum[8] = {};
+  for (int32_t j = 0; j < P.k; ++j) {
+    const int32_t r = P.row[t * P.k + j];
+    if (r < 0) continue;
+    const float w = P.weights ? P.weights[t * P.k + j] : 1.f;
+    float v[8] = {};
+    if (P.rows) {
+      unpack8(*reinterpret_cast<const uint4*>(P.rows + r * P.N + c), v);
+    } else {
+      const float* from = P.part + r * P.N + c;
+#pragma unroll 2
+      for (int32_t s = 0; s < P.splits; ++s) {
+        const float4 a = __ldcg(reinterpret_cast<const float4*>(from + s * P.part_step)),
+                     b = __ldcg(reinterpret_cast<const float4*>(from + s * P.part_step + 4));
+        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+        v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] = fmaf(w, v[i], sum[i]);
+  }
+  *reinterpret_cast<uint4*>(P.y + t * P.N + c) = pack8(sum);
+}
+
+struct DotParams {
+  const __nv_bfloat16 *rows, *dy;
+  const int32_t* row;
+  __nv_bfloat16* dweights;
+  int64_t S, N;
+  int32_t k;
+};
+
+// The gradient of a slot's weight: dy[t] . rows[slot's row], a warp a slot.
+__global__ void __launch_bounds__(256) weight_grad_kernel(const __grid_constant__ DotParams P) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t s = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (s >= P.S) return;
+  const uint32_t lane = threadIdx.x & 31;
+  const int32_t r = P.row[s];
+  float sum = 0.f;
+  if (r >= 0) {
+    const __nv_bfloat16 *a = P.rows + static_cast<int64_t>(r) * P.N, *b = P.dy + s / P.k * P.N;
+#pragma unroll 4
+    for (int64_t c = lane * 8; c < P.N; c += 256) {
+      float u[8], v[8];
+      unpack8(*reinterpret_cast<const uint4*>(a + c), u);
+      unpack8(*reinterpret_cast<const uint4*>(b + c), v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = fmaf(u[i], v[i], sum);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+  if (lane == 0) P.dweights[s] = __float2bfloat16_rn(sum);
+}
+
+// ------------------------------------------------------------------ host
+
+struct Sizes {
+  int p;
+  int64_t E, T, k, h, f;
+  int64_t S, tile_rows, max_tiles, rows;
+  size_t plan_bytes;
+};
+
+// Rows of a tile.  A training step contracts over whole blocks of 128 rows.
+// Without one, a tile's rows past its expert's are read for nothing and a
+// second tile of an expert reads its weights again (from L2), so that the
+// tile goes by the rows that an expert has on average.
+int64_t tile_rows_for(int64_t S, int64_t E, bool train) {
+  const int64_t active = std::max<int64_t>(1, std::min(E, S)), mean = S / active;
+  if (train) return 128;
+  return mean <= 8 ? 16 : mean <= 20 ? 32 : mean <= 48 ? 64 : 128;
+}
+
+bool sizes_of(int p, int64_t E, int64_t T, int64_t k, int64_t h, int64_t f, bool train, Sizes* s) {
+  s->p = p, s->E = E, s->T = T, s->k = k, s->h = h, s->f = f;
+  s->S = T * k;
+  s->tile_rows = tile_rows_for(s->S, E, train);
+  // every expert that has rows leaves at most a tile less one row empty
+  s->max_tiles = (s->S + (s->tile_rows - 1) * std::min(E, s->S)) / s->tile_rows;
+  s->rows = s->max_tiles * s->tile_rows;
+  s->plan_bytes = static_cast<size_t>(cdiv(1 + (E + 1) + s->max_tiles + s->rows + s->S, 64) * 64) * 4;
+  return s->rows <= (int64_t(1) << 31) - 129;
+}
+
+tp_status check_experts(int p, int64_t E, int64_t T, int64_t k, int64_t h, int64_t f) {
+  if (p < 1 || p > kMaxP || E < 1 || T < 0 || k < 1 || h < 1 || f < 1) return TP_ERR_INVALID_ARG;
+  if (E % p != 0 || E > kMaxExperts || k > kMaxK) return TP_ERR_UNSUPPORTED_SHAPE;
+  const int64_t lim = (int64_t(1) << 31) - 1;
+  if (T > lim || T * k > lim / 2 || h > lim || f > lim || E / p * std::max(h, f) > lim) return TP_ERR_UNSUPPORTED_SHAPE;
+  if (h % 8 != 0 || f % 8 != 0) return TP_ERR_ALIGNMENT;
+  return TP_OK;
+}
+
+// The plan's arrays in its memory.
+Fp8Plan plan_at(const Sizes& s, int32_t* at, int32_t** tiles, int32_t** first, int32_t** expert, int32_t** slot, int32_t** row) {
+  *tiles = at;
+  *first = at + 1;
+  *expert = *first + s.E + 1;
+  *slot = *expert + s.max_tiles;
+  *row = *slot + s.rows;
+  Fp8Plan plan;
+  plan.tiles = *tiles;
+  plan.first = *first;
+  plan.expert = *expert;
+  plan.slot = *slot;
+  plan.max_tiles = s.max_tiles;
+  plan.tile_rows = s.tile_rows;
+  plan.E = static_cast<int>(s.E);
+  plan.k = static_cast<int>(s.k);
+  return plan;
+}
+
+// Pieces of a workspace, one after the other; without memory, their size.
+struct Area {
+  uint8_t* base;
+  size_t at = kDataOffset;
+  explicit Area(void* ws) : base(static_cast<uint8_t*>(ws)) {}
+  void* take(size_t bytes) {
+    void* p = base ? base + at : nullptr;
+    at += (bytes + 255) / 256 * 256;
+    return p;
+  }
+  tp_fp8 fp8(int64_t rows, int64_t cols, int64_t blocks) {
+    tp_fp8 o;
+    o.q = take(fp8_q_bytes(rows, cols));
+    o.e = take(static_cast<size_t>(blocks * cdiv(cols, 512)) * 512);
+    return o;
+  }
+};
+
+struct ForwardArea {
+  int32_t* plan;
+  tp_fp8 xq, zq;
+  void* out;
+  float* part;
+  Fp8Launch first, second;
+};
+
+ForwardArea forward_area(const Sizes& s, bool train, Area* a) {
+  ForwardArea f;
+  const int64_t blocks = s.max_tiles * cdiv(s.tile_rows, 128);
+  f.first = fp8_plan(FP8_ROWS, s.rows, s.f, s.h, 1, 1, s.max_tiles, s.rows);
+  f.second = fp8_plan(FP8_ROWS, s.rows, s.h, s.f, 1, 1, s.max_tiles, s.rows);
+  f.plan = static_cast<int32_t*>(train ? nullptr : a->take(s.plan_bytes));
+  f.xq = a->fp8(s.rows, s.h, blocks);
+  f.zq = a->fp8(s.rows, s.f, blocks);
+  f.out = train || f.second.splits > 1 ? nullptr : a->take(static_cast<size_t>(s.rows * s.h) * 2);
+  const size_t part = std::max(f.first.part_bytes, f.second.part_bytes);
+  f.part = static_cast<float*>(part ? a->take(part) : nullptr);
+  return f;
+}
+
+struct BackwardArea {
+  tp_fp8 doq, dot, dhq, dht, xt, zt;
+  void *dh, *dxr;
+  float* part;
+  Fp8Launch first, second;
+};
+
+BackwardArea backward_area(const Sizes& s, Area* a) {
+  BackwardArea b;
+  const int64_t blocks = s.rows / 128;
+  b.first = fp8_plan(FP8_ROWS, s.rows, s.f, s.h, 1, 1, s.max_tiles, s.rows);
+  b.second = fp8_plan(FP8_ROWS, s.rows, s.h, s.f, 1, 1, s.max_tiles, s.rows);
+  b.doq = a->fp8(s.rows, s.h, blocks);
+  b.dot = a->fp8(s.h, s.rows, cdiv(s.h, 128));
+  b.dhq = a->fp8(s.rows, s.f, blocks);
+  b.dht = a->fp8(s.f, s.rows, cdiv(s.f, 128));
+  b.xt = a->fp8(s.h, s.rows, cdiv(s.h, 128));
+  b.zt = a->fp8(s.f, s.rows, cdiv(s.f, 128));
+  b.dh = a->take(static_cast<size_t>(s.rows * s.f) * 2);
+  b.dxr = a->take(static_cast<size_t>(s.rows * s.h) * 2);
+  const size_t part = std::max(b.first.part_bytes, b.second.part_bytes);
+  b.part = static_cast<float*>(part ? a->take(part) : nullptr);
+  return b;
+}
+
+tp_status combine(const CombineParams& P, cudaStream_t stream) {
+  const int64_t blocks = cdiv(P.T * (P.N / 8), 256);
+  if (blocks > 0x7FFFFFFFll) return TP_ERR_UNSUPPORTED_SHAPE;
+  return launch_dependent(combine_kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, P);
+}
+
+const void* const* in(void* const* a) { return const_cast<const void* const*>(a); }
+
+tp_status check_word(const void* p, bool need) {
+  if (!need) return TP_OK;
+  if (p == nullptr) return TP_ERR_INVALID_ARG;
+  return reinterpret_cast<uintptr_t>(p) % 4 == 0 ? TP_OK : TP_ERR_ALIGNMENT;
+}
+
+// Operands of `per` matrices [rows, cols] a shard.
+void add_experts(RangeList* v, const tp_fp8* a, int p, int64_t per, int64_t rows, int64_t cols) { add_fp8(v, a, p, rows, cols, per); }
+
+tp_status check_saved(const tp_experts_saved* s, bool work) {
+  if (s == nullptr) return TP_ERR_INVALID_ARG;
+  TP_TRY(check_ptr(s->plan, work));
+  TP_TRY(check_ptr(s->preact, work));
+  return check_ptr(s->out, work);
+}
+
+void add_saved(RangeList* v, const tp_experts_saved* d, const Sizes& s) {
+  v->push_back({d->plan, s.plan_bytes});
+  v->push_back({d->preact, static_cast<size_t>(s.rows * s.f) * 2});
+  v->push_back({d->out, static_cast<size_t>(s.rows * s.h) * 2});
+}
+
+}  // namespace
+
+extern "C" int64_t tp_experts_rows(int64_t E, int64_t T, int64_t k) {
+  Sizes s;
+  if (check_experts(1, E, T, k, 8, 8) != TP_OK || !sizes_of(1, E, T, k, 8, 8, true, &s)) return 0;
+  return s.rows;
+}
+
+extern "C" size_t tp_experts_plan_size(int64_t E, int64_t T, int64_t k) {
+  Sizes s;
+  if (check_experts(1, E, T, k, 8, 8) != TP_OK || !sizes_of(1, E, T, k, 8, 8, true, &s)) return 0;
+  return s.plan_bytes;
+}
+
+extern "C" size_t tp_experts_workspace_size(int p, int64_t E, int64_t T, int64_t k, int64_t h, int64_t f, int backward) {
+  Sizes s;
+  if (check_experts(p, E, T, k, h, f) != TP_OK || T == 0) return kStatusBytes;
+  size_t most = kStatusBytes;
+  for (int train = 0; train < (backward ? 2 : 1); ++train) {
+    if (!sizes_of(p, E, T, k, h, f, train != 0, &s)) return kStatusBytes;
+    Area a(nullptr);
+    forward_area(s, train != 0, &a);
+    most = std::max(most, a.at);
+    if (train) {
+      Area b(nullptr);
+      backward_area(s, &b);
+      most = std::max(most, b.at);
+    }
+  }
+  return most;
+}
+
+extern "C" tp_status tp_experts_fwd_fp8(const void* x, const void* experts, const void* weights, const tp_fp8* w1, const tp_fp8* w2, void* y,
+                                        const tp_experts_saved* saved, int p, int64_t E, int64_t T, int64_t k, int64_t h, int64_t f, void* ws,
+                                        size_t ws_bytes, cudaStream_t stream) {
+  TP_TRY(check_experts(p, E, T, k, h, f));
+  const bool work = T > 0, train = saved != nullptr;
+  TP_TRY(check_ptr(x, work));
+  TP_TRY(check_word(experts, work));
+  TP_TRY(check_word(weights, work));
+  TP_TRY(check_fp8(w1, p, work));
+  TP_TRY(check_fp8(w2, p, work));
+  TP_TRY(check_ptr(y, work));
+  if (train) TP_TRY(check_saved(saved, work));
+  Sizes s;
+  if (!sizes_of(p, E, T, k, h, f, train, &s)) return TP_ERR_UNSUPPORTED_SHAPE;
+  size_t need = kStatusBytes;
+  if (work) {
+    Area a(nullptr);
+    forward_area(s, train, &a);
+    need = a.at;
+  }
+  TP_TRY(check_ws(ws, ws_bytes, need));
+  if (!work) return TP_OK;
+  const int64_t per = E / p;
+  {
+    RangeList ins, outs;
+    ins.push_back({x, static_cast<size_t>(T * h) * 2});
+    ins.push_back({experts, static_cast<size_t>(s.S) * 4});
+    ins.push_back({weights, static_cast<size_t>(s.S) * 4});
+    add_experts(&ins, w1, p, per, f, h);
+    add_experts(&ins, w2, p, per, h, f);
+    outs.push_back({y, static_cast<size_t>(T * h) * 2});
+    if (train) add_saved(&outs, saved, s);
+    outs.push_back({ws, ws_bytes});
+    if (any_overlap(outs, ins)) return TP_ERR_INVALID_ARG;
+  }
+  DevInfo di;
+  TP_TRY(device_info(&di));
+  Area area(ws);
+  const ForwardArea A = forward_area(s, train, &area);
+  int32_t *tiles, *first, *expert, *slot, *row;
+  const Fp8Plan plan = plan_at(s, train ? static_cast<int32_t*>(saved->plan) : A.plan, &tiles, &first, &expert, &slot, &row);
+  DispatchParams D;
+  D.experts = static_cast<const int32_t*>(experts);
+  D.tiles = tiles, D.first = first, D.expert = expert, D.slot = slot, D.row = row;
+  D.S = static_cast<int32_t>(s.S);
+  D.E = static_cast<int32_t>(E);
+  D.tile_rows = static_cast<int32_t>(s.tile_rows);
+  D.max_tiles = static_cast<int32_t>(s.max_tiles);
+  TP_TRY(launch_dependent(dispatch_kernel, dim3(static_cast<unsigned>(E)), kDispatchThreads, 0, stream, D));
+  Fp8Pack pack;
+  pack.x = &x;
+  pack.q = &A.xq;
+  pack.rows = s.rows;
+  pack.cols = h;
+  pack.plan = &plan;
+  TP_TRY(fp8_pack(pack, stream));
+  uint32_t* status = static_cast<uint32_t*>(ws);
+  void* preact = train ? saved->preact : nullptr;
+  void* out = train ? saved->out : A.out;
+  Fp8Product g;
+  g.mode = FP8_ROWS;
+  g.a = &A.xq;
+  g.b = w1;
+  g.nb = p;
+  g.rows = s.rows;
+  g.cols = f;
+  g.depth = h;
+  g.plan = &plan;
+  g.per = static_cast<int>(per);
+  g.epi = TP_EPI_GELU;
+  g.z = &A.zq;
+  g.aux = preact ? &preact : nullptr;
+  TP_TRY(fp8_product(g, A.first, A.part, status, stream));
+  Fp8Product o;
+  o.mode = FP8_ROWS;
+  o.a = &A.zq;
+  o.b = w2;
+  o.nb = p;
+  o.rows = s.rows;
+  o.cols = h;
+  o.depth = f;
+  o.plan = &plan;
+  o.per = static_cast<int>(per);
+  o.out = &out;
+  o.keep_parts = !train;  // added up with the token's rows
+  TP_TRY(fp8_product(o, A.second, A.part, status, stream));
+  CombineParams C;
+  std::memset(&C, 0, sizeof(C));
+  if (A.second.splits > 1 && !train) {
+    C.part = A.part;
+    C.part_step = s.rows * h;
+    C.splits = A.second.splits;
+  } else {
+    C.rows = static_cast<const __nv_bfloat16*>(out);
+  }
+  C.row = row;
+  C.weights = static_cast<const float*>(weights);
+  C.y = static_cast<__nv_bfloat16*>(y);
+  C.T = T;
+  C.N = h;
+  C.k = static_cast<int32_t>(k);
+  return combine(C, stream);
+}
+
+extern "C" tp_status tp_experts_bwd_fp8(const void* x, const void* weights, const void* dy, const tp_fp8* w1t, const tp_fp8* w2t, void* dx,
+                                        void* dweights, void* const* dw1, void* const* dw2, const tp_experts_saved* saved, int p, int64_t E,
+                                        int64_t T, int64_t k, int64_t h, int64_t f, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  TP_TRY(check_experts(p, E, T, k, h, f));
+  const bool work = T > 0;
+  if (dx == nullptr && dweights == nullptr && dw1 == nullptr && dw2 == nullptr) return TP_ERR_INVALID_ARG;
+  const bool need_h = dx != nullptr || dw1 != nullptr;  // the gradient of the pre-activations
+  TP_TRY(check_ptr(x, work && dw1 != nullptr));
+  TP_TRY(check_word(weights, work));
+  TP_TRY(check_ptr(dy, work));
+  TP_TRY(check_fp8(w1t, p, work && dx != nullptr));
+  TP_TRY(check_fp8(w2t, p, work && need_h));
+  TP_TRY(check_ptr(dx, work && dx != nullptr));
+  if (dweights != nullptr && reinterpret_cast<uintptr_t>(dweights) % 2 != 0) return TP_ERR_ALIGNMENT;
+  TP_TRY(check_ptrs(in(dw1), p, dw1 != nullptr));
+  TP_TRY(check_ptrs(in(dw2), p, dw2 != nullptr));
+  TP_TRY(check_saved(saved, work));
+  Sizes s;
+  if (!sizes_of(p, E, T, k, h, f, true, &s)) return TP_ERR_UNSUPPORTED_SHAPE;
+  size_t need = kStatusBytes;
+  if (work) {
+    Area a(nullptr);
+    backward_area(s, &a);
+    need = a.at;
+  }
+  TP_TRY(check_ws(ws, ws_bytes, need));
+  const int64_t per = E / p;
+  const size_t dw_bytes = static_cast<size_t>(per * h * f) * 2;
+  {
+    RangeList ins, outs;
+    if (work) {
+      ins.push_back({x, x ? static_cast<size_t>(T * h) * 2 : 0});
+      ins.push_back({weights, static_cast<size_t>(s.S) * 4});
+      ins.push_back({dy, static_cast<size_t>(T * h) * 2});
+      if (dx) add_experts(&ins, w1t, p, per, h, f);
+      if (need_h) add_experts(&ins, w2t, p, per, f, h);
+      add_saved(&ins, saved, s);
+    }
+    outs.push_back({dx, dx ? static_cast<size_t>(T * h) * 2 : 0});
+    outs.push_back({dweights, dweights ? static_cast<size_t>(s.S) * 2 : 0});
+    add_ranges(&outs, in(dw1), p, dw_bytes);
+    add_ranges(&outs, in(dw2), p, dw_bytes);
+    outs.push_back({ws, ws_bytes});
+    if (any_overlap(outs, ins)) return TP_ERR_INVALID_ARG;
+  }
+  DevInfo di;
+  TP_TRY(device_info(&di));
+  if (!work) {  // no token: the weights' gradients are zero
+    for (int r = 0; r < p; ++r) {
+      if (dw1 && cudaMemsetAsync(dw1[r], 0, dw_bytes, stream) != cudaSuccess) return TP_ERR_CUDA;
+      if (dw2 && cudaMemsetAsync(dw2[r], 0, dw_bytes, stream) != cudaSuccess) return TP_ERR_CUDA;
+    }
+    return TP_OK;
+  }
+  Area area(ws);
+  const BackwardArea A = backward_area(s, &area);
+  int32_t *tiles, *first, *expert, *slot, *row;
+  const Fp8Plan plan = plan_at(s, static_cast<int32_t*>(saved->plan), &tiles, &first, &expert, &slot, &row);
+  uint32_t* status = static_cast<uint32_t*>(ws);
+  if (dweights) {
+    DotParams D;
+    D.rows = static_cast<const __nv_bfloat16*>(saved->out);
+    D.dy = static_cast<const __nv_bfloat16*>(dy);
+    D.row = row;
+    D.dweights = static_cast<__nv_bfloat16*>(dweights);
+    D.S = s.S;
+    D.N = h;
+    D.k = static_cast<int32_t>(k);
+    TP_TRY(launch_dependent(weight_grad_kernel, dim3(static_cast<unsigned>(cdiv(s.S, 8))), 256, 0, stream, D));
+  }
+  if (!need_h && dw2 == nullptr) return TP_OK;
+  // the rows' gradients, weights * dy
+  Fp8Pack pack;
+  pack.x = &dy;
+  pack.q = need_h ? &A.doq : nullptr;
+  pack.qt = dw2 ? &A.dot : nullptr;
+  pack.rows = s.rows;
+  pack.cols = h;
+  pack.plan = &plan;
+  pack.weights = static_cast<const float*>(weights);
+  TP_TRY(fp8_pack(pack, stream));
+  void *dh = A.dh, *dxr = A.dxr, *preact = saved->preact;
+  if (need_h) {
+    Fp8Product g;
+    g.mode = FP8_ROWS;
+    g.a = &A.doq;
+    g.b = w2t;
+    g.nb = p;
+    g.rows = s.rows;
+    g.cols = f;
+    g.depth = h;
+    g.plan = &plan;
+    g.per = static_cast<int>(per);
+    g.epi = TP_EPI_DGELU;
+    g.out = &dh;
+    g.aux = &preact;
+    TP_TRY(fp8_product(g, A.first, A.part, status, stream));
+    const void* src = dh;
+    pack = Fp8Pack();
+    pack.x = &src;
+    pack.q = dx ? &A.dhq : nullptr;
+    pack.qt = dw1 ? &A.dht : nullptr;
+    pack.rows = s.rows;
+    pack.cols = f;
+    pack.plan = &plan;
+    pack.gather = false;
+    TP_TRY(fp8_pack(pack, stream));
+  }
+  if (dx) {
+    Fp8Product g;
+    g.mode = FP8_ROWS;
+    g.a = &A.dhq;
+    g.b = w1t;
+    g.nb = p;
+    g.rows = s.rows;
+    g.cols = h;
+    g.depth = f;
+    g.plan = &plan;
+    g.per = static_cast<int>(per);
+    g.out = &dxr;
+    TP_TRY(fp8_product(g, A.second, A.part, status, stream));
+    CombineParams C;
+    std::memset(&C, 0, sizeof(C));
+    C.rows = static_cast<const __nv_bfloat16*>(dxr);
+    C.row = row;
+    C.y = static_cast<__nv_bfloat16*>(dx);
+    C.T = T;
+    C.N = h;
+    C.k = static_cast<int32_t>(k);
+    TP_TRY(combine(C, stream));
+  }
+  auto contract = [&](const tp_fp8* a, const tp_fp8* b, int64_t rows, int64_t cols, void* const* out) {
+    Fp8Product g;
+    g.mode = FP8_CONTRACT;
+    g.a = a;
+    g.b = b;
+    g.rows = rows;
+    g.cols = cols;
+    g.depth = s.rows;
+    g.groups = static_cast<int>(E);
+    g.plan = &plan;
+    g.per = static_cast<int>(per);
+    g.out = out;
+    return fp8_product(g, fp8_plan(FP8_CONTRACT, rows, cols, s.rows, g.groups, 1), nullptr, status, stream);
+  };
+  if (dw1) {
+    pack = Fp8Pack();
+    pack.x = &x;
+    pack.qt = &A.xt;
+    pack.rows = s.rows;
+    pack.cols = h;
+    pack.plan = &plan;
+    TP_TRY(fp8_pack(pack, stream));
+    TP_TRY(contract(&A.xt, &A.dht, h, f, dw1));
+  }
+  if (dw2) {
+    const void* src = preact;
+    pack = Fp8Pack();
+    pack.x = &src;
+    pack.qt = &A.zt;
+    pack.rows = s.rows;
+    pack.cols = f;
+    pack.gelu = true;
+    pack.plan = &plan;
+    pack.gather = false;
+    TP_TRY(fp8_pack(pack, stream));
+    TP_TRY(contract(&A.zt, &A.dot, f, h, dw2));
+  }
+  return TP_OK;
+}

@@ -29,7 +29,10 @@ __global__ void __launch_bounds__(kJoinThreads) fp8_join_kernel(const __grid_con
   const int64_t row = unit / blocks;
   const uint32_t b = static_cast<uint32_t>(unit % blocks), g = blockIdx.y;
   if (row >= P.rows) return;
-  if (P.mode == FP8_ROWS && (row >= static_cast<int64_t>(__ldcg(P.plan_tiles)) * P.tile_rows || __ldcg(P.plan_slot + row) < 0)) return;
+  if (P.mode == FP8_ROWS) {  // whole tiles of 128 rows are contracted over in a backward pass: all their rows are written
+    if (row >= static_cast<int64_t>(__ldcg(P.plan_tiles)) * P.tile_rows) return;
+    if (P.tile_rows < 128 && __ldcg(P.plan_slot + row) < 0) return;
+  }
   const int32_t c = static_cast<int32_t>(b * 128 + lane * 4);
   const bool in = c < P.cols;
   float v[4] = {};
@@ -161,6 +164,8 @@ tp_status fp8_product(const Fp8Product& d, const Fp8Launch& l, float* part, uint
     P.plan_expert = d.plan->expert;
     P.plan_first = d.plan->first;
     P.plan_slot = d.plan->slot;
+    P.max_tiles = static_cast<int32_t>(d.plan->max_tiles);
+    P.experts = d.plan->E;
     P.kb_tile = static_cast<int32_t>(d.plan->tile_rows / 128);
   }
   P.epi = d.epi;

@@ -56,6 +56,7 @@ struct Fp8GemmParams {
   const int32_t* plan_expert;   // FP8_ROWS: expert of a row tile
   const int32_t* plan_first;    // FP8_CONTRACT: first row tile of an expert, E + 1
   const int32_t* plan_slot;     // FP8_ROWS: token and choice of a row, or -1
+  int32_t max_tiles, experts;   // bounds of what the plan may say
   int32_t kb_tile;              // FP8_CONTRACT: k-blocks of a row tile
   int32_t epi;                  // tp_epilogue
   __nv_bfloat16* out[8];        // bf16 results, or null
@@ -102,7 +103,7 @@ struct Fp8Unit {
 };
 
 __device__ __forceinline__ int32_t fp8_units(const Fp8GemmParams& P) {
-  if (P.mode == FP8_ROWS) return __ldcg(P.plan_tiles) * P.n_tiles * P.splits;
+  if (P.mode == FP8_ROWS) return min(__ldcg(P.plan_tiles), P.max_tiles) * P.n_tiles * P.splits;
   return P.groups * P.m_tiles * P.n_tiles * P.splits;
 }
 
@@ -119,7 +120,7 @@ __device__ __forceinline__ Fp8Unit fp8_unit(const Fp8GemmParams& P, int32_t t) {
     // an expert's weights are read by its row tiles one after the other
     u.mt = v / P.n_tiles;
     u.nt = v % P.n_tiles;
-    const int32_t e = __ldcg(P.plan_expert + u.mt), local = e % P.per;
+    const int32_t e = min(max(__ldcg(P.plan_expert + u.mt), 0), P.experts - 1), local = e % P.per;
     u.g = 0;
     u.bi = e / P.per;
     u.a_row = u.mt * P.tile_rows * CTAS;
@@ -142,8 +143,8 @@ __device__ __forceinline__ Fp8Unit fp8_unit(const Fp8GemmParams& P, int32_t t) {
   u.b_row = u.nt * Fp8Cfg<CTAS>::BN;
   u.eb = u.nt * CTAS;
   if (P.mode == FP8_CONTRACT) {
-    u.q0 = __ldcg(P.plan_first + u.g) * P.kb_tile;
-    u.q1 = __ldcg(P.plan_first + u.g + 1) * P.kb_tile;
+    u.q0 = min(max(__ldcg(P.plan_first + u.g), 0), P.max_tiles) * P.kb_tile;
+    u.q1 = min(__ldcg(P.plan_first + u.g + 1), P.max_tiles) * P.kb_tile;
     u.bi = u.g / P.per;  // of the outputs
     u.out_off = static_cast<int64_t>(u.g % P.per) * P.rows * P.cols;
   }

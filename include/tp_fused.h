@@ -494,6 +494,50 @@ tp_status tp_route_bwd(const void* logits, const void* experts, const void* dwei
                        const tp_route_desc* d, int64_t T, int64_t E, int64_t k, tp_dtype dtype,
                        cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Routed experts on 8-bit operands.
+ *   y[t] = sum_j weights[t, j] . GeLU(x[t] . W1_e) . W2_e,  e = experts[t, j]
+ * The p shards hold E/p experts each, in order.  A slot (t, j) with a number
+ * outside 0..E-1 has no part in it; the same expert may come twice.
+ *   x, y: bf16 [T, h]; experts: int32 [T, k]; weights: fp32 [T, k];
+ *   w1[r]: E/p operands [f, h], the packed transposes of W1_e [h, f];
+ *   w2[r]: E/p operands [h, f], the packed transposes of W2_e [f, h].
+ * x is packed for the call, the activations from the fp32 values; an
+ * expert's output is rounded to bf16 (unless few tokens let it stay fp32)
+ * and added up in fp32 in the order of j.
+ * E <= TP_ROUTE_MAX_EXPERTS, E % p == 0, k <= 32, h and f multiples of 8.
+ *
+ * saved: NULL, or what the backward call reads: the slots of each expert as
+ * rows in tiles of 128 (plan, tp_experts_plan_size bytes), the
+ * pre-activations (preact, bf16 [tp_experts_rows, f]) and the experts'
+ * outputs (out, bf16 [tp_experts_rows, h]).  A call runs the same products
+ * with and without it, on other tiles.                                      */
+typedef struct {
+  void *plan, *preact, *out;
+} tp_experts_saved;
+int64_t tp_experts_rows(int64_t E, int64_t T, int64_t k);
+size_t tp_experts_plan_size(int64_t E, int64_t T, int64_t k);
+/* Bytes of workspace of the forward call, with `backward` of both calls. */
+size_t tp_experts_workspace_size(int p, int64_t E, int64_t T, int64_t k, int64_t h, int64_t f, int backward);
+tp_status tp_experts_fwd_fp8(const void* x, const void* experts, const void* weights, const tp_fp8* w1,
+                             const tp_fp8* w2, void* y, const tp_experts_saved* saved, int p, int64_t E, int64_t T,
+                             int64_t k, int64_t h, int64_t f, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Gradients.  For the rows r = (t, j) of each expert e:
+ *   dO_r = weights[t, j] dy[t];  dH_r = (dO_r . W2_e^T) * GeLU'(H_r), rounded
+ *   to bf16;  dx[t] = sum_j dH_r . W1_e^T;  dweights[t, j] = dy[t] . out_r
+ *   dW1_e = sum_r x[t]^T . dH_r;  dW2_e = sum_r GeLU(H_r)^T . dO_r
+ * every product on operands of its factors, blocks of 128 rows of an expert
+ * where they are contracted over.
+ *   w1t[r]: E/p operands [h, f] of W1_e; w2t[r]: E/p operands [f, h] of W2_e;
+ *   dx: bf16 [T, h]; dweights: bf16 [T, k]; dw1[r]: bf16 [E/p, h, f]; dw2[r]:
+ *   bf16 [E/p, f, h], zero for an expert without rows.  Each may be NULL, not
+ *   all; x is read for dw1, w1t for dx, w2t for dx and dw1.                  */
+tp_status tp_experts_bwd_fp8(const void* x, const void* weights, const void* dy, const tp_fp8* w1t, const tp_fp8* w2t,
+                             void* dx, void* dweights, void* const* dw1, void* const* dw2,
+                             const tp_experts_saved* saved, int p, int64_t E, int64_t T, int64_t k, int64_t h,
+                             int64_t f, void* ws, size_t ws_bytes, cudaStream_t stream);
+
 /* Unfused baseline of the row-parallel MatMul+AllReduce, for measurement
  * and for the output-error comparison against it.
  * [M027 §04: time the MatMul and the collective separately, compare the
