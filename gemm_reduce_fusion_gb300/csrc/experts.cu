@@ -21,7 +21,6 @@
 #include <cstring>
 
 #include "fp8.h"
-#include "fp8_gemm.cuh"
 #include "vec_util.cuh"
 
 using namespace tpf;
@@ -123,9 +122,7 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const __grid
 
 struct CombineParams {
   const __nv_bfloat16* rows;  // [R, N], or null:
-  const float* part;          // fp32 parts of them [splits][R, N]
-  int64_t part_step;
-  int32_t splits;
+  const float* rows32;        // the same in fp32
   const int32_t* row;         // [T, k]
   const float* weights;       // [T, k] or null (ones)
   __nv_bfloat16* y;           // [T, N]
@@ -141,25 +138,44 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Co
   if (t >= P.T) return;
   const int64_t c = (unit - t * per_row) * 8;
   float sum[8] = {};
-  for (int32_t j = 0; j < P.k; ++j) {
-    const int32_t r = P.row[t * P.k + j];
-    if (r < 0) continue;
-    const float w = P.weights ? P.weights[t * P.k + j] : 1.f;
-    float v[8] = {};
+  for (int32_t j0 = 0; j0 < P.k; j0 += 8) {  // eight rows on their way at a time
+    int32_t r[8];
+    float w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const bool in = j0 + j < P.k;
+      r[j] = in ? P.row[t * P.k + j0 + j] : -1;
+      w[j] = in && P.weights ? P.weights[t * P.k + j0 + j] : 1.f;
+    }
     if (P.rows) {
-      unpack8(*reinterpret_cast<const uint4*>(P.rows + r * P.N + c), v);
+      uint4 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[j] = r[j] >= 0 ? __ldcs(reinterpret_cast<const uint4*>(P.rows + r[j] * P.N + c)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (r[j] < 0) continue;
+        float f[8];
+        unpack8(v[j], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] = fmaf(w[j], f[i], sum[i]);
+      }
     } else {
-      const float* from = P.part + r * P.N + c;
-#pragma unroll 2
-      for (int32_t s = 0; s < P.splits; ++s) {
-        const float4 a = __ldcg(reinterpret_cast<const float4*>(from + s * P.part_step)),
-                     b = __ldcg(reinterpret_cast<const float4*>(from + s * P.part_step + 4));
-        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-        v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+float4 v[8][2];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float4* from = reinterpret_cast<const float4*>(P.rows32 + r[j] * P.N + c);
+        v[j][0] = r[j] >= 0 ? __ldcg(from) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[j][1] = r[j] >= 0 ? __ldcg(from + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (r[j] < 0) continue;
+        const float f[8] = {v[j][0].x, v[j][0].y, v[j][0].z, v[j][0].w, v[j][1].x, v[j][1].y, v[j][1].z, v[j][1].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] = fmaf(w[j], f[i], sum[i]);
       }
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum[i] = fmaf(w, v[i], sum[i]);
   }
   *reinterpret_cast<uint4*>(P.y + t * P.N + c) = pack8(sum);
 }
@@ -236,6 +252,15 @@ tp_status check_experts(int p, int64_t E, int64_t T, int64_t k, int64_t h, int64
   return TP_OK;
 }
 
+Fp8Plan bounds_of(const Sizes& s) {
+  Fp8Plan plan = {};
+  plan.max_tiles = s.max_tiles;
+  plan.tile_rows = s.tile_rows;
+  plan.E = static_cast<int>(s.E);
+  plan.k = static_cast<int>(s.k);
+  return plan;
+}
+
 // The plan's arrays in its memory.
 Fp8Plan plan_at(const Sizes& s, int32_t* at, int32_t** tiles, int32_t** first, int32_t** expert, int32_t** slot, int32_t** row) {
   *tiles = at;
@@ -243,15 +268,11 @@ Fp8Plan plan_at(const Sizes& s, int32_t* at, int32_t** tiles, int32_t** first, i
   *expert = *first + s.E + 1;
   *slot = *expert + s.max_tiles;
   *row = *slot + s.rows;
-  Fp8Plan plan;
+  Fp8Plan plan = bounds_of(s);
   plan.tiles = *tiles;
   plan.first = *first;
   plan.expert = *expert;
   plan.slot = *slot;
-  plan.max_tiles = s.max_tiles;
-  plan.tile_rows = s.tile_rows;
-  plan.E = static_cast<int>(s.E);
-  plan.k = static_cast<int>(s.k);
   return plan;
 }
 
@@ -276,37 +297,41 @@ struct Area {
 struct ForwardArea {
   int32_t* plan;
   tp_fp8 xq, zq;
-  void* out;
-  float* part;
+  void* out;     // the experts' outputs, bf16 or
+  float* out32;  // fp32
+  void* part;
   Fp8Launch first, second;
 };
 
 ForwardArea forward_area(const Sizes& s, bool train, Area* a) {
   ForwardArea f;
   const int64_t blocks = s.max_tiles * cdiv(s.tile_rows, 128);
-  f.first = fp8_plan(FP8_ROWS, s.rows, s.f, s.h, 1, 1, s.max_tiles, s.rows);
-  f.second = fp8_plan(FP8_ROWS, s.rows, s.h, s.f, 1, 1, s.max_tiles, s.rows);
+  const Fp8Plan plan = bounds_of(s);
+  f.first = fp8_plan(FP8_ROWS, s.rows, s.f, s.h, 1, 1, &plan);
+  f.second = fp8_plan(FP8_ROWS, s.rows, s.h, s.f, 1, 1, &plan);
   f.plan = static_cast<int32_t*>(train ? nullptr : a->take(s.plan_bytes));
   f.xq = a->fp8(s.rows, s.h, blocks);
   f.zq = a->fp8(s.rows, s.f, blocks);
-  f.out = train || f.second.splits > 1 ? nullptr : a->take(static_cast<size_t>(s.rows * s.h) * 2);
+  const bool fp32 = s.tile_rows < 128;  // few rows: their bytes do not matter
+  f.out = train || fp32 ? nullptr : a->take(static_cast<size_t>(s.rows * s.h) * 2);
+  f.out32 = static_cast<float*>(fp32 ? a->take(static_cast<size_t>(s.rows * s.h) * 4) : nullptr);
   const size_t part = std::max(f.first.part_bytes, f.second.part_bytes);
-  f.part = static_cast<float*>(part ? a->take(part) : nullptr);
+  f.part = part ? a->take(part) : nullptr;
   return f;
 }
 
 struct BackwardArea {
   tp_fp8 doq, dot, dhq, dht, xt, zt;
-  void *dh, *dxr;
-  float* part;
+  void *dh, *dxr, *part;
   Fp8Launch first, second;
 };
 
 BackwardArea backward_area(const Sizes& s, Area* a) {
   BackwardArea b;
   const int64_t blocks = s.rows / 128;
-  b.first = fp8_plan(FP8_ROWS, s.rows, s.f, s.h, 1, 1, s.max_tiles, s.rows);
-  b.second = fp8_plan(FP8_ROWS, s.rows, s.h, s.f, 1, 1, s.max_tiles, s.rows);
+  const Fp8Plan plan = bounds_of(s);
+  b.first = fp8_plan(FP8_ROWS, s.rows, s.f, s.h, 1, 1, &plan);
+  b.second = fp8_plan(FP8_ROWS, s.rows, s.h, s.f, 1, 1, &plan);
   b.doq = a->fp8(s.rows, s.h, blocks);
   b.dot = a->fp8(s.h, s.rows, cdiv(s.h, 128));
   b.dhq = a->fp8(s.rows, s.f, blocks);
@@ -316,7 +341,7 @@ BackwardArea backward_area(const Sizes& s, Area* a) {
   b.dh = a->take(static_cast<size_t>(s.rows * s.f) * 2);
   b.dxr = a->take(static_cast<size_t>(s.rows * s.h) * 2);
   const size_t part = std::max(b.first.part_bytes, b.second.part_bytes);
-  b.part = static_cast<float*>(part ? a->take(part) : nullptr);
+  b.part = part ? a->take(part) : nullptr;
   return b;
 }
 
@@ -466,17 +491,12 @@ extern "C" tp_status tp_experts_fwd_fp8(const void* x, const void* experts, cons
   o.plan = &plan;
   o.per = static_cast<int>(per);
   o.out = &out;
-  o.keep_parts = !train;  // added up with the token's rows
+  o.out32 = A.out32;
   TP_TRY(fp8_product(o, A.second, A.part, status, stream));
   CombineParams C;
   std::memset(&C, 0, sizeof(C));
-  if (A.second.splits > 1 && !train) {
-    C.part = A.part;
-    C.part_step = s.rows * h;
-    C.splits = A.second.splits;
-  } else {
-    C.rows = static_cast<const __nv_bfloat16*>(out);
-  }
+  C.rows = A.out32 ? nullptr : static_cast<const __nv_bfloat16*>(out);
+  C.rows32 = A.out32;
   C.row = row;
   C.weights = static_cast<const float*>(weights);
   C.y = static_cast<__nv_bfloat16*>(y);

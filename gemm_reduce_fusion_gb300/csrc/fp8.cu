@@ -1,9 +1,13 @@
 // The 8-bit sharded Linear: plans, launches and the C ABI of the products.
 //
 // A product runs on 256 x 256 tiles of CTA pairs or on 128 x 128 tiles of
-// single CTAs (fp8_gemm.cuh).  With fewer tiles than SMs the contraction is
-// split and the parts, kept in the workspace in fp32, are joined in their
-// order by fp8_join_kernel, which then has the epilogue.
+// single CTAs (fp8_gemm.cuh), these either whole or as runs: all tiles'
+// k-blocks laid end to end and cut into as many equal runs as there are SMs,
+// with the parts of a tile that several runs share kept in the workspace in
+// fp32 and added up, in the order of the runs, by a second kernel.  (The CTA
+// that finishes a tile last can do so itself, but waits a microsecond for
+// memory some eight times on the way: the row layer of 77 tokens took 16 us
+// so, 11 with the second kernel.)
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -18,67 +22,7 @@ using namespace tpf;
 namespace {
 
 constexpr int kSMs = 152;
-constexpr int kJoinThreads = 256;
-
-// A warp for 128 columns of an output's row: the parts' sum and the epilogue.
-__global__ void __launch_bounds__(kJoinThreads) fp8_join_kernel(const __grid_constant__ Fp8GemmParams P) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const uint32_t lane = threadIdx.x & 31, blocks = static_cast<uint32_t>((P.cols + 127) / 128);
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
-  const int64_t row = unit / blocks;
-  const uint32_t b = static_cast<uint32_t>(unit % blocks), g = blockIdx.y;
-  if (row >= P.rows) return;
-  if (P.mode == FP8_ROWS) {  // whole tiles of 128 rows are contracted over in a backward pass: all their rows are written
-    if (row >= static_cast<int64_t>(__ldcg(P.plan_tiles)) * P.tile_rows) return;
-    if (P.tile_rows < 128 && __ldcg(P.plan_slot + row) < 0) return;
-  }
-  const int32_t c = static_cast<int32_t>(b * 128 + lane * 4);
-  const bool in = c < P.cols;
-  float v[4] = {};
-  if (in) {
-    const int64_t step = static_cast<int64_t>(P.groups) * P.part_rows * P.cols;
-    const float* from = P.part + (static_cast<int64_t>(g) * P.part_rows + row) * P.cols + c;
-#pragma unroll 4
-    for (int32_t s = 0; s < P.splits; ++s) {
-      const float4 f = __ldcg(reinterpret_cast<const float4*>(from + s * step));
-      v[0] += f.x;
-      v[1] += f.y;
-      v[2] += f.z;
-      v[3] += f.w;
-    }
-    const int64_t at = row * P.cols + c;
-    if (P.bias[g]) {
-      const uint2 w = *reinterpret_cast<const uint2*>(P.bias[g] + c);
-      v[0] += bf_lo(w.x);
-      v[1] += bf_hi(w.x);
-      v[2] += bf_lo(w.y);
-      v[3] += bf_hi(w.y);
-    }
-    if (P.epi == TP_EPI_DGELU) {
-      const uint2 h = *reinterpret_cast<const uint2*>(P.aux[g] + at);
-      times_gelu_prime2(v[0], v[1], bf_lo(h.x), bf_hi(h.x));
-      times_gelu_prime2(v[2], v[3], bf_lo(h.y), bf_hi(h.y));
-    } else if (P.epi == TP_EPI_GELU) {
-      if (P.aux[g]) *reinterpret_cast<uint2*>(P.aux[g] + at) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-      gelu2(v[0], v[1]);
-      gelu2(v[2], v[3]);
-    }
-    if (P.out[g]) *reinterpret_cast<uint2*>(P.out[g] + at) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-  }
-  if (P.zq[g]) {
-    float top = fmaxf(fmaxf(finite_abs(v[0]), finite_abs(v[1])), fmaxf(finite_abs(v[2]), finite_abs(v[3])));
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    const uint32_t e = fp8_exponent(top);
-    *reinterpret_cast<uint32_t*>(P.zq[g] + row * P.zq_ld + c) = fp8_pack4(v[0], v[1], v[2], v[3], fp8_inverse(e));
-    if (lane == 0) {
-      const int64_t block = row / P.tile_rows;
-      P.ze[g][block * P.ze_ld + (b >> 2) * 512 + fp8_e_at(static_cast<uint32_t>(row - block * P.tile_rows), b & 3)] = static_cast<uint8_t>(e);
-    }
-  }
-}
-
+constexpr int64_t kMostParts = 6;  // runs that share a tile (one more at its ends)
 // The values [rows, cols] of an operand, boxes of 128 columns x `box` rows.
 bool encode_q(CUtensorMap* m, const void* q, int64_t rows, int64_t cols, int64_t box) {
   auto fn = encode_fn();
@@ -117,25 +61,30 @@ tp_status launch_gemm(const Fp8GemmParams& P, int64_t units, cudaStream_t stream
 
 namespace tpf {
 
-Fp8Launch fp8_plan(int32_t mode, int64_t rows, int64_t cols, int64_t depth, int groups, int segs, int64_t row_tiles, int64_t plan_rows) {
+Fp8Launch fp8_plan(int32_t mode, int64_t rows, int64_t cols, int64_t depth, int groups, int segs, const Fp8Plan* plan) {
   Fp8Launch l;
   l.ctas = 1;
-  l.splits = 1;
+  l.runs = 0;
+  l.min_run = 1;
+  l.part_bytes = 0;
+  if (rows <= 0 || cols <= 0) return l;
   const int64_t kb = segs * cdiv(depth, 128);
   const int64_t pairs = groups * cdiv(rows, 256) * cdiv(cols, 256);
   if (mode != FP8_ROWS && rows > 128 && cols > 128 && pairs >= kSMs / 4) l.ctas = 2;
-  if (l.ctas == 1 && mode != FP8_CONTRACT) {
-    const int64_t tiles = mode == FP8_ROWS ? row_tiles * cdiv(cols, 128) : groups * cdiv(rows, 128) * cdiv(cols, 128);
-    if (tiles > 0 && tiles < kSMs) l.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({16, 2 * kSMs / tiles, kb / 4})));
-  }
-  l.kb_split = std::max<int64_t>(1, cdiv(kb, l.splits));
-  l.splits = static_cast<int>(std::max<int64_t>(1, cdiv(kb, l.kb_split)));
-  l.part_rows = mode == FP8_ROWS ? plan_rows : rows;
-  l.part_bytes = l.splits > 1 ? static_cast<size_t>(l.splits) * groups * l.part_rows * cols * sizeof(float) : 0;
+  if (l.ctas == 2 || mode == FP8_CONTRACT || kb == 0) return l;
+  // Runs keep every SM busy to the end, for the join kernel and the parts'
+  // bytes (64 KiB at 128 rows, written and read, at each end of a run).
+  // Measured: ...
+  const int64_t tile_rows = mode == FP8_ROWS ? plan->tile_rows : std::min<int64_t>(128, cdiv(rows, 16) * 16);
+  const int64_t tiles = (mode == FP8_ROWS ? plan->max_tiles : groups * cdiv(rows, 128)) * cdiv(cols, 128);
+  if (tiles >= 4 * kSMs || tiles % kSMs == 0) return l;
+  l.min_run = std::max<int64_t>(std::min<int64_t>(4, kb), cdiv(kb, kMostParts));
+  l.runs = static_cast<int>(std::min<int64_t>(kSMs, cdiv(tiles * kb, l.min_run)));
+  l.part_bytes = static_cast<size_t>(2 * l.runs * tile_rows) * 128 * sizeof(float);
   return l;
 }
 
-tp_status fp8_product(const Fp8Product& d, const Fp8Launch& l, float* part, uint32_t* status, cudaStream_t stream) {
+tp_status fp8_product(const Fp8Product& d, const Fp8Launch& l, void* part, uint32_t* status, cudaStream_t stream) {
   if (d.rows <= 0 || d.cols <= 0) return TP_OK;
   Fp8GemmParams P;
   std::memset(&P, 0, sizeof(P));
@@ -152,8 +101,9 @@ tp_status fp8_product(const Fp8Product& d, const Fp8Launch& l, float* part, uint
   P.m_tiles = static_cast<int32_t>(cdiv(d.rows, 128 * l.ctas));
   P.n_tiles = static_cast<int32_t>(cdiv(d.cols, 128 * l.ctas));
   P.kb = static_cast<int32_t>(cdiv(d.depth, 128));
-  P.splits = l.splits;
-  P.kb_split = static_cast<int32_t>(l.kb_split);
+  P.stream = l.runs > 0;
+  P.runs = l.runs;
+  P.min_run = static_cast<int32_t>(l.min_run);
   P.rows = static_cast<int32_t>(d.rows);
   P.cols = static_cast<int32_t>(d.cols);
   P.band = 8;
@@ -179,8 +129,8 @@ tp_status fp8_product(const Fp8Product& d, const Fp8Launch& l, float* part, uint
   }
   P.zq_ld = fp8_pitch(d.cols);
   P.ze_ld = cdiv(d.cols, 512) * 512;
-  P.part = part;
-  P.part_rows = l.part_rows;
+  P.out32 = d.out32;
+  P.part = static_cast<float*>(part);
   P.status = status;
   P.timeout_ns = device_timeout_ns();
   P.drop = static_cast<int32_t>(debug_drop());
@@ -194,18 +144,13 @@ tp_status fp8_product(const Fp8Product& d, const Fp8Launch& l, float* part, uint
     for (int i = 0; i < d.nb; ++i)
       if (!encode_q(&P.b[i], d.b[i].q, b_rows, d.depth, 128) || !encode_e(&P.eb[i], d.b[i].e, b_blocks, d.depth, l.ctas)) return TP_ERR_CUDA;
   }
-  const int64_t row_tiles = by_rows ? d.plan->max_tiles : P.m_tiles;
-  const int64_t units = d.groups * row_tiles * P.n_tiles * P.splits;
-  if (units > 0x7FFFFFFFll) return TP_ERR_UNSUPPORTED_SHAPE;
-  const bool quant = d.z != nullptr && l.splits == 1;
-  if (l.ctas == 2) {
-    TP_TRY(quant ? (launch_gemm<2, true>(P, units, stream)) : (launch_gemm<2, false>(P, units, stream)));
-  } else {
-    TP_TRY(quant ? (launch_gemm<1, true>(P, units, stream)) : (launch_gemm<1, false>(P, units, stream)));
-  }
-  if (l.splits == 1 || d.keep_parts) return TP_OK;
-  const int64_t warps = d.rows * cdiv(d.cols, 128);
-  return launch_dependent(fp8_join_kernel, dim3(static_cast<unsigned>(cdiv(warps, kJoinThreads / 32)), static_cast<unsigned>(d.groups)),
+  const int64_t tiles = d.groups * (by_rows ? d.plan->max_tiles : P.m_tiles) * P.n_tiles;
+  if (tiles > 0x7FFFFFFFll) return TP_ERR_UNSUPPORTED_SHAPE;
+  const int64_t ctas = l.runs > 0 ? l.runs : tiles;
+  if (l.ctas == 2) return d.z ? (launch_gemm<2, true>(P, ctas, stream)) : (launch_gemm<2, false>(P, ctas, stream));
+  TP_TRY(d.z ? (launch_gemm<1, true>(P, ctas, stream)) : (launch_gemm<1, false>(P, ctas, stream)));
+  if (l.runs < 2) return TP_OK;
+  return launch_dependent(fp8_join_kernel, dim3(static_cast<unsigned>(l.runs - 1), static_cast<unsigned>(cdiv(P.tile_rows, kJoinThreads / 32))),
                           kJoinThreads, 0, stream, P);
 }
 
@@ -230,7 +175,7 @@ namespace {
 
 const void* const* in(void* const* a) { return const_cast<const void* const*>(a); }
 
-float* parts_of(void* ws) { return reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kDataOffset); }
+void* parts_of(void* ws) { return static_cast<uint8_t*>(ws) + kDataOffset; }
 
 // A bias is read 8 (or 4) columns at a time.
 tp_status check_bias(const void* const* bias, int n, bool work) {

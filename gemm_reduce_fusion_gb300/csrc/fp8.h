@@ -31,6 +31,12 @@ struct Fp8Plan {
 
 // ------------------------------------------------------------------ products
 
+enum Fp8Mode : int32_t {
+  FP8_DENSE = 0,     // groups x segments of whole matrices
+  FP8_ROWS = 1,      // row tiles of the experts: tile -> expert by the plan
+  FP8_CONTRACT = 2,  // a product for each expert, contracted over its rows
+};
+
 // D = A B^T over segments of the contraction (see fp8_gemm.cuh).
 struct Fp8Product {
   int32_t mode = 0;              // Fp8Mode
@@ -44,20 +50,20 @@ struct Fp8Product {
   tp_epilogue epi = TP_EPI_NONE;
   void* const* out = nullptr;
   const tp_fp8* z = nullptr;     // or 8-bit outputs
-  int64_t z_tile_rows = 128;     // rows of an output that share 128 rows of exponents
   void* const* aux = nullptr;    // H, out (GELU) or in (DGELU)
   const void* const* bias = nullptr;
-  bool keep_parts = false;       // FP8_ROWS: the sums of a split contraction are joined by the caller
+  float* out32 = nullptr;        // FP8_ROWS: or fp32 outputs
 };
 
 struct Fp8Launch {
-  int ctas, splits;
-  int64_t kb_split, part_rows;
-  size_t part_bytes;
+  int ctas;
+  int runs;           // runs of k-blocks, 0: whole tiles
+  int64_t min_run;    // k-blocks of the shortest
+  size_t part_bytes;  // of the parts of shared tiles
 };
-// How a product is run; max_tiles: FP8_ROWS, the tiles that a call is likely to have.
-Fp8Launch fp8_plan(int32_t mode, int64_t rows, int64_t cols, int64_t depth, int groups, int segs, int64_t row_tiles = 0, int64_t plan_rows = 0);
-tp_status fp8_product(const Fp8Product& d, const Fp8Launch& l, float* part, uint32_t* status, cudaStream_t stream);
+// How a product is run.
+Fp8Launch fp8_plan(int32_t mode, int64_t rows, int64_t cols, int64_t depth, int groups, int segs, const Fp8Plan* plan = nullptr);
+tp_status fp8_product(const Fp8Product& d, const Fp8Launch& l, void* part, uint32_t* status, cudaStream_t stream);
 
 // ------------------------------------------------------------------ packing
 

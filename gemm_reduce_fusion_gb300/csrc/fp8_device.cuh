@@ -27,6 +27,14 @@ __device__ __forceinline__ uint32_t fp8_exponent(float top) {
 // 2^(127 - e), e <= 248: exact, so that a scaled value is rounded once.
 __device__ __forceinline__ float fp8_inverse(uint32_t e) { return __uint_as_float((254u - e) << 23); }
 
+// Four finite values in e4m3, rounded to nearest even.
+__device__ __forceinline__ uint32_t fp8_pack4_finite(float a, float b, float c, float d, float inv) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b * inv), "f"(a * inv));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d * inv), "f"(c * inv));
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
 // Four values in e4m3, rounded to nearest even; an infinity or NaN is NaN.
 __device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d, float inv) {
   const float inf = __uint_as_float(0x7F800000u), nan = __uint_as_float(0x7FC00000u);

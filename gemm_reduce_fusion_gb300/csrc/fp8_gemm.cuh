@@ -28,17 +28,12 @@
 #include <cstdint>
 
 #include "device_wait.cuh"
+#include "fp8.h"
 #include "fp8_device.cuh"
 #include "gelu.cuh"
 #include "vec_util.cuh"
 
 namespace tpf {
-
-enum Fp8Mode : int32_t {
-  FP8_DENSE = 0,     // groups x segments of whole matrices
-  FP8_ROWS = 1,      // row tiles of the experts: tile -> expert by the plan
-  FP8_CONTRACT = 2,  // a product for each expert, contracted over its rows
-};
 
 struct Fp8GemmParams {
   CUtensorMap a[8], b[8], ea[8], eb[8];
@@ -47,7 +42,8 @@ struct Fp8GemmParams {
   int32_t a_by_g, a_by_s, b_by_g, b_by_s;
   int32_t m_tiles, n_tiles;     // of a group (FP8_ROWS: m_tiles from the plan)
   int32_t kb;                   // k-blocks of a segment
-  int32_t splits, kb_split;     // parts of the contraction, k-blocks of a part
+  int32_t stream;               // runs of k-blocks instead of whole tiles (CTAS = 1)
+  int32_t min_run;              // the shortest of them
   int32_t rows, cols;           // of an output (FP8_ROWS: rows not used)
   int32_t tile_rows;            // rows of an A tile that are loaded (CTAS = 1: 16 .. 128)
   int32_t band;                 // m-tiles that go together through the n-tiles
@@ -65,8 +61,9 @@ struct Fp8GemmParams {
   uint8_t* ze[8];
   const __nv_bfloat16* bias[8];
   int64_t zq_ld, ze_ld;         // bytes of a row of zq, of 128 rows of ze
-  float* part;                  // splits > 1: fp32 sums [split][group][row][cols]
-  int64_t part_rows;            // rows of a group's sums
+  float* out32;                 // FP8_ROWS: fp32 results instead, or null
+  float* part;                  // fp32 sums of the tiles that runs share
+  int32_t runs;
   uint32_t* status;
   uint64_t timeout_ns;
   int32_t drop;                 // test hook (TP_DEBUG_DROP_LOAD)
@@ -94,7 +91,8 @@ struct Fp8Cfg {
 };
 
 struct Fp8Unit {
-  int32_t g, mt, nt, split;
+  int32_t t;          // tile
+  int32_t g, mt, nt;
   int32_t q0, q1;     // k-blocks
   int32_t a_row, ea;  // first row of A's tile (CTA 0), its block of exponents
   int32_t b_row, eb;
@@ -102,20 +100,19 @@ struct Fp8Unit {
   int64_t out_off;    // FP8_CONTRACT: the expert's place in its shard
 };
 
-__device__ __forceinline__ int32_t fp8_units(const Fp8GemmParams& P) {
-  if (P.mode == FP8_ROWS) return min(__ldcg(P.plan_tiles), P.max_tiles) * P.n_tiles * P.splits;
-  return P.groups * P.m_tiles * P.n_tiles * P.splits;
+__device__ __forceinline__ int32_t fp8_tiles(const Fp8GemmParams& P) {
+  if (P.mode == FP8_ROWS) return min(__ldcg(P.plan_tiles), P.max_tiles) * P.n_tiles;
+  return P.groups * P.m_tiles * P.n_tiles;
 }
 
 template <int CTAS>
 __device__ __forceinline__ Fp8Unit fp8_unit(const Fp8GemmParams& P, int32_t t) {
   Fp8Unit u;
-  u.split = t % P.splits;
-  int32_t v = t / P.splits;
+  u.t = t;
+  int32_t v = t;
   u.out_off = 0;
-  const int32_t total = P.segs * P.kb;
-  u.q0 = u.split * P.kb_split;
-  u.q1 = min(u.q0 + P.kb_split, total);
+  u.q0 = 0;
+  u.q1 = P.segs * P.kb;
   if (P.mode == FP8_ROWS) {
     // an expert's weights are read by its row tiles one after the other
     u.mt = v / P.n_tiles;
@@ -150,6 +147,45 @@ __device__ __forceinline__ Fp8Unit fp8_unit(const Fp8GemmParams& P, int32_t t) {
   }
   return u;
 }
+
+// What a CTA (or pair) goes through: whole tiles, `stride` apart, or with
+// P.stream its run of all tiles' k-blocks laid end to end.
+template <int CTAS>
+struct Fp8Walk {
+  int32_t at, end, stride;  // tiles; or k-blocks, stride 0
+  int32_t run, depth;       // k-blocks of a run, of a tile
+
+  __device__ __forceinline__ Fp8Walk(const Fp8GemmParams& P) {
+    const int32_t me = static_cast<int32_t>(blockIdx.x) / CTAS, all = static_cast<int32_t>(gridDim.x) / CTAS, tiles = fp8_tiles(P);
+    depth = P.segs * P.kb;
+    if (CTAS == 1 && P.stream) {
+      const int32_t work = tiles * depth;
+      run = max((work + P.runs - 1) / P.runs, P.min_run);
+      at = min(me * run, work);
+      end = min(at + run, work);
+      stride = 0;
+    } else {
+      run = 0;
+      at = me;
+      end = tiles;
+      stride = all;
+    }
+  }
+  __device__ __forceinline__ bool next(const Fp8GemmParams& P, Fp8Unit& u) {
+    if (at >= end) return false;
+    if (CTAS == 1 && stride == 0) {
+      const int32_t t = at / depth;
+      u = fp8_unit<CTAS>(P, t);
+      u.q0 = at - t * depth;
+      u.q1 = min(depth, u.q0 + end - at);
+      at += u.q1 - u.q0;
+    } else {
+      u = fp8_unit<CTAS>(P, at);
+      at += stride;
+    }
+    return true;
+  }
+};
 
 // The maps of k-block q and its place in them.
 struct Fp8Block {
@@ -231,18 +267,23 @@ __device__ __forceinline__ void stage_bf16(const float (&v)[32], uint32_t stg, u
                             pack_bf16(v[8 * i + 6], v[8 * i + 7])));
 }
 
-__device__ __forceinline__ void load32(uint32_t taddr, bool empty, float (&v)[32]) {
-  uint32_t r[32];
-  if (empty) {
+// 32 columns of a warp's 128 of the accumulator.
+struct FromTmem {
+  uint32_t taddr;
+  bool empty;  // no contraction: zeros
+  __device__ __forceinline__ void operator()(int j, float (&v)[32]) const {
+    if (empty) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = 0.f;
-    return;
+      for (int i = 0; i < 32; ++i) v[i] = 0.f;
+      return;
+    }
+    uint32_t r[32];
+    tmem_ld_32x32b_x32(taddr + j * 32, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
   }
-  tmem_ld_32x32b_x32(taddr, r);
-  tmem_wait_ld();
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
+};
 
 // One warp's 32 rows x 128 columns of a finished tile.  `released` is called
 // once the columns that both accumulators have are in registers: they are
@@ -256,8 +297,8 @@ struct Fp8Place {
 };
 
 template <typename Released>
-__device__ __forceinline__ void drain_bf16(const Fp8GemmParams& P, const Fp8Place& w, uint32_t taddr, bool empty, bool second_first,
-                                           uint32_t stg, uint32_t lane, Released released) {
+__device__ __forceinline__ void drain_bf16(const Fp8GemmParams& P, const Fp8Place& w, const FromTmem& load, bool second_first, uint32_t stg,
+                                           uint32_t lane, Released released) {
   const int64_t pitch = static_cast<int64_t>(P.cols) * 2;
   const __nv_bfloat16* bias = P.bias[w.o];
 #pragma unroll 1
@@ -266,8 +307,8 @@ __device__ __forceinline__ void drain_bf16(const Fp8GemmParams& P, const Fp8Plac
     const int32_t c = w.col + half * 64, bytes = min(P.cols - c, 64) * 2;
     const int64_t at = (w.off + static_cast<int64_t>(w.row) * P.cols + c) * 2;
     float v[2][32];
-    load32(taddr + half * 64, empty, v[0]);
-    load32(taddr + half * 64 + 32, empty, v[1]);
+    load(2 * half, v[0]);
+    load(2 * half + 1, v[1]);
     if (part == 0) released();
     if (bytes <= 0) continue;
     if (bias) {
@@ -306,13 +347,13 @@ __device__ __forceinline__ void drain_bf16(const Fp8GemmParams& P, const Fp8Plac
 // The same with the result in 8 bits: a thread has the 128 columns of its
 // row that share an exponent.
 template <typename Released>
-__device__ __forceinline__ void drain_fp8(const Fp8GemmParams& P, const Fp8Place& w, uint32_t taddr, bool empty, uint32_t stg, uint32_t lane,
+__device__ __forceinline__ void drain_fp8(const Fp8GemmParams& P, const Fp8Place& w, const FromTmem& load, uint32_t stg, uint32_t lane,
                                           Released released) {
   const int64_t pitch = static_cast<int64_t>(P.cols) * 2;
   const __nv_bfloat16* bias = P.bias[w.o];
   float v[4][32];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) load32(taddr + j * 32, empty, v[j]);
+  for (int j = 0; j < 4; ++j) load(j, v[j]);
   released();
   if (w.col >= P.cols) return;
   float top = 0.f;
@@ -366,23 +407,101 @@ __device__ __forceinline__ void drain_fp8(const Fp8GemmParams& P, const Fp8Place
   }
 }
 
-// fp32 sums of a part of the contraction.
+// fp32 results: 128 columns from `to` on, of which `cols` are there.
 template <typename Released>
-__device__ __forceinline__ void drain_part(const Fp8GemmParams& P, const Fp8Place& w, float* part, uint32_t taddr, bool empty,
-                                           uint32_t lane, Released released) {
-  const bool mine = static_cast<int32_t>(lane) < w.rows;
-  float* to = part + (static_cast<int64_t>(w.row) + lane) * P.cols + w.col;
+__device__ __forceinline__ void drain_f32(float* to, int64_t pitch, int32_t cols, int32_t rows, const FromTmem& load, uint32_t stg,
+                                          uint32_t lane, Released released) {
 #pragma unroll 1
   for (int j = 0; j < 4; ++j) {
     float v[32];
-    load32(taddr + j * 32, empty, v);
-    if (mine) {
+    load(j, v);
+    if (j == 3) released();
+    if (j * 32 >= cols) continue;
 #pragma unroll
-      for (int i = 0; i < 32; i += 4)
-        if (w.col + j * 32 + i < P.cols) __stcg(reinterpret_cast<float4*>(to + j * 32 + i), make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
-    }
+    for (uint32_t i = 0; i < 8; ++i)
+      st_shared_v4(stg_at(stg, lane, i), make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                                                    __float_as_uint(v[4 * i + 3])));
+    stg_out(stg, reinterpret_cast<uint8_t*>(to + j * 32), pitch * 4, rows, min(cols - j * 32, 32) * 4, lane);
   }
-  released();
+}
+
+template <bool QUANT, typename Released>
+__device__ __forceinline__ void drain(const Fp8GemmParams& P, const Fp8Place& w, const FromTmem& load, bool second_first, uint32_t stg,
+                                      uint32_t lane, Released released) {
+  if constexpr (QUANT) drain_fp8(P, w, load, stg, lane, released);
+  else if (P.out32)
+    drain_f32(P.out32 + static_cast<int64_t>(w.row) * P.cols + w.col, P.cols, P.cols - w.col, w.rows, load, stg, lane, released);
+  else drain_bf16(P, w, load, second_first, stg, lane, released);
+}
+
+// ------------------------------------------------------------------ tiles that several runs share (CTAS = 1)
+//
+// A run has at most two parts, [tile_rows][128] each: of the tile that is not
+// finished when it ends (the even one) and of the one that was not when it
+// began.  The join kernel adds them up in the order of the runs.
+
+__device__ __forceinline__ float* part_at(const Fp8GemmParams& P, int32_t run, bool begins) {
+  return P.part + (static_cast<int64_t>(2 * run + (begins ? 0 : 1)) * P.tile_rows) * 128;
+}
+
+constexpr int kJoinThreads = 256;
+
+// blockIdx.x: the end of a run inside a tile, the first in it; a warp has a
+// row, a lane four of its columns.
+__global__ void __launch_bounds__(kJoinThreads) fp8_join_kernel(const __grid_constant__ Fp8GemmParams P) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const uint32_t lane = threadIdx.x & 31;
+  const int32_t i = static_cast<int32_t>(blockIdx.x) + 1;
+  const int32_t depth = P.segs * P.kb, work = fp8_tiles(P) * depth, run = max((work + P.runs - 1) / P.runs, P.min_run);
+  const int32_t end = i * run, t = end / depth, from = t * depth;
+  if (end >= work || end == from || end - run > from) return;
+  const int32_t lo = i - 1, hi = (from + depth - 1) / run;
+  const Fp8Unit u = fp8_unit<1>(P, t);
+  const int32_t r = static_cast<int32_t>(blockIdx.y) * (kJoinThreads / 32) + static_cast<int32_t>(threadIdx.x >> 5);
+  const int64_t row = static_cast<int64_t>(u.mt) * P.tile_rows + r;
+  if (r >= P.tile_rows || (P.mode != FP8_ROWS && row >= P.rows)) return;
+  const int32_t o = P.mode == FP8_DENSE ? u.g : 0, c = u.nt * 128 + static_cast<int32_t>(lane) * 4;
+  float v[4] = {};
+#pragma unroll 4
+  for (int32_t k = lo; k <= hi; ++k) {
+    const float4 f = __ldcg(reinterpret_cast<const float4*>(part_at(P, k, k == lo) + r * 128) + lane);
+    v[0] += f.x;
+    v[1] += f.y;
+    v[2] += f.z;
+    v[3] += f.w;
+  }
+  if (c < P.cols) {
+    const int64_t at = row * P.cols + c;
+    if (P.bias[o]) {
+      const uint2 w = *reinterpret_cast<const uint2*>(P.bias[o] + c);
+      v[0] += bf_lo(w.x);
+      v[1] += bf_hi(w.x);
+      v[2] += bf_lo(w.y);
+      v[3] += bf_hi(w.y);
+    }
+    if (P.epi == TP_EPI_DGELU) {
+      const uint2 h = *reinterpret_cast<const uint2*>(P.aux[o] + at);
+      times_gelu_prime2(v[0], v[1], bf_lo(h.x), bf_hi(h.x));
+      times_gelu_prime2(v[2], v[3], bf_lo(h.y), bf_hi(h.y));
+    } else if (P.epi == TP_EPI_GELU) {
+      if (P.aux[o]) *reinterpret_cast<uint2*>(P.aux[o] + at) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+      gelu2(v[0], v[1]);
+      gelu2(v[2], v[3]);
+    }
+    if (P.out32) *reinterpret_cast<float4*>(P.out32 + at) = make_float4(v[0], v[1], v[2], v[3]);
+    else if (P.out[o]) *reinterpret_cast<uint2*>(P.out[o] + at) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+  } else {
+    v[0] = v[1] = v[2] = v[3] = 0.f;
+  }
+  if (P.zq[o]) {
+    float top = fmaxf(fmaxf(finite_abs(v[0]), finite_abs(v[1])), fmaxf(finite_abs(v[2]), finite_abs(v[3])));
+#pragma unroll
+    for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
+    const uint32_t e = fp8_exponent(top);
+    *reinterpret_cast<uint32_t*>(P.zq[o] + row * P.zq_ld + c) = fp8_pack4(v[0], v[1], v[2], v[3], fp8_inverse(e));
+    if (lane == 0) P.ze[o][u.mt * P.ze_ld + (u.nt >> 2) * 512 + fp8_e_at(static_cast<uint32_t>(r), u.nt & 3)] = static_cast<uint8_t>(e);
+  }
 }
 
 // ------------------------------------------------------------------ kernel
@@ -437,8 +556,8 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
   griddep_wait();
   griddep_launch_dependents();
 
-  const int32_t first = static_cast<int32_t>(blockIdx.x) / CTAS, stride = static_cast<int32_t>(gridDim.x) / CTAS;
-  const int32_t units = fp8_units(P);
+  Fp8Walk<CTAS> walk(P);
+  Fp8Unit u;
   auto wait = [&](uint32_t bar, uint32_t parity, uint32_t role) {
     return wait_bar(bar, parity & 1u, P.timeout_ns, P.status, abort_flag, role);
   };
@@ -451,8 +570,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
       int32_t issued = 0;
       bool ok = true;
       const uint32_t stage_bytes = static_cast<uint32_t>(P.mode == FP8_CONTRACT ? 128 : P.tile_rows) * 128 + C::B_BYTES;
-      for (int32_t t = first; t < units && ok; t += stride) {
-        const Fp8Unit u = fp8_unit<CTAS>(P, t);
+      while (ok && walk.next(P, u)) {
         const int32_t a_row = u.a_row + static_cast<int32_t>(crank) * 128, b_row = u.b_row + static_cast<int32_t>(crank) * 128;
         for (int32_t q = u.q0; q < u.q1; ++q) {
           if (!wait(empty_bar(stage), phase ^ 1u, 1u)) {
@@ -505,8 +623,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
       int stage = 0;
       uint32_t phase = 0, n = 0, quads = 0;
       bool ok = true;
-      for (int32_t t = first; t < units && ok; t += stride, ++n) {
-        const Fp8Unit u = fp8_unit<CTAS>(P, t);
+      for (; ok && walk.next(P, u); ++n) {
         // the epilogue has begun the tile before: it is done with the one
         // before that, and with the columns that both accumulators have
         if (n > 0 && !wait(begun_bar, n - 1, 2u)) break;
@@ -552,8 +669,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
     const uint32_t quarter = warp & 3, part = (warp - 2) >> 2;  // lanes of tensor memory, 128 columns
     const uint32_t stg = base + C::STG_OFF + (warp - 2) * C::STG_BYTES;
     uint32_t n = 0;
-    for (int32_t t = first; t < units; t += stride, ++n) {
-      const Fp8Unit u = fp8_unit<CTAS>(P, t);
+    for (; walk.next(P, u); ++n) {
       const bool ok = wait(tfull_bar(n & 1), n >> 1, 4u);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       tc_fence_after();
@@ -589,15 +705,11 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
       auto released = [&] {
         if (!early) begun();
       };
-      if (w.rows > 0) {
-        if (P.splits > 1) {
-          float* to = P.part + (static_cast<int64_t>(u.split) * P.groups + u.g) * P.part_rows * P.cols;
-          drain_part(P, w, to, taddr, empty, lane, released);
-        } else if constexpr (QUANT) {
-          drain_fp8(P, w, taddr, empty, stg, lane, released);
-        } else {
-          drain_bf16(P, w, taddr, empty, (n & 1) == 0, stg, lane, released);
-        }
+      const FromTmem acc{taddr, empty};
+      if (w.rows > 0 && CTAS == 1 && walk.stride == 0 && u.q1 - u.q0 < walk.depth) {
+        drain_f32(part_at(P, static_cast<int32_t>(blockIdx.x), u.q0 == 0) + tile_row * 128, 128, 128, w.rows, acc, stg, lane, [] {});
+      } else if (w.rows > 0) {
+        drain<QUANT>(P, w, acc, (n & 1) == 0, stg, lane, released);
       }
       tc_fence_before();
     }

@@ -6,11 +6,10 @@
 // only one.  (Against a scale of max|x| / 448 this costs up to one bit of the
 // block's range and none of its precision above 2^-6 of the largest value.)
 //
-// fp8_pack_kernel: a thread block takes 128 rows x 512 columns, 128 x 128 at a
-// time: what it reads gives the row operand from registers and, through
-// shared memory, the transposed one, so that x is read once for both.  Four
-// blocks of columns fill the words of exponents.  Bound by HBM, 2 bytes read
-// and 1 or 2 written an element.
+// fp8_pack_kernel: a thread block takes 128 rows x 128 columns: what it reads
+// gives the row operand from registers and, through shared memory, the
+// transposed one, so that x is read once for both.  Bound by HBM, 2 bytes
+// read and 1 or 2 written an element.
 //
 // fp8_pack_rows_kernel: a warp for each 128 columns of a row, where there are
 // too few rows for the blocks above to fill the GPU.
@@ -57,135 +56,217 @@ __device__ __forceinline__ const __nv_bfloat16* source(const PackParams& P, cons
   return x + (P.gather ? s / P.k : r) * P.cols;
 }
 
-template <bool Q, bool QT>
+// What becomes of an element before it is packed.
+enum Source : int { PLAIN = 0, GELU = 1, WEIGHTED = 2 };
+
+// The largest magnitude of bf16 pairs, as 15-bit integers (an infinity or NaN
+// is at least 0x7F80, and the magnitudes are then looked at one by one).
+__device__ __forceinline__ uint32_t max_abs(uint32_t a, uint32_t b) { return __vmaxu2(a, b & 0x7FFF7FFFu); }
+constexpr uint32_t kInfinite = 0x7F80u;
+
+// Two neighbours of a row, as they are packed.
+template <int SRC>
+__device__ __forceinline__ void pair_of(uint32_t u, float w, float& lo, float& hi) {
+  lo = bf_lo(u);
+  hi = bf_hi(u);
+  if constexpr (SRC == GELU) gelu2(lo, hi);
+  if constexpr (SRC == WEIGHTED) lo *= w, hi *= w;
+}
+
+template <bool FINITE>
+__device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d, float inv) {
+  return FINITE ? fp8_pack4_finite(a, b, c, d, inv) : fp8_pack4(a, b, c, d, inv);
+}
+
+// Two columns x 32 rows of the tile, from shared memory or (SRC other than
+// PLAIN) as they were formed, to the transposed operand's two rows.
+template <bool FINITE, int SRC>
+__device__ __forceinline__ void put_columns(const uint8_t* from, const float* keep, float ilo, float ihi, uint8_t* to, int64_t ld) {
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t lo4[4], hi4[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      float lo[4], hi[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = half * 16 + n * 4 + j;
+        if (SRC == PLAIN) {
+          const uint32_t u = *reinterpret_cast<const uint32_t*>(from + i * kPitch);
+          lo[j] = bf_lo(u);
+          hi[j] = bf_hi(u);
+        } else {
+          lo[j] = keep[SRC == PLAIN ? 0 : 2 * i];
+          hi[j] = keep[SRC == PLAIN ? 0 : 2 * i + 1];
+        }
+      }
+      lo4[n] = pack4<FINITE>(lo[0], lo[1], lo[2], lo[3], ilo);
+      hi4[n] = pack4<FINITE>(hi[0], hi[1], hi[2], hi[3], ihi);
+    }
+    *reinterpret_cast<uint4*>(to + half * 16) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
+    *reinterpret_cast<uint4*>(to + ld + half * 16) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
+  }
+}
+
+template <bool Q, bool QT, int SRC>
 __global__ void __launch_bounds__(kThreads) fp8_pack_kernel(const __grid_constant__ PackParams P) {
   __shared__ __align__(16) uint8_t tile[QT ? 128 * kPitch : 16];
-  __shared__ float red[4][128], row_w[128], warp_top[8];
-  __shared__ uint32_t words[128];
+  __shared__ float2 red[4][64];
+  __shared__ float row_w[128], warp_top[8];
+  __shared__ int64_t row_at[128];  // element of x at which a row begins, or -1
   griddep_wait();
   griddep_launch_dependents();
-  const uint32_t t = blockIdx.z / P.batch, mat = blockIdx.z % P.batch, strip = blockIdx.y;
-  if (P.plan_tiles != nullptr && strip * 128 >= __ldcg(P.plan_tiles) * P.tile_rows) return;
+  const uint32_t t = blockIdx.z / P.batch, mat = blockIdx.z % P.batch, strip = blockIdx.y, b = blockIdx.x;
+  if (P.plan_tiles != nullptr && strip * 128 >= static_cast<uint32_t>(__ldcg(P.plan_tiles) * P.tile_rows)) return;
   const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const __nv_bfloat16* x = P.x[t] + mat * P.rows * P.cols;
   const int64_t r0 = static_cast<int64_t>(strip) * 128;
   const uint32_t sub = lane >> 4, piece = lane & 15;  // row of two, 16 bytes of a row
-  const __nv_bfloat16* src[8];
+  const int64_t c = static_cast<int64_t>(b) * 128 + piece * 8;
+  if (P.slot != nullptr) {
+    if (tid < 128) {
+      float w;
+      const __nv_bfloat16* src = source(P, x, r0 + tid, w);
+      row_at[tid] = src ? src - x : -1;
+      row_w[tid] = w;
+    }
+    __syncthreads();
+  }
+  uint4 v[8];
   float w[8];
 #pragma unroll
-  for (uint32_t i = 0; i < 8; ++i) src[i] = source(P, x, r0 + warp * 16 + i * 2 + sub, w[i]);
-  if (QT && P.weights && piece == 0) {
-#pragma unroll
-    for (uint32_t i = 0; i < 8; ++i) row_w[warp * 16 + i * 2 + sub] = w[i];
+  for (uint32_t i = 0; i < 8; ++i) {
+    const uint32_t r = warp * 16 + i * 2 + sub;
+    const int64_t at = P.slot != nullptr ? row_at[r] : r0 + r < P.rows ? (r0 + r) * P.cols : -1;
+    w[i] = SRC == WEIGHTED ? row_w[r] : 1.f;
+    v[i] = at >= 0 && c < P.cols ? *reinterpret_cast<const uint4*>(x + at + c) : make_uint4(0, 0, 0, 0);
   }
-  if (tid < 128) words[tid] = 0;
-  const uint32_t blocks = static_cast<uint32_t>((P.cols + 127) / 128);
-  for (uint32_t b = blockIdx.x * 4; b < min(blockIdx.x * 4 + 4, blocks); ++b) {
-    const int64_t c = static_cast<int64_t>(b) * 128 + piece * 8;
-    uint4 v[8];
+  if (QT) {
 #pragma unroll
-    for (uint32_t i = 0; i < 8; ++i)
-      v[i] = src[i] != nullptr && c < P.cols ? __ldcs(reinterpret_cast<const uint4*>(src[i] + c)) : make_uint4(0, 0, 0, 0);
-    __syncthreads();  // the tile before is used up; `words` is clear
-    if (QT) {
+    for (uint32_t i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(tile + (warp * 16 + i * 2 + sub) * kPitch + piece * 16) = v[i];
+  }
+  float all = 0.f;
+  if (P.tiles) {
 #pragma unroll
-      for (uint32_t i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(tile + (warp * 16 + i * 2 + sub) * kPitch + piece * 16) = v[i];
-    }
-    float all = 0.f;
-    if (P.tiles) {
+    for (uint32_t i = 0; i < 8; ++i) {
+      const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-      for (uint32_t i = 0; i < 8; ++i) {
-        float f[8];
-        unpack8(v[i], f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) all = fmaxf(all, finite_abs(gelu_if(P.gelu, f[j])));
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xFFFFFFFFu, all, o));
-      if (lane == 0) warp_top[warp] = all;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 8; ++i) all = fmaxf(all, warp_top[i]);
-    }
-    if (Q) {
-      uint8_t* q = P.q[t] + (mat * P.rows + r0) * P.ldq + b * 128 + piece * 8;
-#pragma unroll
-      for (uint32_t i = 0; i < 8; ++i) {
-        const uint32_t r = warp * 16 + i * 2 + sub;
-        float f[8], top = 0.f;
-        unpack8(v[i], f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          f[j] = gelu_if(P.gelu, f[j]);
-          if (P.weights) f[j] *= w[i];
-          top = fmaxf(top, finite_abs(f[j]));
-        }
-#pragma unroll
-        for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        const uint32_t e = fp8_exponent(P.tiles ? all : top);
-        const float inv = fp8_inverse(e);
-        if (r0 + r < P.rows) {
-          *reinterpret_cast<uint2*>(q + r * P.ldq) = make_uint2(fp8_pack4(f[0], f[1], f[2], f[3], inv), fp8_pack4(f[4], f[5], f[6], f[7], inv));
-          if (piece == 0) reinterpret_cast<uint8_t*>(words + (r & 31) * 4 + (r >> 5))[b & 3] = static_cast<uint8_t>(e);
-        }
+      for (int j = 0; j < 4; ++j) {
+        float lo, hi;
+        pair_of<SRC>(u[j], w[i], lo, hi);
+        all = fmaxf(all, fmaxf(finite_abs(lo), finite_abs(hi)));
       }
     }
-    if (QT) {
-      // two columns and a quarter of the rows a thread
-      __syncthreads();
-      const uint32_t pair = tid & 63, quarter = tid >> 6;
-      float lo[32], hi[32], tlo = 0.f, thi = 0.f;
 #pragma unroll
-      for (uint32_t i = 0; i < 32; ++i) {
-        const uint32_t r = quarter * 32 + i;
-        const uint32_t u = *reinterpret_cast<const uint32_t*>(tile + r * kPitch + pair * 4);
-        lo[i] = gelu_if(P.gelu, bf_lo(u));
-        hi[i] = gelu_if(P.gelu, bf_hi(u));
-        if (P.weights) {
-          lo[i] *= row_w[r];
-          hi[i] *= row_w[r];
-        }
-        tlo = fmaxf(tlo, finite_abs(lo[i]));
-        thi = fmaxf(thi, finite_abs(hi[i]));
-      }
-      if (P.tiles) {
-        tlo = thi = all;
-      } else {
-        *reinterpret_cast<float2*>(&red[quarter][pair * 2]) = make_float2(tlo, thi);
-        __syncthreads();
+    for (int o = 16; o; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xFFFFFFFFu, all, o));
+    if (lane == 0) warp_top[warp] = all;
+    __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          tlo = fmaxf(tlo, red[i][pair * 2]);
-          thi = fmaxf(thi, red[i][pair * 2 + 1]);
-        }
-      }
-      const uint32_t elo = fp8_exponent(tlo), ehi = fp8_exponent(thi);
-      const float ilo = fp8_inverse(elo), ihi = fp8_inverse(ehi);
-      const int64_t col = static_cast<int64_t>(b) * 128 + pair * 2;
-      if (col < P.cols) {
-        uint8_t* to = P.qt[t] + (mat * P.cols + col) * P.ldqt + r0 + quarter * 32;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int o = half * 16;
-          *reinterpret_cast<uint4*>(to + o) =
-              make_uint4(fp8_pack4(lo[o], lo[o + 1], lo[o + 2], lo[o + 3], ilo), fp8_pack4(lo[o + 4], lo[o + 5], lo[o + 6], lo[o + 7], ilo),
-                         fp8_pack4(lo[o + 8], lo[o + 9], lo[o + 10], lo[o + 11], ilo), fp8_pack4(lo[o + 12], lo[o + 13], lo[o + 14], lo[o + 15], ilo));
-          *reinterpret_cast<uint4*>(to + P.ldqt + o) =
-              make_uint4(fp8_pack4(hi[o], hi[o + 1], hi[o + 2], hi[o + 3], ihi), fp8_pack4(hi[o + 4], hi[o + 5], hi[o + 6], hi[o + 7], ihi),
-                         fp8_pack4(hi[o + 8], hi[o + 9], hi[o + 10], hi[o + 11], ihi), fp8_pack4(hi[o + 12], hi[o + 13], hi[o + 14], hi[o + 15], ihi));
-        }
-      }
-      if (quarter == 0) {  // columns past the matrix: exponent 0
-        uint8_t* e = P.et[t] + mat * P.et_mat + b * P.et_block + static_cast<int64_t>(strip >> 2) * 512;
-        e[fp8_e_at(pair * 2, strip & 3)] = static_cast<uint8_t>(elo);
-        e[fp8_e_at(pair * 2 + 1, strip & 3)] = static_cast<uint8_t>(ehi);
-      }
-    }
+    for (int i = 0; i < 8; ++i) all = fmaxf(all, warp_top[i]);
   }
   if (Q) {
+    uint8_t* q = P.q[t] + (mat * P.rows + r0) * P.ldq + b * 128 + piece * 8;
+    uint8_t* e = P.e[t] + mat * P.e_mat + strip * P.e_block + static_cast<int64_t>(b >> 2) * 512;
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) {
+      const uint32_t r = warp * 16 + i * 2 + sub;
+      float f[8], top = 0.f;
+      bool finite = false;
+      pair_of<SRC>(v[i].x, w[i], f[0], f[1]);
+      pair_of<SRC>(v[i].y, w[i], f[2], f[3]);
+      pair_of<SRC>(v[i].z, w[i], f[4], f[5]);
+      pair_of<SRC>(v[i].w, w[i], f[6], f[7]);
+      if (SRC == PLAIN && !P.tiles) {
+        uint32_t m = max_abs(max_abs(max_abs(max_abs(0, v[i].x), v[i].y), v[i].z), v[i].w);
+        m = max(m & 0xFFFFu, m >> 16);
+#pragma unroll
+        for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        finite = m < kInfinite;
+        top = __uint_as_float(m << 16);
+      }
+      const bool warp_finite = SRC == PLAIN && __all_sync(0xFFFFFFFFu, finite);
+      if (!warp_finite) {
+        top = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_abs(f[j]));
+#pragma unroll
+        for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      }
+      const uint32_t ex = fp8_exponent(P.tiles ? all : top);
+      const float inv = fp8_inverse(ex);
+      uint2 o;
+      if (warp_finite) o = make_uint2(fp8_pack4_finite(f[0], f[1], f[2], f[3], inv), fp8_pack4_finite(f[4], f[5], f[6], f[7], inv));
+      else o = make_uint2(fp8_pack4(f[0], f[1], f[2], f[3], inv), fp8_pack4(f[4], f[5], f[6], f[7], inv));
+      if (r0 + r < P.rows) *reinterpret_cast<uint2*>(q + r * P.ldq) = o;
+      if (piece == 0) e[fp8_e_at(r, b & 3)] = r0 + r < P.rows ? static_cast<uint8_t>(ex) : 0;
+    }
+  }
+  if (QT) {
+    // two columns and a quarter of the rows a thread
     __syncthreads();
-    if (tid < 128)
-      reinterpret_cast<uint32_t*>(P.e[t] + mat * P.e_mat + strip * P.e_block + static_cast<int64_t>(blockIdx.x) * 512)[tid] = words[tid];
+    const uint32_t pair = tid & 63, quarter = tid >> 6;
+    const uint8_t* from = tile + quarter * 32 * kPitch + pair * 4;
+    float tlo = all, thi = all;
+    bool finite = false;
+    if (SRC == PLAIN && !P.tiles) {
+      uint32_t m = 0;
+#pragma unroll
+      for (uint32_t i = 0; i < 32; ++i) m = max_abs(m, *reinterpret_cast<const uint32_t*>(from + i * kPitch));
+      red[quarter][pair].x = __uint_as_float(m);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = __vmaxu2(m, __float_as_uint(red[i][pair].x));
+      tlo = __uint_as_float(m << 16);
+      thi = __uint_as_float(m & 0xFFFF0000u);
+      finite = (m & 0xFFFFu) < kInfinite && (m >> 16) < kInfinite;
+    }
+    // GeLU and weighted values are formed once, others again when packed
+    float keep[SRC == PLAIN ? 1 : 64];
+    if (SRC != PLAIN) {
+      tlo = thi = 0.f;
+#pragma unroll
+      for (uint32_t i = 0; i < 32; ++i) {
+        float &lo = keep[SRC == PLAIN ? 0 : 2 * i], &hi = keep[SRC == PLAIN ? 0 : 2 * i + 1];
+        pair_of<SRC>(*reinterpret_cast<const uint32_t*>(from + i * kPitch), SRC == WEIGHTED ? row_w[quarter * 32 + i] : 1.f, lo, hi);
+        tlo = fmaxf(tlo, finite_abs(lo));
+        thi = fmaxf(thi, finite_abs(hi));
+      }
+      red[quarter][pair] = make_float2(tlo, thi);
+    }
+    const bool all_finite = SRC == PLAIN && !P.tiles && !__syncthreads_or(!finite);
+    if (!all_finite && !P.tiles) {
+      if (SRC == PLAIN) {  // an infinity or NaN in the tile: magnitudes one by one
+        tlo = thi = 0.f;
+#pragma unroll 4
+        for (uint32_t i = 0; i < 32; ++i) {
+          const uint32_t u = *reinterpret_cast<const uint32_t*>(from + i * kPitch);
+          tlo = fmaxf(tlo, finite_abs(bf_lo(u)));
+          thi = fmaxf(thi, finite_abs(bf_hi(u)));
+        }
+        red[quarter][pair] = make_float2(tlo, thi);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 o = red[i][pair];
+        tlo = fmaxf(tlo, o.x);
+        thi = fmaxf(thi, o.y);
+      }
+    }
+    if (P.tiles) tlo = thi = all;
+    const uint32_t elo = fp8_exponent(tlo), ehi = fp8_exponent(thi);
+    const float ilo = fp8_inverse(elo), ihi = fp8_inverse(ehi);
+    const int64_t col = static_cast<int64_t>(b) * 128 + pair * 2;
+    if (col < P.cols) {
+      uint8_t* to = P.qt[t] + (mat * P.cols + col) * P.ldqt + r0 + quarter * 32;
+if (all_finite) put_columns<true, SRC>(from, keep, ilo, ihi, to, P.ldqt);
+      else put_columns<false, SRC>(from, keep, ilo, ihi, to, P.ldqt);
+    }
+    if (quarter == 0) {  // columns past the matrix: exponent 0
+      uint8_t* e = P.et[t] + mat * P.et_mat + b * P.et_block + static_cast<int64_t>(strip >> 2) * 512;
+      e[fp8_e_at(pair * 2, strip & 3)] = static_cast<uint8_t>(elo);
+      e[fp8_e_at(pair * 2 + 1, strip & 3)] = static_cast<uint8_t>(ehi);
+    }
   }
 }
 
@@ -219,6 +300,13 @@ __global__ void __launch_bounds__(kThreads) fp8_pack_rows_kernel(const __grid_co
     const int64_t block = r / P.tile_rows;
     P.e[t][block * P.e_block + (b >> 2) * 512 + fp8_e_at(static_cast<uint32_t>(r - block * P.tile_rows), b & 3)] = static_cast<uint8_t>(e);
   }
+}
+
+template <int SRC>
+tp_status launch_pack(const Fp8Pack& d, dim3 grid, const PackParams& P, cudaStream_t stream) {
+  if (d.q && d.qt) return launch_dependent(fp8_pack_kernel<true, true, SRC>, grid, kThreads, 0, stream, P);
+  if (d.q) return launch_dependent(fp8_pack_kernel<true, false, SRC>, grid, kThreads, 0, stream, P);
+  return launch_dependent(fp8_pack_kernel<false, true, SRC>, grid, kThreads, 0, stream, P);
 }
 
 struct UnpackParams {
@@ -311,10 +399,10 @@ tp_status fp8_pack(const Fp8Pack& d, cudaStream_t stream) {
                             stream, P);
   }
   if (P.strips > 65535u || d.batch * d.n > 65535) return TP_ERR_UNSUPPORTED_SHAPE;
-  const dim3 grid(static_cast<unsigned>(cdiv(d.cols, 512)), P.strips, static_cast<unsigned>(d.batch * d.n));
-  if (d.q && d.qt) return launch_dependent(fp8_pack_kernel<true, true>, grid, kThreads, 0, stream, P);
-  if (d.q) return launch_dependent(fp8_pack_kernel<true, false>, grid, kThreads, 0, stream, P);
-  return launch_dependent(fp8_pack_kernel<false, true>, grid, kThreads, 0, stream, P);
+  const dim3 grid(static_cast<unsigned>(cdiv(d.cols, 128)), P.strips, static_cast<unsigned>(d.batch * d.n));
+  if (d.gelu) return launch_pack<GELU>(d, grid, P, stream);
+  if (d.weights) return launch_pack<WEIGHTED>(d, grid, P, stream);
+  return launch_pack<PLAIN>(d, grid, P, stream);
 }
 
 }  // namespace tpf

@@ -85,7 +85,7 @@ def test_forward_refusals():
         return L.tp_experts_fwd_fp8(x, e, w, a, b, y, ctypes.byref(s) if s else None, p, E, T, k, h, f, ws, n, None)
     for kw in (dict(x=None), dict(e=None), dict(w=None), dict(a=None), dict(b=pairs(at(5), None)), dict(y=None), dict(p=0), dict(p=9), dict(E=0),
                dict(T=-1), dict(k=0), dict(h=0), dict(f=0), dict(y=at(0)), dict(y=at(5)), dict(ws=at(1)), dict(ws=None),
-               dict(s=SV(at(9), at(10), None), n=1 << 22), dict(s=SV(at(9), at(10), at(0)), n=1 << 22)):
+               dict(s=SV(at(9), at(10), None), n=1 << 26, ws=at(30)), dict(s=SV(at(9), at(10), at(0)), n=1 << 26, ws=at(30))):
         assert fwd(**kw) == BAD, kw
     assert fwd(n=need - 1) == SMALL
     assert fwd(p=3) == SHAPE and fwd(E=514) == SHAPE and fwd(k=33) == SHAPE and fwd(T=1 << 30, k=4) == SHAPE
@@ -98,7 +98,7 @@ def test_backward_refusals():
     s = SV(at(20), at(21), at(22))
 
     def bwd(x=at(0), w=at(1), dy=at(2), a=pairs(at(3), at(4)), b=pairs(at(5), at(6)), dx=at(7), dw=at(8), d1=arr(at(9), at(10)), d2=arr(at(11), at(12)),
-            s=s, ws=at(13), n=n, **o):
+            s=s, ws=at(30), n=n, **o):
         o = {**dict(p=p, E=E, T=T, k=k, h=h, f=f), **o}
         return L.tp_experts_bwd_fp8(x, w, dy, a, b, dx, dw, d1, d2, ctypes.byref(s) if s else None, *o.values(), ws, n, None)
     for kw in (dict(dx=None, dw=None, d1=None, d2=None), dict(x=None), dict(w=None), dict(dy=None), dict(a=None), dict(b=None), dict(s=None),
