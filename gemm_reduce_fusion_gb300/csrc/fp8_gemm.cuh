@@ -12,8 +12,8 @@
 //
 // CTAS = 1: 128 x 128 tiles of one CTA; CTAS = 2: 256 x 256 tiles of a CTA
 // pair, each of which holds 128 rows of A and of B.  A k-block is 128 deep:
-// 32 KiB a stage and CTA in both.  A pair moves 64 bytes an SM and cycle from
-// L2 at the full MMA rate, a single CTA's tile 128.
+// 32 KiB a CTA in both.  A pair moves 64 bytes an SM and cycle from L2 at the
+// full MMA rate, a single CTA's tile 128.
 //
 // Roles: warp 0 loads, warp 1 issues the MMAs, the others (four for each 128
 // columns) are the epilogue, which overlaps the next tile's MMAs on the other
@@ -72,15 +72,19 @@ struct Fp8GemmParams {
 template <int CTAS>
 struct Fp8Cfg {
   static constexpr int BN = 128 * CTAS;
-  static constexpr uint32_t A_BYTES = 128 * 128, B_BYTES = 128 * 128;
-  static constexpr uint32_t EA_BYTES = 512, EB_BYTES = 512 * CTAS;
-  static constexpr uint32_t E_BYTES = 2048;  // of a stage, padded
-  static constexpr int STAGES = CTAS == 1 ? 6 : 5;
+  // A stage has two k-blocks of A, two of B and their exponents.  (With one,
+  // the loads alone of the MLP's launches took 148 us, with two 115: each
+  // stage costs its loader some 150 ns beside the copies.)
+  static constexpr int DEEP = 2;
+  static constexpr uint32_t A_BYTES = 128 * 128, B_BYTES = 128 * 128;  // of a k-block
+  static constexpr uint32_t EA_BYTES = 512, EB_BYTES = 512 * CTAS, E_BYTES = EA_BYTES + EB_BYTES;
+  static constexpr uint32_t STAGE = DEEP * (A_BYTES + B_BYTES);
+  static constexpr int STAGES = 3;
   static constexpr int EPI_WARPS = 4 * CTAS;
   static constexpr int THREADS = 64 + 32 * EPI_WARPS;
-  static constexpr uint32_t STG_BYTES = 4096;  // staging of an epilogue warp
-  static constexpr uint32_t A_OFF = 0, B_OFF = STAGES * A_BYTES, E_OFF = B_OFF + STAGES * B_BYTES,
-                            STG_OFF = E_OFF + STAGES * E_BYTES, BAR_OFF = STG_OFF + EPI_WARPS * STG_BYTES;
+  static constexpr uint32_t STG_BYTES = 2048;  // staging of an epilogue warp
+  static constexpr uint32_t E_OFF = STAGES * STAGE, STG_OFF = E_OFF + STAGES * DEEP * E_BYTES,
+                            BAR_OFF = STG_OFF + EPI_WARPS * STG_BYTES;
   static constexpr uint32_t SMEM = 1024 + BAR_OFF + 256;
   // tensor memory: accumulators of BN columns at 0 and ACC1, scales from SF
   // on (A 4 columns, B 4 CTAS), two of them by turns
@@ -88,6 +92,10 @@ struct Fp8Cfg {
   static constexpr uint32_t ACC1 = BN - SHARED, SF = 480;
   static_assert(ACC1 + BN <= SF, "accumulators before the scales");
   static_assert(SMEM <= 227 * 1024, "shared memory of a CTA");
+  // in a stage: A's k-blocks, B's
+  static __device__ __forceinline__ uint32_t a(uint32_t base, int stage, int d) { return base + stage * STAGE + d * A_BYTES; }
+  static __device__ __forceinline__ uint32_t b(uint32_t base, int stage, int d) { return base + stage * STAGE + DEEP * A_BYTES + d * B_BYTES; }
+  static __device__ __forceinline__ uint32_t e(uint32_t base, int stage, int d) { return base + E_OFF + (stage * DEEP + d) * E_BYTES; }
 };
 
 struct Fp8Unit {
@@ -208,24 +216,24 @@ __device__ __forceinline__ Fp8Block fp8_block(const Fp8GemmParams& P, const Fp8U
 
 // ------------------------------------------------------------------ epilogue
 
-// 32 rows x 128 bytes of the warp's staging buffer, 16-byte pieces swizzled.
+// 32 rows x 64 bytes of the warp's staging buffer, 16-byte pieces swizzled.
 __device__ __forceinline__ uint32_t stg_at(uint32_t stg, uint32_t row, uint32_t piece) {
-  return stg + row * 128 + ((piece ^ (row & 7)) << 4);
+  return stg + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
 }
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// Rows of 64 bf16 (or 128 bytes): staging buffer -> memory, four rows an
-// instruction, 128 bytes each.  `bytes`: of a row that are the matrix's.
+// Staging buffer -> memory, eight rows an instruction, 64 bytes each.
+// `bytes`: of a row that are the matrix's.
 __device__ __forceinline__ void stg_out(uint32_t stg, uint8_t* to, int64_t pitch, int32_t rows, int32_t bytes, uint32_t lane) {
   __syncwarp();
-  const uint32_t piece = lane & 7;
+  const uint32_t piece = lane & 3;
   if (static_cast<int32_t>(piece * 16) < bytes) {
 #pragma unroll
-    for (uint32_t i = 0; i < 8; ++i) {
-      const uint32_t r = i * 4 + (lane >> 3);
+    for (uint32_t i = 0; i < 4; ++i) {
+      const uint32_t r = i * 8 + (lane >> 2);
       if (static_cast<int32_t>(r) < rows) *reinterpret_cast<uint4*>(to + r * pitch + piece * 16) = ld_shared_v4(stg_at(stg, r, piece));
     }
   }
@@ -233,17 +241,17 @@ __device__ __forceinline__ void stg_out(uint32_t stg, uint8_t* to, int64_t pitch
 }
 
 __device__ __forceinline__ void stg_in(uint32_t stg, const uint8_t* from, int64_t pitch, int32_t rows, int32_t bytes, uint32_t lane) {
-  __syncwarp();
-  const uint32_t piece = lane & 7;
+  const uint32_t piece = lane & 3;
   const bool some = static_cast<int32_t>(piece * 16) < bytes;
-  uint4 v[8];
+  uint4 v[4];
 #pragma unroll
-  for (uint32_t i = 0; i < 8; ++i) {
-    const uint32_t r = i * 4 + (lane >> 3);
+  for (uint32_t i = 0; i < 4; ++i) {
+    const uint32_t r = i * 8 + (lane >> 2);
     v[i] = some && static_cast<int32_t>(r) < rows ? *reinterpret_cast<const uint4*>(from + r * pitch + piece * 16) : make_uint4(0, 0, 0, 0);
   }
+  __syncwarp();
 #pragma unroll
-  for (uint32_t i = 0; i < 8; ++i) st_shared_v4(stg_at(stg, i * 4 + (lane >> 3), piece), v[i]);
+  for (uint32_t i = 0; i < 4; ++i) st_shared_v4(stg_at(stg, i * 8 + (lane >> 2), piece), v[i]);
   __syncwarp();
 }
 
@@ -259,10 +267,10 @@ __device__ __forceinline__ void add_bias(float (&v)[32], const __nv_bfloat16* bi
   }
 }
 
-__device__ __forceinline__ void stage_bf16(const float (&v)[32], uint32_t stg, uint32_t row, uint32_t piece0) {
+__device__ __forceinline__ void stage_bf16(const float (&v)[32], uint32_t stg, uint32_t row) {
 #pragma unroll
   for (uint32_t i = 0; i < 4; ++i)
-    st_shared_v4(stg_at(stg, row, piece0 + i),
+    st_shared_v4(stg_at(stg, row, i),
                  make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]), pack_bf16(v[8 * i + 4], v[8 * i + 5]),
                             pack_bf16(v[8 * i + 6], v[8 * i + 7])));
 }
@@ -286,8 +294,8 @@ struct FromTmem {
 };
 
 // One warp's 32 rows x 128 columns of a finished tile.  `released` is called
-// once the columns that both accumulators have are in registers: they are
-// among the 64 that drain_bf16 takes first.
+// once the columns that both accumulators have are in registers: the 32 that
+// drain_bf16 takes first.
 struct Fp8Place {
   int32_t row, rows;  // first row in the output, rows of the warp that are the output's
   int32_t col;        // first column
@@ -297,49 +305,39 @@ struct Fp8Place {
 };
 
 template <typename Released>
-__device__ __forceinline__ void drain_bf16(const Fp8GemmParams& P, const Fp8Place& w, const FromTmem& load, bool second_first, uint32_t stg,
+__device__ __forceinline__ void drain_bf16(const Fp8GemmParams& P, const Fp8Place& w, const FromTmem& load, bool last_first, uint32_t stg,
                                            uint32_t lane, Released released) {
   const int64_t pitch = static_cast<int64_t>(P.cols) * 2;
   const __nv_bfloat16* bias = P.bias[w.o];
 #pragma unroll 1
-  for (int part = 0; part < 2; ++part) {
-    const int half = second_first ? 1 - part : part;
-    const int32_t c = w.col + half * 64, bytes = min(P.cols - c, 64) * 2;
+  for (int part = 0; part < 4; ++part) {
+    const int j = last_first ? (part + 3) & 3 : part;
+    const int32_t c = w.col + j * 32, bytes = min(P.cols - c, 32) * 2;
     const int64_t at = (w.off + static_cast<int64_t>(w.row) * P.cols + c) * 2;
-    float v[2][32];
-    load(2 * half, v[0]);
-    load(2 * half + 1, v[1]);
+    float v[32];
+    load(j, v);
     if (part == 0) released();
     if (bytes <= 0) continue;
-    if (bias) {
-      add_bias(v[0], bias, c, P.cols);
-      add_bias(v[1], bias, c + 32, P.cols);
-    }
+    if (bias) add_bias(v, bias, c, P.cols);
     if (P.epi == TP_EPI_DGELU) {
       stg_in(stg, reinterpret_cast<const uint8_t*>(P.aux[w.o]) + at, pitch, w.rows, bytes, lane);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (uint32_t i = 0; i < 4; ++i) {
+        float h[8];
+        unpack8(ld_shared_v4(stg_at(stg, lane, i)), h);
 #pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) {
-          float h[8];
-          unpack8(ld_shared_v4(stg_at(stg, lane, j * 4 + i)), h);
-#pragma unroll
-          for (int m = 0; m < 8; m += 2) times_gelu_prime2(v[j][8 * i + m], v[j][8 * i + m + 1], h[m], h[m + 1]);
-        }
+        for (int m = 0; m < 8; m += 2) times_gelu_prime2(v[8 * i + m], v[8 * i + m + 1], h[m], h[m + 1]);
+      }
       __syncwarp();
     } else if (P.epi == TP_EPI_GELU) {
       if (P.aux[w.o]) {
-        stage_bf16(v[0], stg, lane, 0);
-        stage_bf16(v[1], stg, lane, 4);
+        stage_bf16(v, stg, lane);
         stg_out(stg, reinterpret_cast<uint8_t*>(P.aux[w.o]) + at, pitch, w.rows, bytes, lane);
       }
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) gelu2(v[j][i], v[j][i + 1]);
+      for (int i = 0; i < 32; i += 2) gelu2(v[i], v[i + 1]);
     }
-    stage_bf16(v[0], stg, lane, 0);
-    stage_bf16(v[1], stg, lane, 4);
+    stage_bf16(v, stg, lane);
     stg_out(stg, reinterpret_cast<uint8_t*>(P.out[w.o]) + at, pitch, w.rows, bytes, lane);
   }
 }
@@ -358,49 +356,37 @@ __device__ __forceinline__ void drain_fp8(const Fp8GemmParams& P, const Fp8Place
   if (w.col >= P.cols) return;
   float top = 0.f;
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int32_t c = w.col + half * 64, bytes = min(P.cols - c, 64) * 2;
+  for (int j = 0; j < 4; ++j) {
+    const int32_t c = w.col + j * 32, bytes = min(P.cols - c, 32) * 2;
     const int64_t at = (w.off + static_cast<int64_t>(w.row) * P.cols + c) * 2;
-    float(&v0)[32] = v[2 * half];
-    float(&v1)[32] = v[2 * half + 1];
-    if (bias) {
-      add_bias(v0, bias, c, P.cols);
-      add_bias(v1, bias, c + 32, P.cols);
-    }
+    if (bias) add_bias(v[j], bias, c, P.cols);
     if (P.aux[w.o] && bytes > 0) {
-      stage_bf16(v0, stg, lane, 0);
-      stage_bf16(v1, stg, lane, 4);
+      stage_bf16(v[j], stg, lane);
       stg_out(stg, reinterpret_cast<uint8_t*>(P.aux[w.o]) + at, pitch, w.rows, bytes, lane);
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        float &x0 = v[2 * half + j][i], &x1 = v[2 * half + j][i + 1];
-        if (P.epi == TP_EPI_GELU) gelu2(x0, x1);
-        if ((i & 7) == 0 && c + 32 * j + i >= P.cols) {  // past the matrix, in eights: zeros
-#pragma unroll
-          for (int m = 0; m < 8; ++m) v[2 * half + j][i + m] = 0.f;
-        }
-      }
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int i = 0; i < 32; ++i) top = fmaxf(top, finite_abs(v[2 * half + j][i]));
+    for (int i = 0; i < 32; i += 2) {
+      if (P.epi == TP_EPI_GELU) gelu2(v[j][i], v[j][i + 1]);
+      if (c + (i & ~7) >= P.cols) v[j][i] = v[j][i + 1] = 0.f;  // past the matrix, in eights: zeros
+      top = fmaxf(top, fmaxf(finite_abs(v[j][i]), finite_abs(v[j][i + 1])));
+    }
   }
   const uint32_t e = fp8_exponent(top);
   const float inv = fp8_inverse(e);
 #pragma unroll
-  for (uint32_t j = 0; j < 8; ++j) {
-    uint32_t o[4];
+  for (uint32_t half = 0; half < 2; ++half) {
 #pragma unroll
-    for (uint32_t i = 0; i < 4; ++i) {
-      const uint32_t n = j * 16 + i * 4;
-      o[i] = fp8_pack4(v[n / 32][n % 32], v[n / 32][n % 32 + 1], v[n / 32][n % 32 + 2], v[n / 32][n % 32 + 3], inv);
+    for (uint32_t j = 0; j < 4; ++j) {
+      uint32_t o[4];
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) {
+        const uint32_t n = half * 64 + j * 16 + i * 4;
+        o[i] = fp8_pack4(v[n / 32][n % 32], v[n / 32][n % 32 + 1], v[n / 32][n % 32 + 2], v[n / 32][n % 32 + 3], inv);
+      }
+      st_shared_v4(stg_at(stg, lane, j), make_uint4(o[0], o[1], o[2], o[3]));
     }
-    st_shared_v4(stg_at(stg, lane, j), make_uint4(o[0], o[1], o[2], o[3]));
+    stg_out(stg, P.zq[w.o] + w.row * P.zq_ld + w.col + half * 64, P.zq_ld, w.rows, 64, lane);
   }
-  stg_out(stg, P.zq[w.o] + w.row * P.zq_ld + w.col, P.zq_ld, w.rows, 128, lane);
   if (static_cast<int32_t>(lane) < w.rows) {
     const int32_t b = w.col / 128;
     P.ze[w.o][w.eblock * P.ze_ld + (b >> 2) * 512 + fp8_e_at(static_cast<uint32_t>(w.erow) + lane, b & 3)] = static_cast<uint8_t>(e);
@@ -416,22 +402,28 @@ __device__ __forceinline__ void drain_f32(float* to, int64_t pitch, int32_t cols
     float v[32];
     load(j, v);
     if (j == 3) released();
-    if (j * 32 >= cols) continue;
 #pragma unroll
-    for (uint32_t i = 0; i < 8; ++i)
-      st_shared_v4(stg_at(stg, lane, i), make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
-                                                    __float_as_uint(v[4 * i + 3])));
-    stg_out(stg, reinterpret_cast<uint8_t*>(to + j * 32), pitch * 4, rows, min(cols - j * 32, 32) * 4, lane);
+    for (int half = 0; half < 2; ++half) {
+      const int32_t c = j * 32 + half * 16;
+      if (c >= cols) continue;
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) {
+        const int n = half * 16 + i * 4;
+        st_shared_v4(stg_at(stg, lane, i), make_uint4(__float_as_uint(v[n]), __float_as_uint(v[n + 1]), __float_as_uint(v[n + 2]),
+                                                      __float_as_uint(v[n + 3])));
+      }
+      stg_out(stg, reinterpret_cast<uint8_t*>(to + c), pitch * 4, rows, min(cols - c, 16) * 4, lane);
+    }
   }
 }
 
 template <bool QUANT, typename Released>
-__device__ __forceinline__ void drain(const Fp8GemmParams& P, const Fp8Place& w, const FromTmem& load, bool second_first, uint32_t stg,
+__device__ __forceinline__ void drain(const Fp8GemmParams& P, const Fp8Place& w, const FromTmem& load, bool last_first, uint32_t stg,
                                       uint32_t lane, Released released) {
   if constexpr (QUANT) drain_fp8(P, w, load, stg, lane, released);
   else if (P.out32)
     drain_f32(P.out32 + static_cast<int64_t>(w.row) * P.cols + w.col, P.cols, P.cols - w.col, w.rows, load, stg, lane, released);
-  else drain_bf16(P, w, load, second_first, stg, lane, released);
+  else drain_bf16(P, w, load, last_first, stg, lane, released);
 }
 
 // ------------------------------------------------------------------ tiles that several runs share (CTAS = 1)
@@ -569,38 +561,50 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
       uint32_t phase = 0, armed = 0, armed_parity = 0;
       int32_t issued = 0;
       bool ok = true;
-      const uint32_t stage_bytes = static_cast<uint32_t>(P.mode == FP8_CONTRACT ? 128 : P.tile_rows) * 128 + C::B_BYTES;
+      const uint32_t block_bytes = static_cast<uint32_t>(P.mode == FP8_CONTRACT ? 128 : P.tile_rows) * 128 + C::B_BYTES;
       while (ok && walk.next(P, u)) {
         const int32_t a_row = u.a_row + static_cast<int32_t>(crank) * 128, b_row = u.b_row + static_cast<int32_t>(crank) * 128;
-        for (int32_t q = u.q0; q < u.q1; ++q) {
+        Fp8Block b = fp8_block(P, u, u.q0);
+        for (int32_t q = u.q0; q < u.q1; q += C::DEEP) {
+          const int32_t deep = min(u.q1 - q, C::DEEP);
           if (!wait(empty_bar(stage), phase ^ 1u, 1u)) {
             ok = false;
             break;
           }
           const bool drop = blockIdx.x == 0 && issued++ == P.drop;  // test hook: the consumer's wait runs out
+          // bytes of the stage: exponents with its first k-block and the first of every four
+          uint32_t bytes = deep * block_bytes;
+          const uint32_t fb = CTAS == 2 ? mapa_shared(full_bar(stage), 0) : full_bar(stage);
+          Fp8Block at[C::DEEP];
+          bool scales[C::DEEP];
+#pragma unroll
+          for (int d = 0; d < C::DEEP; ++d) {
+            at[d] = b;
+            scales[d] = d < deep && (q + d == u.q0 || (b.k & 3) == 0);
+            bytes += scales[d] ? C::E_BYTES : 0u;
+            if (++b.k == P.kb && P.mode == FP8_DENSE) b = fp8_block(P, u, q + d + 1);
+          }
           if (!drop) {
-            const Fp8Block b = fp8_block(P, u, q);
-            const bool scales = q == u.q0 || (b.k & 3) == 0;
-            const uint32_t bytes = stage_bytes + (scales ? C::EA_BYTES + C::EB_BYTES : 0u);
-            const uint32_t sa = base + C::A_OFF + stage * C::A_BYTES, sb = base + C::B_OFF + stage * C::B_BYTES,
-                           se = base + C::E_OFF + stage * C::E_BYTES;
-            if (CTAS == 2) {
-              const uint32_t fb = mapa_shared(full_bar(stage), 0);
-              if (leader) mbar_arrive_expect_tx(full_bar(stage), 2 * bytes);
-              tma_load_2d_pair(sa, &P.a[b.ai], fb, b.k * 128, a_row);
-              tma_load_2d_pair(sb, &P.b[b.bi], fb, b.k * 128, b_row);
-              if (scales) {
-                tma_load_3d_pair_plain(se, &P.ea[b.ai], fb, 0, b.k >> 2, u.ea + static_cast<int32_t>(crank));
-                tma_load_3d_pair_plain(se + C::EA_BYTES, &P.eb[b.bi], fb, 0, b.k >> 2, u.eb);
-              }
-            } else {
-              const uint32_t fb = full_bar(stage);
-              mbar_arrive_expect_tx(fb, bytes);
-              tma_load_2d(sa, &P.a[b.ai], fb, b.k * 128, a_row);
-              tma_load_2d(sb, &P.b[b.bi], fb, b.k * 128, b_row);
-              if (scales) {
-                tma_load_3d_plain(se, &P.ea[b.ai], fb, 0, b.k >> 2, u.ea);
-                tma_load_3d_plain(se + C::EA_BYTES, &P.eb[b.bi], fb, 0, b.k >> 2, u.eb);
+            if (leader) mbar_arrive_expect_tx(full_bar(stage), CTAS * bytes);
+#pragma unroll
+            for (int d = 0; d < C::DEEP; ++d) {
+              if (d >= deep) continue;
+              const CUtensorMap *am = &P.a[at[d].ai], *bm = &P.b[at[d].bi];
+              const uint32_t sa = C::a(base, stage, d), sb = C::b(base, stage, d), se = C::e(base, stage, d);
+              if (CTAS == 2) {
+                tma_load_2d_pair(sa, am, fb, at[d].k * 128, a_row);
+                tma_load_2d_pair(sb, bm, fb, at[d].k * 128, b_row);
+                if (scales[d]) {
+                  tma_load_3d_pair_plain(se, &P.ea[at[d].ai], fb, 0, at[d].k >> 2, u.ea + static_cast<int32_t>(crank));
+                  tma_load_3d_pair_plain(se + C::EA_BYTES, &P.eb[at[d].bi], fb, 0, at[d].k >> 2, u.eb);
+                }
+              } else {
+                tma_load_2d(sa, am, fb, at[d].k * 128, a_row);
+                tma_load_2d(sb, bm, fb, at[d].k * 128, b_row);
+                if (scales[d]) {
+                  tma_load_3d_plain(se, &P.ea[at[d].ai], fb, 0, at[d].k >> 2, u.ea);
+                  tma_load_3d_plain(se + C::EA_BYTES, &P.eb[at[d].bi], fb, 0, at[d].k >> 2, u.eb);
+                }
               }
             }
             armed |= 1u << stage;
@@ -628,27 +632,32 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
         // before that, and with the columns that both accumulators have
         if (n > 0 && !wait(begun_bar, n - 1, 2u)) break;
         tc_fence_after();
-        const uint32_t d = tmem + ((n & 1) ? C::ACC1 : 0);
+        const uint32_t d_tmem = tmem + ((n & 1) ? C::ACC1 : 0);
         uint32_t sf = tmem + C::SF;
-        for (int32_t q = u.q0; q < u.q1; ++q) {
+        int32_t k = fp8_block(P, u, u.q0).k;
+        for (int32_t q = u.q0; q < u.q1; q += C::DEEP) {
           if (!wait(full_bar(stage), phase, 3u)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const int32_t k = fp8_block(P, u, q).k;
-          const uint32_t sa = base + C::A_OFF + stage * C::A_BYTES, sb = base + C::B_OFF + stage * C::B_BYTES,
-                         se = base + C::E_OFF + stage * C::E_BYTES;
-          if (q == u.q0 || (k & 3) == 0) {
-            // copies and MMAs of a thread run in the order in which they are issued
-            sf = tmem + C::SF + (quads++ & 1) * 16;
 #pragma unroll
-            for (int i = 0; i < 1 + CTAS; ++i) tmem_cp_scales<CTAS>(sf + 4 * i, se + 512 * i);
+          for (int d = 0; d < C::DEEP; ++d) {
+            if (q + d >= u.q1) continue;
+            if (q + d == u.q0 || (k & 3) == 0) {
+              // copies and MMAs of a thread run in the order in which they are issued
+              sf = tmem + C::SF + (quads++ & 1) * 16;
+              const uint32_t se = C::e(base, stage, d);
+#pragma unroll
+              for (int i = 0; i < 1 + CTAS; ++i) tmem_cp_scales<CTAS>(sf + 4 * i, se + 512 * i);
+            }
+            const uint32_t idesc = make_idesc_mxf8(128 * CTAS, C::BN, k & 3);
+            const uint64_t ad = make_sw128_desc(C::a(base, stage, d), 16, 1024), bd = make_sw128_desc(C::b(base, stage, d), 16, 1024);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              umma_mxf8<CTAS>(d_tmem, ad + 2 * i, bd + 2 * i, idesc, sf, sf + 4, (q + d > u.q0 || i > 0) ? 1u : 0u);
+            if (++k == P.kb && P.mode == FP8_DENSE) k = 0;
           }
-          const uint32_t idesc = make_idesc_mxf8(128 * CTAS, C::BN, k & 3);
-          const uint64_t ad = make_sw128_desc(sa, 16, 1024), bd = make_sw128_desc(sb, 16, 1024);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) umma_mxf8<CTAS>(d, ad + 2 * i, bd + 2 * i, idesc, sf, sf + 4, (q > u.q0 || i > 0) ? 1u : 0u);
           if (CTAS == 2) umma_commit_pair(empty_bar(stage), 0x3);
           else umma_commit(empty_bar(stage));
           if (++stage == STAGES) {
