@@ -7,18 +7,18 @@
 // An expert whose logit is -infinity or NaN is closed.
 //
 // The choice is the one that exact arithmetic makes.  The scores are formed
-// in fp32, within kBand of their values; where two that the choice has to
-// tell apart are nearer than that, the warp forms the row's scores again in
-// 64 bits and chooses by those (about one row in two hundred of 256 experts
-// with a bias; the GPU has few 64-bit units, so that a row takes as long as
-// some hundred others).  Without a bias and groups no score is compared at
-// all: both functions grow with the logit, and the logits are exact.
+// in fp32, within band_of() of their values; where two that the choice has to
+// tell apart are nearer than that, the warp forms the row's scores again as
+// pairs of fp32 numbers, to some 2^-45 (in 64-bit arithmetic, for which the GPU
+// has few units, such a row took 16 us), and chooses by those.  Without a bias
+// and groups no score is compared at all: both functions grow with the logit,
+// and the logits are exact.
 //
-// A warp has a row, its experts spread over the lanes (expert 32 i + lane in
-// register i).  A largest value is found by two reductions over the warp, of
-// its bits in an order-preserving form and of the lowest expert that has it.
-// Bound by latency: 4 MB of logits of 8192 tokens take 0.7 us at the copy
-// rate.
+// A warp has a row, lane t the experts PER t .. PER t + PER - 1, so that a row
+// is read in vectors, a group of experts is a few neighbouring lanes, and the
+// lowest lane with a value has the lowest expert.  A largest value is found by
+// one reduction over the warp of its bits in an order-preserving form, and the
+// lane that has it looks which expert it is.  Bound by instructions: ...
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -37,11 +37,13 @@ constexpr int kMaxExperts = TP_ROUTE_MAX_EXPERTS, kMaxK = 32, kMaxGroups = 32;
 constexpr int kWarps = 4;  // of a thread block
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr uint32_t kNone = 0xFFFFFFFFu;
-// How near two fp32 scores (with their biases, relative to the larger of 1
-// and |v|) may be and still be told apart: the sum over the row has an error
-// of PER + 5 roundings of 2^-24, expf, the division and the addition some
-// units each, and there are two of them.
-constexpr float band_of(int per) { return static_cast<float>(per + 12) * 1.1920929e-7f; }
+// How near two fp32 values (relative to the larger of 1 and |v|) may be and
+// still be told apart, in units of 2^-23.  Sigmoid: exp and the reciprocal are
+// off by one unit of theirs, 1 + exp and the sum with the bias by half: with
+// s (1 - s) <= 1/4 that is 2.3 units of a value up to 1, for two of them 4.6.
+// Softmax: the sum over the row has PER + 5 additions of positive values.
+constexpr float kUlp = 1.1920929e-7f;
+__device__ __forceinline__ float band_of(int per, bool sigmoid) { return (sigmoid ? 6 : per + 12) * kUlp; }
 
 struct RouteParams {
   const void* logits;
@@ -54,31 +56,102 @@ struct RouteParams {
   int64_t T;
   int32_t E, k, groups, tops, best;
   int32_t f32, sigmoid, renorm;
+  int32_t vector;       // a lane's logits are one aligned vector
+  int32_t group_lanes;  // lanes of a group, 0: groups do not end between lanes
   float scale;
 };
 
+// Order-preserving bits: a larger number for a larger value.
 __device__ __forceinline__ uint32_t ordered(float v) {
   const uint32_t b = __float_as_uint(v);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
 }
-__device__ __forceinline__ uint64_t ordered(double v) {
-  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v));
-  return b >> 63 ? ~b : b | 0x8000000000000000ull;
+__device__ __forceinline__ float unordered(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
+constexpr uint32_t kShut = 0x007FFFFFu;  // ordered(-infinity)
+
+// ------------------------------------------------------------------ pairs of fp32 numbers
+//
+// hi + lo, |lo| at most half a unit in hi's last place; sums and products by
+// Dekker (1971) and Knuth (TAOCP 2, 4.2.2), with the product's error from a
+// fused multiply-add.
+
+struct Df {
+  float hi, lo;
+};
+__device__ __forceinline__ Df two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
 }
+__device__ __forceinline__ Df quick_sum(float a, float b) {  // |a| >= |b|
+  const float s = __fadd_rn(a, b);
+  return {s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+__device__ __forceinline__ Df add(Df a, Df b) {
+  const Df s = two_sum(a.hi, b.hi), t = two_sum(a.lo, b.lo);
+  const Df u = quick_sum(s.hi, __fadd_rn(s.lo, t.hi));
+  return quick_sum(u.hi, __fadd_rn(u.lo, t.lo));
+}
+__device__ __forceinline__ Df mul(Df a, Df b) {
+  const float p = __fmul_rn(a.hi, b.hi);
+  return quick_sum(p, __fadd_rn(__fmaf_rn(a.hi, b.hi, -p), __fmaf_rn(a.hi, b.lo, __fmul_rn(a.lo, b.hi))));
+}
+
+// exp(x) for x <= 0, 0 below -80: x = n ln 2 + 4 y, |y| < 0.087, with ln 2 in
+// three parts (the first of 16 bits, so that n times it is exact), the series
+// of exp(y) up to y^8, and two squarings.
+__device__ __forceinline__ Df exp_df(Df x) {
+  const float n = rintf(x.hi * 1.44269504f);
+  const float r1 = __fmaf_rn(-n, 0x1.62e4p-1f, x.hi);
+  const float c2 = 0x1.7f7d1cp-20f, p = __fmul_rn(n, c2), pe = __fmaf_rn(n, c2, -p);
+  Df r = add(two_sum(r1, x.lo), Df{-p, -pe});
+  r = quick_sum(r.hi, __fadd_rn(r.lo, -n * 0x1.ef357ap-45f));
+  const Df y = {0.25f * r.hi, 0.25f * r.lo};
+  const float q = fmaf(fmaf(fmaf(y.hi, 1.f / 40320.f, 1.f / 5040.f), y.hi, 1.f / 720.f), y.hi, 1.f / 120.f);
+  Df h = add(Df{0x1.555556p-5f, -0x1.555556p-30f}, Df{y.hi * q, 0.f});
+  h = add(Df{0x1.555556p-3f, -0x1.555556p-28f}, mul(y, h));
+  h = add(Df{0.5f, 0.f}, mul(y, h));
+  h = add(Df{1.f, 0.f}, mul(y, h));
+  h = add(Df{1.f, 0.f}, mul(y, h));
+  h = mul(h, h);
+  h = mul(h, h);
+  const float two = __uint_as_float(static_cast<uint32_t>(static_cast<int32_t>(n) + 127) << 23);
+  return x.hi < -80.f ? Df{0.f, 0.f} : Df{h.hi * two, h.lo * two};
+}
+__device__ __forceinline__ Df inverse(Df d) {  // of 1 and above
+  const float q = __fdiv_rn(1.f, d.hi);
+  return quick_sum(q, q * __fmaf_rn(-q, d.lo, __fmaf_rn(-q, d.hi, 1.f)));
+}
+__device__ __forceinline__ Df shfl(Df v, int lane) { return {__shfl_sync(kAll, v.hi, lane), __shfl_sync(kAll, v.lo, lane)}; }
+__device__ __forceinline__ Df shfl_xor(Df v, int o) { return {__shfl_xor_sync(kAll, v.hi, o), __shfl_xor_sync(kAll, v.lo, o)}; }
+__device__ __forceinline__ bool greater(Df a, Df b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
+__device__ __forceinline__ bool open(Df v) { return v.hi > -INFINITY; }
+__device__ __forceinline__ Df larger(Df a, Df b) { return greater(b, a) ? b : a; }
+__device__ __forceinline__ Df smaller(Df a, Df b) { return greater(b, a) ? a : b; }
+
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float shfl(float v, int lane) { return __shfl_sync(kAll, v, lane); }
+__device__ __forceinline__ float shfl_xor(float v, int o) { return __shfl_xor_sync(kAll, v, o); }
+__device__ __forceinline__ bool greater(float a, float b) { return a > b; }
+__device__ __forceinline__ bool open(float v) { return v > -INFINITY; }
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
+
+template <typename T>
+__device__ __forceinline__ T of(float v) {
+  if constexpr (sizeof(T) == 8) return T{v, 0.f};
+  else return v;
+}
+
 __device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(kAll, v); }
 __device__ __forceinline__ uint64_t warp_max(uint64_t v) {
   const uint32_t hi = warp_max(static_cast<uint32_t>(v >> 32));
   const uint32_t lo = warp_max(static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
   return static_cast<uint64_t>(hi) << 32 | lo;
 }
-__device__ __forceinline__ double warp_sum(double v) {
+template <typename T>
+__device__ __forceinline__ T warp_sum(T v) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-  return v;
-}
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  for (int o = 16; o; o >>= 1) v = add(v, shfl_xor(v, o));
   return v;
 }
 
@@ -87,175 +160,377 @@ __device__ __forceinline__ float clean(float l) {
   return l > -INFINITY ? fminf(l, FLT_MAX) + 0.f : -INFINITY;  // one zero
 }
 
+// PER neighbours of a row, as one vector where rows and pointer allow it.
 template <int PER>
 __device__ __forceinline__ void load_row(const RouteParams& P, int64_t row, uint32_t lane, float (&l)[PER]) {
+  const int32_t e0 = static_cast<int32_t>(lane) * PER;
+  const int64_t at = row * P.E + e0;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int32_t e = i * 32 + static_cast<int32_t>(lane);
-    l[i] = -INFINITY;
-    if (e < P.E) {
-      const int64_t at = row * P.E + e;
-      l[i] = clean(P.f32 ? static_cast<const float*>(P.logits)[at] : __bfloat162float(static_cast<const __nv_bfloat16*>(P.logits)[at]));
+  for (int i = 0; i < PER; ++i) l[i] = -INFINITY;
+  if (P.vector) {
+    if (e0 < P.E) {
+      if (P.f32) {
+        const float4* from = reinterpret_cast<const float4*>(static_cast<const float*>(P.logits) + at);
+        if constexpr (PER >= 4) {
+#pragma unroll
+          for (int i = 0; i < PER / 4; ++i) {
+            const float4 f = from[i];
+            l[4 * i] = f.x, l[4 * i + 1] = f.y, l[4 * i + 2] = f.z, l[4 * i + 3] = f.w;
+          }
+        } else {
+          const float2 f = *reinterpret_cast<const float2*>(from);
+          l[0] = f.x, l[1] = f.y;
+        }
+      } else {
+        const uint32_t* from = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(P.logits) + at);
+        uint32_t w[PER / 2];
+        if constexpr (PER >= 8) {
+#pragma unroll
+          for (int i = 0; i < PER / 8; ++i) {
+            const uint4 u = reinterpret_cast<const uint4*>(from)[i];
+            w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+          }
+        } else if constexpr (PER == 4) {
+          const uint2 u = *reinterpret_cast<const uint2*>(from);
+          w[0] = u.x, w[1] = u.y;
+        } else {
+          w[0] = *from;
+        }
+#pragma unroll
+        for (int i = 0; i < PER / 2; ++i) l[2 * i] = bf_lo(w[i]), l[2 * i + 1] = bf_hi(w[i]);
+      }
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (e0 + i < P.E) l[i] = P.f32 ? static_cast<const float*>(P.logits)[at + i] : __bfloat162float(static_cast<const __nv_bfloat16*>(P.logits)[at + i]);
   }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) l[i] = clean(l[i]);
 }
 
-template <typename T>
-__device__ __forceinline__ T exp_of(T x) {
-  if constexpr (sizeof(T) == 8) return exp(x);
-  else return expf(x);
-}
+__device__ __forceinline__ float inverse(float x) { return rcp_approx(x); }  // of 1 .. infinity; 0 for what is below 2^-126
+
+// What a softmax score is formed from: exp(l - top) * r.
+struct Norm {
+  float top, r;
+};
 
 // Scores of the row's experts; 0 of closed ones.
-template <typename T, int PER>
-__device__ __forceinline__ void scores(const RouteParams& P, const float (&l)[PER], T (&s)[PER]) {
-  if (P.sigmoid) {
+template <int PER>
+__device__ __forceinline__ Norm scores(const RouteParams& P, const float (&l)[PER], float (&s)[PER]) {
+  if (P.sigmoid) {  // exp(infinity) for a closed one: 0
 #pragma unroll
-    for (int i = 0; i < PER; ++i) s[i] = l[i] > -INFINITY ? T(1) / (T(1) + exp_of<T>(-static_cast<T>(l[i]))) : T(0);
-    return;
+    for (int i = 0; i < PER; ++i) s[i] = inverse(1.f + expf(-l[i]));
+    return {0.f, 1.f};
   }
   float top = -INFINITY;
 #pragma unroll
   for (int i = 0; i < PER; ++i) top = fmaxf(top, l[i]);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-  T sum = 0;
+  top = unordered(warp_max(ordered(top)));
+  if (top == -INFINITY) top = 0.f;
+  float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    // both finite, their difference perhaps not: then its exponential is 0
-    s[i] = l[i] > -INFINITY ? exp_of<T>(static_cast<T>(l[i]) - static_cast<T>(top)) : T(0);
+    s[i] = expf(l[i] - top);
     sum += s[i];
   }
   sum = warp_sum(sum);
-  const T r = sum > 0 ? T(1) / sum : T(0);
+  const float r = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) s[i] *= r;
+  return {top, r};
+}
+
+__device__ __forceinline__ float logit(const RouteParams& P, int64_t row, uint32_t e) {
+  const int64_t at = row * P.E + e;
+  return clean(P.f32 ? static_cast<const float*>(P.logits)[at] : __bfloat162float(static_cast<const __nv_bfloat16*>(P.logits)[at]));
+}
+
+// A lane's experts in falling order of v (ordered values), the lower expert
+// first of equal ones: neighbours are exchanged where the second is larger.
+template <int PER>
+__device__ __forceinline__ void sort(uint32_t (&v)[PER], uint32_t (&at)[PER]) {
+#pragma unroll
+  for (int n = PER - 1; n > 0; --n)
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const bool less = v[i] < v[i + 1];
+      const uint32_t a = v[i], b = v[i + 1], c = at[i], d = at[i + 1];
+      v[i] = less ? b : a;
+      v[i + 1] = less ? a : b;
+      at[i] = less ? d : c;
+      at[i + 1] = less ? c : d;
+    }
 }
 
 // The chosen experts, in order: choice j in lane j of `mine` (kNone: none).
-// False if two values that the choice compares are within `band`.  v is used
-// up; it is -infinity where an expert cannot be chosen.
-template <typename T, int PER>
-__device__ __forceinline__ bool choose(const RouteParams& P, const float (&l)[PER], T (&v)[PER], float band, uint32_t lane, uint32_t& mine) {
+// False if two of the values that the choice compares are within `band`
+// (> 0; only with a bias) and do not tie exactly;
+// lowest: the last of those.  v: ordered values, kShut or less where an expert cannot be chosen.
+template <int PER>
+__device__ __forceinline__ bool choose(const RouteParams& P, int64_t row, uint32_t (&v)[PER], float band, uint32_t lane, uint32_t& mine,
+                                       float& lowest) {
   bool clear = true;
-  T before = 0;
-  float l_before = 0.f, b_before = 0.f;
   mine = kNone;
-  const T shut = -INFINITY;
+  uint32_t at[PER], last = kNone;
+  float before = 0.f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) at[i] = lane * PER + i;
+  sort<PER>(v, at);
   const int32_t rounds = band > 0.f ? P.k + 1 : P.k;  // the first that is left out has to be told apart too
   for (int32_t j = 0; j < rounds; ++j) {
-    T own = shut;
-    int at = 0;
+    const uint32_t top = warp_max(v[0]);
+    if (top <= kShut) break;
+    const uint32_t owner = __ffs(__ballot_sync(kAll, v[0] == top)) - 1, who = __shfl_sync(kAll, at[0], owner);
+    if (static_cast<int32_t>(lane) == j) mine = who;
+    const bool own = lane == owner;
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (v[i] > own) {
-        own = v[i];
-        at = i;
-      }
-    const auto top = warp_max(ordered(own));
-    if (top == ordered(shut)) break;
-    const uint32_t who = __reduce_min_sync(kAll, ordered(own) == top ? at * 32 + lane : kNone);
-    const T val = __shfl_sync(kAll, own, who & 31);
-    if (j < P.k && static_cast<int32_t>(lane) == j) mine = who;
-    const int slot = static_cast<int>(who >> 5);
-    float lv = 0.f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (i == slot) {
-        lv = l[i];
-        if ((who & 31) == lane) v[i] = shut;
-      }
-    if (band > 0.f) {
-      // equal logits and biases are equal exactly
-      lv = __shfl_sync(kAll, lv, who & 31);
-      const float b = P.bias[who];
-      if (j > 0 && before - val <= static_cast<T>(band) * fmaxf(1.f, fabsf(static_cast<float>(val))) && !(lv == l_before && b == b_before))
-        clear = false;
-      l_before = lv;
-      b_before = b;
+    for (int i = 0; i + 1 < PER; ++i) {
+      v[i] = own ? v[i + 1] : v[i];
+      at[i] = own ? at[i + 1] : at[i];
     }
-    before = val;
+    if (own) v[PER - 1] = 0;
+    if (band > 0.f) {
+      const float val = unordered(top);
+      if (j > 0 && before - val <= band * fmaxf(1.f, fabsf(val)) && !(P.bias[last] == P.bias[who] && logit(P, row, last) == logit(P, row, who)))
+        clear = false;
+      before = lowest = val;
+      last = who;
+    }
   }
+  if (static_cast<int32_t>(lane) >= P.k) mine = kNone;
   return clear;
 }
 
-// Closes the experts of groups that are not among the best.
+// Whether a lane's group is among the best; score: the group's, `lanes` lanes
+// each.  near: the last that is and the first that is not are within `band`.
+template <typename T>
+__device__ __forceinline__ bool among_best(const RouteParams& P, T score, int32_t group, int32_t lanes, float band, bool& near) {
+  int32_t rank = 0;
+#pragma unroll 1
+  for (int32_t g = 0; g < P.groups; ++g) {
+    const T other = shfl(score, g * lanes);
+    if (greater(other, score) || (!greater(score, other) && g < group)) ++rank;
+  }
+  near = false;
+  if constexpr (sizeof(T) == 4) {
+    if (band > 0.f && P.tops < P.groups) {
+      const bool real = group < P.groups;
+      const float last = unordered(warp_max(real && rank == P.tops - 1 ? ordered(score) : 0u)),
+                  first = unordered(warp_max(real && rank == P.tops ? ordered(score) : 0u));
+      near = first > -INFINITY && last - first <= 2.f * band * fmaxf(1.f, fabsf(last));
+    }
+  }
+  return group < P.groups && rank < P.tops && open(score);
+}
+
+// Closes the experts (v: -infinity) of groups that are not among the best;
+// false if that is within `band`.
 template <typename T, int PER>
 __device__ __forceinline__ bool keep_groups(const RouteParams& P, T (&v)[PER], float band, uint32_t lane) {
-  const T shut = -INFINITY;
+  const T shut = of<T>(-INFINITY);
   const int32_t size = P.E / P.groups;
+  bool near;
+  if (P.group_lanes > 0) {  // a group is that many neighbouring lanes, a power of two
+    T a = shut, b = shut;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      b = larger(b, smaller(a, v[i]));
+      a = larger(a, v[i]);
+    }
+    for (int o = 1; o < P.group_lanes; o <<= 1) {
+      const T c = shfl_xor(a, o), d = shfl_xor(b, o);
+      b = larger(smaller(a, c), larger(b, d));
+      a = larger(a, c);
+    }
+    const T score = P.best == 2 && open(b) ? add(a, b) : a;
+    if (!among_best<T>(P, score, static_cast<int32_t>(lane) / P.group_lanes, P.group_lanes, band, near)) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) v[i] = shut;
+    }
+    return !near;
+  }
   T score = shut;  // of group `lane`
   for (int32_t g = 0; g < P.groups; ++g) {
-    T sum = shut;
-    uint32_t taken = kNone;
-    for (int32_t b = 0; b < P.best; ++b) {
-      T own = shut;
-      uint32_t at = kNone;
+    T a = shut, b = shut;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const uint32_t e = i * 32 + lane;
-        if (static_cast<int32_t>(e) >= g * size && static_cast<int32_t>(e) < (g + 1) * size && e != taken && v[i] > own) {
-          own = v[i];
-          at = e;
-        }
+    for (int i = 0; i < PER; ++i) {
+      const int32_t e = static_cast<int32_t>(lane) * PER + i;
+      if (e >= g * size && e < (g + 1) * size) {
+        b = larger(b, smaller(a, v[i]));
+        a = larger(a, v[i]);
       }
-      const auto top = warp_max(ordered(own));
-      if (top == ordered(shut)) break;
-      taken = __reduce_min_sync(kAll, ordered(own) == top ? at : kNone);
-      const T val = __shfl_sync(kAll, own, taken & 31);
-      sum = b == 0 ? val : sum + val;
     }
-    if (static_cast<int32_t>(lane) == g) score = sum;
-  }
-  // rank of each group among all
-  bool clear = true;
-  int32_t rank = 0;
-  for (int32_t g = 0; g < P.groups; ++g) {
-    const T other = __shfl_sync(kAll, score, g);
-    if (other > score || (other == score && g < static_cast<int32_t>(lane))) ++rank;
-  }
-  const bool in = static_cast<int32_t>(lane) < P.groups && rank < P.tops && score > shut;
-  if (band > 0.f && P.tops < P.groups) {
-    // the last that stays and the first that goes
-    T last = in ? score : static_cast<T>(INFINITY), first = !in && static_cast<int32_t>(lane) < P.groups ? score : shut;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const T a = __shfl_xor_sync(kAll, last, o), b = __shfl_xor_sync(kAll, first, o);
-      last = a < last ? a : last;
-      first = b > first ? b : first;
+    for (int o = 1; o < 32; o <<= 1) {
+      const T c = shfl_xor(a, o), d = shfl_xor(b, o);
+      b = larger(smaller(a, c), larger(b, d));
+      a = larger(a, c);
     }
-    if (first > shut && last - first <= static_cast<T>(2 * band) * fmaxf(1.f, fabsf(static_cast<float>(last)))) clear = false;
+    if (static_cast<int32_t>(lane) == g) score = P.best == 2 && open(b) ? add(a, b) : a;
   }
-  const uint32_t kept = __ballot_sync(kAll, in);
+  const uint32_t kept = __ballot_sync(kAll, among_best<T>(P, score, static_cast<int32_t>(lane), 1, band, near));
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const uint32_t e = i * 32 + lane;
-    if (static_cast<int32_t>(e) < P.E && !(kept >> (e / size) & 1u)) v[i] = shut;
+    const int32_t e = static_cast<int32_t>(lane) * PER + i;
+    if (e < P.E && !(kept >> (e / size) & 1u)) v[i] = shut;
   }
-  return clear;
+  return !near;
 }
 
+// The values that the choice goes by, from the scores.
 template <typename T, int PER>
-__device__ __forceinline__ bool select(const RouteParams& P, const float (&l)[PER], const T (&s)[PER], float band, uint32_t lane,
-                                       uint32_t& mine) {
-  T v[PER];
-  const bool by_logit = P.bias == nullptr && (P.groups == 1 || P.best == 1);
+__device__ __forceinline__ void values(const RouteParams& P, const float (&l)[PER], const T (&s)[PER], uint32_t lane, T (&v)[PER]) {
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int32_t e = i * 32 + static_cast<int32_t>(lane);
-    if (by_logit) v[i] = static_cast<T>(l[i]);
-    else v[i] = l[i] > -INFINITY ? s[i] + (P.bias && e < P.E ? static_cast<T>(P.bias[e]) : T(0)) : static_cast<T>(-INFINITY);
+    const int32_t e = static_cast<int32_t>(lane) * PER + i;
+    v[i] = l[i] > -INFINITY ? (P.bias ? add(s[i], of<T>(P.bias[e])) : s[i]) : of<T>(-INFINITY);
   }
-  bool clear = true;
-  if (P.groups > 1) {
-    clear = keep_groups<T, PER>(P, v, by_logit ? 0.f : band, lane);
-    if (P.bias == nullptr && !by_logit) {  // what is left is told apart by its logits
+}
+
+// Sigmoid: t = exp(-|l|), then 1 / (1 + t), or t times that.
+__device__ __forceinline__ Df sigmoid_df(float l) {
+  const Df t = exp_df(Df{-fminf(fabsf(l), 100.f), 0.f}), u = inverse(add(Df{1.f, 0.f}, t));
+  return l >= 0.f ? u : mul(t, u);
+}
+
+// The choice by scores as pairs, for rows that need it.
+template <int PER>
+__device__ __noinline__ uint32_t choose_exactly(const RouteParams& P, int64_t row, uint32_t lane) {
+  float l[PER];
+  Df v[PER];
+  load_row<PER>(P, row, lane, l);
+  if (P.sigmoid) {
 #pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (v[i] > static_cast<T>(-INFINITY)) v[i] = static_cast<T>(l[i]);
+    for (int i = 0; i < PER; ++i) v[i] = sigmoid_df(l[i]);
+  } else {
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) top = fmaxf(top, l[i]);
+    top = unordered(warp_max(ordered(top)));
+    if (top == -INFINITY) top = 0.f;
+    Df sum = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      v[i] = l[i] > -INFINITY ? exp_df(l[i] - top < -100.f ? Df{-100.f, 0.f} : two_sum(l[i], -top)) : Df{0.f, 0.f};
+      sum = add(sum, v[i]);
+    }
+    sum = warp_sum(sum);
+    const Df r = sum.hi > 0.f ? inverse(sum) : Df{0.f, 0.f};  // the largest score's exponential is 1
+#pragma unroll
+    for (int i = 0; i < PER; ++i) v[i] = mul(v[i], r);
+  }
+  values<Df, PER>(P, l, v, lane, v);
+  if (P.groups > 1) keep_groups<Df, PER>(P, v, 0.f, lane);
+  // without a bias what is left is told apart by its logits
+  uint64_t key[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const Df x = P.bias ? v[i] : Df{l[i], 0.f};
+    key[i] = open(v[i]) ? static_cast<uint64_t>(ordered(x.hi)) << 32 | ordered(x.lo + 0.f) : 0u;
+  }
+  uint32_t mine = kNone;
+  for (int32_t j = 0; j < P.k; ++j) {
+    uint64_t best = 0;
+    uint32_t which = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        which = i;
+      }
+    const uint64_t most = warp_max(best);
+    if (most == 0) break;
+    const uint32_t owner = __ffs(__ballot_sync(kAll, best == most)) - 1;
+    const uint32_t who = owner * PER + __shfl_sync(kAll, which, owner);
+    if (static_cast<int32_t>(lane) == j) mine = who;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (lane == owner && static_cast<uint32_t>(i) == which) key[i] = 0;
+  }
+  return mine;
+}
+
+// The same where the groups are clear and a score is its logit's alone: only
+// the experts from `least` on, one a lane.  `few`: a warp's memory.  kMany if
+// there are more of them than lanes.
+struct Few {
+  uint32_t e[32];
+  float l[32];
+};
+constexpr uint32_t kMany = 0xFFFFFFFEu;
+template <int PER>
+__device__ __noinline__ uint32_t choose_among_few(const RouteParams& P, int64_t row, float least, Few* few, uint32_t lane) {
+  float l[PER], s[PER], v[PER];
+  load_row<PER>(P, row, lane, l);
+  scores<PER>(P, l, s);
+  values<float, PER>(P, l, s, lane, v);
+  if (P.groups > 1) keep_groups<float, PER>(P, v, 0.f, lane);
+  uint32_t n = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const bool in = v[i] >= least;
+    const uint32_t mask = __ballot_sync(kAll, in), at = n + __popc(mask & ((1u << lane) - 1));
+    if (in && at < 32) {
+      few->e[at] = lane * PER + i;
+      few->l[at] = l[i];
+    }
+    n += __popc(mask);
+  }
+  if (n > 32) return kMany;
+  __syncwarp();
+  Df mine = {-INFINITY, 0.f};
+  uint32_t e = kNone;
+  if (lane < n) {
+    e = few->e[lane];
+    mine = add(sigmoid_df(few->l[lane]), Df{P.bias[e], 0.f});
+  }
+  uint32_t rank = 0;
+  for (uint32_t i = 0; i < n; ++i) {
+    const Df other = shfl(mine, i);
+    const uint32_t oe = __shfl_sync(kAll, e, i);
+    if (greater(other, mine) || (!greater(mine, other) && oe < e)) ++rank;
+  }
+  __syncwarp();
+  if (lane < n) few->e[rank] = e;
+  __syncwarp();
+  const uint32_t out = lane < n && static_cast<int32_t>(lane) < P.k ? few->e[lane] : kNone;
+  __syncwarp();
+  return out;
+}
+
+// The chosen experts of a row, choice j in lane j, and what their scores are
+// formed from.
+template <int PER>
+__device__ __forceinline__ uint32_t select(const RouteParams& P, int64_t row, Few* few, uint32_t lane, Norm& norm) {
+  float l[PER], s[PER];
+  load_row<PER>(P, row, lane, l);
+  const bool by_logit = P.bias == nullptr && (P.groups == 1 || P.best == 1);  // both scores grow with it
+  if (!by_logit || !P.sigmoid) norm = scores<PER>(P, l, s);
+  uint32_t key[PER], mine;
+  float lowest = 0.f;
+  if (by_logit) {
+    if (P.groups > 1) keep_groups<float, PER>(P, l, 0.f, lane);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) key[i] = ordered(l[i]);
+    choose<PER>(P, row, key, 0.f, lane, mine, lowest);
+    return mine;
+  }
+  const float band = band_of(PER, P.sigmoid);
+  float v[PER];
+  values<float, PER>(P, l, s, lane, v);
+  const bool clear = P.groups == 1 || keep_groups<float, PER>(P, v, band, lane);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) key[i] = open(v[i]) ? ordered(P.bias ? v[i] : l[i]) : 0u;
+  if (clear) {
+    if (choose<PER>(P, row, key, P.bias ? band : 0.f, lane, mine, lowest)) return mine;
+    if (P.sigmoid) {
+      mine = choose_among_few<PER>(P, row, lowest - 2.f * band * fmaxf(1.f, fabsf(lowest)), few, lane);
+      if (mine != kMany) return mine;
     }
   }
-  return choose<T, PER>(P, l, v, P.bias == nullptr ? 0.f : band, lane, mine) && clear;
+  return choose_exactly<PER>(P, row, lane);
 }
 
 // The value of expert e, another one for each lane; 0 for none.
@@ -264,53 +539,65 @@ __device__ __forceinline__ float pick(const float (&s)[PER], uint32_t e) {
   float v = 0.f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const float o = __shfl_sync(kAll, s[i], e & 31);
-    if (e != kNone && static_cast<uint32_t>(i) == e >> 5) v = o;
+    const float o = __shfl_sync(kAll, s[i], (e / PER) & 31);
+    if (e != kNone && e % PER == i) v = o;
   }
   return v;
 }
 
 template <int PER>
 __global__ void __launch_bounds__(kWarps * 32) route_fwd_kernel(const __grid_constant__ RouteParams P) {
-  extern __shared__ int32_t hist[];
+  __shared__ Few few[kWarps];
+  __shared__ int32_t hist[kMaxExperts];
   griddep_wait();
   griddep_launch_dependents();
   const uint32_t lane = threadIdx.x & 31;
-  if (P.counts) {
+  const bool count = P.counts && gridDim.x == 1;  // of several blocks' rows: route_count_kernel
+  if (count) {
     for (int32_t e = threadIdx.x; e < P.E; e += kWarps * 32) hist[e] = 0;
     __syncthreads();
+  } else if (P.counts && blockIdx.x == 0) {
+    for (int32_t e = threadIdx.x; e < P.E; e += kWarps * 32) P.counts[e] = 0;
   }
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); row < P.T; row += static_cast<int64_t>(gridDim.x) * kWarps) {
-    float l[PER], s[PER];
-    load_row<PER>(P, row, lane, l);
-    scores<float, PER>(P, l, s);
-    uint32_t mine;
-    if (!select<float, PER>(P, l, s, band_of(PER), lane, mine)) {
-      double sd[PER];
-      scores<double, PER>(P, l, sd);
-      select<double, PER>(P, l, sd, 0.f, lane, mine);
+    Norm norm;
+    const uint32_t mine = select<PER>(P, row, few + (threadIdx.x >> 5), lane, norm);
+    float sc = 0.f;
+    if (mine != kNone) {
+      const float l = logit(P, row, mine);
+      sc = P.sigmoid ? inverse(1.f + expf(-l)) : expf(l - norm.top) * norm.r;
     }
-    const float sc = pick<PER>(s, mine);
     const float total = P.renorm ? fmaxf(warp_sum(sc), FLT_MIN) : 1.f;
     if (static_cast<int32_t>(lane) < P.k) {
       P.experts[row * P.k + lane] = mine == kNone ? -1 : static_cast<int32_t>(mine);
       P.weights[row * P.k + lane] = P.scale * (sc / total);
-      if (P.counts && mine != kNone) atomicAdd(hist + mine, 1);
+      if (count && mine != kNone) atomicAdd(hist + mine, 1);
     }
   }
-  if (P.counts) {
+  if (count) {
     __syncthreads();
-    for (int32_t e = threadIdx.x; e < P.E; e += kWarps * 32) {
-      if (gridDim.x == 1) P.counts[e] = hist[e];
-      else if (hist[e]) atomicAdd(P.counts + e, hist[e]);  // whole numbers: their sum has no order
-    }
+    for (int32_t e = threadIdx.x; e < P.E; e += kWarps * 32) P.counts[e] = hist[e];
   }
 }
 
-__global__ void route_clear_kernel(const __grid_constant__ RouteParams P) {
+// How often each expert was chosen, where several thread blocks had the rows
+// (which left zeros): some thousands of slots a block, so that the atomics on
+// the same few counters are few.  Whole numbers: their sum has no order.
+constexpr int kCountThreads = 512;
+__global__ void __launch_bounds__(kCountThreads) route_count_kernel(const __grid_constant__ RouteParams P) {
+  __shared__ int32_t hist[kMaxExperts];
   griddep_wait();
   griddep_launch_dependents();
-  for (int32_t e = threadIdx.x; e < P.E; e += blockDim.x) P.counts[e] = 0;
+  for (int32_t e = threadIdx.x; e < P.E; e += kCountThreads) hist[e] = 0;
+  __syncthreads();
+  const int64_t slots = P.T * P.k;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kCountThreads + threadIdx.x; i < slots; i += static_cast<int64_t>(gridDim.x) * kCountThreads) {
+    const int32_t e = __ldcg(P.experts + i);
+    if (e >= 0) atomicAdd(hist + e, 1);
+  }
+  __syncthreads();
+  for (int32_t e = threadIdx.x; e < P.E; e += kCountThreads)
+    if (hist[e]) atomicAdd(P.counts + e, hist[e]);
 }
 
 template <int PER>
@@ -321,7 +608,6 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const __grid_con
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); row < P.T; row += static_cast<int64_t>(gridDim.x) * kWarps) {
     float l[PER], s[PER];
     load_row<PER>(P, row, lane, l);
-    scores<float, PER>(P, l, s);
     uint32_t mine = kNone;
     float g = 0.f;
     if (static_cast<int32_t>(lane) < P.k) {
@@ -331,41 +617,67 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const __grid_con
         g = P.scale * P.dweights[row * P.k + lane];
       }
     }
-    const float sc = pick<PER>(s, mine);
+    // the chosen scores: sigmoid's from their own logits, and its gradient
+    // s (1 - s) without the difference
+    float sc, slope = 0.f;
+    if (P.sigmoid) {
+      const float x = pick<PER>(l, mine), t = expf(-fabsf(x)), u = inverse(1.f + t);
+      const bool open = mine != kNone && x > -INFINITY;
+      sc = open ? (x >= 0.f ? u : t * u) : 0.f;
+      slope = open ? t * u * u : 0.f;
+    } else {
+      scores<PER>(P, l, s);
+      sc = pick<PER>(s, mine);
+    }
     if (P.renorm) {  // w = s / sum s
-      const float total = fmaxf(warp_sum(sc), FLT_MIN);
-      const float all = warp_sum(g * sc) / total;
+      const float total = fmaxf(warp_sum(sc), FLT_MIN), all = warp_sum(g * sc) / total;
       g = mine == kNone ? 0.f : (g - all) / total;
     }
-    // the gradient of each expert's score
-    float ds[PER];
+    if (P.sigmoid) g *= slope;
+    // the gradient of each expert's score (sigmoid: logit)
+    float d[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) ds[i] = 0.f;
+    for (int i = 0; i < PER; ++i) d[i] = 0.f;
     for (int32_t j = 0; j < P.k; ++j) {
       const uint32_t e = __shfl_sync(kAll, mine, j);
       const float v = __shfl_sync(kAll, g, j);
+      if (e / PER == lane) {
 #pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (e == i * 32 + lane) ds[i] += v;
+        for (int i = 0; i < PER; ++i)
+          if (e % PER == i) d[i] += v;
+      }
     }
-    float dot = 0.f;
     if (!P.sigmoid) {
+      float dot = 0.f;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) dot += ds[i] * s[i];
+      for (int i = 0; i < PER; ++i) dot += d[i] * s[i];
       dot = warp_sum(dot);
-    }
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int32_t e = i * 32 + static_cast<int32_t>(lane);
-      if (e < P.E) {
-        float d = s[i] * (ds[i] - dot);
-        if (P.sigmoid) {  // s (1 - s) without the difference
-          const float t = expf(-fabsf(l[i]));
-          d = ds[i] * (t / ((1.f + t) * (1.f + t)));
+      for (int i = 0; i < PER; ++i) d[i] = s[i] * (d[i] - dot);
+    }
+    const int32_t e0 = static_cast<int32_t>(lane) * PER;
+    const int64_t at = row * P.E + e0;
+    if (P.vector) {
+      if (e0 < P.E) {
+        uint32_t w[PER];
+        const int n = P.f32 ? PER : PER / 2;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) w[i] = P.f32 ? __float_as_uint(d[i]) : 2 * i < PER ? pack_bf16(d[(2 * i) % PER], d[(2 * i + 1) % PER]) : 0u;
+        uint32_t* to = P.f32 ? reinterpret_cast<uint32_t*>(static_cast<float*>(P.dlogits) + at)
+                             : reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(P.dlogits) + at);
+#pragma unroll
+        for (int i = 0; i < PER; i += 4) {
+          if (PER >= 4 && i + 4 <= n) *reinterpret_cast<uint4*>(to + i) = make_uint4(w[i], w[(i + 1) % PER], w[(i + 2) % PER], w[(i + 3) % PER]);
+          else if (i + 2 <= n) *reinterpret_cast<uint2*>(to + i) = make_uint2(w[i], w[(i + 1) % PER]);
+          else if (i < n) to[i] = w[i];
         }
-        const int64_t at = row * P.E + e;
-        if (P.f32) static_cast<float*>(P.dlogits)[at] = d;
-        else static_cast<__nv_bfloat16*>(P.dlogits)[at] = __float2bfloat16_rn(d);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if (e0 + i >= P.E) continue;
+        if (P.f32) static_cast<float*>(P.dlogits)[at + i] = d[i];
+        else static_cast<__nv_bfloat16*>(P.dlogits)[at + i] = __float2bfloat16_rn(d[i]);
       }
     }
   }
@@ -409,12 +721,17 @@ void fill(RouteParams* P, const tp_route_desc* d, int64_t T, int64_t E, int64_t 
 unsigned grid_of(int64_t T) { return static_cast<unsigned>(std::min<int64_t>(cdiv(T, kWarps), 152 * 16)); }
 
 template <int PER>
-tp_status run(bool fwd, const RouteParams& P, cudaStream_t stream) {
-  return fwd ? launch_dependent(route_fwd_kernel<PER>, dim3(grid_of(P.T)), kWarps * 32, P.counts ? P.E * sizeof(int32_t) : 0, stream, P)
+tp_status run(bool fwd, RouteParams& P, cudaStream_t stream) {
+  const size_t size = (P.f32 ? 4 : 2) * PER;
+  P.vector = P.E % PER == 0 && reinterpret_cast<uintptr_t>(P.logits) % std::min<size_t>(size, 16) == 0 &&
+             reinterpret_cast<uintptr_t>(P.dlogits) % std::min<size_t>(size, 16) == 0;
+  const int32_t each = P.E / P.groups, lanes = each / PER;
+  P.group_lanes = each % PER == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+  return fwd ? launch_dependent(route_fwd_kernel<PER>, dim3(grid_of(P.T)), kWarps * 32, 0, stream, P)
              : launch_dependent(route_bwd_kernel<PER>, dim3(grid_of(P.T)), kWarps * 32, 0, stream, P);
 }
 
-tp_status run(bool fwd, const RouteParams& P, cudaStream_t stream) {
+tp_status run(bool fwd, RouteParams& P, cudaStream_t stream) {
   if (P.E <= 64) return run<2>(fwd, P, stream);
   if (P.E <= 128) return run<4>(fwd, P, stream);
   if (P.E <= 256) return run<8>(fwd, P, stream);
@@ -451,9 +768,12 @@ extern "C" tp_status tp_route_fwd(const void* logits, const void* bias, void* ex
   P.experts = static_cast<int32_t*>(experts);
   P.weights = static_cast<float*>(weights);
   P.counts = static_cast<int32_t*>(counts);
-  // one thread block writes its counts, several add theirs to zeros
-  if (counts && (!work || grid_of(T) > 1)) TP_TRY(launch_dependent(route_clear_kernel, dim3(1), 256, 0, stream, P));
-  return work ? run(true, P, stream) : TP_OK;
+  const bool one = work && grid_of(T) == 1;
+  if (!work) return launch_dependent(route_fwd_kernel<2>, dim3(1), kWarps * 32, 0, stream, P);  // counts of no row
+  TP_TRY(run(true, P, stream));
+  if (counts == nullptr || one) return TP_OK;
+  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(cdiv(T * k, 2 * kCountThreads), 152));
+  return launch_dependent(route_count_kernel, dim3(blocks), kCountThreads, 0, stream, P);
 }
 
 extern "C" tp_status tp_route_bwd(const void* logits, const void* experts, const void* dweights, void* dlogits, const tp_route_desc* d,

@@ -464,9 +464,10 @@ tp_status tp_row_linear_bwd_fp8(const tp_fp8* xt, const tp_fp8* w, const tp_fp8*
  *   experts[t, 0..k-1]: the k largest v that are left, in falling order, ties
  *     to the lower number; bias moves the choice only:
  *   weights[t, j] = scale * s of that expert, renorm: divided by the sum of
- *     the chosen s.
- * The choice is that of exact arithmetic on the given logits and biases (in
- * 64 bits where it is close), whatever E, T and the other rows are.
+ *     the chosen s (by 2^-126 where that is less).
+ * The choice is that of exact arithmetic on the given logits and biases
+ * (values are told apart down to 2^-43, and with a bias a score below 2^-115
+ * counts as 0), whatever E, T and the other rows are.
  * An expert whose logit is -infinity or NaN is closed: s = 0, and it is not
  * chosen.  A slot without an open expert has experts = -1, weights = 0; a row
  * that is closed throughout has only those.  A logit of +infinity counts as
