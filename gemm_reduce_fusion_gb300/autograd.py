@@ -26,7 +26,9 @@ sequence-parallel MLP       AG+MatMul+GeLU, row + ReduceScatter  both sequence-p
 
 GeLU exists only inside the MLP functions: its derivative is applied in the
 epilogue of FC2's backward GEMM, so no separate elementwise kernel is
-needed.  Biases are optional: a column layer adds rank k's block b_k before
+needed.  ``parallel_mlp_fp8`` is the MLP on 8-bit operands; ``route`` and
+``routed_experts`` choose experts for each token and run them, on 8-bit
+operands too.  Biases are optional: a column layer adds rank k's block b_k before
 the activation, a row layer adds its b once after the reduction (TP §三/§四),
 and their gradients are the row sums of the output gradient, computed by
 the backward call.  Tensors are bf16 CUDA tensors; weights are ``[in, out]``
@@ -39,27 +41,31 @@ from __future__ import annotations
 from typing import Sequence
 
 import torch
+from torch.autograd.function import once_differentiable
 
-from . import (TP_EPI_GELU, TP_OP_AG_MM, TP_OP_AG_MM_BWD, TP_OP_BLOCK_NORM_BWD, TP_OP_COL_BWD, TP_OP_COL_FWD, TP_OP_COL_W4,
-               TP_OP_ROW_AR, TP_OP_ROW_BWD, TP_OP_ROW_RS, TP_OP_ROW_RS_BWD, TP_OP_ROW_W4, tp_ag_matmul, tp_ag_matmul_bwd,
-               tp_col_linear_bwd, tp_col_linear_fwd, tp_row_linear_bwd, tp_row_linear_bwd_reducescatter,
-               tp_row_linear_fwd_allreduce, tp_row_linear_fwd_reducescatter, tp_workspace_size)
+from . import (TP_EPI_GELU, TP_OP_AG_MM, TP_OP_AG_MM_BWD, TP_OP_BLOCK_NORM_BWD, TP_OP_COL_BWD, TP_OP_COL_BWD_FP8, TP_OP_COL_FP8,
+               TP_OP_COL_FWD, TP_OP_COL_W4, TP_OP_ROW_AR, TP_OP_ROW_BWD, TP_OP_ROW_BWD_FP8, TP_OP_ROW_FP8, TP_OP_ROW_RS,
+               TP_OP_ROW_RS_BWD, TP_OP_ROW_W4, TP_ROUTE_SIGMOID, TP_ROUTE_SOFTMAX, ExpertsSaved, Fp8, experts_saved, fp8_empty, tp_ag_matmul,
+               tp_ag_matmul_bwd, tp_col_linear_bwd, tp_col_linear_bwd_fp8, tp_col_linear_fwd, tp_col_linear_fwd_fp8,
+               tp_experts_bwd_fp8, tp_experts_fwd_fp8, tp_experts_workspace_size, tp_fp8_pack, tp_route_bwd, tp_route_fwd,
+               tp_row_linear_bwd, tp_row_linear_bwd_fp8, tp_row_linear_bwd_reducescatter, tp_row_linear_fwd_allreduce,
+               tp_row_linear_fwd_fp8, tp_row_linear_fwd_reducescatter, tp_workspace_size)
 
 _WS: dict[tuple[int, int], torch.Tensor] = {}  # by device and stream
 _HEAD = 16384  # a workspace's status word and slice counters lie in its first bytes
-_COUNT_NOTHING = {TP_OP_BLOCK_NORM_BWD, TP_OP_COL_W4, TP_OP_ROW_W4}
+_COUNT_NOTHING = {TP_OP_BLOCK_NORM_BWD, TP_OP_COL_W4, TP_OP_ROW_W4, TP_OP_COL_FP8, TP_OP_ROW_FP8, TP_OP_COL_BWD_FP8, TP_OP_ROW_BWD_FP8}
 
 
-def _workspace(device: torch.device, calls) -> torch.Tensor:
+def _workspace(device: torch.device, calls, least: int = 256) -> torch.Tensor:
     """A workspace for every call in ``calls`` (tuples of tp_workspace_size
-    arguments): the current stream's, whose calls are ordered, grown
-    (zero-filled) where it is too small.
+    arguments), of at least ``least`` bytes: the current stream's, whose calls
+    are ordered, grown (zero-filled) where it is too small.
 
     A call that is captured into a CUDA graph gets one of the graph's own,
     from the graph's memory: the stream's may be outgrown and freed while the
     graph still points to it, and graphs may be replayed side by side.  What
     has to start at zero is cleared in the graph."""
-    need = (max(tp_workspace_size(*c) for c in calls) + 255) // 256 * 256
+    need = (max([least, *(tp_workspace_size(*c) for c in calls)]) + 255) // 256 * 256
     idx = device.index if device.index is not None else torch.cuda.current_device()
     if torch.cuda.is_current_stream_capturing():
         ws = torch.empty(need, dtype=torch.uint8, device=device)
@@ -354,6 +360,151 @@ class _SequenceParallelMLPFn(torch.autograd.Function):
         return (None, db2, *dx, *dw1, *dw2, *(db1 or [None] * p))
 
 
+# ------------------------------------------------------------------ 8-bit operands
+
+def _operands(ts, rows=None, cols=None, tiles=False, epi=0):
+    """Packed from the matrices ``ts`` ([M, N], or [B, M, N]): their operands if
+    ``rows``, those of their transposes if ``cols``."""
+    *lead, M, N = ts[0].shape
+    make = lambda r, c: [fp8_empty(r, c, *lead, device=ts[0].device) for _ in ts]  # noqa: E731
+    q, qt = make(M, N) if rows else None, make(N, M) if cols else None
+    for i in range(0, len(ts), 8):  # shards a call
+        tp_fp8_pack(ts[i:i + 8], q and q[i:i + 8], qt and qt[i:i + 8], tiles=tiles, epi=epi)
+    return q, qt
+
+
+def _flat(ops):
+    return [t for op in ops for t in op]
+
+
+def _paired(ts):
+    return [Fp8(q, e) for q, e in zip(ts[::2], ts[1::2])]
+
+
+class _Fp8MLPFn(torch.autograd.Function):
+    """sum_k GeLU(X A1_k) A2_k with every product on 8-bit operands, a power of
+    two for each block of 128: X and the activations packed in rows, the
+    weights in 128 x 128 (so that they and their transposes hold the same
+    values).
+
+    Backward: dH_k = (dY A2_k^T) GeLU'(H_k), dX = sum_k dH_k A1_k^T,
+    dA2_k = GeLU(H_k)^T dY, dA1_k = X^T dH_k, each on operands of its factors.
+    Saves H in bf16, and X and the weights as the operands that the backward
+    products take."""
+
+    @staticmethod
+    def forward(ctx, p, x, *wb):
+        x = _bf16(x, "x")
+        w1 = [_bf16(a, "FC1 weight shard") for a in wb[:p]]
+        w2 = [_bf16(a, "FC2 weight shard") for a in wb[p:]]
+        (M, h), nk = x.shape, w1[0].shape[1]
+        train = any(ctx.needs_input_grad)
+        ws = _workspace(x.device, [(TP_OP_COL_FP8, p, M, nk, h), (TP_OP_ROW_FP8, p, M, h, nk)])
+        back1, fwd1 = _operands(w1, train, True, tiles=True)
+        back2, fwd2 = _operands(w2, train, True, tiles=True)
+        xq, xt = _operands([x], True, train)
+        hh = [_empty((M, nk), x) for _ in range(p)] if train else None
+        z = [fp8_empty(M, nk, device=x.device) for _ in range(p)]
+        tp_col_linear_fwd_fp8(xq[0], fwd1, None, ws, epi=TP_EPI_GELU, preact=hh, z=z)
+        y = _empty((M, h), x)
+        tp_row_linear_fwd_fp8(z, fwd2, y, ws)
+        if train:
+            ctx.p = p
+            ctx.save_for_backward(*hh, *_flat(xt), *_flat(back1), *_flat(back2))
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        p, s = ctx.p, list(ctx.saved_tensors)
+        hh, xt = s[:p], _paired(s[p:p + 2])[0]
+        back1, back2 = _paired(s[p + 2:3 * p + 2]), _paired(s[3 * p + 2:])
+        M, nk = hh[0].shape
+        h = back1[0].q.shape[0]
+        dy = _grad(dy, hh[0].new_empty((M, h)))
+        ws = _workspace(dy.device, [(TP_OP_ROW_BWD_FP8, p, M, h, nk), (TP_OP_COL_BWD_FP8, p, M, nk, h)])
+        dyq, dyt = _operands([dy], True, True)
+        _, zt = _operands(hh, False, True, epi=TP_EPI_GELU)
+        dh = [_empty((M, nk), dy) for _ in range(p)]
+        dw1, dw2 = [_empty((h, nk), dy) for _ in range(p)], [_empty((nk, h), dy) for _ in range(p)]
+        tp_row_linear_bwd_fp8(zt, back2, dyq[0], dyt[0], dh, dw2, ws, preact=hh)
+        dhq, dht = _operands(dh, True, True)
+        dx = _empty((M, h), dy)
+        tp_col_linear_bwd_fp8(xt, back1, dhq, dht, dx, dw1, ws)
+        return (None, dx, *dw1, *dw2)
+
+
+class _RouteFn(torch.autograd.Function):
+    """(weights, experts, counts) of the k experts of each row of logits; the
+    weights are differentiable in the logits, the choice is not."""
+
+    @staticmethod
+    def forward(ctx, logits, k, how, bias, groups):
+        if not logits.is_cuda or logits.dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"logits: expected a bfloat16 or float32 CUDA tensor, got {logits.dtype} on {logits.device}")
+        logits = logits.contiguous()
+        T, E = logits.shape
+        on = dict(device=logits.device)
+        experts, weights = torch.empty((T, k), dtype=torch.int32, **on), torch.empty((T, k), dtype=torch.float32, **on)
+        counts = torch.empty(E, dtype=torch.int32, **on)
+        tp_route_fwd(logits, experts, weights, counts=counts, bias=bias, **groups, **how)
+        ctx.how = how
+        ctx.save_for_backward(logits, experts)
+        ctx.mark_non_differentiable(experts, counts)
+        return weights, experts, counts
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dweights, *_):
+        logits, experts = ctx.saved_tensors
+        if dweights is None:
+            return torch.zeros_like(logits), None, None, None, None
+        dlogits = torch.empty_like(logits)
+        tp_route_bwd(logits, experts, dweights.contiguous(), dlogits, **ctx.how)
+        return dlogits, None, None, None, None
+
+
+class _ExpertsFn(torch.autograd.Function):
+    """y[t] = sum_j weights[t, j] GeLU(x[t] W1_e) W2_e on 8-bit operands; the
+    p shards hold E/p experts each.  Saves x, dispatched slots, pre-activations
+    and the experts' outputs, and the weights as operands."""
+
+    @staticmethod
+    def forward(ctx, p, x, experts, weights, *wb):
+        x = _bf16(x, "x")
+        w1 = [_bf16(a, "FC1 weights of the experts") for a in wb[:p]]
+        w2 = [_bf16(a, "FC2 weights of the experts") for a in wb[p:]]
+        (T, h), (per, _, f), k = x.shape, w1[0].shape, experts.shape[1]
+        train = any(ctx.needs_input_grad)
+        ws = _workspace(x.device, [], tp_experts_workspace_size(p, p * per, T, k, h, f, train))
+        back1, fwd1 = _operands(w1, train, True, tiles=True)
+        back2, fwd2 = _operands(w2, train, True, tiles=True)
+        saved = experts_saved(p * per, T, k, h, f, device=x.device) if train else None
+        y = _empty((T, h), x)
+        tp_experts_fwd_fp8(x, experts, weights, fwd1, fwd2, y, ws, saved=saved)
+        if train:
+            ctx.p = p
+            ctx.save_for_backward(x, weights, *saved, *_flat(back1), *_flat(back2))
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        p, s = ctx.p, ctx.saved_tensors
+        x, weights, saved = s[0], s[1], ExpertsSaved(*s[2:5])
+        back1, back2 = _paired(s[5:5 + 2 * p]), _paired(s[5 + 2 * p:])
+        (T, h), k, (per, f) = x.shape, weights.shape[1], back2[0].q.shape[:2]
+        dy = _grad(dy, x)
+        ws = _workspace(x.device, [], tp_experts_workspace_size(p, p * per, T, k, h, f, True))
+        need = ctx.needs_input_grad
+        dx = _empty((T, h), x) if need[1] else None
+        dw = _empty((T, k), x) if need[3] else None
+        dw1 = [_empty((per, h, f), x) for _ in range(p)] if any(need[4:4 + p]) else None
+        dw2 = [_empty((per, f, h), x) for _ in range(p)] if any(need[4 + p:]) else None
+        tp_experts_bwd_fp8(x, weights, dy, back1, back2, dx, dw, dw1, dw2, saved, ws)
+        return (None, dx, None, dw.float() if dw is not None else None, *(dw1 or [None] * p), *(dw2 or [None] * p))
+
+
 # ------------------------------------------------------------------ functional API
 
 def _blocks(b, p):
@@ -406,6 +557,35 @@ def sequence_parallel_mlp(xs: Sequence[torch.Tensor], w1: Sequence[torch.Tensor]
         raise ValueError("one token shard and one FC1/FC2 shard per rank")
     p = len(xs)
     return _SequenceParallelMLPFn.apply(p, b2, *xs, *w1, *w2, *_blocks(b1, p))
+
+
+def parallel_mlp_fp8(x: torch.Tensor, w1: Sequence[torch.Tensor], w2: Sequence[torch.Tensor]) -> torch.Tensor:
+    """Y = sum_k GeLU(X A1_k) A2_k, every product on 8-bit operands (see _Fp8MLPFn)."""
+    if len(w1) != len(w2):
+        raise ValueError("FC1 and FC2 need the same number of shards")
+    return _Fp8MLPFn.apply(len(w1), x, *w1, *w2)
+
+
+SCORES = {"softmax": TP_ROUTE_SOFTMAX, "sigmoid": TP_ROUTE_SIGMOID}
+
+
+def route(logits: torch.Tensor, k: int, *, score: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
+          group_best: int = 1, renorm: bool = False, scale: float = 1.0) -> tuple:
+    """(weights [T, k], experts [T, k], counts [E]) of the k best experts of each row of logits [T, E]
+    (see tp_route_fwd); the weights are differentiable in the logits."""
+    if score not in SCORES:
+        raise ValueError(f"score is one of {sorted(SCORES)}, got {score!r}")
+    return _RouteFn.apply(logits, k, dict(score=SCORES[score], renorm=renorm, scale=scale), bias,
+                          dict(groups=groups, top_groups=top_groups, group_best=group_best))
+
+
+def routed_experts(x: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, w1: Sequence[torch.Tensor],
+                   w2: Sequence[torch.Tensor]) -> torch.Tensor:
+    """y[t] = sum_j weights[t, j] GeLU(x[t] W1_e) W2_e with e = experts[t, j]; shard r of w1 [E/p, h, f] and
+    w2 [E/p, f, h] holds E/p experts.  Differentiable in x, the weights and every shard."""
+    if len(w1) != len(w2):
+        raise ValueError("FC1 and FC2 need the same number of shards")
+    return _ExpertsFn.apply(len(w1), x, experts, weights, *w1, *w2)
 
 
 # ------------------------------------------------------------------ modules

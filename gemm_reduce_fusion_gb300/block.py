@@ -12,9 +12,14 @@ so that blocks chain as ``x, n = block(x, n)``; the stream begins with
 
 ``MLPBlock`` trains: the MLP saves its input X and its pre-activations H in
 8 bits, 33/32 bytes an FFN element where H and Z = GeLU(H) in bfloat16 take 4
-(Z is restored from H).  ``W4MLPBlock``
+(Z is restored from H); with ``fp8`` its products run on 8-bit floating-point
+operands instead.  ``W4MLPBlock``
 serves it: 4-bit weights, single tokens and small batches straight from
 them, prompts through weights unpacked for the call.
+
+``RoutedMLPBlock`` has experts in the MLP's place, each token sent to k of
+them by a router, their products on 8-bit operands; ``serve()`` gives the
+block for serving, its weights packed once.
 
 Tensors are [tokens, h], or lists of p token shards [tokens / p, h] with
 ``sequence_parallel`` (the ReduceScatter layouts).  The stream is bfloat16 or
@@ -32,10 +37,11 @@ from . import (TP_EPI_GELU, TP_NORM_LAYER, TP_NORM_NONE, TP_NORM_RMS, TP_OP_AG_M
                TP_OP_BLOCK_NORM_BWD, TP_OP_COL_BWD_CKPT, TP_OP_COL_FWD, TP_OP_COL_W4, TP_OP_ROW_AR, TP_OP_ROW_BWD_CKPT,
                TP_OP_ROW_RS, TP_OP_ROW_RS_BWD_CKPT, TP_OP_ROW_W4, TP_W4_MAX_M, ckpt_shapes, tp_ag_matmul,
                tp_ag_matmul_bwd_ckpt, tp_block_norm_bwd, tp_block_norm_fwd, tp_ckpt_pack, tp_col_linear_bwd_ckpt,
-               tp_col_linear_fwd, tp_col_linear_fwd_w4, tp_row_linear_bwd_ckpt, tp_row_linear_bwd_reducescatter_ckpt,
+               tp_col_linear_fwd, tp_col_linear_fwd_w4, tp_experts_fwd_fp8, tp_experts_workspace_size, tp_row_linear_bwd_ckpt, tp_row_linear_bwd_reducescatter_ckpt,
                tp_row_linear_fwd_allreduce, tp_row_linear_fwd_reducescatter, tp_row_linear_fwd_w4, tp_w4_pack, tp_w4_unpack,
                w4_shapes)
-from .autograd import _bf16, _empty, _grad, _params, _shards, _workspace
+from .autograd import (_bf16, _empty, _grad, _operands, _params, _shards, _workspace, column_parallel_linear, parallel_mlp_fp8, route,
+                       routed_experts)
 
 NORMS = {"none": TP_NORM_NONE, "rms": TP_NORM_RMS, "layer": TP_NORM_LAYER}
 
@@ -185,32 +191,44 @@ def parallel_mlp_ckpt(x, w1: Sequence[torch.Tensor], w2: Sequence[torch.Tensor])
 
 # ------------------------------------------------------------------ modules
 
+def _boundary_params(block, h, device, post, pre, gate, alpha, eps) -> None:
+    """The vectors of a block's boundary, as its parameters."""
+    like = dict(dtype=torch.bfloat16, device=device)
+    block.post, block.pre, block.alpha, block.eps = post, pre, alpha, eps
+    vec = lambda on, make: torch.nn.Parameter(make(h, **like)) if on else None  # noqa: E731
+    block.w_post, block.b_post = vec(_kind(post), torch.ones), vec(post == "layer", torch.zeros)
+    block.w_pre, block.b_pre = vec(_kind(pre), torch.ones), vec(pre == "layer", torch.zeros)
+    block.gate = torch.nn.Parameter(gate.to(torch.bfloat16).contiguous()) if gate is not None else None
+
+
+def _boundary_of(block) -> dict:
+    return dict(post=block.post, w_post=block.w_post, b_post=block.b_post, pre=block.pre, w_pre=block.w_pre, b_pre=block.b_pre,
+                gate=block.gate, alpha=block.alpha, eps=block.eps)
+
+
 class MLPBlock(torch.nn.Module):
     """A trained block: ``y, n = block(x, n)``.
 
     w1 [h, ffn] and w2 [ffn, h] are split into p shards.  ``post`` / ``pre``
     name the norms of the boundary ("none", "rms" or "layer"; layer norms have
     biases), ``gate`` is an optional [rows, h] gate (one row: per channel),
-    ``alpha`` the residual scale."""
+    ``alpha`` the residual scale.  ``fp8``: the products on 8-bit
+    floating-point operands (whole token tensors only)."""
 
     def __init__(self, w1: torch.Tensor, w2: torch.Tensor, p: int, *, post: str = "rms", pre: str = "rms", gate=None,
-                 alpha: float = 1.0, eps: float = 1e-5, sequence_parallel: bool = False):
+                 alpha: float = 1.0, eps: float = 1e-5, sequence_parallel: bool = False, fp8: bool = False):
         super().__init__()
-        h, like = w1.shape[0], dict(dtype=torch.bfloat16, device=w1.device)
-        self.p, self.sequence_parallel = p, sequence_parallel
-        self.post, self.pre, self.alpha, self.eps = post, pre, alpha, eps
+        if fp8 and sequence_parallel:
+            raise ValueError("the 8-bit products take whole token tensors, not shards")
+        self.p, self.sequence_parallel, self.fp8 = p, sequence_parallel, fp8
         self.w1, self.w2 = _params(_shards(w1, p, 1)), _params(_shards(w2, p, 0))
-        vec = lambda on, make: torch.nn.Parameter(make(h, **like)) if on else None  # noqa: E731
-        self.w_post, self.b_post = vec(_kind(post), torch.ones), vec(post == "layer", torch.zeros)
-        self.w_pre, self.b_pre = vec(_kind(pre), torch.ones), vec(pre == "layer", torch.zeros)
-        self.gate = torch.nn.Parameter(gate.to(torch.bfloat16).contiguous()) if gate is not None else None
+        _boundary_params(self, w1.shape[0], w1.device, post, pre, gate, alpha, eps)
 
     def boundary(self) -> dict:
-        return dict(post=self.post, w_post=self.w_post, b_post=self.b_post, pre=self.pre, w_pre=self.w_pre,
-                    b_pre=self.b_pre, gate=self.gate, alpha=self.alpha, eps=self.eps)
+        return _boundary_of(self)
 
     def forward(self, x, n):
-        z = parallel_mlp_ckpt(n, list(self.w1), list(self.w2))
+        z = (parallel_mlp_fp8 if self.fp8 else parallel_mlp_ckpt)(n, list(self.w1), list(self.w2))
         if self.sequence_parallel:
             return block_boundary(x, z, **self.boundary())
         ys, ns = block_boundary([x], [z], **self.boundary())
@@ -266,5 +284,74 @@ class W4MLPBlock:
             tp_col_linear_fwd(n, self._unpack(self.fc1), a, ws, epi=TP_EPI_GELU)
             tp_row_linear_fwd_allreduce(a, self._unpack(self.fc2), [z], ws)
         out = _empty((M, h), n) if self.how["pre"] else None
+        tp_block_norm_fwd([x], [z], [x], [out] if out is not None else None, **self.how)
+        return x, out
+
+
+class RoutedMLPBlock(torch.nn.Module):
+    """A trained block with experts in the MLP's place: ``y, n = block(x, n)``.
+
+        z[t] = sum_j weights[t, j] GeLU(n[t] W1_e) W2_e,  e = experts[t, j]
+
+    router [h, E], w1 [E, h, f] and w2 [E, f, h] bfloat16, the experts split
+    into p shards.  ``k`` experts a token; ``score``, ``groups``,
+    ``top_groups``, ``group_best``, ``renorm`` and ``scale`` as in ``route``.
+    ``bias`` (float32 [E], zeros at first, no parameter) moves the choice only:
+    a program balances the load by it, from ``counts``, how often each expert
+    was chosen in the last call.  The boundary is MLPBlock's."""
+
+    def __init__(self, router: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor, p: int, k: int, *, score: str = "softmax",
+                 groups: int = 1, top_groups: int = 1, group_best: int = 1, renorm: bool = False, scale: float = 1.0,
+                 post: str = "rms", pre: str = "rms", gate=None, alpha: float = 1.0, eps: float = 1e-5):
+        super().__init__()
+        E, h, f = w1.shape
+        if tuple(router.shape) != (h, E) or tuple(w2.shape) != (E, f, h):
+            raise ValueError(f"router [h, E], w1 [E, h, f], w2 [E, f, h]: got {tuple(router.shape)}, {tuple(w1.shape)}, {tuple(w2.shape)}")
+        self.p, self.k = p, k
+        self.routing = dict(score=score, groups=groups, top_groups=top_groups, group_best=group_best, renorm=renorm, scale=scale)
+        self.router = torch.nn.Parameter(router.contiguous())
+        self.w1, self.w2 = _params(_shards(w1, p, 0)), _params(_shards(w2, p, 0))
+        self.register_buffer("bias", torch.zeros(E, dtype=torch.float32, device=w1.device))
+        self.counts = None
+        _boundary_params(self, h, w1.device, post, pre, gate, alpha, eps)
+
+    def forward(self, x, n):
+        logits, = column_parallel_linear(n, [self.router])
+        weights, experts, self.counts = route(logits, self.k, bias=self.bias, **self.routing)
+        z = routed_experts(n, experts, weights, list(self.w1), list(self.w2))
+        ys, ns = block_boundary([x], [z], **_boundary_of(self))
+        return ys[0], (ns[0] if ns else None)
+
+    def serve(self) -> "ServedRoutedMLPBlock":
+        """This block for serving, its experts' weights packed once."""
+        return ServedRoutedMLPBlock(self)
+
+
+class ServedRoutedMLPBlock:
+    """A routed block that serves: ``y, n = block(x, n)`` on [tokens, h]
+    tensors.  It keeps copies of what the block holds when it is made, the
+    experts' weights in 8 bits.  The stream x is updated in place.  A gate of
+    several rows serves multiples of them only."""
+
+    def __init__(self, block: RoutedMLPBlock):
+        self.p, self.k, self.routing = block.p, block.k, dict(block.routing)
+        with torch.no_grad():
+            copy = lambda v: v.detach().clone() if torch.is_tensor(v) else v  # noqa: E731
+            self.how = {k: copy(v) for k, v in _boundary_of(block).items()}
+            self.router, self.bias = copy(block.router), copy(block.bias)
+            _, self.w1 = _operands([w.detach() for w in block.w1], False, True, tiles=True)
+            _, self.w2 = _operands([w.detach() for w in block.w2], False, True, tiles=True)
+        self.how.update(post=_kind(self.how["post"]), pre=_kind(self.how["pre"]))
+
+    @torch.no_grad()
+    def __call__(self, x: torch.Tensor, n: torch.Tensor) -> tuple:
+        p, (T, h), (per, f) = self.p, n.shape, self.w1[0].q.shape[:2]
+        E = p * per
+        ws = _workspace(n.device, [(TP_OP_COL_FWD, 1, T, E, h)], tp_experts_workspace_size(p, E, T, self.k, h, f))
+        logits, z = _empty((T, E), n), _empty((T, h), n)
+        tp_col_linear_fwd(n, [self.router], [logits], ws)
+        weights, experts, _ = route(logits, self.k, bias=self.bias, **self.routing)
+        tp_experts_fwd_fp8(n, experts, weights, self.w1, self.w2, z, ws)
+        out = _empty((T, h), n) if self.how["pre"] else None
         tp_block_norm_fwd([x], [z], [x], [out] if out is not None else None, **self.how)
         return x, out

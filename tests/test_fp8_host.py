@@ -114,10 +114,10 @@ def test_packing_refusals():
 
 
 def test_forward_refusals():
-    need = tp.tp_workspace_size(tp.TP_OP_COL_FP8, 2, 16, 64, 1024)
+    need = tp.tp_workspace_size(tp.TP_OP_COL_FP8, 2, 16, 64, 8192)
     assert need > 256
 
-    def col(x=pairs(at(0)), w=pairs(at(1), at(2)), bias=None, y=arr(at(3), at(4)), z=None, pre=None, epi=0, p=2, M=16, N=64, K=1024, ws=at(7),
+    def col(x=pairs(at(0)), w=pairs(at(1), at(2)), bias=None, y=arr(at(3), at(4)), z=None, pre=None, epi=0, p=2, M=16, N=64, K=8192, ws=at(7),
             n=need):
         return L.tp_col_linear_fwd_fp8(x, w, bias, y, z, pre, epi, p, M, N, K, ws, n, None)
     for kw in (dict(x=None), dict(w=None), dict(w=pairs(at(1), None)), dict(y=None), dict(z=pairs(at(5), at(6))), dict(epi=2),
@@ -127,9 +127,9 @@ def test_forward_refusals():
     assert col(n=need - 1) == SMALL and col(N=60) == ALIGN and col(x=pairs(at(0) + 8)) == ALIGN and col(bias=arr(at(8) + 2, None)) == ALIGN
     assert col(ws=at(7) + 8) == ALIGN
 
-    need = tp.tp_workspace_size(tp.TP_OP_ROW_FP8, 2, 16, 64, 1024)
+    need = tp.tp_workspace_size(tp.TP_OP_ROW_FP8, 2, 16, 64, 8192)
 
-    def row(x=pairs(at(0), at(1)), w=pairs(at(2), at(3)), bias=None, y=at(4), p=2, M=16, N=64, K=1024, ws=at(7), n=need):
+    def row(x=pairs(at(0), at(1)), w=pairs(at(2), at(3)), bias=None, y=at(4), p=2, M=16, N=64, K=8192, ws=at(7), n=need):
         return L.tp_row_linear_fwd_fp8(x, w, bias, y, p, M, N, K, ws, n, None)
     for kw in (dict(x=None), dict(w=pairs(None, at(2))), dict(y=None), dict(y=at(1)), dict(ws=at(2))):
         assert row(**kw) == BAD, kw
