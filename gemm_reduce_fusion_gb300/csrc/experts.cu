@@ -28,46 +28,67 @@ using namespace tpf;
 namespace {
 
 constexpr int kMaxExperts = TP_ROUTE_MAX_EXPERTS, kMaxK = 32;
-constexpr int kDispatchThreads = 512;
+constexpr int kDispatchThreads = 1024;
+constexpr int32_t kSingleTile = 1 << 30;  // fp8_gemm.cuh: kSingle
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
 // ------------------------------------------------------------------ plan
 
 struct DispatchParams {
   const int32_t* experts;  // [S]
-  int32_t *tiles, *first, *expert, *slot, *row;
-  int32_t S, E, tile_rows, max_tiles;
+  int32_t *tiles, *pairs, *first, *expert, *pair, *slot, *row;
+  int32_t S, E, tile_rows, aligned;
 };
 
 __device__ __forceinline__ int32_t tiles_of(int32_t n, int32_t tile_rows) { return (n + tile_rows - 1) / tile_rows; }
 
+// Four slots' experts, -1 past the last.
+__device__ __forceinline__ int4 four_slots(const DispatchParams& P, int32_t i) {
+  if (P.aligned && i + 4 <= P.S) return *reinterpret_cast<const int4*>(P.experts + i);
+  return make_int4(i < P.S ? P.experts[i] : -1, i + 1 < P.S ? P.experts[i + 1] : -1, i + 2 < P.S ? P.experts[i + 2] : -1,
+                   i + 3 < P.S ? P.experts[i + 3] : -1);
+}
+
 // A thread block an expert.  Each counts all experts' slots, so that no
-// kernel has to run before it: 2 x 4 bytes a slot from L2.
+// kernel has to run before it, and keeps the first 32768 in registers for the
+// second pass, which gives its own their rows, in their order.
 __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const __grid_constant__ DispatchParams P) {
+  constexpr int kKeep = 8, kRound = kDispatchThreads * 4;
   __shared__ int32_t count[kMaxExperts];
-  __shared__ int32_t warp_sum[kDispatchThreads / 32], begin, total;
+  __shared__ int32_t warp_sum[2][kDispatchThreads / 32], begin, total, pair_begin, pair_total;
   griddep_wait();
   griddep_launch_dependents();
   const int32_t me = static_cast<int32_t>(blockIdx.x), tid = static_cast<int32_t>(threadIdx.x);
   const uint32_t lane = tid & 31, warp = tid >> 5;
   for (int32_t e = tid; e < P.E; e += kDispatchThreads) count[e] = 0;
+  if (tid == 0) begin = total = pair_begin = pair_total = 0;
+  int4 keep[kKeep];
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) keep[i] = i * kRound < P.S ? four_slots(P, i * kRound + tid * 4) : make_int4(-1, -1, -1, -1);
   __syncthreads();
-  for (int32_t i = tid; i < P.S; i += kDispatchThreads) {
-    const int32_t e = P.experts[i];
+  auto add = [&](int32_t e) {
     if (e >= 0 && e < P.E) atomicAdd(count + e, 1);
+  };
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i)
+    if (i * kRound < P.S) add(keep[i].x), add(keep[i].y), add(keep[i].z), add(keep[i].w);
+  for (int32_t base = kKeep * kRound; base < P.S; base += kRound) {
+    const int4 v = four_slots(P, base + tid * 4);
+    add(v.x), add(v.y), add(v.z), add(v.w);
   }
   __syncthreads();
-  // tiles before this expert's, and all of them
-  int32_t before = 0, all = 0;
-  for (int32_t e = tid; e < P.E; e += kDispatchThreads) {
-    const int32_t n = tiles_of(count[e], P.tile_rows);
-    all += n;
-    if (e < me) before += n;
+  // tiles (and pairs) before this expert's, and all of them
+  if (tid < kMaxExperts) {
+    const int32_t n = tid < P.E ? tiles_of(count[tid], P.tile_rows) : 0, pairs = (n + 1) / 2;
+    const int32_t a = __reduce_add_sync(kAll, tid < me ? n : 0), b = __reduce_add_sync(kAll, n),
+                  c = __reduce_add_sync(kAll, tid < me ? pairs : 0), d = __reduce_add_sync(kAll, pairs);
+    if (lane == 0 && b) {
+      atomicAdd(&begin, a);
+      atomicAdd(&total, b);
+      atomicAdd(&pair_begin, c);
+      atomicAdd(&pair_total, d);
+    }
   }
-  if (tid == 0) begin = total = 0;
-  __syncthreads();
-  if (before) atomicAdd(&begin, before);
-  if (all) atomicAdd(&total, all);
   __syncthreads();
   const int32_t mine = tiles_of(count[me], P.tile_rows);
   if (tid == 0) {
@@ -75,35 +96,29 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const __grid
     if (me == P.E - 1) {
       P.first[P.E] = total;
       *P.tiles = total;
+      *P.pairs = pair_total;
     }
   }
-  for (int32_t i = tid; i < mine; i += kDispatchThreads) P.expert[begin + i] = me;
+  for (int32_t i = tid; i < mine; i += kDispatchThreads) {
+    P.expert[begin + i] = me;
+    if ((i & 1) == 0) P.pair[pair_begin + i / 2] = (begin + i) | (i + 1 == mine ? kSingleTile : 0);
+  }
   // the slots, in their order
   int32_t at = begin * P.tile_rows;
-  for (int32_t base = 0; base < P.S; base += kDispatchThreads * 4) {
-    const int32_t i0 = base + tid * 4;
-    int32_t e[4], n = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      e[j] = i0 + j < P.S ? P.experts[i0 + j] : -1;
-      n += e[j] == me;
-    }
+  auto place = [&](int32_t base, const int4& v, int round) {
+    const int32_t e[4] = {v.x, v.y, v.z, v.w}, i0 = base + tid * 4;
+    const int32_t n = (e[0] == me) + (e[1] == me) + (e[2] == me) + (e[3] == me);
     int32_t sum = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int32_t v = __shfl_up_sync(kAll, sum, o);
-      if (static_cast<int32_t>(lane) >= o) sum += v;
+      const int32_t u = __shfl_up_sync(kAll, sum, o);
+      if (static_cast<int32_t>(lane) >= o) sum += u;
     }
+    if (lane == 31) warp_sum[round & 1][warp] = sum;
     __syncthreads();
-    if (lane == 31) warp_sum[warp] = sum;
-    __syncthreads();
-    int32_t here = at + sum - n, round = 0;
-#pragma unroll
-    for (uint32_t w = 0; w < kDispatchThreads / 32; ++w) {
-      const int32_t v = warp_sum[w];
-      if (w < warp) here += v;
-      round += v;
-    }
+    const int32_t other = lane < kDispatchThreads / 32 ? warp_sum[round & 1][lane] : 0;
+    int32_t here = at + sum - n + __reduce_add_sync(kAll, lane < warp ? other : 0);
+    at += __reduce_add_sync(kAll, other);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (e[j] == me) {
@@ -113,8 +128,12 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const __grid
         P.row[i0 + j] = -1;
       }
     }
-    at += round;
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i)
+    if (i * kRound < P.S) place(i * kRound, keep[i], i);
+  int round = kKeep;
+  for (int32_t base = kKeep * kRound; base < P.S; base += kRound, ++round) place(base, four_slots(P, base + tid * 4), round);
   for (int32_t r = at + tid; r < (begin + mine) * P.tile_rows; r += kDispatchThreads) P.slot[r] = -1;
 }
 
@@ -218,7 +237,8 @@ __global__ void __launch_bounds__(256) weight_grad_kernel(const __grid_constant_
 struct Sizes {
   int p;
   int64_t E, T, k, h, f;
-  int64_t S, tile_rows, max_tiles, rows;
+  int64_t S, tile_rows, max_tiles, max_pairs, rows;
+  bool pairs;  // products on CTA pairs
   size_t plan_bytes;
 };
 
@@ -238,8 +258,12 @@ bool sizes_of(int p, int64_t E, int64_t T, int64_t k, int64_t h, int64_t f, bool
   s->tile_rows = tile_rows_for(s->S, E, train);
   // every expert that has rows leaves at most a tile less one row empty
   s->max_tiles = (s->S + (s->tile_rows - 1) * std::min(E, s->S)) / s->tile_rows;
+  s->max_pairs = (s->max_tiles + std::min(E, s->S) + 1) / 2;
   s->rows = s->max_tiles * s->tile_rows;
-  s->plan_bytes = static_cast<size_t>(cdiv(1 + (E + 1) + s->max_tiles + s->rows + s->S, 64) * 64) * 4;
+  // A pair's 256 x 256 tile takes 0.7 of the time of its four 128 x 128 ones,
+  // but an expert's last pair may have one tile: from 1.5 tiles on average on.
+  s->pairs = s->tile_rows == 128 && s->S >= 192 * std::min(E, s->S);
+  s->plan_bytes = static_cast<size_t>(cdiv(2 + (E + 1) + s->max_tiles + s->max_pairs + s->rows + s->S, 64) * 64) * 4;
   return s->rows <= (int64_t(1) << 31) - 129;
 }
 
@@ -254,6 +278,7 @@ tp_status check_experts(int p, int64_t E, int64_t T, int64_t k, int64_t h, int64
 
 Fp8Plan bounds_of(const Sizes& s) {
   Fp8Plan plan = {};
+  plan.paired = s.pairs;
   plan.max_tiles = s.max_tiles;
   plan.tile_rows = s.tile_rows;
   plan.E = static_cast<int>(s.E);
@@ -262,17 +287,24 @@ Fp8Plan bounds_of(const Sizes& s) {
 }
 
 // The plan's arrays in its memory.
-Fp8Plan plan_at(const Sizes& s, int32_t* at, int32_t** tiles, int32_t** first, int32_t** expert, int32_t** slot, int32_t** row) {
-  *tiles = at;
-  *first = at + 1;
-  *expert = *first + s.E + 1;
-  *slot = *expert + s.max_tiles;
-  *row = *slot + s.rows;
+struct PlanArrays {
+  int32_t *tiles, *pairs, *first, *expert, *pair, *slot, *row;
+};
+Fp8Plan plan_at(const Sizes& s, int32_t* at, PlanArrays* a) {
+  a->tiles = at;
+  a->pairs = at + 1;
+  a->first = at + 2;
+  a->expert = a->first + s.E + 1;
+  a->pair = a->expert + s.max_tiles;
+  a->slot = a->pair + s.max_pairs;
+  a->row = a->slot + s.rows;
   Fp8Plan plan = bounds_of(s);
-  plan.tiles = *tiles;
-  plan.first = *first;
-  plan.expert = *expert;
-  plan.slot = *slot;
+  plan.tiles = a->tiles;
+  plan.pairs = a->pairs;
+  plan.pair = a->pair;
+  plan.first = a->first;
+  plan.expert = a->expert;
+  plan.slot = a->slot;
   return plan;
 }
 
@@ -446,15 +478,15 @@ extern "C" tp_status tp_experts_fwd_fp8(const void* x, const void* experts, cons
   TP_TRY(device_info(&di));
   Area area(ws);
   const ForwardArea A = forward_area(s, train, &area);
-  int32_t *tiles, *first, *expert, *slot, *row;
-  const Fp8Plan plan = plan_at(s, train ? static_cast<int32_t*>(saved->plan) : A.plan, &tiles, &first, &expert, &slot, &row);
+  PlanArrays at;
+  const Fp8Plan plan = plan_at(s, train ? static_cast<int32_t*>(saved->plan) : A.plan, &at);
   DispatchParams D;
   D.experts = static_cast<const int32_t*>(experts);
-  D.tiles = tiles, D.first = first, D.expert = expert, D.slot = slot, D.row = row;
+  D.tiles = at.tiles, D.pairs = at.pairs, D.first = at.first, D.expert = at.expert, D.pair = at.pair, D.slot = at.slot, D.row = at.row;
   D.S = static_cast<int32_t>(s.S);
   D.E = static_cast<int32_t>(E);
   D.tile_rows = static_cast<int32_t>(s.tile_rows);
-  D.max_tiles = static_cast<int32_t>(s.max_tiles);
+  D.aligned = aligned16(experts);
   TP_TRY(launch_dependent(dispatch_kernel, dim3(static_cast<unsigned>(E)), kDispatchThreads, 0, stream, D));
   Fp8Pack pack;
   pack.x = &x;
@@ -497,7 +529,7 @@ extern "C" tp_status tp_experts_fwd_fp8(const void* x, const void* experts, cons
   std::memset(&C, 0, sizeof(C));
   C.rows = A.out32 ? nullptr : static_cast<const __nv_bfloat16*>(out);
   C.rows32 = A.out32;
-  C.row = row;
+  C.row = at.row;
   C.weights = static_cast<const float*>(weights);
   C.y = static_cast<__nv_bfloat16*>(y);
   C.T = T;
@@ -562,14 +594,14 @@ extern "C" tp_status tp_experts_bwd_fp8(const void* x, const void* weights, cons
   }
   Area area(ws);
   const BackwardArea A = backward_area(s, &area);
-  int32_t *tiles, *first, *expert, *slot, *row;
-  const Fp8Plan plan = plan_at(s, static_cast<int32_t*>(saved->plan), &tiles, &first, &expert, &slot, &row);
+  PlanArrays at;
+  const Fp8Plan plan = plan_at(s, static_cast<int32_t*>(saved->plan), &at);
   uint32_t* status = static_cast<uint32_t*>(ws);
   if (dweights) {
     DotParams D;
     D.rows = static_cast<const __nv_bfloat16*>(saved->out);
     D.dy = static_cast<const __nv_bfloat16*>(dy);
-    D.row = row;
+    D.row = at.row;
     D.dweights = static_cast<__nv_bfloat16*>(dweights);
     D.S = s.S;
     D.N = h;
@@ -630,7 +662,7 @@ extern "C" tp_status tp_experts_bwd_fp8(const void* x, const void* weights, cons
     CombineParams C;
     std::memset(&C, 0, sizeof(C));
     C.rows = static_cast<const __nv_bfloat16*>(dxr);
-    C.row = row;
+    C.row = at.row;
     C.y = static_cast<__nv_bfloat16*>(dx);
     C.T = T;
     C.N = h;

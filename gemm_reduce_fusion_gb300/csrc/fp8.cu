@@ -61,6 +61,10 @@ tp_status launch_gemm(const Fp8GemmParams& P, int64_t units, cudaStream_t stream
 
 namespace tpf {
 
+static int64_t tile_rows_of(int32_t mode, int64_t rows, const Fp8Plan* plan) {
+  return mode == FP8_ROWS ? plan->tile_rows : std::min<int64_t>(128, cdiv(rows, 16) * 16);
+}
+
 Fp8Launch fp8_plan(int32_t mode, int64_t rows, int64_t cols, int64_t depth, int groups, int segs, const Fp8Plan* plan) {
   Fp8Launch l;
   l.ctas = 1;
@@ -71,11 +75,12 @@ Fp8Launch fp8_plan(int32_t mode, int64_t rows, int64_t cols, int64_t depth, int 
   const int64_t kb = segs * cdiv(depth, 128);
   const int64_t pairs = groups * cdiv(rows, 256) * cdiv(cols, 256);
   if (mode != FP8_ROWS && rows > 128 && cols > 128 && pairs >= kSMs / 4) l.ctas = 2;
+  if (mode == FP8_ROWS && cols > 128 && plan->paired) l.ctas = 2;
   if (l.ctas == 2 || mode == FP8_CONTRACT || kb == 0) return l;
   // Whole tiles leave SMs idle in their last wave, runs do not, but the join
   // kernel and the parts (64 KiB at 128 rows, written and read, at each end of
   // a run) take as long as some 16 k-blocks.
-  const int64_t tile_rows = mode == FP8_ROWS ? plan->tile_rows : std::min<int64_t>(128, cdiv(rows, 16) * 16);
+  const int64_t tile_rows = tile_rows_of(mode, rows, plan);
   const int64_t tiles = (mode == FP8_ROWS ? plan->max_tiles : groups * cdiv(rows, 128)) * cdiv(cols, 128);
   if (cdiv(tiles, kSMs) * kb <= tiles * kb / kSMs + 16 || tiles * kb > (int64_t(1) << 30)) return l;
   l.min_run = std::max<int64_t>(std::min<int64_t>(4, kb), cdiv(kb, kMostParts));
@@ -96,8 +101,9 @@ tp_status fp8_product(const Fp8Product& d, const Fp8Launch& l, void* part, uint3
   P.a_by_s = d.na > 1 && d.segs > 1;
   P.b_by_g = d.nb > 1 && d.groups > 1;
   P.b_by_s = d.nb > 1 && d.segs > 1;
-  P.tile_rows = by_rows ? static_cast<int32_t>(std::min<int64_t>(d.plan->tile_rows, 128))
-                        : static_cast<int32_t>(std::min<int64_t>(128, cdiv(d.rows, 16) * 16));
+  P.tile_rows = static_cast<int32_t>(tile_rows_of(d.mode, d.rows, d.plan));
+  // Four warps with 32 rows each are as fast by themselves from 128 rows on.
+  P.together = l.ctas == 1 && P.tile_rows <= 64;
   P.m_tiles = static_cast<int32_t>(cdiv(d.rows, 128 * l.ctas));
   P.n_tiles = static_cast<int32_t>(cdiv(d.cols, 128 * l.ctas));
   P.kb = static_cast<int32_t>(cdiv(d.depth, 128));
@@ -112,6 +118,8 @@ tp_status fp8_product(const Fp8Product& d, const Fp8Launch& l, void* part, uint3
   if (d.plan) {
     P.plan_tiles = d.plan->tiles;
     P.plan_expert = d.plan->expert;
+    P.plan_pairs = d.plan->pairs;
+    P.plan_pair = d.plan->pair;
     P.plan_first = d.plan->first;
     P.plan_slot = d.plan->slot;
     P.max_tiles = static_cast<int32_t>(d.plan->max_tiles);
@@ -136,7 +144,7 @@ tp_status fp8_product(const Fp8Product& d, const Fp8Launch& l, void* part, uint3
   P.drop = static_cast<int32_t>(debug_drop());
   if (d.depth > 0) {
     // rows of an operand's matrix, and blocks of its exponents
-    const int64_t a_blocks = by_rows ? d.plan->max_tiles * cdiv(d.plan->tile_rows, 128) : cdiv(d.rows, 128);
+    const int64_t a_blocks = by_rows ? d.plan->max_tiles : cdiv(d.rows, 128);
     const int64_t b_rows = by_rows ? d.per * d.cols : d.cols, b_blocks = by_rows ? d.per * cdiv(d.cols, 128) : cdiv(d.cols, 128);
     for (int i = 0; i < d.na; ++i)
       if (!encode_q(&P.a[i], d.a[i].q, d.rows, d.depth, contract ? 128 : P.tile_rows) || !encode_e(&P.ea[i], d.a[i].e, a_blocks, d.depth, 1))

@@ -44,12 +44,14 @@ struct Fp8GemmParams {
   int32_t kb;                   // k-blocks of a segment
   int32_t stream;               // runs of k-blocks instead of whole tiles (CTAS = 1)
   int32_t min_run;              // the shortest of them
+  int32_t together;             // the epilogue's warps share a tile's rows (CTAS = 1)
   int32_t rows, cols;           // of an output (FP8_ROWS: rows not used)
   int32_t tile_rows;            // rows of an A tile that are loaded (CTAS = 1: 16 .. 128)
   int32_t band;                 // m-tiles that go together through the n-tiles
   int32_t per, eb_blocks;       // experts of a shard; 128-row blocks of an expert's B
   const int32_t* plan_tiles;    // FP8_ROWS, FP8_CONTRACT: row tiles in use
   const int32_t* plan_expert;   // FP8_ROWS: expert of a row tile
+  const int32_t *plan_pairs, *plan_pair;  // FP8_ROWS, CTAS = 2: pairs of row tiles; the first, + kSingle if alone
   const int32_t* plan_first;    // FP8_CONTRACT: first row tile of an expert, E + 1
   const int32_t* plan_slot;     // FP8_ROWS: token and choice of a row, or -1
   int32_t max_tiles, experts;   // bounds of what the plan may say
@@ -69,6 +71,8 @@ struct Fp8GemmParams {
   int32_t drop;                 // test hook (TP_DEBUG_DROP_LOAD)
 };
 
+constexpr int32_t kSingle = 1 << 30;
+
 template <int CTAS>
 struct Fp8Cfg {
   static constexpr int BN = 128 * CTAS;
@@ -82,7 +86,7 @@ struct Fp8Cfg {
   static constexpr int STAGES = 3;
   static constexpr int EPI_WARPS = 4 * CTAS;
   static constexpr int THREADS = 64 + 32 * EPI_WARPS;
-  static constexpr uint32_t STG_BYTES = 2048;  // staging of an epilogue warp
+  static constexpr uint32_t STG_BYTES = CTAS == 1 ? 4096 : 2048;  // staging of an epilogue warp
   static constexpr uint32_t E_OFF = STAGES * STAGE, STG_OFF = E_OFF + STAGES * DEEP * E_BYTES,
                             BAR_OFF = STG_OFF + EPI_WARPS * STG_BYTES;
   static constexpr uint32_t SMEM = 1024 + BAR_OFF + 256;
@@ -100,7 +104,9 @@ struct Fp8Cfg {
 
 struct Fp8Unit {
   int32_t t;          // tile
-  int32_t g, mt, nt;
+  int32_t g, nt;
+  int32_t tile;       // row tile (of CTA 0)
+  bool single;        // FP8_ROWS: CTA 1 has no row tile
   int32_t q0, q1;     // k-blocks
   int32_t a_row, ea;  // first row of A's tile (CTA 0), its block of exponents
   int32_t b_row, eb;
@@ -108,8 +114,9 @@ struct Fp8Unit {
   int64_t out_off;    // FP8_CONTRACT: the expert's place in its shard
 };
 
+template <int CTAS>
 __device__ __forceinline__ int32_t fp8_tiles(const Fp8GemmParams& P) {
-  if (P.mode == FP8_ROWS) return min(__ldcg(P.plan_tiles), P.max_tiles) * P.n_tiles;
+  if (P.mode == FP8_ROWS) return min(__ldcg(CTAS == 2 ? P.plan_pairs : P.plan_tiles), P.max_tiles) * P.n_tiles;
   return P.groups * P.m_tiles * P.n_tiles;
 }
 
@@ -119,17 +126,23 @@ __device__ __forceinline__ Fp8Unit fp8_unit(const Fp8GemmParams& P, int32_t t) {
   u.t = t;
   int32_t v = t;
   u.out_off = 0;
+  u.single = false;
   u.q0 = 0;
   u.q1 = P.segs * P.kb;
   if (P.mode == FP8_ROWS) {
     // an expert's weights are read by its row tiles one after the other
-    u.mt = v / P.n_tiles;
+    u.tile = v / P.n_tiles;
     u.nt = v % P.n_tiles;
-    const int32_t e = min(max(__ldcg(P.plan_expert + u.mt), 0), P.experts - 1), local = e % P.per;
+    if (CTAS == 2) {
+      const int32_t pair = __ldcg(P.plan_pair + u.tile);
+      u.single = (pair & kSingle) != 0;
+      u.tile = min(max(pair & (kSingle - 1), 0), P.max_tiles - 1);
+    }
+    const int32_t e = min(max(__ldcg(P.plan_expert + u.tile), 0), P.experts - 1), local = e % P.per;
     u.g = 0;
     u.bi = e / P.per;
-    u.a_row = u.mt * P.tile_rows * CTAS;
-    u.ea = u.mt * CTAS;
+    u.a_row = u.tile * P.tile_rows;
+    u.ea = u.tile;
     u.b_row = local * P.cols + u.nt * Fp8Cfg<CTAS>::BN;
     u.eb = local * P.eb_blocks + u.nt * CTAS;
     return u;
@@ -141,10 +154,10 @@ __device__ __forceinline__ Fp8Unit fp8_unit(const Fp8GemmParams& P, int32_t t) {
   const int32_t tall = min(P.band, P.m_tiles - first);
   v -= first * P.n_tiles;
   u.nt = v / tall;
-  u.mt = first + v % tall;
+  u.tile = (first + v % tall) * CTAS;
   u.bi = 0;
-  u.a_row = u.mt * 128 * CTAS;
-  u.ea = u.mt * CTAS;
+  u.a_row = u.tile * 128;
+  u.ea = u.tile;
   u.b_row = u.nt * Fp8Cfg<CTAS>::BN;
   u.eb = u.nt * CTAS;
   if (P.mode == FP8_CONTRACT) {
@@ -164,7 +177,7 @@ struct Fp8Walk {
   int32_t run, depth;       // k-blocks of a run, of a tile
 
   __device__ __forceinline__ Fp8Walk(const Fp8GemmParams& P) {
-    const int32_t me = static_cast<int32_t>(blockIdx.x) / CTAS, all = static_cast<int32_t>(gridDim.x) / CTAS, tiles = fp8_tiles(P);
+    const int32_t me = static_cast<int32_t>(blockIdx.x) / CTAS, all = static_cast<int32_t>(gridDim.x) / CTAS, tiles = fp8_tiles<CTAS>(P);
     depth = P.segs * P.kb;
     if (CTAS == 1 && P.stream) {
       const int32_t work = tiles * depth;
@@ -426,6 +439,103 @@ __device__ __forceinline__ void drain(const Fp8GemmParams& P, const Fp8Place& w,
   else drain_bf16(P, w, load, last_first, stg, lane, released);
 }
 
+// ------------------------------------------------------------------ tiles of few rows (CTAS = 1)
+//
+// A warp's lanes of tensor memory are 32 of the rows, so that with few rows
+// one warp would do the epilogue of 128 columns, 7 us of it with GeLU and
+// packing.  It passes 32 rows on in shared memory instead, and all 128 threads
+// take a share: G neighbours a row, four columns each at a time.
+
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool epilogue_all(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.and.pred p, 1, 128, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(all)
+      : "r"(ok ? 1u : 0u)
+      : "memory");
+  return all != 0;
+}
+__device__ __forceinline__ uint32_t pass_at(uint32_t buf, uint32_t row, uint32_t piece) { return buf + row * 512 + ((piece ^ (row & 7)) << 4); }
+
+__device__ __forceinline__ void pass_rows(const FromTmem& load, uint32_t buf, uint32_t lane) {
+#pragma unroll 1
+  for (uint32_t j = 0; j < 4; ++j) {
+    float v[32];
+    load(j, v);
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i)
+      st_shared_v4(pass_at(buf, lane, j * 8 + i), make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                                                              __float_as_uint(v[4 * i + 3])));
+  }
+}
+
+// part: fp32 sums [rows][128] instead of results, or null.
+template <bool QUANT, int G>
+__device__ __forceinline__ void drain_together(const Fp8GemmParams& P, const Fp8Place& w, float* part, uint32_t buf, uint32_t t) {
+  constexpr int N = 32 / G;
+  const uint32_t r = t / G, g = t % G;
+  const bool mine = static_cast<int32_t>(r) < w.rows;
+  const int64_t at = w.off + (static_cast<int64_t>(w.row) + r) * P.cols + w.col;
+  float v[N][4], top = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint4 f = ld_shared_v4(pass_at(buf, r, i * G + g));
+    v[i][0] = __uint_as_float(f.x), v[i][1] = __uint_as_float(f.y), v[i][2] = __uint_as_float(f.z), v[i][3] = __uint_as_float(f.w);
+  }
+  if (part) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (mine) __stcg(reinterpret_cast<float4*>(part + r * 128) + i * G + g, make_float4(v[i][0], v[i][1], v[i][2], v[i][3]));
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int32_t c = (i * G + static_cast<int32_t>(g)) * 4;  // of the tile
+    const bool in = mine && w.col + c < P.cols;
+    if (in) {
+      if (P.bias[w.o]) {
+        const uint2 b = *reinterpret_cast<const uint2*>(P.bias[w.o] + w.col + c);
+        v[i][0] += bf_lo(b.x), v[i][1] += bf_hi(b.x), v[i][2] += bf_lo(b.y), v[i][3] += bf_hi(b.y);
+      }
+      if (P.epi == TP_EPI_DGELU) {
+        const uint2 h = *reinterpret_cast<const uint2*>(P.aux[w.o] + at + c);
+        times_gelu_prime2(v[i][0], v[i][1], bf_lo(h.x), bf_hi(h.x));
+        times_gelu_prime2(v[i][2], v[i][3], bf_lo(h.y), bf_hi(h.y));
+      } else if (P.epi == TP_EPI_GELU) {
+        if (P.aux[w.o]) *reinterpret_cast<uint2*>(P.aux[w.o] + at + c) = make_uint2(pack_bf16(v[i][0], v[i][1]), pack_bf16(v[i][2], v[i][3]));
+        gelu2(v[i][0], v[i][1]);
+        gelu2(v[i][2], v[i][3]);
+      }
+      if constexpr (!QUANT) {
+        if (P.out32) *reinterpret_cast<float4*>(P.out32 + at + c) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+        else *reinterpret_cast<uint2*>(P.out[w.o] + at + c) = make_uint2(pack_bf16(v[i][0], v[i][1]), pack_bf16(v[i][2], v[i][3]));
+      }
+    } else {
+      v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
+    }
+    if constexpr (QUANT) top = fmaxf(top, fmaxf(fmaxf(finite_abs(v[i][0]), finite_abs(v[i][1])), fmaxf(finite_abs(v[i][2]), finite_abs(v[i][3]))));
+  }
+  if constexpr (QUANT) {
+    if (w.col >= P.cols) return;
+#pragma unroll
+    for (int o = G / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    const uint32_t e = fp8_exponent(top);
+    const float inv = fp8_inverse(e);
+    if (mine) {
+      uint32_t* to = reinterpret_cast<uint32_t*>(P.zq[w.o] + (static_cast<int64_t>(w.row) + r) * P.zq_ld + w.col);
+#pragma unroll
+      for (int i = 0; i < N; ++i) to[i * G + g] = fp8_pack4(v[i][0], v[i][1], v[i][2], v[i][3], inv);
+      const int32_t b = w.col / 128;
+      if (g == 0)
+        P.ze[w.o][w.eblock * P.ze_ld + (b >> 2) * 512 + fp8_e_at(static_cast<uint32_t>(w.erow) + r, b & 3)] = static_cast<uint8_t>(e);
+    }
+  }
+}
+
 // ------------------------------------------------------------------ tiles that several runs share (CTAS = 1)
 //
 // A run has at most two parts, [tile_rows][128] each: of the tile that is not
@@ -445,13 +555,13 @@ __global__ void __launch_bounds__(kJoinThreads) fp8_join_kernel(const __grid_con
   griddep_launch_dependents();
   const uint32_t lane = threadIdx.x & 31;
   const int32_t i = static_cast<int32_t>(blockIdx.x) + 1;
-  const int32_t depth = P.segs * P.kb, work = fp8_tiles(P) * depth, run = max((work + P.runs - 1) / P.runs, P.min_run);
+  const int32_t depth = P.segs * P.kb, work = fp8_tiles<1>(P) * depth, run = max((work + P.runs - 1) / P.runs, P.min_run);
   const int32_t end = i * run, t = end / depth, from = t * depth;
   if (end >= work || end == from || end - run > from) return;
   const int32_t lo = i - 1, hi = (from + depth - 1) / run;
   const Fp8Unit u = fp8_unit<1>(P, t);
   const int32_t r = static_cast<int32_t>(blockIdx.y) * (kJoinThreads / 32) + static_cast<int32_t>(threadIdx.x >> 5);
-  const int64_t row = static_cast<int64_t>(u.mt) * P.tile_rows + r;
+  const int64_t row = static_cast<int64_t>(u.tile) * P.tile_rows + r;
   if (r >= P.tile_rows || (P.mode != FP8_ROWS && row >= P.rows)) return;
   const int32_t o = P.mode == FP8_DENSE ? u.g : 0, c = u.nt * 128 + static_cast<int32_t>(lane) * 4;
   float v[4] = {};
@@ -492,7 +602,7 @@ __global__ void __launch_bounds__(kJoinThreads) fp8_join_kernel(const __grid_con
     for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
     const uint32_t e = fp8_exponent(top);
     *reinterpret_cast<uint32_t*>(P.zq[o] + row * P.zq_ld + c) = fp8_pack4(v[0], v[1], v[2], v[3], fp8_inverse(e));
-    if (lane == 0) P.ze[o][u.mt * P.ze_ld + (u.nt >> 2) * 512 + fp8_e_at(static_cast<uint32_t>(r), u.nt & 3)] = static_cast<uint8_t>(e);
+    if (lane == 0) P.ze[o][u.tile * P.ze_ld + (u.nt >> 2) * 512 + fp8_e_at(static_cast<uint32_t>(r), u.nt & 3)] = static_cast<uint8_t>(e);
   }
 }
 
@@ -679,8 +789,10 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
     const uint32_t stg = base + C::STG_OFF + (warp - 2) * C::STG_BYTES;
     uint32_t n = 0;
     for (; walk.next(P, u); ++n) {
-      const bool ok = wait(tfull_bar(n & 1), n >> 1, 4u);
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      bool ok = wait(tfull_bar(n & 1), n >> 1, 4u);
+      // the warps that meet at barriers below give up together
+      ok = CTAS == 1 && P.together ? epilogue_all(ok) : __all_sync(0xFFFFFFFFu, ok) != 0;
+      if (!ok) break;
       tc_fence_after();
       const uint32_t taddr = tmem + ((quarter * 32) << 16) + ((n & 1) ? C::ACC1 : 0) + part * 128;
       const bool empty = u.q0 >= u.q1;
@@ -697,14 +809,17 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
       w.off = u.out_off;
       w.col = u.nt * C::BN + static_cast<int32_t>(part) * 128;
       const int32_t tile_row = static_cast<int32_t>(quarter) * 32;
+      const int32_t tile = u.tile + static_cast<int32_t>(crank);
+      int32_t all_rows;  // of the tile
       if (P.mode == FP8_ROWS) {
-        w.row = (u.mt * CTAS + static_cast<int32_t>(crank)) * P.tile_rows + tile_row;
-        w.rows = min(max(P.tile_rows - tile_row, 0), 32);
+        w.row = tile * P.tile_rows + tile_row;
+        all_rows = u.single && crank == 1 ? 0 : P.tile_rows;
       } else {
-        w.row = (u.mt * CTAS + static_cast<int32_t>(crank)) * 128 + tile_row;
-        w.rows = min(max(P.rows - w.row, 0), 32);
+        w.row = tile * 128 + tile_row;
+        all_rows = P.rows - tile * 128;
       }
-      w.eblock = u.mt * CTAS + static_cast<int32_t>(crank);
+      w.rows = min(max(all_rows - tile_row, 0), 32);
+      w.eblock = tile;
       w.erow = tile_row;
       // The shared columns are the first accumulator's last 32 and the
       // second's first; without them the tile counts as begun at once.
@@ -715,7 +830,22 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
         if (!early) begun();
       };
       const FromTmem acc{taddr, empty};
-      if (w.rows > 0 && CTAS == 1 && walk.stride == 0 && u.q1 - u.q0 < walk.depth) {
+      const bool partial = CTAS == 1 && walk.stride == 0 && u.q1 - u.q0 < walk.depth;
+      if (CTAS == 1 && P.together) {
+        const uint32_t buf = base + C::STG_OFF, t = threadIdx.x - 64;
+        float* part = partial ? part_at(P, static_cast<int32_t>(blockIdx.x), u.q0 == 0) : nullptr;
+        w.row -= tile_row;
+        for (int32_t q = 0; q * 32 < all_rows && q < 4; ++q) {
+          if (static_cast<int32_t>(quarter) == q) pass_rows(acc, buf, lane);
+          epilogue_sync();
+          w.rows = min(all_rows - q * 32, 32);
+          w.erow = q * 32;
+          if (P.tile_rows <= 16) drain_together<QUANT, 8>(P, w, part, buf, t);
+          else drain_together<QUANT, 4>(P, w, part ? part + q * 32 * 128 : nullptr, buf, t);
+          w.row += 32;
+          epilogue_sync();
+        }
+      } else if (w.rows > 0 && partial) {
         drain_f32(part_at(P, static_cast<int32_t>(blockIdx.x), u.q0 == 0) + tile_row * 128, 128, 128, w.rows, acc, stg, lane, [] {});
       } else if (w.rows > 0) {
         drain<QUANT>(P, w, acc, (n & 1) == 0, stg, lane, released);

@@ -153,7 +153,7 @@ def test_training_step(tp, p, E, T, k, h, f, closed, skew):
     tp.tp_experts_bwd_fp8(P.x, P.weights, P.dy, P.t1, P.t2, dx, dw, d1, d2, saved, ws)
     assert tp.tp_get_device_status(ws) == tp.TP_OK
     # the plan: tiles of 128 rows of one expert, slots in their order
-    n, first = int(saved.plan[0]), saved.plan[1:E + 2].tolist()
+    n, pairs, first = int(saved.plan[0]), int(saved.plan[1]), saved.plan[2:E + 3].tolist()
     row_of = torch.full((T * k,), -1, dtype=torch.int64)
     rows = 0
     for e in range(E):
@@ -162,6 +162,7 @@ def test_training_step(tp, p, E, T, k, h, f, closed, skew):
         row_of[(t * k + j).cpu()] = rows + torch.arange(t.numel())
         rows += -(-t.numel() // 128) * 128
     assert n == first[E] == rows // 128
+    assert pairs == sum((b - a + 1) // 2 for a, b in zip(first, first[1:]))
     row_of = row_of.cuda()
     zero = torch.zeros((), dtype=D, device="cuda")
     gx, ex, sx = (torch.zeros((T, h), dtype=D, device="cuda") for _ in range(3))
