@@ -102,8 +102,7 @@ tp_status fp8_product(const Fp8Product& d, const Fp8Launch& l, void* part, uint3
   P.b_by_g = d.nb > 1 && d.groups > 1;
   P.b_by_s = d.nb > 1 && d.segs > 1;
   P.tile_rows = static_cast<int32_t>(tile_rows_of(d.mode, d.rows, d.plan));
-  // Four warps with 32 rows each are as fast by themselves from 128 rows on.
-  P.together = l.ctas == 1 && P.tile_rows <= 64;
+  P.few = l.ctas == 1 && P.tile_rows <= 64;
   P.m_tiles = static_cast<int32_t>(cdiv(d.rows, 128 * l.ctas));
   P.n_tiles = static_cast<int32_t>(cdiv(d.cols, 128 * l.ctas));
   P.kb = static_cast<int32_t>(cdiv(d.depth, 128));
@@ -147,7 +146,7 @@ tp_status fp8_product(const Fp8Product& d, const Fp8Launch& l, void* part, uint3
     const int64_t a_blocks = by_rows ? d.plan->max_tiles : cdiv(d.rows, 128);
     const int64_t b_rows = by_rows ? d.per * d.cols : d.cols, b_blocks = by_rows ? d.per * cdiv(d.cols, 128) : cdiv(d.cols, 128);
     for (int i = 0; i < d.na; ++i)
-      if (!encode_q(&P.a[i], d.a[i].q, d.rows, d.depth, contract ? 128 : P.tile_rows) || !encode_e(&P.ea[i], d.a[i].e, a_blocks, d.depth, 1))
+      if (!encode_q(&P.a[i], d.a[i].q, d.rows, d.depth, P.tile_rows) || !encode_e(&P.ea[i], d.a[i].e, a_blocks, d.depth, 1))
         return TP_ERR_CUDA;
     for (int i = 0; i < d.nb; ++i)
       if (!encode_q(&P.b[i], d.b[i].q, b_rows, d.depth, 128) || !encode_e(&P.eb[i], d.b[i].e, b_blocks, d.depth, l.ctas)) return TP_ERR_CUDA;

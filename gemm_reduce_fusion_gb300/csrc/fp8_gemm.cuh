@@ -15,9 +15,9 @@
 // 32 KiB a CTA in both.  A pair moves 64 bytes an SM and cycle from L2 at the
 // full MMA rate, a single CTA's tile 128.
 //
-// Roles: warp 0 loads, warp 1 issues the MMAs, the others (four for each 128
-// columns) are the epilogue, which overlaps the next tile's MMAs on the other
-// accumulator.  With 256 columns the two accumulators share 32 columns of
+// Roles: warp 0 loads, warp 1 issues the MMAs, eight others are the epilogue,
+// each with 32 rows and half of the columns, which overlaps the next tile's
+// MMAs on the other accumulator.  With 256 columns the two accumulators share 32 columns of
 // tensor memory, which the epilogue reads first: 480 of the 512 columns, the
 // rest for the scales.
 //
@@ -44,7 +44,7 @@ struct Fp8GemmParams {
   int32_t kb;                   // k-blocks of a segment
   int32_t stream;               // runs of k-blocks instead of whole tiles (CTAS = 1)
   int32_t min_run;              // the shortest of them
-  int32_t together;             // the epilogue's warps share a tile's rows (CTAS = 1)
+  int32_t few;                  // tiles of few rows, the N of the MMAs (CTAS = 1)
   int32_t rows, cols;           // of an output (FP8_ROWS: rows not used)
   int32_t tile_rows;            // rows of an A tile that are loaded (CTAS = 1: 16 .. 128)
   int32_t band;                 // m-tiles that go together through the n-tiles
@@ -73,22 +73,36 @@ struct Fp8GemmParams {
 
 constexpr int32_t kSingle = 1 << 30;
 
+// Places of a stage: A's k-blocks, of `rows` rows each, then B's.  (With 65 to
+// 127 rows the MMA reads 128 from where A begins: what lies behind its rows
+// goes into rows of D that are not used.)
+template <int CTAS>
+struct Fp8Ring {
+  uint32_t base, a_bytes, stage_bytes;
+  int count;
+  __device__ __forceinline__ Fp8Ring(uint32_t base, int32_t rows);
+  __device__ __forceinline__ uint32_t a(int stage, int d) const { return base + stage * stage_bytes + d * a_bytes; }
+  __device__ __forceinline__ uint32_t b(int stage, int d) const;
+  __device__ __forceinline__ uint32_t e(int stage, int d) const;
+};
+
 template <int CTAS>
 struct Fp8Cfg {
   static constexpr int BN = 128 * CTAS;
   // A stage has two k-blocks of A, two of B and their exponents.  (With one,
   // the loads alone of the MLP's launches took 148 us, with two 115: each
-  // stage costs its loader some 150 ns beside the copies.)
+  // stage costs its loader some 150 ns beside the copies.)  A pair has three
+  // stages; a single CTA's are shorter, and more, where a tile has few rows.
   static constexpr int DEEP = 2;
-  static constexpr uint32_t A_BYTES = 128 * 128, B_BYTES = 128 * 128;  // of a k-block
+  static constexpr uint32_t B_BYTES = 128 * 128;  // of a k-block
   static constexpr uint32_t EA_BYTES = 512, EB_BYTES = 512 * CTAS, E_BYTES = EA_BYTES + EB_BYTES;
-  static constexpr uint32_t STAGE = DEEP * (A_BYTES + B_BYTES);
-  static constexpr int STAGES = 3;
-  static constexpr int EPI_WARPS = 4 * CTAS;
+  static constexpr uint32_t RING = 192 * 1024;
+  static constexpr int MAX_STAGES = CTAS == 1 ? 5 : 3;
+  static constexpr int EPI_WARPS = 8;
+  static constexpr int COLS = BN / 2;  // of an epilogue warp
   static constexpr int THREADS = 64 + 32 * EPI_WARPS;
-  static constexpr uint32_t STG_BYTES = CTAS == 1 ? 4096 : 2048;  // staging of an epilogue warp
-  static constexpr uint32_t E_OFF = STAGES * STAGE, STG_OFF = E_OFF + STAGES * DEEP * E_BYTES,
-                            BAR_OFF = STG_OFF + EPI_WARPS * STG_BYTES;
+  static constexpr uint32_t STG_BYTES = 2048;  // staging of an epilogue warp
+  static constexpr uint32_t E_OFF = RING, STG_OFF = E_OFF + MAX_STAGES * DEEP * E_BYTES, BAR_OFF = STG_OFF + EPI_WARPS * STG_BYTES;
   static constexpr uint32_t SMEM = 1024 + BAR_OFF + 256;
   // tensor memory: accumulators of BN columns at 0 and ACC1, scales from SF
   // on (A 4 columns, B 4 CTAS), two of them by turns
@@ -96,11 +110,24 @@ struct Fp8Cfg {
   static constexpr uint32_t ACC1 = BN - SHARED, SF = 480;
   static_assert(ACC1 + BN <= SF, "accumulators before the scales");
   static_assert(SMEM <= 227 * 1024, "shared memory of a CTA");
-  // in a stage: A's k-blocks, B's
-  static __device__ __forceinline__ uint32_t a(uint32_t base, int stage, int d) { return base + stage * STAGE + d * A_BYTES; }
-  static __device__ __forceinline__ uint32_t b(uint32_t base, int stage, int d) { return base + stage * STAGE + DEEP * A_BYTES + d * B_BYTES; }
-  static __device__ __forceinline__ uint32_t e(uint32_t base, int stage, int d) { return base + E_OFF + (stage * DEEP + d) * E_BYTES; }
 };
+
+template <int CTAS>
+__device__ __forceinline__ Fp8Ring<CTAS>::Fp8Ring(uint32_t at, int32_t rows) {
+  using C = Fp8Cfg<CTAS>;
+  base = at;
+  a_bytes = (CTAS == 2 ? 128u : static_cast<uint32_t>(rows)) * 128u;
+  stage_bytes = C::DEEP * (a_bytes + C::B_BYTES);
+  count = CTAS == 2 ? C::MAX_STAGES : min(static_cast<int>(C::RING / stage_bytes), C::MAX_STAGES);
+}
+template <int CTAS>
+__device__ __forceinline__ uint32_t Fp8Ring<CTAS>::b(int stage, int d) const {
+  return base + stage * stage_bytes + Fp8Cfg<CTAS>::DEEP * a_bytes + d * Fp8Cfg<CTAS>::B_BYTES;
+}
+template <int CTAS>
+__device__ __forceinline__ uint32_t Fp8Ring<CTAS>::e(int stage, int d) const {
+  return base + Fp8Cfg<CTAS>::E_OFF + (stage * Fp8Cfg<CTAS>::DEEP + d) * Fp8Cfg<CTAS>::E_BYTES;
+}
 
 struct Fp8Unit {
   int32_t t;          // tile
@@ -114,9 +141,12 @@ struct Fp8Unit {
   int64_t out_off;    // FP8_CONTRACT: the expert's place in its shard
 };
 
+// What all lanes of a warp have, in a form that the compiler knows to be so.
+__device__ __forceinline__ int32_t uniform(int32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
 template <int CTAS>
 __device__ __forceinline__ int32_t fp8_tiles(const Fp8GemmParams& P) {
-  if (P.mode == FP8_ROWS) return min(__ldcg(CTAS == 2 ? P.plan_pairs : P.plan_tiles), P.max_tiles) * P.n_tiles;
+  if (P.mode == FP8_ROWS) return min(uniform(__ldcg(CTAS == 2 ? P.plan_pairs : P.plan_tiles)), P.max_tiles) * P.n_tiles;
   return P.groups * P.m_tiles * P.n_tiles;
 }
 
@@ -134,11 +164,11 @@ __device__ __forceinline__ Fp8Unit fp8_unit(const Fp8GemmParams& P, int32_t t) {
     u.tile = v / P.n_tiles;
     u.nt = v % P.n_tiles;
     if (CTAS == 2) {
-      const int32_t pair = __ldcg(P.plan_pair + u.tile);
+      const int32_t pair = uniform(__ldcg(P.plan_pair + u.tile));
       u.single = (pair & kSingle) != 0;
       u.tile = min(max(pair & (kSingle - 1), 0), P.max_tiles - 1);
     }
-    const int32_t e = min(max(__ldcg(P.plan_expert + u.tile), 0), P.experts - 1), local = e % P.per;
+    const int32_t e = min(max(uniform(__ldcg(P.plan_expert + u.tile)), 0), P.experts - 1), local = e % P.per;
     u.g = 0;
     u.bi = e / P.per;
     u.a_row = u.tile * P.tile_rows;
@@ -161,8 +191,8 @@ __device__ __forceinline__ Fp8Unit fp8_unit(const Fp8GemmParams& P, int32_t t) {
   u.b_row = u.nt * Fp8Cfg<CTAS>::BN;
   u.eb = u.nt * CTAS;
   if (P.mode == FP8_CONTRACT) {
-    u.q0 = min(max(__ldcg(P.plan_first + u.g), 0), P.max_tiles) * P.kb_tile;
-    u.q1 = min(__ldcg(P.plan_first + u.g + 1), P.max_tiles) * P.kb_tile;
+    u.q0 = min(max(uniform(__ldcg(P.plan_first + u.g)), 0), P.max_tiles) * P.kb_tile;
+    u.q1 = min(uniform(__ldcg(P.plan_first + u.g + 1)), P.max_tiles) * P.kb_tile;
     u.bi = u.g / P.per;  // of the outputs
     u.out_off = static_cast<int64_t>(u.g % P.per) * P.rows * P.cols;
   }
@@ -288,7 +318,7 @@ __device__ __forceinline__ void stage_bf16(const float (&v)[32], uint32_t stg, u
                             pack_bf16(v[8 * i + 6], v[8 * i + 7])));
 }
 
-// 32 columns of a warp's 128 of the accumulator.
+// 32 columns of a warp's of the accumulator.
 struct FromTmem {
   uint32_t taddr;
   bool empty;  // no contraction: zeros
@@ -306,7 +336,7 @@ struct FromTmem {
   }
 };
 
-// One warp's 32 rows x 128 columns of a finished tile.  `released` is called
+// One warp's 32 rows x COLS columns of a finished tile.  `released` is called
 // once the columns that both accumulators have are in registers: the 32 that
 // drain_bf16 takes first.
 struct Fp8Place {
@@ -317,14 +347,14 @@ struct Fp8Place {
   int32_t eblock, erow;  // 128 rows of exponents of an 8-bit result, first row in them
 };
 
-template <typename Released>
+template <int COLS, typename Released>
 __device__ __forceinline__ void drain_bf16(const Fp8GemmParams& P, const Fp8Place& w, const FromTmem& load, bool last_first, uint32_t stg,
                                            uint32_t lane, Released released) {
   const int64_t pitch = static_cast<int64_t>(P.cols) * 2;
   const __nv_bfloat16* bias = P.bias[w.o];
 #pragma unroll 1
-  for (int part = 0; part < 4; ++part) {
-    const int j = last_first ? (part + 3) & 3 : part;
+  for (int part = 0; part < COLS / 32; ++part) {
+    const int j = last_first ? (part + COLS / 32 - 1) % (COLS / 32) : part;
     const int32_t c = w.col + j * 32, bytes = min(P.cols - c, 32) * 2;
     const int64_t at = (w.off + static_cast<int64_t>(w.row) * P.cols + c) * 2;
     float v[32];
@@ -355,21 +385,23 @@ __device__ __forceinline__ void drain_bf16(const Fp8GemmParams& P, const Fp8Plac
   }
 }
 
-// The same with the result in 8 bits: a thread has the 128 columns of its
-// row that share an exponent.
-template <typename Released>
+// The same with the result in 8 bits.  COLS = 128: a thread has the columns of
+// its row that share an exponent; 64: half of them, and `red` (of this warp's
+// rows: [2][32], `half` its own) and a barrier with the other half's warp.
+template <int COLS, typename Released>
 __device__ __forceinline__ void drain_fp8(const Fp8GemmParams& P, const Fp8Place& w, const FromTmem& load, uint32_t stg, uint32_t lane,
-                                          Released released) {
+                                          float (*red)[32], uint32_t half, uint32_t barrier, Released released) {
   const int64_t pitch = static_cast<int64_t>(P.cols) * 2;
   const __nv_bfloat16* bias = P.bias[w.o];
-  float v[4][32];
+  float v[COLS / 32][32];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) load(j, v[j]);
+  for (int j = 0; j < COLS / 32; ++j) load(j, v[j]);
   released();
-  if (w.col >= P.cols) return;
+  const int32_t block = w.col / 128;
+  if (block * 128 >= P.cols) return;
   float top = 0.f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < COLS / 32; ++j) {
     const int32_t c = w.col + j * 32, bytes = min(P.cols - c, 32) * 2;
     const int64_t at = (w.off + static_cast<int64_t>(w.row) * P.cols + c) * 2;
     if (bias) add_bias(v[j], bias, c, P.cols);
@@ -384,37 +416,41 @@ __device__ __forceinline__ void drain_fp8(const Fp8GemmParams& P, const Fp8Place
       top = fmaxf(top, fmaxf(finite_abs(v[j][i]), finite_abs(v[j][i + 1])));
     }
   }
+  if constexpr (COLS == 64) {
+    red[half][lane] = top;
+    asm volatile("bar.sync %0, 64;" ::"r"(barrier) : "memory");
+    top = fmaxf(top, red[half ^ 1][lane]);
+    asm volatile("bar.sync %0, 64;" ::"r"(barrier) : "memory");  // read, before the next tile's is written
+  }
   const uint32_t e = fp8_exponent(top);
   const float inv = fp8_inverse(e);
 #pragma unroll
-  for (uint32_t half = 0; half < 2; ++half) {
+  for (uint32_t piece = 0; piece < COLS / 64; ++piece) {
 #pragma unroll
     for (uint32_t j = 0; j < 4; ++j) {
       uint32_t o[4];
 #pragma unroll
       for (uint32_t i = 0; i < 4; ++i) {
-        const uint32_t n = half * 64 + j * 16 + i * 4;
+        const uint32_t n = piece * 64 + j * 16 + i * 4;
         o[i] = fp8_pack4(v[n / 32][n % 32], v[n / 32][n % 32 + 1], v[n / 32][n % 32 + 2], v[n / 32][n % 32 + 3], inv);
       }
       st_shared_v4(stg_at(stg, lane, j), make_uint4(o[0], o[1], o[2], o[3]));
     }
-    stg_out(stg, P.zq[w.o] + w.row * P.zq_ld + w.col + half * 64, P.zq_ld, w.rows, 64, lane);
+    stg_out(stg, P.zq[w.o] + w.row * P.zq_ld + w.col + piece * 64, P.zq_ld, w.rows, 64, lane);
   }
-  if (static_cast<int32_t>(lane) < w.rows) {
-    const int32_t b = w.col / 128;
-    P.ze[w.o][w.eblock * P.ze_ld + (b >> 2) * 512 + fp8_e_at(static_cast<uint32_t>(w.erow) + lane, b & 3)] = static_cast<uint8_t>(e);
-  }
+  if (static_cast<int32_t>(lane) < w.rows && (COLS == 128 || half == 0))
+    P.ze[w.o][w.eblock * P.ze_ld + (block >> 2) * 512 + fp8_e_at(static_cast<uint32_t>(w.erow) + lane, block & 3)] = static_cast<uint8_t>(e);
 }
 
-// fp32 results: 128 columns from `to` on, of which `cols` are there.
-template <typename Released>
+// fp32 results: COLS columns from `to` on, of which `cols` are there.
+template <int COLS, typename Released>
 __device__ __forceinline__ void drain_f32(float* to, int64_t pitch, int32_t cols, int32_t rows, const FromTmem& load, uint32_t stg,
                                           uint32_t lane, Released released) {
 #pragma unroll 1
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < COLS / 32; ++j) {
     float v[32];
     load(j, v);
-    if (j == 3) released();
+    if (j == COLS / 32 - 1) released();
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int32_t c = j * 32 + half * 16;
@@ -430,29 +466,24 @@ __device__ __forceinline__ void drain_f32(float* to, int64_t pitch, int32_t cols
   }
 }
 
-template <bool QUANT, typename Released>
-__device__ __forceinline__ void drain(const Fp8GemmParams& P, const Fp8Place& w, const FromTmem& load, bool last_first, uint32_t stg,
-                                      uint32_t lane, Released released) {
-  if constexpr (QUANT) drain_fp8(P, w, load, stg, lane, released);
-  else if (P.out32)
-    drain_f32(P.out32 + static_cast<int64_t>(w.row) * P.cols + w.col, P.cols, P.cols - w.col, w.rows, load, stg, lane, released);
-  else drain_bf16(P, w, load, last_first, stg, lane, released);
-}
-
 // ------------------------------------------------------------------ tiles of few rows (CTAS = 1)
 //
-// A warp's lanes of tensor memory are 32 of the rows, so that with few rows
-// one warp would do the epilogue of 128 columns, 7 us of it with GeLU and
-// packing.  It passes 32 rows on in shared memory instead, and all 128 threads
-// take a share: G neighbours a row, four columns each at a time.
+// Up to 64 rows are the N of the MMAs and the 128 columns their M: the tensor
+// cores then read the weights' 16 KiB of a k-block from shared memory and the
+// rows', not 128 rows, half of which or more would be for nothing (a k-block
+// took 530 cycles so, whatever the rows; shared memory's bandwidth, which TMA
+// needs too, is what bounds it).  A lane of tensor memory has a column then, a
+// column of it a row: the epilogue turns 32 rows at a time in shared memory,
+// where all 256 threads take a share, G neighbours a row, four columns each at
+// a time.
 
-__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ bool epilogue_all(bool ok) {
   uint32_t all;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 q, %1, 0;\n\t"
-      "bar.red.and.pred p, 1, 128, q;\n\t"
+      "bar.red.and.pred p, 1, 256, q;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(all)
       : "r"(ok ? 1u : 0u)
@@ -461,21 +492,24 @@ __device__ __forceinline__ bool epilogue_all(bool ok) {
 }
 __device__ __forceinline__ uint32_t pass_at(uint32_t buf, uint32_t row, uint32_t piece) { return buf + row * 512 + ((piece ^ (row & 7)) << 4); }
 
-__device__ __forceinline__ void pass_rows(const FromTmem& load, uint32_t buf, uint32_t lane) {
-#pragma unroll 1
-  for (uint32_t j = 0; j < 4; ++j) {
-    float v[32];
-    load(j, v);
+// 16 rows, from `row` of the 32 on, of the warp's 32 columns.
+__device__ __forceinline__ void pass_rows(uint32_t taddr, bool empty, uint32_t buf, uint32_t row, uint32_t col) {
+  uint32_t v[16];
+  if (empty) {
 #pragma unroll
-    for (uint32_t i = 0; i < 8; ++i)
-      st_shared_v4(pass_at(buf, lane, j * 8 + i), make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
-                                                              __float_as_uint(v[4 * i + 3])));
+    for (int i = 0; i < 16; ++i) v[i] = 0;
+  } else {
+    tmem_ld_32x32b_x16(taddr, v);
+    tmem_wait_ld();
   }
+#pragma unroll
+  for (uint32_t i = 0; i < 16; ++i)
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(pass_at(buf, row + i, col >> 2) + (col & 3) * 4), "r"(v[i]) : "memory");
 }
 
 // part: fp32 sums [rows][128] instead of results, or null.
 template <bool QUANT, int G>
-__device__ __forceinline__ void drain_together(const Fp8GemmParams& P, const Fp8Place& w, float* part, uint32_t buf, uint32_t t) {
+__device__ __forceinline__ void drain_few(const Fp8GemmParams& P, const Fp8Place& w, float* part, uint32_t buf, uint32_t t) {
   constexpr int N = 32 / G;
   const uint32_t r = t / G, g = t % G;
   const bool mine = static_cast<int32_t>(r) < w.rows;
@@ -611,18 +645,20 @@ __global__ void __launch_bounds__(kJoinThreads) fp8_join_kernel(const __grid_con
 template <int CTAS, bool QUANT>
 __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(const __grid_constant__ Fp8GemmParams P) {
   using C = Fp8Cfg<CTAS>;
-  constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+  __shared__ float red[CTAS == 1 && QUANT ? 4 : 1][2][32];
+  const Fp8Ring<CTAS> ring(base, P.tile_rows);
+  const int STAGES = ring.count;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem_raw + (base - raw) + C::BAR_OFF);
   const uint32_t bar0 = base + C::BAR_OFF;
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
-  auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
-  auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
-  const uint32_t begun_bar = bar0 + 8u * (2 * STAGES + 2), drain_bar = begun_bar + 8u;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 4);
+  auto empty_bar = [&](int s) { return bar0 + 8u * (C::MAX_STAGES + s); };
+  auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * C::MAX_STAGES + b); };
+  const uint32_t begun_bar = bar0 + 8u * (2 * C::MAX_STAGES + 2), drain_bar = begun_bar + 8u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * C::MAX_STAGES + 4);
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
-  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t warp = static_cast<uint32_t>(uniform(static_cast<int32_t>(threadIdx.x >> 5))), lane = threadIdx.x & 31;
   const uint32_t crank = CTAS == 2 ? cluster_ctarank() : 0;
   const bool leader = crank == 0;
 
@@ -636,6 +672,15 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_barrier_init();
+    // maps that the first loads need
+    for (int i = 0; i < (P.kb == 0 ? 0 : P.a_by_s ? P.segs : 1); ++i) {
+      tma_prefetch_desc(&P.a[i]);
+      tma_prefetch_desc(&P.ea[i]);
+    }
+    if (P.kb > 0) {
+      tma_prefetch_desc(&P.b[0]);
+      tma_prefetch_desc(&P.eb[0]);
+    }
   }
   if (warp == 1) {
     if (CTAS == 2) {
@@ -654,7 +699,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
     __syncthreads();
   }
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = static_cast<uint32_t>(uniform(static_cast<int32_t>(*tmem_slot)));
   griddep_wait();
   griddep_launch_dependents();
 
@@ -664,89 +709,83 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
     return wait_bar(bar, parity & 1u, P.timeout_ns, P.status, abort_flag, role);
   };
 
+  // Waits of the loading and the issuing warp: all lanes give up together.
+  auto wait_warp = [&](uint32_t bar, uint32_t parity, uint32_t role) { return __all_sync(0xFFFFFFFFu, wait(bar, parity, role)) != 0; };
+
   if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ loads (both CTAs)
-      int stage = 0;
-      uint32_t phase = 0, armed = 0, armed_parity = 0;
-      int32_t issued = 0;
-      bool ok = true;
-      const uint32_t block_bytes = static_cast<uint32_t>(P.mode == FP8_CONTRACT ? 128 : P.tile_rows) * 128 + C::B_BYTES;
-      while (ok && walk.next(P, u)) {
-        const int32_t a_row = u.a_row + static_cast<int32_t>(crank) * 128, b_row = u.b_row + static_cast<int32_t>(crank) * 128;
-        Fp8Block b = fp8_block(P, u, u.q0);
-        for (int32_t q = u.q0; q < u.q1; q += C::DEEP) {
-          const int32_t deep = min(u.q1 - q, C::DEEP);
-          if (!wait(empty_bar(stage), phase ^ 1u, 1u)) {
-            ok = false;
-            break;
-          }
-          const bool drop = blockIdx.x == 0 && issued++ == P.drop;  // test hook: the consumer's wait runs out
-          // bytes of the stage: exponents with its first k-block and the first of every four
-          uint32_t bytes = deep * block_bytes;
-          const uint32_t fb = CTAS == 2 ? mapa_shared(full_bar(stage), 0) : full_bar(stage);
-          Fp8Block at[C::DEEP];
-          bool scales[C::DEEP];
+    // -------------------------------------------------------------- loads (both CTAs)
+    const uint32_t one = elect_one();
+    int stage = 0;
+    uint32_t phase = 0, armed = 0, armed_parity = 0;
+    int32_t issued = 0;
+    bool ok = true;
+    const uint32_t block_bytes = ring.a_bytes + C::B_BYTES;
+    while (ok && walk.next(P, u)) {
+      const int32_t a_row = u.a_row + static_cast<int32_t>(crank) * 128, b_row = u.b_row + static_cast<int32_t>(crank) * 128;
+      Fp8Block b = fp8_block(P, u, u.q0);
+      for (int32_t q = u.q0; q < u.q1; q += C::DEEP) {
+        const int32_t deep = min(u.q1 - q, C::DEEP);
+        if (!wait_warp(empty_bar(stage), phase ^ 1u, 1u)) {
+          ok = false;
+          break;
+        }
+        const bool drop = blockIdx.x == 0 && issued++ == P.drop;  // test hook: the consumer's wait runs out
+        // bytes of the stage: exponents with its first k-block and the first of every four
+        uint32_t bytes = deep * block_bytes;
+        const uint32_t fb = CTAS == 2 ? mapa_shared(full_bar(stage), 0) : full_bar(stage);
+        Fp8Block at[C::DEEP];
+        bool scales[C::DEEP];
+#pragma unroll
+        for (int d = 0; d < C::DEEP; ++d) {
+          at[d] = b;
+          scales[d] = d < deep && (q + d == u.q0 || (b.k & 3) == 0);
+          bytes += scales[d] ? C::E_BYTES : 0u;
+          if (++b.k == P.kb && P.mode == FP8_DENSE) b = fp8_block(P, u, q + d + 1);
+        }
+        if (!drop) {
+          if (leader) expect_bytes(one, full_bar(stage), CTAS * bytes);
 #pragma unroll
           for (int d = 0; d < C::DEEP; ++d) {
-            at[d] = b;
-            scales[d] = d < deep && (q + d == u.q0 || (b.k & 3) == 0);
-            bytes += scales[d] ? C::E_BYTES : 0u;
-            if (++b.k == P.kb && P.mode == FP8_DENSE) b = fp8_block(P, u, q + d + 1);
-          }
-          if (!drop) {
-            if (leader) mbar_arrive_expect_tx(full_bar(stage), CTAS * bytes);
-#pragma unroll
-            for (int d = 0; d < C::DEEP; ++d) {
-              if (d >= deep) continue;
-              const CUtensorMap *am = &P.a[at[d].ai], *bm = &P.b[at[d].bi];
-              const uint32_t sa = C::a(base, stage, d), sb = C::b(base, stage, d), se = C::e(base, stage, d);
-              if (CTAS == 2) {
-                tma_load_2d_pair(sa, am, fb, at[d].k * 128, a_row);
-                tma_load_2d_pair(sb, bm, fb, at[d].k * 128, b_row);
-                if (scales[d]) {
-                  tma_load_3d_pair_plain(se, &P.ea[at[d].ai], fb, 0, at[d].k >> 2, u.ea + static_cast<int32_t>(crank));
-                  tma_load_3d_pair_plain(se + C::EA_BYTES, &P.eb[at[d].bi], fb, 0, at[d].k >> 2, u.eb);
-                }
-              } else {
-                tma_load_2d(sa, am, fb, at[d].k * 128, a_row);
-                tma_load_2d(sb, bm, fb, at[d].k * 128, b_row);
-                if (scales[d]) {
-                  tma_load_3d_plain(se, &P.ea[at[d].ai], fb, 0, at[d].k >> 2, u.ea);
-                  tma_load_3d_plain(se + C::EA_BYTES, &P.eb[at[d].bi], fb, 0, at[d].k >> 2, u.eb);
-                }
-              }
+            if (d >= deep) continue;
+            load_2d<CTAS>(one, ring.a(stage, d), &P.a[at[d].ai], fb, at[d].k * 128, a_row);
+            load_2d<CTAS>(one, ring.b(stage, d), &P.b[at[d].bi], fb, at[d].k * 128, b_row);
+            if (scales[d]) {
+              const uint32_t se = ring.e(stage, d);
+              load_3d<CTAS>(one, se, &P.ea[at[d].ai], fb, 0, at[d].k >> 2, u.ea + static_cast<int32_t>(crank));
+              load_3d<CTAS>(one, se + C::EA_BYTES, &P.eb[at[d].bi], fb, 0, at[d].k >> 2, u.eb);
             }
-            armed |= 1u << stage;
-            armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
           }
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          armed |= 1u << stage;
+          armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+        }
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      // every armed stage's last bytes have landed before the CTA goes on
-      if (leader)
-        for (int s = 0; s < STAGES; ++s)
-          if (armed & (1u << s)) drain_wait(full_bar(s), (armed_parity >> s) & 1u, P.timeout_ns);
     }
+    // every armed stage's last bytes have landed before the CTA goes on
+    if (leader)
+      for (int s = 0; s < STAGES; ++s)
+        if (armed & (1u << s)) drain_wait(full_bar(s), (armed_parity >> s) & 1u, P.timeout_ns);
+    __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if (leader) {
       // ------------------------------------------------------------ MMAs (CTA 0)
+      const uint32_t one = elect_one();
       int stage = 0;
       uint32_t phase = 0, n = 0, quads = 0;
       bool ok = true;
       for (; ok && walk.next(P, u); ++n) {
         // the epilogue has begun the tile before: it is done with the one
         // before that, and with the columns that both accumulators have
-        if (n > 0 && !wait(begun_bar, n - 1, 2u)) break;
+        if (n > 0 && !wait_warp(begun_bar, n - 1, 2u)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem + ((n & 1) ? C::ACC1 : 0);
         uint32_t sf = tmem + C::SF;
         int32_t k = fp8_block(P, u, u.q0).k;
         for (int32_t q = u.q0; q < u.q1; q += C::DEEP) {
-          if (!wait(full_bar(stage), phase, 3u)) {
+          if (!wait_warp(full_bar(stage), phase, 3u)) {
             ok = false;
             break;
           }
@@ -757,44 +796,45 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
             if (q + d == u.q0 || (k & 3) == 0) {
               // copies and MMAs of a thread run in the order in which they are issued
               sf = tmem + C::SF + (quads++ & 1) * 16;
-              const uint32_t se = C::e(base, stage, d);
+              const uint32_t se = ring.e(stage, d);
 #pragma unroll
-              for (int i = 0; i < 1 + CTAS; ++i) tmem_cp_scales<CTAS>(sf + 4 * i, se + 512 * i);
+              for (int i = 0; i < 1 + CTAS; ++i) tmem_cp_scales<CTAS>(one, sf + 4 * i, se + 512 * i);
             }
-            const uint32_t idesc = make_idesc_mxf8(128 * CTAS, C::BN, k & 3);
-            const uint64_t ad = make_sw128_desc(C::a(base, stage, d), 16, 1024), bd = make_sw128_desc(C::b(base, stage, d), 16, 1024);
+            const bool few = CTAS == 1 && P.few;  // the rows are the N
+            const uint32_t idesc = few ? make_idesc_mxf8(128, P.tile_rows, k & 3) : make_idesc_mxf8(128 * CTAS, C::BN, k & 3);
+            const uint64_t ra = make_sw128_desc(ring.a(stage, d), 16, 1024), rb = make_sw128_desc(ring.b(stage, d), 16, 1024);
+            const uint64_t ad = few ? rb : ra, bd = few ? ra : rb;
+            const uint32_t sfa = few ? sf + 4 : sf, sfb = few ? sf : sf + 4;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              umma_mxf8<CTAS>(d_tmem, ad + 2 * i, bd + 2 * i, idesc, sf, sf + 4, (q + d > u.q0 || i > 0) ? 1u : 0u);
+              umma_mxf8<CTAS>(one, d_tmem, ad + 2 * i, bd + 2 * i, idesc, sfa, sfb, (q + d > u.q0 || i > 0) ? 1u : 0u);
             if (++k == P.kb && P.mode == FP8_DENSE) k = 0;
           }
-          if (CTAS == 2) umma_commit_pair(empty_bar(stage), 0x3);
-          else umma_commit(empty_bar(stage));
+          commit_to<CTAS>(one, empty_bar(stage), 0x3);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        if (CTAS == 2) umma_commit_pair(tfull_bar(n & 1), 0x3);
-        else umma_commit(tfull_bar(n & 1));
+        commit_to<CTAS>(one, tfull_bar(n & 1), 0x3);
       }
-      if (CTAS == 2) umma_commit_pair(drain_bar, 0x1);
-      else umma_commit(drain_bar);
+      commit_to<CTAS>(one, drain_bar, 0x1);
       drain_wait(drain_bar, 0, P.timeout_ns);
+      __syncwarp();
     }
   } else {
     // -------------------------------------------------------------- epilogue (both CTAs)
-    const uint32_t quarter = warp & 3, part = (warp - 2) >> 2;  // lanes of tensor memory, 128 columns
+    const uint32_t quarter = warp & 3, part = (warp - 2) >> 2;  // lanes of tensor memory, half of the columns
     const uint32_t stg = base + C::STG_OFF + (warp - 2) * C::STG_BYTES;
     uint32_t n = 0;
     for (; walk.next(P, u); ++n) {
       bool ok = wait(tfull_bar(n & 1), n >> 1, 4u);
       // the warps that meet at barriers below give up together
-      ok = CTAS == 1 && P.together ? epilogue_all(ok) : __all_sync(0xFFFFFFFFu, ok) != 0;
+      ok = CTAS == 1 ? epilogue_all(ok) : __all_sync(0xFFFFFFFFu, ok) != 0;
       if (!ok) break;
       tc_fence_after();
-      const uint32_t taddr = tmem + ((quarter * 32) << 16) + ((n & 1) ? C::ACC1 : 0) + part * 128;
+      const uint32_t taddr = tmem + ((quarter * 32) << 16) + ((n & 1) ? C::ACC1 : 0) + part * C::COLS;
       const bool empty = u.q0 >= u.q1;
       auto begun = [&] {
         tc_fence_before();
@@ -807,7 +847,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
       Fp8Place w;
       w.o = P.mode == FP8_DENSE ? u.g : P.mode == FP8_CONTRACT ? u.bi : 0;
       w.off = u.out_off;
-      w.col = u.nt * C::BN + static_cast<int32_t>(part) * 128;
+      w.col = u.nt * C::BN + static_cast<int32_t>(part) * C::COLS;
       const int32_t tile_row = static_cast<int32_t>(quarter) * 32;
       const int32_t tile = u.tile + static_cast<int32_t>(crank);
       int32_t all_rows;  // of the tile
@@ -831,24 +871,33 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
       };
       const FromTmem acc{taddr, empty};
       const bool partial = CTAS == 1 && walk.stride == 0 && u.q1 - u.q0 < walk.depth;
-      if (CTAS == 1 && P.together) {
+      if (CTAS == 1 && P.few) {
         const uint32_t buf = base + C::STG_OFF, t = threadIdx.x - 64;
-        float* part = partial ? part_at(P, static_cast<int32_t>(blockIdx.x), u.q0 == 0) : nullptr;
+        float* part32 = partial ? part_at(P, static_cast<int32_t>(blockIdx.x), u.q0 == 0) : nullptr;
         w.row -= tile_row;
+        w.col = u.nt * C::BN;
         for (int32_t q = 0; q * 32 < all_rows && q < 4; ++q) {
-          if (static_cast<int32_t>(quarter) == q) pass_rows(acc, buf, lane);
+          if (q * 32 + static_cast<int32_t>(part) * 16 < P.tile_rows)
+            pass_rows(tmem + ((quarter * 32) << 16) + ((n & 1) ? C::ACC1 : 0) + q * 32 + part * 16, empty, buf, part * 16, quarter * 32 + lane);
           epilogue_sync();
           w.rows = min(all_rows - q * 32, 32);
           w.erow = q * 32;
-          if (P.tile_rows <= 16) drain_together<QUANT, 8>(P, w, part, buf, t);
-          else drain_together<QUANT, 4>(P, w, part ? part + q * 32 * 128 : nullptr, buf, t);
+          if (P.tile_rows <= 16) drain_few<QUANT, 16>(P, w, part32, buf, t);
+          else drain_few<QUANT, 8>(P, w, part32 ? part32 + q * 32 * 128 : nullptr, buf, t);
           w.row += 32;
           epilogue_sync();
         }
-      } else if (w.rows > 0 && partial) {
-        drain_f32(part_at(P, static_cast<int32_t>(blockIdx.x), u.q0 == 0) + tile_row * 128, 128, 128, w.rows, acc, stg, lane, [] {});
       } else if (w.rows > 0) {
-        drain<QUANT>(P, w, acc, (n & 1) == 0, stg, lane, released);
+        if (partial) {
+          float* to = part_at(P, static_cast<int32_t>(blockIdx.x), u.q0 == 0) + tile_row * 128 + part * C::COLS;
+          drain_f32<C::COLS>(to, 128, C::COLS, w.rows, acc, stg, lane, [] {});
+        } else if constexpr (QUANT) {
+          drain_fp8<C::COLS>(P, w, acc, stg, lane, red[CTAS == 1 ? quarter : 0], part, 2 + quarter, released);
+        } else if (P.out32) {
+          drain_f32<C::COLS>(P.out32 + static_cast<int64_t>(w.row) * P.cols + w.col, P.cols, P.cols - w.col, w.rows, acc, stg, lane, released);
+        } else {
+          drain_bf16<C::COLS>(P, w, acc, (n & 1) == 0, stg, lane, released);
+        }
       }
       tc_fence_before();
     }
