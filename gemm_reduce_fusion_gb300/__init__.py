@@ -226,7 +226,7 @@ def _out_dtype(*groups) -> int:
 
 
 def _ws(ws):
-    return _ptr(ws), ws.numel() * ws.element_size()
+    return _ptr(ws), ws.nbytes
 
 
 def _check(status: int, where: str) -> None:
@@ -244,9 +244,17 @@ def _check(status: int, where: str) -> None:
 # CUDA device (the device the library runs the call on).  None stands for a
 # NULL pointer; the library decides where NULL is allowed.
 
+_GET_DEVICE = None
+
+
 def _current_device() -> int:
-    import torch
-    return torch.cuda.current_device()
+    global _GET_DEVICE
+    if _GET_DEVICE is None:
+        import torch
+        dev = torch.cuda.current_device()  # initialises CUDA
+        _GET_DEVICE = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        return dev
+    return _GET_DEVICE()
 
 
 def _need(where: str, name: str, t, shape, bf16: bool, dev: int) -> None:
@@ -849,13 +857,14 @@ def _fp8s(where: str, name: str, ts, count: int, rows: int, cols: int, dev: int,
         return None
     if len(ts) != count:
         raise ValueError(f"{where}: {name} holds {len(ts)} operands, expected {count}")
-    qs, es = fp8_shapes(rows, cols)
-    qs, es, arr, i = lead + qs, lead + es, _ARRAY[2 * count](), 0
+    qs, es = (*lead, rows, (cols + 127) // 128 * 128), (*lead, (rows + 127) // 128, (cols + 511) // 512, 512)
+    arr, i = _ARRAY[2 * count](), 0
     for q, e in ts:
-        if q.shape != qs or q.dtype is not _E4M3 or q.get_device() != dev or not q.is_contiguous():
-            _refuse(where, f"{name}[{i // 2}].q", q, qs, _E4M3, dev)
-        if e.shape != es or e.dtype is not _UINT8 or e.get_device() != dev or not e.is_contiguous():
-            _refuse(where, f"{name}[{i // 2}].e", e, es, _UINT8, dev)
+        if (q.shape != qs or e.shape != es or q.dtype is not _E4M3 or e.dtype is not _UINT8 or q.get_device() != dev
+                or e.get_device() != dev or not q.is_contiguous() or not e.is_contiguous()):
+            for part, t, shape, dtype in (("q", q, qs, _E4M3), ("e", e, es, _UINT8)):
+                if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+                    _refuse(where, f"{name}[{i // 2}].{part}", t, shape, dtype, dev)
         arr[i] = q.data_ptr()
         arr[i + 1] = e.data_ptr()
         i += 2

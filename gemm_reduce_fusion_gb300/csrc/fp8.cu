@@ -145,11 +145,17 @@ tp_status fp8_product(const Fp8Product& d, const Fp8Launch& l, void* part, uint3
     // rows of an operand's matrix, and blocks of its exponents
     const int64_t a_blocks = by_rows ? d.plan->max_tiles : cdiv(d.rows, 128);
     const int64_t b_rows = by_rows ? d.per * d.cols : d.cols, b_blocks = by_rows ? d.per * cdiv(d.cols, 128) : cdiv(d.cols, 128);
-    for (int i = 0; i < d.na; ++i)
-      if (!encode_q(&P.a[i], d.a[i].q, d.rows, d.depth, P.tile_rows) || !encode_e(&P.ea[i], d.a[i].e, a_blocks, d.depth, 1))
-        return TP_ERR_CUDA;
-    for (int i = 0; i < d.nb; ++i)
-      if (!encode_q(&P.b[i], d.b[i].q, b_rows, d.depth, 128) || !encode_e(&P.eb[i], d.b[i].e, b_blocks, d.depth, l.ctas)) return TP_ERR_CUDA;
+    P.fours = static_cast<int32_t>(cdiv(d.depth, 512));
+    for (int i = 0; i < d.na; ++i) {
+      if (!encode_q(&P.a[i], d.a[i].q, d.rows, d.depth, P.tile_rows)) return TP_ERR_CUDA;
+      P.ea_at[i] = static_cast<const uint8_t*>(d.a[i].e);
+      if (l.ctas == 2 && !encode_e(&P.ea[i], d.a[i].e, a_blocks, d.depth, 1)) return TP_ERR_CUDA;
+    }
+    for (int i = 0; i < d.nb; ++i) {
+      if (!encode_q(&P.b[i], d.b[i].q, b_rows, d.depth, 128)) return TP_ERR_CUDA;
+      P.eb_at[i] = static_cast<const uint8_t*>(d.b[i].e);
+      if (l.ctas == 2 && !encode_e(&P.eb[i], d.b[i].e, b_blocks, d.depth, l.ctas)) return TP_ERR_CUDA;
+    }
   }
   const int64_t tiles = d.groups * (by_rows ? d.plan->max_tiles : P.m_tiles) * P.n_tiles;
   if (tiles > 0x7FFFFFFFll) return TP_ERR_UNSUPPORTED_SHAPE;

@@ -99,21 +99,20 @@ __device__ __forceinline__ void load_2d(uint32_t one, uint32_t dst, const void* 
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar), "r"(one)
         : "memory");
 }
-template <int CTAS>
-__device__ __forceinline__ void load_3d(uint32_t one, uint32_t dst, const void* tmap, uint32_t bar, int32_t x, int32_t y, int32_t z) {
-  if constexpr (CTAS == 2)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-        "@p cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-        " [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(one)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-        "@p cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(one)
-        : "memory");
+__device__ __forceinline__ void load_3d_pair(uint32_t one, uint32_t dst, const void* tmap, uint32_t bar, int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+      "@p cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void load_512(uint32_t one, uint32_t dst, const void* src, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+      "@p cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], 512, [%2];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bar), "r"(one)
+      : "memory");
 }
 __device__ __forceinline__ void expect_bytes(uint32_t one, uint32_t bar, uint32_t bytes) {
   asm volatile(

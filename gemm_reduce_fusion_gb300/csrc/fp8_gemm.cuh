@@ -36,7 +36,9 @@
 namespace tpf {
 
 struct Fp8GemmParams {
-  CUtensorMap a[8], b[8], ea[8], eb[8];
+  CUtensorMap a[8], b[8], ea[8], eb[8];  // ea, eb: CTAS = 2
+  const uint8_t *ea_at[8], *eb_at[8];    // CTAS = 1: the exponents themselves
+  int32_t fours;                         // of k-blocks, in a block of exponents
   int32_t mode;
   int32_t groups, segs;         // outputs; contraction segments (ranks reduced)
   int32_t a_by_g, a_by_s, b_by_g, b_by_s;
@@ -673,13 +675,13 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
     *abort_flag = 0;
     fence_barrier_init();
     // maps that the first loads need
-    for (int i = 0; i < (P.kb == 0 ? 0 : P.a_by_s ? P.segs : 1); ++i) {
-      tma_prefetch_desc(&P.a[i]);
-      tma_prefetch_desc(&P.ea[i]);
-    }
     if (P.kb > 0) {
+      for (int i = 0; i < (P.a_by_s ? P.segs : 1); ++i) tma_prefetch_desc(&P.a[i]);
       tma_prefetch_desc(&P.b[0]);
-      tma_prefetch_desc(&P.eb[0]);
+      if (CTAS == 2) {
+        tma_prefetch_desc(&P.ea[0]);
+        tma_prefetch_desc(&P.eb[0]);
+      }
     }
   }
   if (warp == 1) {
@@ -751,8 +753,13 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
             load_2d<CTAS>(one, ring.b(stage, d), &P.b[at[d].bi], fb, at[d].k * 128, b_row);
             if (scales[d]) {
               const uint32_t se = ring.e(stage, d);
-              load_3d<CTAS>(one, se, &P.ea[at[d].ai], fb, 0, at[d].k >> 2, u.ea + static_cast<int32_t>(crank));
-              load_3d<CTAS>(one, se + C::EA_BYTES, &P.eb[at[d].bi], fb, 0, at[d].k >> 2, u.eb);
+              if constexpr (CTAS == 2) {
+                load_3d_pair(one, se, &P.ea[at[d].ai], fb, 0, at[d].k >> 2, u.ea + static_cast<int32_t>(crank));
+                load_3d_pair(one, se + C::EA_BYTES, &P.eb[at[d].bi], fb, 0, at[d].k >> 2, u.eb);
+              } else {
+                load_512(one, se, P.ea_at[at[d].ai] + (static_cast<int64_t>(u.ea) * P.fours + (at[d].k >> 2)) * 512, fb);
+                load_512(one, se + C::EA_BYTES, P.eb_at[at[d].bi] + (static_cast<int64_t>(u.eb) * P.fours + (at[d].k >> 2)) * 512, fb);
+              }
             }
           }
           armed |= 1u << stage;
