@@ -29,7 +29,6 @@ namespace {
 
 constexpr int kMaxExperts = TP_ROUTE_MAX_EXPERTS, kMaxK = 32;
 constexpr int kDispatchThreads = 1024;
-constexpr int32_t kSingleTile = 1 << 30;  // fp8_gemm.cuh: kSingle
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
 // ------------------------------------------------------------------ plan
@@ -100,8 +99,13 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const __grid
     }
   }
   for (int32_t i = tid; i < mine; i += kDispatchThreads) {
-    P.expert[begin + i] = me;
-    if ((i & 1) == 0) P.pair[pair_begin + i / 2] = (begin + i) | (i + 1 == mine ? kSingleTile : 0);
+    const int32_t rows = count[me] - i * P.tile_rows;
+    P.expert[begin + i] = me << 9 | min(rows, P.tile_rows);
+    if ((i & 1) == 0) {
+      int32_t* pair = P.pair + 2 * (pair_begin + i / 2);
+      pair[0] = begin + i;
+      pair[1] = me << 9 | min(rows, 2 * P.tile_rows);
+    }
   }
   // the slots, in their order
   int32_t at = begin * P.tile_rows;
@@ -263,7 +267,7 @@ bool sizes_of(int p, int64_t E, int64_t T, int64_t k, int64_t h, int64_t f, bool
   // A pair's 256 x 256 tile takes 0.7 of the time of its four 128 x 128 ones,
   // but an expert's last pair may have one tile: from 1.5 tiles on average on.
   s->pairs = s->tile_rows == 128 && s->S >= 192 * std::min(E, s->S);
-  s->plan_bytes = static_cast<size_t>(cdiv(2 + (E + 1) + s->max_tiles + s->max_pairs + s->rows + s->S, 64) * 64) * 4;
+  s->plan_bytes = static_cast<size_t>(cdiv(2 + (E + 1) + s->max_tiles + 2 * s->max_pairs + s->rows + s->S, 64) * 64) * 4;
   return s->rows <= (int64_t(1) << 31) - 129;
 }
 
@@ -296,7 +300,7 @@ Fp8Plan plan_at(const Sizes& s, int32_t* at, PlanArrays* a) {
   a->first = at + 2;
   a->expert = a->first + s.E + 1;
   a->pair = a->expert + s.max_tiles;
-  a->slot = a->pair + s.max_pairs;
+  a->slot = a->pair + 2 * s.max_pairs;
   a->row = a->slot + s.rows;
   Fp8Plan plan = bounds_of(s);
   plan.tiles = a->tiles;

@@ -45,16 +45,20 @@ bool encode_e(CUtensorMap* m, const void* e, int64_t blocks, int64_t cols, int b
             CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int CTAS, bool QUANT>
+template <int CTAS, bool QUANT, bool TURNED>
 tp_status launch_gemm(const Fp8GemmParams& P, int64_t units, cudaStream_t stream) {
   static KernelInfo info;
-  using C = Fp8Cfg<CTAS>;
-  void (*k)(Fp8GemmParams) = fp8_gemm_kernel<CTAS, QUANT>;
+  using C = Fp8Cfg<CTAS, TURNED>;
+  void (*k)(Fp8GemmParams) = fp8_gemm_kernel<CTAS, QUANT, TURNED>;
   int regs = 0;
   TP_TRY(kernel_regs(reinterpret_cast<const void*>(k), &info, &regs));
   const int64_t clusters = std::min<int64_t>(units, kSMs / CTAS);
   return launch_dependent(k, dim3(static_cast<unsigned>(clusters * CTAS)), static_cast<unsigned>(C::THREADS), static_cast<size_t>(C::SMEM),
                           stream, P, CTAS);
+}
+template <int CTAS, bool TURNED>
+tp_status launch_gemm(bool quant, const Fp8GemmParams& P, int64_t units, cudaStream_t stream) {
+  return quant ? launch_gemm<CTAS, true, TURNED>(P, units, stream) : launch_gemm<CTAS, false, TURNED>(P, units, stream);
 }
 
 }  // namespace
@@ -102,7 +106,7 @@ tp_status fp8_product(const Fp8Product& d, const Fp8Launch& l, void* part, uint3
   P.b_by_g = d.nb > 1 && d.groups > 1;
   P.b_by_s = d.nb > 1 && d.segs > 1;
   P.tile_rows = static_cast<int32_t>(tile_rows_of(d.mode, d.rows, d.plan));
-  P.few = l.ctas == 1 && P.tile_rows <= 64;
+  const bool turned = by_rows || (l.ctas == 1 && P.tile_rows <= 64);
   P.m_tiles = static_cast<int32_t>(cdiv(d.rows, 128 * l.ctas));
   P.n_tiles = static_cast<int32_t>(cdiv(d.cols, 128 * l.ctas));
   P.kb = static_cast<int32_t>(cdiv(d.depth, 128));
@@ -120,7 +124,6 @@ tp_status fp8_product(const Fp8Product& d, const Fp8Launch& l, void* part, uint3
     P.plan_pairs = d.plan->pairs;
     P.plan_pair = d.plan->pair;
     P.plan_first = d.plan->first;
-    P.plan_slot = d.plan->slot;
     P.max_tiles = static_cast<int32_t>(d.plan->max_tiles);
     P.experts = d.plan->E;
     P.kb_tile = static_cast<int32_t>(d.plan->tile_rows / 128);
@@ -148,20 +151,21 @@ tp_status fp8_product(const Fp8Product& d, const Fp8Launch& l, void* part, uint3
     P.fours = static_cast<int32_t>(cdiv(d.depth, 512));
     for (int i = 0; i < d.na; ++i) {
       if (!encode_q(&P.a[i], d.a[i].q, d.rows, d.depth, P.tile_rows)) return TP_ERR_CUDA;
+      if (by_rows && l.ctas == 2 && !encode_q(&P.a[1], d.a[0].q, d.rows, d.depth, 32)) return TP_ERR_CUDA;
       P.ea_at[i] = static_cast<const uint8_t*>(d.a[i].e);
-      if (l.ctas == 2 && !encode_e(&P.ea[i], d.a[i].e, a_blocks, d.depth, 1)) return TP_ERR_CUDA;
+      if (l.ctas == 2 && !encode_e(&P.ea[i], d.a[i].e, a_blocks, d.depth, turned ? 2 : 1)) return TP_ERR_CUDA;
     }
     for (int i = 0; i < d.nb; ++i) {
       if (!encode_q(&P.b[i], d.b[i].q, b_rows, d.depth, 128)) return TP_ERR_CUDA;
       P.eb_at[i] = static_cast<const uint8_t*>(d.b[i].e);
-      if (l.ctas == 2 && !encode_e(&P.eb[i], d.b[i].e, b_blocks, d.depth, l.ctas)) return TP_ERR_CUDA;
+      if (l.ctas == 2 && !encode_e(&P.eb[i], d.b[i].e, b_blocks, d.depth, turned ? 1 : 2)) return TP_ERR_CUDA;
     }
   }
   const int64_t tiles = d.groups * (by_rows ? d.plan->max_tiles : P.m_tiles) * P.n_tiles;
   if (tiles > 0x7FFFFFFFll) return TP_ERR_UNSUPPORTED_SHAPE;
   const int64_t ctas = l.runs > 0 ? l.runs : tiles;
-  if (l.ctas == 2) return d.z ? (launch_gemm<2, true>(P, ctas, stream)) : (launch_gemm<2, false>(P, ctas, stream));
-  TP_TRY(d.z ? (launch_gemm<1, true>(P, ctas, stream)) : (launch_gemm<1, false>(P, ctas, stream)));
+  if (l.ctas == 2) return turned ? launch_gemm<2, true>(d.z != nullptr, P, ctas, stream) : launch_gemm<2, false>(d.z != nullptr, P, ctas, stream);
+  TP_TRY(turned ? (launch_gemm<1, true>(d.z != nullptr, P, ctas, stream)) : (launch_gemm<1, false>(d.z != nullptr, P, ctas, stream)));
   if (l.runs < 2) return TP_OK;
   return launch_dependent(fp8_join_kernel, dim3(static_cast<unsigned>(l.runs - 1), static_cast<unsigned>(cdiv(P.tile_rows, kJoinThreads / 32))),
                           kJoinThreads, 0, stream, P);

@@ -23,8 +23,8 @@ void add_fp8(RangeList* v, const tp_fp8* a, int n, int64_t rows, int64_t cols, i
 struct Fp8Plan {
   const int32_t* tiles;   // row tiles in use
   const int32_t* pairs;   // pairs of them, for CTA pairs: two tiles of an expert, or its last one
-  const int32_t* pair;    // first tile of a pair (fp8_gemm.cuh: kSingle)
-  const int32_t* expert;  // expert of a tile
+  const int32_t* pair;    // first tile of a pair, and its expert << 9 | rows that it has
+  const int32_t* expert;  // expert << 9 | rows of a tile
   const int32_t* first;   // first tile of an expert, E + 1
   const int32_t* slot;    // token * k + choice of a row, or -1
   int64_t max_tiles, tile_rows;

@@ -36,7 +36,7 @@
 namespace tpf {
 
 struct Fp8GemmParams {
-  CUtensorMap a[8], b[8], ea[8], eb[8];  // ea, eb: CTAS = 2
+  CUtensorMap a[8], b[8], ea[8], eb[8];  // ea, eb: CTAS = 2; a[1] of FP8_ROWS: a[0]'s in 32 rows at a time
   const uint8_t *ea_at[8], *eb_at[8];    // CTAS = 1: the exponents themselves
   int32_t fours;                         // of k-blocks, in a block of exponents
   int32_t mode;
@@ -46,16 +46,14 @@ struct Fp8GemmParams {
   int32_t kb;                   // k-blocks of a segment
   int32_t stream;               // runs of k-blocks instead of whole tiles (CTAS = 1)
   int32_t min_run;              // the shortest of them
-  int32_t few;                  // tiles of few rows, the N of the MMAs (CTAS = 1)
   int32_t rows, cols;           // of an output (FP8_ROWS: rows not used)
   int32_t tile_rows;            // rows of an A tile that are loaded (CTAS = 1: 16 .. 128)
   int32_t band;                 // m-tiles that go together through the n-tiles
   int32_t per, eb_blocks;       // experts of a shard; 128-row blocks of an expert's B
   const int32_t* plan_tiles;    // FP8_ROWS, FP8_CONTRACT: row tiles in use
-  const int32_t* plan_expert;   // FP8_ROWS: expert of a row tile
-  const int32_t *plan_pairs, *plan_pair;  // FP8_ROWS, CTAS = 2: pairs of row tiles; the first, + kSingle if alone
+  const int32_t* plan_expert;   // FP8_ROWS: expert of a row tile, and how many rows it has (expert_rows)
+  const int32_t *plan_pairs, *plan_pair;  // FP8_ROWS, CTAS = 2: pairs of row tiles; of each the first tile, expert and rows
   const int32_t* plan_first;    // FP8_CONTRACT: first row tile of an expert, E + 1
-  const int32_t* plan_slot;     // FP8_ROWS: token and choice of a row, or -1
   int32_t max_tiles, experts;   // bounds of what the plan may say
   int32_t kb_tile;              // FP8_CONTRACT: k-blocks of a row tile
   int32_t epi;                  // tp_epilogue
@@ -73,7 +71,9 @@ struct Fp8GemmParams {
   int32_t drop;                 // test hook (TP_DEBUG_DROP_LOAD)
 };
 
-constexpr int32_t kSingle = 1 << 30;
+// A word of the plan: an expert and the rows, up to 256, that its tile or pair of tiles has.
+__device__ __forceinline__ int32_t word_rows(int32_t w) { return min(max(w & 511, 1), 256); }
+__device__ __forceinline__ int32_t word_expert(int32_t w) { return w >> 9; }
 
 // Places of a stage: A's k-blocks, of `rows` rows each, then B's.  (With 65 to
 // 127 rows the MMA reads 128 from where A begins: what lies behind its rows
@@ -88,7 +88,8 @@ struct Fp8Ring {
   __device__ __forceinline__ uint32_t e(int stage, int d) const;
 };
 
-template <int CTAS>
+// TURNED: the rows are the N of the MMAs.
+template <int CTAS, bool TURNED = false>
 struct Fp8Cfg {
   static constexpr int BN = 128 * CTAS;
   // A stage has two k-blocks of A, two of B and their exponents.  (With one,
@@ -100,11 +101,11 @@ struct Fp8Cfg {
   static constexpr uint32_t EA_BYTES = 512, EB_BYTES = 512 * CTAS, E_BYTES = EA_BYTES + EB_BYTES;
   static constexpr uint32_t RING = 192 * 1024;
   static constexpr int MAX_STAGES = CTAS == 1 ? 5 : 3;
-  static constexpr int EPI_WARPS = 8;
-  static constexpr int COLS = BN / 2;  // of an epilogue warp
+  static constexpr int EPI_WARPS = TURNED ? 8 * CTAS : 8;
+  static constexpr int COLS = BN / 2;  // of an epilogue warp, not TURNED
   static constexpr int THREADS = 64 + 32 * EPI_WARPS;
-  static constexpr uint32_t STG_BYTES = 2048;  // staging of an epilogue warp
-  static constexpr uint32_t E_OFF = RING, STG_OFF = E_OFF + MAX_STAGES * DEEP * E_BYTES, BAR_OFF = STG_OFF + EPI_WARPS * STG_BYTES;
+  static constexpr uint32_t STG_BYTES = 2048;  // staging of an epilogue warp, not TURNED
+  static constexpr uint32_t E_OFF = RING, STG_OFF = E_OFF + MAX_STAGES * DEEP * E_BYTES, BAR_OFF = STG_OFF + 8 * STG_BYTES;
   static constexpr uint32_t SMEM = 1024 + BAR_OFF + 256;
   // tensor memory: accumulators of BN columns at 0 and ACC1, scales from SF
   // on (A 4 columns, B 4 CTAS), two of them by turns
@@ -135,7 +136,7 @@ struct Fp8Unit {
   int32_t t;          // tile
   int32_t g, nt;
   int32_t tile;       // row tile (of CTA 0)
-  bool single;        // FP8_ROWS: CTA 1 has no row tile
+  int32_t rows;       // that it has (with few, and CTA 1's)
   int32_t q0, q1;     // k-blocks
   int32_t a_row, ea;  // first row of A's tile (CTA 0), its block of exponents
   int32_t b_row, eb;
@@ -152,25 +153,45 @@ __device__ __forceinline__ int32_t fp8_tiles(const Fp8GemmParams& P) {
   return P.groups * P.m_tiles * P.n_tiles;
 }
 
+// What the plan says about a tile.  It is read a tile ahead: from L2 that
+// takes as long as two k-blocks.
+struct Fp8Words {
+  int32_t a, b;
+};
 template <int CTAS>
-__device__ __forceinline__ Fp8Unit fp8_unit(const Fp8GemmParams& P, int32_t t) {
+__device__ __forceinline__ Fp8Words fp8_words(const Fp8GemmParams& P, int32_t t) {
+  Fp8Words w = {0, 0};
+  if (P.mode == FP8_ROWS) {
+    const int32_t v = t / P.n_tiles;
+    if (CTAS == 2) {
+      w.a = __ldcg(P.plan_pair + 2 * v);
+      w.b = __ldcg(P.plan_pair + 2 * v + 1);
+    } else {
+      w.a = v;
+      w.b = __ldcg(P.plan_expert + v);
+    }
+  } else if (P.mode == FP8_CONTRACT) {
+    const int32_t g = t / (P.m_tiles * P.n_tiles);
+    w.a = __ldcg(P.plan_first + g);
+    w.b = __ldcg(P.plan_first + g + 1);
+  }
+  return w;
+}
+
+template <int CTAS>
+__device__ __forceinline__ Fp8Unit fp8_unit(const Fp8GemmParams& P, int32_t t, const Fp8Words& words) {
   Fp8Unit u;
   u.t = t;
   int32_t v = t;
   u.out_off = 0;
-  u.single = false;
   u.q0 = 0;
   u.q1 = P.segs * P.kb;
   if (P.mode == FP8_ROWS) {
     // an expert's weights are read by its row tiles one after the other
-    u.tile = v / P.n_tiles;
     u.nt = v % P.n_tiles;
-    if (CTAS == 2) {
-      const int32_t pair = uniform(__ldcg(P.plan_pair + u.tile));
-      u.single = (pair & kSingle) != 0;
-      u.tile = min(max(pair & (kSingle - 1), 0), P.max_tiles - 1);
-    }
-    const int32_t e = min(max(uniform(__ldcg(P.plan_expert + u.tile)), 0), P.experts - 1), local = e % P.per;
+    u.tile = min(max(uniform(words.a), 0), P.max_tiles - 1);
+    const int32_t word = uniform(words.b), e = min(max(word_expert(word), 0), P.experts - 1), local = e % P.per;
+    u.rows = min(word_rows(word), P.tile_rows * CTAS);
     u.g = 0;
     u.bi = e / P.per;
     u.a_row = u.tile * P.tile_rows;
@@ -189,12 +210,13 @@ __device__ __forceinline__ Fp8Unit fp8_unit(const Fp8GemmParams& P, int32_t t) {
   u.tile = (first + v % tall) * CTAS;
   u.bi = 0;
   u.a_row = u.tile * 128;
+  u.rows = min(P.rows - u.a_row, P.tile_rows * CTAS);
   u.ea = u.tile;
   u.b_row = u.nt * Fp8Cfg<CTAS>::BN;
   u.eb = u.nt * CTAS;
   if (P.mode == FP8_CONTRACT) {
-    u.q0 = min(max(uniform(__ldcg(P.plan_first + u.g)), 0), P.max_tiles) * P.kb_tile;
-    u.q1 = min(uniform(__ldcg(P.plan_first + u.g + 1)), P.max_tiles) * P.kb_tile;
+    u.q0 = min(max(uniform(words.a), 0), P.max_tiles) * P.kb_tile;
+    u.q1 = min(uniform(words.b), P.max_tiles) * P.kb_tile;
     u.bi = u.g / P.per;  // of the outputs
     u.out_off = static_cast<int64_t>(u.g % P.per) * P.rows * P.cols;
   }
@@ -207,6 +229,7 @@ template <int CTAS>
 struct Fp8Walk {
   int32_t at, end, stride;  // tiles; or k-blocks, stride 0
   int32_t run, depth;       // k-blocks of a run, of a tile
+  Fp8Words words;           // of the next
 
   __device__ __forceinline__ Fp8Walk(const Fp8GemmParams& P) {
     const int32_t me = static_cast<int32_t>(blockIdx.x) / CTAS, all = static_cast<int32_t>(gridDim.x) / CTAS, tiles = fp8_tiles<CTAS>(P);
@@ -223,19 +246,21 @@ struct Fp8Walk {
       end = tiles;
       stride = all;
     }
+    if (at < end) words = fp8_words<CTAS>(P, stride ? at : at / depth);
   }
   __device__ __forceinline__ bool next(const Fp8GemmParams& P, Fp8Unit& u) {
     if (at >= end) return false;
     if (CTAS == 1 && stride == 0) {
       const int32_t t = at / depth;
-      u = fp8_unit<CTAS>(P, t);
+      u = fp8_unit<CTAS>(P, t, words);
       u.q0 = at - t * depth;
       u.q1 = min(depth, u.q0 + end - at);
       at += u.q1 - u.q0;
     } else {
-      u = fp8_unit<CTAS>(P, at);
+      u = fp8_unit<CTAS>(P, at, words);
       at += stride;
     }
+    if (at < end) words = fp8_words<CTAS>(P, stride ? at : at / depth);
     return true;
   }
 };
@@ -468,107 +493,177 @@ __device__ __forceinline__ void drain_f32(float* to, int64_t pitch, int32_t cols
   }
 }
 
-// ------------------------------------------------------------------ tiles of few rows (CTAS = 1)
+// ------------------------------------------------------------------ rows as the N of the MMAs
 //
-// Up to 64 rows are the N of the MMAs and the 128 columns their M: the tensor
-// cores then read the weights' 16 KiB of a k-block from shared memory and the
-// rows', not 128 rows, half of which or more would be for nothing (a k-block
-// took 530 cycles so, whatever the rows; shared memory's bandwidth, which TMA
-// needs too, is what bounds it).  A lane of tensor memory has a column then, a
-// column of it a row: the epilogue turns 32 rows at a time in shared memory,
-// where all 256 threads take a share, G neighbours a row, four columns each at
-// a time.
+// With the rows as N and the columns (the weights' rows) as M a tile costs
+// what its rows cost, in steps of 16 (32 of a pair): the tiles of few rows of
+// a decode step, and the experts' tiles, of which each expert's last is
+// filled by chance.  As M a tile of few rows took 530 cycles a k-block,
+// whatever the rows, and an expert's last pair of tiles counted as 256.
+//
+// A lane of tensor memory has a column then, a column of it a row.  Neighbours
+// exchange halves (two bf16, or four bytes of four rows) so that each stores
+// four bytes of a row; 32 lanes write 64 or 32 bytes of each.  (Turned in
+// shared memory instead, 32 rows at a time with two barriers, the epilogue of
+// 128 x 256 took longer than the MMAs of a contraction of 2048.)
 
-__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+template <int THREADS>
 __device__ __forceinline__ bool epilogue_all(bool ok) {
   uint32_t all;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 q, %1, 0;\n\t"
-      "bar.red.and.pred p, 1, 256, q;\n\t"
+      "bar.red.and.pred p, 1, %2, q;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(all)
-      : "r"(ok ? 1u : 0u)
+      : "r"(ok ? 1u : 0u), "n"(THREADS)
       : "memory");
   return all != 0;
 }
-__device__ __forceinline__ uint32_t pass_at(uint32_t buf, uint32_t row, uint32_t piece) { return buf + row * 512 + ((piece ^ (row & 7)) << 4); }
 
-// 16 rows, from `row` of the 32 on, of the warp's 32 columns.
-__device__ __forceinline__ void pass_rows(uint32_t taddr, bool empty, uint32_t buf, uint32_t row, uint32_t col) {
-  uint32_t v[16];
-  if (empty) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0;
-  } else {
-    tmem_ld_32x32b_x16(taddr, v);
-    tmem_wait_ld();
-  }
-#pragma unroll
-  for (uint32_t i = 0; i < 16; ++i)
-    asm volatile("st.shared.b32 [%0], %1;" ::"r"(pass_at(buf, row + i, col >> 2) + (col & 3) * 4), "r"(v[i]) : "memory");
+// Two rows of a lane's column -> the column and its neighbour of one of them
+// (even lanes the first), and back.
+__device__ __forceinline__ uint32_t turn2(uint32_t own, uint32_t odd) {
+  const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
+  return __byte_perm(own, other, odd ? 0x3276 : 0x5410);
+}
+// Four rows of a lane's column, a byte each -> four columns of row lane % 4.
+__device__ __forceinline__ uint32_t turn4(uint32_t own, uint32_t lane) {
+  uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
+  own = __byte_perm(own, other, (lane & 1) ? 0x3715 : 0x6240);
+  other = __shfl_xor_sync(0xFFFFFFFFu, own, 2);
+  return __byte_perm(own, other, (lane & 2) ? 0x3276 : 0x5410);
 }
 
-// part: fp32 sums [rows][128] instead of results, or null.
-template <bool QUANT, int G>
-__device__ __forceinline__ void drain_few(const Fp8GemmParams& P, const Fp8Place& w, float* part, uint32_t buf, uint32_t t) {
-  constexpr int N = 32 / G;
-  const uint32_t r = t / G, g = t % G;
-  const bool mine = static_cast<int32_t>(r) < w.rows;
-  const int64_t at = w.off + (static_cast<int64_t>(w.row) + r) * P.cols + w.col;
-  float v[N][4], top = 0.f;
+struct Fp8Lane {
+  uint32_t lane, quarter;        // 32 columns
+  uint32_t part, parts;          // every parts-th chunk of 16 rows
+  uint32_t barrier;              // of the four quarters
+};
+
+// n <= N of the 16 rows of a chunk, from `first` of the tile on.
+template <bool QUANT, int N>
+__device__ __forceinline__ void turned_chunk(const Fp8GemmParams& P, const Fp8Place& w, int32_t first, int32_t n, float (&v)[16], float bias,
+                                             int32_t col, const Fp8Lane& me, float (*exchange)[16]) {
+  const int32_t odd = me.lane & 1;
+  const bool in = col < P.cols;
+  // of the lane's row of two, its column and the neighbour's
+  const int64_t at2 = w.off + (static_cast<int64_t>(w.row) + first + odd) * P.cols + (col & ~1);
+  const int64_t two = static_cast<int64_t>(P.cols) * 2;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const uint4 f = ld_shared_v4(pass_at(buf, r, i * G + g));
-    v[i][0] = __uint_as_float(f.x), v[i][1] = __uint_as_float(f.y), v[i][2] = __uint_as_float(f.z), v[i][3] = __uint_as_float(f.w);
+  for (int j = 0; j < N; ++j) v[j] += bias;
+  if (P.epi == TP_EPI_DGELU) {
+    uint32_t h[N / 2];
+    const __nv_bfloat16* from = P.aux[w.o] + at2;
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) h[j] = in && 2 * j + odd < n ? *reinterpret_cast<const uint32_t*>(from + j * two) : 0u;
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) {
+      const uint32_t f = turn2(h[j], odd);
+      times_gelu_prime2(v[2 * j], v[2 * j + 1], bf_lo(f), bf_hi(f));
+    }
+  } else if (P.epi == TP_EPI_GELU) {
+    if (P.aux[w.o]) {
+      __nv_bfloat16* to = P.aux[w.o] + at2;
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) {
+        const uint32_t o = turn2(pack_bf16(v[2 * j], v[2 * j + 1]), odd);
+        if (in && 2 * j + odd < n) *reinterpret_cast<uint32_t*>(to + j * two) = o;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < N; j += 2) gelu2(v[j], v[j + 1]);
   }
-  if (part) {
+  if constexpr (!QUANT) {
+    if (P.out32) {
+      float* to = P.out32 + (static_cast<int64_t>(w.row) + first) * P.cols + col;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (mine) __stcg(reinterpret_cast<float4*>(part + r * 128) + i * G + g, make_float4(v[i][0], v[i][1], v[i][2], v[i][3]));
+      for (int j = 0; j < N; ++j)
+        if (in && j < n) to[static_cast<int64_t>(j) * P.cols] = v[j];
+      return;
+    }
+    __nv_bfloat16* to = P.out[w.o] + at2;
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) {
+      const uint32_t o = turn2(pack_bf16(v[2 * j], v[2 * j + 1]), odd);
+      if (in && 2 * j + odd < n) *reinterpret_cast<uint32_t*>(to + j * two) = o;
+    }
+  } else {
+    uint32_t top[N], most = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (!in || j >= n) v[j] = 0.f;  // past the matrix: zeros
+      top[j] = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(v[j])));
+      most = max(most, top[j]);
+    }
+    const bool finite = most < 0x7F800000u;
+    if (!finite) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) top[j] = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(finite_abs(v[j])));
+    }
+    uint32_t mine = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) mine = me.lane == j ? top[j] : mine;
+    if (me.lane < 16) exchange[me.quarter][me.lane] = __uint_as_float(mine);
+    asm volatile("bar.sync %0, 128;" ::"r"(me.barrier) : "memory");
+    float all = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) all = fmaxf(all, exchange[j][me.lane & 15]);
+    const uint32_t e = fp8_exponent(all);
+    const float inv = fp8_inverse(e);
+    const int32_t block = w.col / 128;
+    if (me.quarter == 0 && static_cast<int32_t>(me.lane) < n)
+      P.ze[w.o][(w.eblock + (first >> 7)) * P.ze_ld + (block >> 2) * 512 + fp8_e_at((first & 127) + me.lane, block & 3)] = static_cast<uint8_t>(e);
+    uint8_t* to = P.zq[w.o] + (static_cast<int64_t>(w.row) + first + (me.lane & 3)) * P.zq_ld + (col & ~3);
+    const int64_t four = P.zq_ld * 4;
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+      float f[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) f[m] = v[j + m] * __shfl_sync(0xFFFFFFFFu, inv, j + m);
+      const uint32_t o = turn4(finite ? fp8_pack4_finite(f[0], f[1], f[2], f[3], 1.f) : fp8_pack4(f[0], f[1], f[2], f[3], 1.f), me.lane);
+      if (j + static_cast<int32_t>(me.lane & 3) < n) *reinterpret_cast<uint32_t*>(to + (j / 4) * four) = o;
+    }
+  }
+}
+
+// A finished tile, `rows` rows from w.row on, 128 columns from w.col on.
+// sums: fp32 sums [rows][128] instead of results, or null.  red: [2][4][16].
+template <bool QUANT, typename Released>
+__device__ __forceinline__ void drain_turned(const Fp8GemmParams& P, const Fp8Place& w, int32_t rows, float* sums, uint32_t taddr, bool empty,
+                                             bool last_first, const Fp8Lane& me, float (*red)[4][16], uint32_t& turn, Released released) {
+  const int32_t part = static_cast<int32_t>(me.part), parts = static_cast<int32_t>(me.parts);
+  const int32_t mine = ((rows + 15) / 16 - part + parts - 1) / parts;
+  if (mine <= 0 || w.col >= P.cols) {
+    released();
     return;
   }
+  const int32_t in_tile = static_cast<int32_t>(me.quarter * 32 + me.lane), col = w.col + in_tile;
+  const float bias = P.bias[w.o] && col < P.cols ? __bfloat162float(P.bias[w.o][col]) : 0.f;
+#pragma unroll 1
+  for (int32_t i = 0; i < mine; ++i) {
+    const int32_t first = (part + parts * (last_first ? mine - 1 - i : i)) * 16, n = min(rows - first, 16);
+    float v[16];
+    if (empty) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int32_t c = (i * G + static_cast<int32_t>(g)) * 4;  // of the tile
-    const bool in = mine && w.col + c < P.cols;
-    if (in) {
-      if (P.bias[w.o]) {
-        const uint2 b = *reinterpret_cast<const uint2*>(P.bias[w.o] + w.col + c);
-        v[i][0] += bf_lo(b.x), v[i][1] += bf_hi(b.x), v[i][2] += bf_lo(b.y), v[i][3] += bf_hi(b.y);
-      }
-      if (P.epi == TP_EPI_DGELU) {
-        const uint2 h = *reinterpret_cast<const uint2*>(P.aux[w.o] + at + c);
-        times_gelu_prime2(v[i][0], v[i][1], bf_lo(h.x), bf_hi(h.x));
-        times_gelu_prime2(v[i][2], v[i][3], bf_lo(h.y), bf_hi(h.y));
-      } else if (P.epi == TP_EPI_GELU) {
-        if (P.aux[w.o]) *reinterpret_cast<uint2*>(P.aux[w.o] + at + c) = make_uint2(pack_bf16(v[i][0], v[i][1]), pack_bf16(v[i][2], v[i][3]));
-        gelu2(v[i][0], v[i][1]);
-        gelu2(v[i][2], v[i][3]);
-      }
-      if constexpr (!QUANT) {
-        if (P.out32) *reinterpret_cast<float4*>(P.out32 + at + c) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
-        else *reinterpret_cast<uint2*>(P.out[w.o] + at + c) = make_uint2(pack_bf16(v[i][0], v[i][1]), pack_bf16(v[i][2], v[i][3]));
-      }
+      for (int j = 0; j < 16; ++j) v[j] = 0.f;
     } else {
-      v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
-    }
-    if constexpr (QUANT) top = fmaxf(top, fmaxf(fmaxf(finite_abs(v[i][0]), finite_abs(v[i][1])), fmaxf(finite_abs(v[i][2]), finite_abs(v[i][3]))));
-  }
-  if constexpr (QUANT) {
-    if (w.col >= P.cols) return;
+      uint32_t r[16];
+      tmem_ld_32x32b_x16(taddr + first, r);
+      tmem_wait_ld();
 #pragma unroll
-    for (int o = G / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    const uint32_t e = fp8_exponent(top);
-    const float inv = fp8_inverse(e);
-    if (mine) {
-      uint32_t* to = reinterpret_cast<uint32_t*>(P.zq[w.o] + (static_cast<int64_t>(w.row) + r) * P.zq_ld + w.col);
-#pragma unroll
-      for (int i = 0; i < N; ++i) to[i * G + g] = fp8_pack4(v[i][0], v[i][1], v[i][2], v[i][3], inv);
-      const int32_t b = w.col / 128;
-      if (g == 0)
-        P.ze[w.o][w.eblock * P.ze_ld + (b >> 2) * 512 + fp8_e_at(static_cast<uint32_t>(w.erow) + r, b & 3)] = static_cast<uint8_t>(e);
+      for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
     }
+    if (i == 0) released();
+    if (sums) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (j < n) __stcg(sums + (first + j) * 128 + in_tile, v[j]);
+      continue;
+    }
+    float (*exchange)[16] = red[QUANT ? turn++ & 1 : 0];
+    if (n <= 4) turned_chunk<QUANT, 4>(P, w, first, n, v, bias, col, me, exchange);
+    else turned_chunk<QUANT, 16>(P, w, first, n, v, bias, col, me, exchange);
   }
 }
 
@@ -595,10 +690,10 @@ __global__ void __launch_bounds__(kJoinThreads) fp8_join_kernel(const __grid_con
   const int32_t end = i * run, t = end / depth, from = t * depth;
   if (end >= work || end == from || end - run > from) return;
   const int32_t lo = i - 1, hi = (from + depth - 1) / run;
-  const Fp8Unit u = fp8_unit<1>(P, t);
+  const Fp8Unit u = fp8_unit<1>(P, t, fp8_words<1>(P, t));
   const int32_t r = static_cast<int32_t>(blockIdx.y) * (kJoinThreads / 32) + static_cast<int32_t>(threadIdx.x >> 5);
   const int64_t row = static_cast<int64_t>(u.tile) * P.tile_rows + r;
-  if (r >= P.tile_rows || (P.mode != FP8_ROWS && row >= P.rows)) return;
+  if (r >= u.rows) return;
   const int32_t o = P.mode == FP8_DENSE ? u.g : 0, c = u.nt * 128 + static_cast<int32_t>(lane) * 4;
   float v[4] = {};
 #pragma unroll 4
@@ -644,12 +739,13 @@ __global__ void __launch_bounds__(kJoinThreads) fp8_join_kernel(const __grid_con
 
 // ------------------------------------------------------------------ kernel
 
-template <int CTAS, bool QUANT>
-__global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(const __grid_constant__ Fp8GemmParams P) {
-  using C = Fp8Cfg<CTAS>;
+template <int CTAS, bool QUANT, bool TURNED>
+__global__ void __launch_bounds__(Fp8Cfg<CTAS, TURNED>::THREADS, 1) fp8_gemm_kernel(const __grid_constant__ Fp8GemmParams P) {
+  using C = Fp8Cfg<CTAS, TURNED>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
-  __shared__ float red[CTAS == 1 && QUANT ? 4 : 1][2][32];
+  __shared__ float red[CTAS == 1 && QUANT && !TURNED ? 4 : 1][2][32];
+  __shared__ float turned[QUANT && TURNED ? 2 * CTAS : 1][2][4][16];
   const Fp8Ring<CTAS> ring(base, P.tile_rows);
   const int STAGES = ring.count;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem_raw + (base - raw) + C::BAR_OFF);
@@ -657,8 +753,9 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (C::MAX_STAGES + s); };
   auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * C::MAX_STAGES + b); };
-  const uint32_t begun_bar = bar0 + 8u * (2 * C::MAX_STAGES + 2), drain_bar = begun_bar + 8u;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * C::MAX_STAGES + 4);
+  const uint32_t begun_bar = bar0 + 8u * (2 * C::MAX_STAGES + 2), drain_bar = begun_bar + 16u;
+  auto done_bar = [&](uint32_t n) { return begun_bar + 8u * (n & 1); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * C::MAX_STAGES + 5);
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
   const uint32_t warp = static_cast<uint32_t>(uniform(static_cast<int32_t>(threadIdx.x >> 5))), lane = threadIdx.x & 31;
   const uint32_t crank = CTAS == 2 ? cluster_ctarank() : 0;
@@ -671,6 +768,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
     }
     for (int b = 0; b < 2; ++b) mbar_init(tfull_bar(b), 1);
     mbar_init(begun_bar, CTAS * C::EPI_WARPS);
+    if (CTAS == 1) mbar_init(done_bar(1), C::EPI_WARPS);
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -721,9 +819,12 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
     uint32_t phase = 0, armed = 0, armed_parity = 0;
     int32_t issued = 0;
     bool ok = true;
-    const uint32_t block_bytes = ring.a_bytes + C::B_BYTES;
     while (ok && walk.next(P, u)) {
-      const int32_t a_row = u.a_row + static_cast<int32_t>(crank) * 128, b_row = u.b_row + static_cast<int32_t>(crank) * 128;
+      // a CTA of a pair holds half of the rows that are the N
+      const int32_t a_half = TURNED ? (u.rows + 31) / 32 * 16 : 128;
+      const bool whole = CTAS == 1 || !TURNED || a_half > 96;  // else 32 rows at a time: single tiles load half as much
+      const uint32_t block_bytes = C::B_BYTES + (whole ? ring.a_bytes : static_cast<uint32_t>((a_half + 31) / 32) * 4096u);
+      const int32_t a_row = u.a_row + static_cast<int32_t>(crank) * a_half, b_row = u.b_row + static_cast<int32_t>(crank) * 128;
       Fp8Block b = fp8_block(P, u, u.q0);
       for (int32_t q = u.q0; q < u.q1; q += C::DEEP) {
         const int32_t deep = min(u.q1 - q, C::DEEP);
@@ -749,16 +850,22 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
 #pragma unroll
           for (int d = 0; d < C::DEEP; ++d) {
             if (d >= deep) continue;
-            load_2d<CTAS>(one, ring.a(stage, d), &P.a[at[d].ai], fb, at[d].k * 128, a_row);
+            if (whole) {
+              load_2d<CTAS>(one, ring.a(stage, d), &P.a[at[d].ai], fb, at[d].k * 128, a_row);
+            } else {
+              for (int32_t r = 0; r < a_half; r += 32) load_2d<CTAS>(one, ring.a(stage, d) + r * 128, &P.a[1], fb, at[d].k * 128, a_row + r);
+            }
             load_2d<CTAS>(one, ring.b(stage, d), &P.b[at[d].bi], fb, at[d].k * 128, b_row);
             if (scales[d]) {
               const uint32_t se = ring.e(stage, d);
               if constexpr (CTAS == 2) {
-                load_3d_pair(one, se, &P.ea[at[d].ai], fb, 0, at[d].k >> 2, u.ea + static_cast<int32_t>(crank));
-                load_3d_pair(one, se + C::EA_BYTES, &P.eb[at[d].bi], fb, 0, at[d].k >> 2, u.eb);
+                // 512 bytes of the M of this CTA, 1024 of the pair's N
+                const int32_t my = static_cast<int32_t>(crank);
+                load_3d_pair(one, TURNED ? se + C::EA_BYTES : se, &P.ea[at[d].ai], fb, 0, at[d].k >> 2, TURNED ? u.ea : u.ea + my);
+                load_3d_pair(one, TURNED ? se : se + C::EA_BYTES, &P.eb[at[d].bi], fb, 0, at[d].k >> 2, TURNED ? u.eb + my : u.eb);
               } else {
-                load_512(one, se, P.ea_at[at[d].ai] + (static_cast<int64_t>(u.ea) * P.fours + (at[d].k >> 2)) * 512, fb);
-                load_512(one, se + C::EA_BYTES, P.eb_at[at[d].bi] + (static_cast<int64_t>(u.eb) * P.fours + (at[d].k >> 2)) * 512, fb);
+                load_512(one, TURNED ? se + C::EA_BYTES : se, P.ea_at[at[d].ai] + (static_cast<int64_t>(u.ea) * P.fours + (at[d].k >> 2)) * 512, fb);
+                load_512(one, TURNED ? se : se + C::EA_BYTES, P.eb_at[at[d].bi] + (static_cast<int64_t>(u.eb) * P.fours + (at[d].k >> 2)) * 512, fb);
               }
             }
           }
@@ -784,12 +891,14 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
       uint32_t phase = 0, n = 0, quads = 0;
       bool ok = true;
       for (; ok && walk.next(P, u); ++n) {
-        // the epilogue has begun the tile before: it is done with the one
-        // before that, and with the columns that both accumulators have
-        if (n > 0 && !wait_warp(begun_bar, n - 1, 2u)) break;
+        // CTAS = 2: the epilogue has begun the tile before, so that it is done
+        // with the one before that, and with the columns that both accumulators
+        // have; CTAS = 1: it is done with the tile before the last
+        if (CTAS == 2 ? n > 0 && !wait_warp(begun_bar, n - 1, 2u) : n > 1 && !wait_warp(done_bar(n), (n >> 1) - 1, 2u)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem + ((n & 1) ? C::ACC1 : 0);
         uint32_t sf = tmem + C::SF;
+        const uint32_t n_of = TURNED ? (u.rows + 16 * CTAS - 1) / (16 * CTAS) * (16 * CTAS) : C::BN;
         int32_t k = fp8_block(P, u, u.q0).k;
         for (int32_t q = u.q0; q < u.q1; q += C::DEEP) {
           if (!wait_warp(full_bar(stage), phase, 3u)) {
@@ -807,14 +916,12 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
 #pragma unroll
               for (int i = 0; i < 1 + CTAS; ++i) tmem_cp_scales<CTAS>(one, sf + 4 * i, se + 512 * i);
             }
-            const bool few = CTAS == 1 && P.few;  // the rows are the N
-            const uint32_t idesc = few ? make_idesc_mxf8(128, P.tile_rows, k & 3) : make_idesc_mxf8(128 * CTAS, C::BN, k & 3);
+            const uint32_t idesc = make_idesc_mxf8(128 * CTAS, n_of, k & 3);
             const uint64_t ra = make_sw128_desc(ring.a(stage, d), 16, 1024), rb = make_sw128_desc(ring.b(stage, d), 16, 1024);
-            const uint64_t ad = few ? rb : ra, bd = few ? ra : rb;
-            const uint32_t sfa = few ? sf + 4 : sf, sfb = few ? sf : sf + 4;
+            const uint64_t ad = TURNED ? rb : ra, bd = TURNED ? ra : rb;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              umma_mxf8<CTAS>(one, d_tmem, ad + 2 * i, bd + 2 * i, idesc, sfa, sfb, (q + d > u.q0 || i > 0) ? 1u : 0u);
+              umma_mxf8<CTAS>(one, d_tmem, ad + 2 * i, bd + 2 * i, idesc, sf, sf + 4, (q + d > u.q0 || i > 0) ? 1u : 0u);
             if (++k == P.kb && P.mode == FP8_DENSE) k = 0;
           }
           commit_to<CTAS>(one, empty_bar(stage), 0x3);
@@ -832,13 +939,13 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
     }
   } else {
     // -------------------------------------------------------------- epilogue (both CTAs)
-    const uint32_t quarter = warp & 3, part = (warp - 2) >> 2;  // lanes of tensor memory, half of the columns
+    const uint32_t quarter = warp & 3, part = (warp - 2) >> 2;  // lanes of tensor memory; half of the columns, or some of the rows
     const uint32_t stg = base + C::STG_OFF + (warp - 2) * C::STG_BYTES;
-    uint32_t n = 0;
+    uint32_t n = 0, turn = 0;
     for (; walk.next(P, u); ++n) {
       bool ok = wait(tfull_bar(n & 1), n >> 1, 4u);
       // the warps that meet at barriers below give up together
-      ok = CTAS == 1 ? epilogue_all(ok) : __all_sync(0xFFFFFFFFu, ok) != 0;
+      ok = QUANT && (CTAS == 1 || TURNED) ? epilogue_all<32 * C::EPI_WARPS>(ok) : __all_sync(0xFFFFFFFFu, ok) != 0;
       if (!ok) break;
       tc_fence_after();
       const uint32_t taddr = tmem + ((quarter * 32) << 16) + ((n & 1) ? C::ACC1 : 0) + part * C::COLS;
@@ -848,7 +955,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
         __syncwarp();
         if (lane == 0) {
           if (CTAS == 2) mbar_arrive_cluster(mapa_shared(begun_bar, 0));
-          else mbar_arrive(begun_bar);
+          else mbar_arrive(done_bar(n));
         }
       };
       Fp8Place w;
@@ -857,56 +964,40 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS>::THREADS, 1) fp8_gemm_kernel(cons
       w.col = u.nt * C::BN + static_cast<int32_t>(part) * C::COLS;
       const int32_t tile_row = static_cast<int32_t>(quarter) * 32;
       const int32_t tile = u.tile + static_cast<int32_t>(crank);
-      int32_t all_rows;  // of the tile
-      if (P.mode == FP8_ROWS) {
-        w.row = tile * P.tile_rows + tile_row;
-        all_rows = u.single && crank == 1 ? 0 : P.tile_rows;
-      } else {
-        w.row = tile * 128 + tile_row;
-        all_rows = P.rows - tile * 128;
-      }
+      w.row = u.a_row + static_cast<int32_t>(crank) * 128 + tile_row;
+      const int32_t all_rows = u.rows - static_cast<int32_t>(crank) * 128;
       w.rows = min(max(all_rows - tile_row, 0), 32);
       w.eblock = tile;
       w.erow = tile_row;
       // The shared columns are the first accumulator's last 32 and the
       // second's first; without them the tile counts as begun at once.
       const bool shared_mine = C::SHARED != 0 && part == ((n & 1) ? 0u : 1u);
-      const bool early = !shared_mine || w.rows == 0;
+      const bool early = CTAS == 2 && !TURNED && (!shared_mine || w.rows == 0);
       if (early) begun();
       auto released = [&] {
-        if (!early) begun();
+        if (CTAS == 2 && !early) begun();
       };
       const FromTmem acc{taddr, empty};
       const bool partial = CTAS == 1 && walk.stride == 0 && u.q1 - u.q0 < walk.depth;
-      if (CTAS == 1 && P.few) {
-        const uint32_t buf = base + C::STG_OFF, t = threadIdx.x - 64;
-        float* part32 = partial ? part_at(P, static_cast<int32_t>(blockIdx.x), u.q0 == 0) : nullptr;
-        w.row -= tile_row;
-        w.col = u.nt * C::BN;
-        for (int32_t q = 0; q * 32 < all_rows && q < 4; ++q) {
-          if (q * 32 + static_cast<int32_t>(part) * 16 < P.tile_rows)
-            pass_rows(tmem + ((quarter * 32) << 16) + ((n & 1) ? C::ACC1 : 0) + q * 32 + part * 16, empty, buf, part * 16, quarter * 32 + lane);
-          epilogue_sync();
-          w.rows = min(all_rows - q * 32, 32);
-          w.erow = q * 32;
-          if (P.tile_rows <= 16) drain_few<QUANT, 16>(P, w, part32, buf, t);
-          else drain_few<QUANT, 8>(P, w, part32 ? part32 + q * 32 * 128 : nullptr, buf, t);
-          w.row += 32;
-          epilogue_sync();
-        }
+      if constexpr (TURNED) {
+        float* sums = partial ? part_at(P, static_cast<int32_t>(blockIdx.x), u.q0 == 0) : nullptr;
+        w.row = u.a_row;
+        w.eblock = u.tile;
+        w.col = u.nt * C::BN + static_cast<int32_t>(crank) * 128;
+        // the chunks in the shared columns first
+        drain_turned<QUANT>(P, w, u.rows, sums, tmem + ((quarter * 32) << 16) + ((n & 1) ? C::ACC1 : 0), empty, (n & 1) == 0,
+                            Fp8Lane{lane, quarter, part, C::EPI_WARPS / 4, 2 + part}, turned[QUANT ? part : 0], turn, released);
       } else if (w.rows > 0) {
         if (partial) {
           float* to = part_at(P, static_cast<int32_t>(blockIdx.x), u.q0 == 0) + tile_row * 128 + part * C::COLS;
           drain_f32<C::COLS>(to, 128, C::COLS, w.rows, acc, stg, lane, [] {});
         } else if constexpr (QUANT) {
           drain_fp8<C::COLS>(P, w, acc, stg, lane, red[CTAS == 1 ? quarter : 0], part, 2 + quarter, released);
-        } else if (P.out32) {
-          drain_f32<C::COLS>(P.out32 + static_cast<int64_t>(w.row) * P.cols + w.col, P.cols, P.cols - w.col, w.rows, acc, stg, lane, released);
         } else {
           drain_bf16<C::COLS>(P, w, acc, (n & 1) == 0, stg, lane, released);
         }
       }
-      tc_fence_before();
+      if (CTAS == 1) begun();
     }
   }
 
