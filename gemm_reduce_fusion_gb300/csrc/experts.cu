@@ -309,6 +309,7 @@ Fp8Plan plan_at(const Sizes& s, int32_t* at, PlanArrays* a) {
   plan.first = a->first;
   plan.expert = a->expert;
   plan.slot = a->slot;
+  plan.row = a->row;
   return plan;
 }
 
@@ -498,6 +499,7 @@ extern "C" tp_status tp_experts_fwd_fp8(const void* x, const void* experts, cons
   pack.rows = s.rows;
   pack.cols = h;
   pack.plan = &plan;
+  pack.tokens = T;
   TP_TRY(fp8_pack(pack, stream));
   uint32_t* status = static_cast<uint32_t*>(ws);
   void* preact = train ? saved->preact : nullptr;

@@ -438,7 +438,7 @@ __device__ __forceinline__ void drain_fp8(const Fp8GemmParams& P, const Fp8Place
     }
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
-      if (P.epi == TP_EPI_GELU) gelu2(v[j][i], v[j][i + 1]);
+      if (P.epi == TP_EPI_GELU) gelu2_to8(v[j][i], v[j][i + 1]);
       if (c + (i & ~7) >= P.cols) v[j][i] = v[j][i + 1] = 0.f;  // past the matrix, in eights: zeros
       top = fmaxf(top, fmaxf(finite_abs(v[j][i]), finite_abs(v[j][i + 1])));
     }
@@ -572,7 +572,10 @@ __device__ __forceinline__ void turned_chunk(const Fp8GemmParams& P, const Fp8Pl
       }
     }
 #pragma unroll
-    for (int j = 0; j < N; j += 2) gelu2(v[j], v[j + 1]);
+    for (int j = 0; j < N; j += 2) {
+      if constexpr (QUANT) gelu2_to8(v[j], v[j + 1]);
+      else gelu2(v[j], v[j + 1]);
+    }
   }
   if constexpr (!QUANT) {
     if (P.out32) {

@@ -39,11 +39,11 @@ struct PackParams {
   uint32_t batch, strips;      // matrices a tensor; strips of 128 rows of a matrix
   int32_t tiles, gelu;
   const int32_t *plan_tiles, *slot;  // or null
+  const int32_t* row;                // of a slot, or -1: packing by tokens
+  int64_t tokens;
   const float* weights;              // of the slots, or null
   int32_t gather, k, tile_rows;
 };
-
-__device__ __forceinline__ float gelu_if(int32_t on, float v) { return on ? gelu_f(v) : v; }
 
 // The source row of row r of the plan (or of the matrix), null for none.
 __device__ __forceinline__ const __nv_bfloat16* source(const PackParams& P, const __nv_bfloat16* x, int64_t r, float& w) {
@@ -69,7 +69,7 @@ template <int SRC>
 __device__ __forceinline__ void pair_of(uint32_t u, float w, float& lo, float& hi) {
   lo = bf_lo(u);
   hi = bf_hi(u);
-  if constexpr (SRC == GELU) gelu2(lo, hi);
+  if constexpr (SRC == GELU) gelu2_to8(lo, hi);
   if constexpr (SRC == WEIGHTED) lo *= w, hi *= w;
 }
 
@@ -78,10 +78,10 @@ __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d, fl
   return FINITE ? fp8_pack4_finite(a, b, c, d, inv) : fp8_pack4(a, b, c, d, inv);
 }
 
-// Two columns x 32 rows of the tile, from shared memory or (SRC other than
-// PLAIN) as they were formed, to the transposed operand's two rows.
+// Two columns x 32 rows of the tile, as they were read (PLAIN) or formed, to
+// the transposed operand's two rows.
 template <bool FINITE, int SRC>
-__device__ __forceinline__ void put_columns(const uint8_t* from, const float* keep, float ilo, float ihi, uint8_t* to, int64_t ld) {
+__device__ __forceinline__ void put_columns(const uint32_t* raw, const float* keep, float ilo, float ihi, uint8_t* to, int64_t ld) {
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     uint32_t lo4[4], hi4[4];
@@ -92,9 +92,8 @@ __device__ __forceinline__ void put_columns(const uint8_t* from, const float* ke
       for (int j = 0; j < 4; ++j) {
         const int i = half * 16 + n * 4 + j;
         if (SRC == PLAIN) {
-          const uint32_t u = *reinterpret_cast<const uint32_t*>(from + i * kPitch);
-          lo[j] = bf_lo(u);
-          hi[j] = bf_hi(u);
+          lo[j] = bf_lo(raw[SRC == PLAIN ? i : 0]);
+          hi[j] = bf_hi(raw[SRC == PLAIN ? i : 0]);
         } else {
           lo[j] = keep[SRC == PLAIN ? 0 : 2 * i];
           hi[j] = keep[SRC == PLAIN ? 0 : 2 * i + 1];
@@ -207,45 +206,42 @@ __global__ void __launch_bounds__(kThreads) fp8_pack_kernel(const __grid_constan
     const uint32_t pair = tid & 63, quarter = tid >> 6;
     const uint8_t* from = tile + quarter * 32 * kPitch + pair * 4;
     float tlo = all, thi = all;
-    bool finite = false;
-    if (SRC == PLAIN && !P.tiles) {
+    uint32_t raw[SRC == PLAIN ? 32 : 1];
+    float keep[SRC == PLAIN ? 1 : 64];
+    uint32_t mlo = 0, mhi = 0;  // the largest magnitudes, as integers
+    if (SRC == PLAIN) {
       uint32_t m = 0;
 #pragma unroll
-      for (uint32_t i = 0; i < 32; ++i) m = max_abs(m, *reinterpret_cast<const uint32_t*>(from + i * kPitch));
-      red[quarter][pair].x = __uint_as_float(m);
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) m = __vmaxu2(m, __float_as_uint(red[i][pair].x));
-      tlo = __uint_as_float(m << 16);
-      thi = __uint_as_float(m & 0xFFFF0000u);
-      finite = (m & 0xFFFFu) < kInfinite && (m >> 16) < kInfinite;
-    }
-    // GeLU and weighted values are formed once, others again when packed
-    float keep[SRC == PLAIN ? 1 : 64];
-    if (SRC != PLAIN) {
-      tlo = thi = 0.f;
+      for (uint32_t i = 0; i < 32; ++i) {
+        raw[SRC == PLAIN ? i : 0] = *reinterpret_cast<const uint32_t*>(from + i * kPitch);
+        m = max_abs(m, raw[SRC == PLAIN ? i : 0]);
+      }
+      mlo = m << 16;
+      mhi = m & 0xFFFF0000u;
+    } else {
 #pragma unroll
       for (uint32_t i = 0; i < 32; ++i) {
         float &lo = keep[SRC == PLAIN ? 0 : 2 * i], &hi = keep[SRC == PLAIN ? 0 : 2 * i + 1];
         pair_of<SRC>(*reinterpret_cast<const uint32_t*>(from + i * kPitch), SRC == WEIGHTED ? row_w[quarter * 32 + i] : 1.f, lo, hi);
-        tlo = fmaxf(tlo, finite_abs(lo));
-        thi = fmaxf(thi, finite_abs(hi));
+        mlo = max(mlo, __float_as_uint(fabsf(lo)));
+        mhi = max(mhi, __float_as_uint(fabsf(hi)));
       }
-      red[quarter][pair] = make_float2(tlo, thi);
     }
-    const bool all_finite = SRC == PLAIN && !P.tiles && !__syncthreads_or(!finite);
-    if (!all_finite && !P.tiles) {
-      if (SRC == PLAIN) {  // an infinity or NaN in the tile: magnitudes one by one
-        tlo = thi = 0.f;
-#pragma unroll 4
+    const bool all_finite = !P.tiles && !__syncthreads_or(max(mlo, mhi) >= kInfinite << 16);
+    if (!P.tiles) {
+      if (!all_finite) {  // an infinity or NaN in the tile: magnitudes of the others
+        float lo = 0.f, hi = 0.f;
+#pragma unroll
         for (uint32_t i = 0; i < 32; ++i) {
-          const uint32_t u = *reinterpret_cast<const uint32_t*>(from + i * kPitch);
-          tlo = fmaxf(tlo, finite_abs(bf_lo(u)));
-          thi = fmaxf(thi, finite_abs(bf_hi(u)));
+          lo = fmaxf(lo, finite_abs(SRC == PLAIN ? bf_lo(raw[SRC == PLAIN ? i : 0]) : keep[SRC == PLAIN ? 0 : 2 * i]));
+          hi = fmaxf(hi, finite_abs(SRC == PLAIN ? bf_hi(raw[SRC == PLAIN ? i : 0]) : keep[SRC == PLAIN ? 0 : 2 * i + 1]));
         }
-        red[quarter][pair] = make_float2(tlo, thi);
+        mlo = __float_as_uint(lo);
+        mhi = __float_as_uint(hi);
       }
+      red[quarter][pair] = make_float2(__uint_as_float(mlo), __uint_as_float(mhi));
       __syncthreads();
+      tlo = thi = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 o = red[i][pair];
@@ -253,14 +249,13 @@ __global__ void __launch_bounds__(kThreads) fp8_pack_kernel(const __grid_constan
         thi = fmaxf(thi, o.y);
       }
     }
-    if (P.tiles) tlo = thi = all;
     const uint32_t elo = fp8_exponent(tlo), ehi = fp8_exponent(thi);
     const float ilo = fp8_inverse(elo), ihi = fp8_inverse(ehi);
     const int64_t col = static_cast<int64_t>(b) * 128 + pair * 2;
     if (col < P.cols) {
       uint8_t* to = P.qt[t] + (mat * P.cols + col) * P.ldqt + r0 + quarter * 32;
-if (all_finite) put_columns<true, SRC>(from, keep, ilo, ihi, to, P.ldqt);
-      else put_columns<false, SRC>(from, keep, ilo, ihi, to, P.ldqt);
+      if (all_finite) put_columns<true, SRC>(raw, keep, ilo, ihi, to, P.ldqt);
+      else put_columns<false, SRC>(raw, keep, ilo, ihi, to, P.ldqt);
     }
     if (quarter == 0) {  // columns past the matrix: exponent 0
       uint8_t* e = P.et[t] + mat * P.et_mat + b * P.et_block + static_cast<int64_t>(strip >> 2) * 512;
@@ -279,26 +274,75 @@ __global__ void __launch_bounds__(kThreads) fp8_pack_rows_kernel(const __grid_co
   const int64_t r = unit / blocks;
   const uint32_t b = static_cast<uint32_t>(unit % blocks), t = blockIdx.y;
   if (r >= P.rows) return;
-  if (P.plan_tiles != nullptr && r >= static_cast<int64_t>(__ldcg(P.plan_tiles)) * P.tile_rows) return;
-  float w;
-  const __nv_bfloat16* src = source(P, P.x[t], r, w);
-  if (src == nullptr) return;  // a row of the plan that no token has
   const int64_t c = static_cast<int64_t>(b) * 128 + lane * 4;
-  const uint2 v = c < P.cols ? *reinterpret_cast<const uint2*>(src + c) : make_uint2(0, 0);
+  const uint2 v = c < P.cols ? *reinterpret_cast<const uint2*>(P.x[t] + r * P.cols + c) : make_uint2(0, 0);
   float f[4] = {bf_lo(v.x), bf_hi(v.x), bf_lo(v.y), bf_hi(v.y)}, top = 0.f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    f[j] = gelu_if(P.gelu, f[j]);
-    if (P.weights) f[j] *= w;
+    if (P.gelu) f[j] = gelu_f(f[j]);
     top = fmaxf(top, finite_abs(f[j]));
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
   const uint32_t e = fp8_exponent(top);
   *reinterpret_cast<uint32_t*>(P.q[t] + r * P.ldq + b * 128 + lane * 4) = fp8_pack4(f[0], f[1], f[2], f[3], fp8_inverse(e));
-  if (lane == 0) {
+  if (lane == 0) P.e[t][r / 128 * P.e_block + (b >> 2) * 512 + fp8_e_at(static_cast<uint32_t>(r % 128), b & 3)] = static_cast<uint8_t>(e);
+}
+
+// A warp for 512 columns of a token, which go to the rows of all of its
+// slots: read and packed once.  (Gathered by the rows, each of six slots packed
+// for itself, 4096 tokens of 4096 took 60 us, so 23 us.)  Rows without a slot are
+// not written.
+__global__ void __launch_bounds__(kThreads) fp8_pack_tokens_kernel(const __grid_constant__ PackParams P) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const uint32_t fours = static_cast<uint32_t>(P.e_block / 512), lane = threadIdx.x & 31;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5), t = unit / fours;
+  if (t >= P.tokens) return;
+  const uint32_t four = static_cast<uint32_t>(unit % fours);
+  const int32_t my_row = static_cast<int32_t>(lane) < P.k ? __ldcg(P.row + t * P.k + lane) : -1;  // k <= 32
+  const int64_t c = static_cast<int64_t>(four) * 512 + lane * 16;
+  const __nv_bfloat16* x = P.x[0] + t * P.cols;
+  const uint4 a = c < P.cols ? *reinterpret_cast<const uint4*>(x + c) : make_uint4(0, 0, 0, 0);
+  const uint4 b = c + 8 < P.cols ? *reinterpret_cast<const uint4*>(x + c + 8) : make_uint4(0, 0, 0, 0);
+  const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  float f[16];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    m = max_abs(m, u[i]);
+    f[2 * i] = bf_lo(u[i]);
+    f[2 * i + 1] = bf_hi(u[i]);
+  }
+  m = max(m & 0xFFFFu, m >> 16);
+#pragma unroll
+  for (int o = 4; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));  // of 128 columns
+  float top = __uint_as_float(m << 16);
+  const bool finite = __all_sync(0xFFFFFFFFu, m < kInfinite);
+  if (!finite) {
+    top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = fmaxf(top, finite_abs(f[i]));
+#pragma unroll
+    for (int o = 4; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  }
+  const uint32_t e = fp8_exponent(top);
+  const float inv = fp8_inverse(e);
+  uint32_t q[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    q[i] = finite ? fp8_pack4_finite(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3], inv)
+                  : fp8_pack4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3], inv);
+  uint32_t es = 0;  // the four blocks' exponents, which lie side by side
+#pragma unroll
+  for (int i = 0; i < 4; ++i) es |= __shfl_sync(0xFFFFFFFFu, e, i * 8) << (i * 8);
+  for (int32_t j = 0; j < P.k; ++j) {
+    const int64_t r = __shfl_sync(0xFFFFFFFFu, my_row, j);
+    if (r < 0) continue;
+    if (c < P.ldq) *reinterpret_cast<uint4*>(P.q[0] + r * P.ldq + c) = make_uint4(q[0], q[1], q[2], q[3]);
     const int64_t block = r / P.tile_rows;
-    P.e[t][block * P.e_block + (b >> 2) * 512 + fp8_e_at(static_cast<uint32_t>(r - block * P.tile_rows), b & 3)] = static_cast<uint8_t>(e);
+    if (lane == 0)
+      *reinterpret_cast<uint32_t*>(P.e[0] + block * P.e_block + four * 512 + fp8_e_at(static_cast<uint32_t>(r - block * P.tile_rows), 0)) = es;
   }
 }
 
@@ -382,6 +426,7 @@ tp_status fp8_pack(const Fp8Pack& d, cudaStream_t stream) {
   P.gelu = d.gelu;
   P.tile_rows = 128;
   if (d.plan) {
+    P.row = d.plan->row;
     P.plan_tiles = d.plan->tiles;
     P.slot = d.plan->slot;
     P.weights = d.weights;
@@ -389,10 +434,15 @@ tp_status fp8_pack(const Fp8Pack& d, cudaStream_t stream) {
     P.k = d.plan->k;
     P.tile_rows = static_cast<int32_t>(d.plan->tile_rows);
   }
-  // A block of 128 rows for each 512 columns fills the GPU's 152 SMs from
-  // some 256 rows on; a plan of smaller tiles has its own blocks of exponents.
-  const bool few = d.qt == nullptr && !d.tiles && d.batch == 1 && (P.tile_rows < 128 || (d.plan == nullptr && d.rows <= 256));
-  if (few) {
+  if (d.plan && d.tokens > 0) {
+    P.tokens = d.tokens;
+    const int64_t blocks = cdiv(d.tokens * (P.e_block / 512), kThreads / 32);
+    if (blocks > 0x7FFFFFFFll) return TP_ERR_UNSUPPORTED_SHAPE;
+    return launch_dependent(fp8_pack_tokens_kernel, dim3(static_cast<unsigned>(blocks)), kThreads, 0, stream, P);
+  }
+  // A block of 128 rows for each 128 columns fills the GPU's 152 SMs from some
+  // 256 rows on.
+  if (d.qt == nullptr && !d.tiles && d.batch == 1 && d.plan == nullptr && d.rows <= 256) {
     const int64_t units = d.rows * (P.ldq / 128);
     if (cdiv(units, kThreads / 32) > 0x7FFFFFFFll) return TP_ERR_UNSUPPORTED_SHAPE;
     return launch_dependent(fp8_pack_rows_kernel, dim3(static_cast<unsigned>(cdiv(units, kThreads / 32)), static_cast<unsigned>(d.n)), kThreads, 0,

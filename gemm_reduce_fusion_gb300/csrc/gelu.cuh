@@ -106,4 +106,10 @@ __device__ __forceinline__ uint64_t gelu_scaled2(float r0, float r1, uint64_t s,
   return mul2(s, fma2(mag, c, pk2(fmaxf(r0, 0.0f), fmaxf(r1, 0.0f))));
 }
 
+// GeLU of two values on their way to 8 bits, where what is not finite is NaN:
+// the form above, in which an infinity becomes one.
+__device__ __forceinline__ void gelu2_to8(float& x0, float& x1) {
+  upk2(gelu_scaled2(x0, x1, pk2(1.0f, 1.0f), pk2(kTailRoot, kTailRoot)), x0, x1);
+}
+
 }  // namespace tpf
