@@ -45,6 +45,17 @@ bool encode_e(CUtensorMap* m, const void* e, int64_t blocks, int64_t cols, int b
             CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// bf16 results: `mats` matrices [rows, cols], boxes of an epilogue warp's 32 x 32.
+bool encode_out(CUtensorMap* m, void* out, int64_t mats, int64_t rows, int64_t cols) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t n = static_cast<cuuint64_t>(cols), r = static_cast<cuuint64_t>(rows);
+  const cuuint64_t dims[3] = {n, r, static_cast<cuuint64_t>(mats)}, strides[2] = {n * 2, n * r * 2};
+  const cuuint32_t boxes[3] = {32u, 32u, 1u}, estr[3] = {1u, 1u, 1u};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, out, dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int CTAS, bool QUANT, bool TURNED>
 tp_status launch_gemm(const Fp8GemmParams& P, int64_t units, cudaStream_t stream) {
   static KernelInfo info;
@@ -161,6 +172,8 @@ tp_status fp8_product(const Fp8Product& d, const Fp8Launch& l, void* part, uint3
       if (l.ctas == 2 && !encode_e(&P.eb[i], d.b[i].e, b_blocks, d.depth, turned ? 1 : 2)) return TP_ERR_CUDA;
     }
   }
+  for (int i = 0; i < outs; ++i)
+    if (!turned && d.out && !encode_out(&P.out_map[i], d.out[i], contract ? d.per : 1, d.rows, d.cols)) return TP_ERR_CUDA;
   const int64_t tiles = d.groups * (by_rows ? d.plan->max_tiles : P.m_tiles) * P.n_tiles;
   if (tiles > 0x7FFFFFFFll) return TP_ERR_UNSUPPORTED_SHAPE;
   const int64_t ctas = l.runs > 0 ? l.runs : tiles;

@@ -184,4 +184,11 @@ __device__ __forceinline__ void commit_to(uint32_t one, uint32_t bar, uint16_t m
         : "memory");
 }
 
+// A staged box to memory; what lies outside the tensor is not written.
+__device__ __forceinline__ void store_3d(const void* map, uint32_t src, int32_t x, int32_t y, int32_t z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
+
 }  // namespace tpf

@@ -37,6 +37,7 @@ namespace tpf {
 
 struct Fp8GemmParams {
   CUtensorMap a[8], b[8], ea[8], eb[8];  // ea, eb: CTAS = 2; a[1] of FP8_ROWS: a[0]'s in 32 rows at a time
+  CUtensorMap out_map[8];                // bf16 results, not TURNED
   const uint8_t *ea_at[8], *eb_at[8];    // CTAS = 1: the exponents themselves
   int32_t fours;                         // of k-blocks, in a block of exponents
   int32_t mode;
@@ -371,6 +372,7 @@ struct Fp8Place {
   int32_t col;        // first column
   int32_t o;          // which output
   int64_t off;        // elements before the output's matrix
+  int32_t mat;        // and matrices
   int32_t eblock, erow;  // 128 rows of exponents of an 8-bit result, first row in them
 };
 
@@ -389,6 +391,8 @@ __device__ __forceinline__ void drain_bf16(const Fp8GemmParams& P, const Fp8Plac
     if (part == 0) released();
     if (bytes <= 0) continue;
     if (bias) add_bias(v, bias, c, P.cols);
+    if (lane == 0) bulk_wait_read_all();  // the staging buffer is free
+    __syncwarp();
     if (P.epi == TP_EPI_DGELU) {
       stg_in(stg, reinterpret_cast<const uint8_t*>(P.aux[w.o]) + at, pitch, w.rows, bytes, lane);
 #pragma unroll
@@ -408,7 +412,12 @@ __device__ __forceinline__ void drain_bf16(const Fp8GemmParams& P, const Fp8Plac
       for (int i = 0; i < 32; i += 2) gelu2(v[i], v[i + 1]);
     }
     stage_bf16(v, stg, lane);
-    stg_out(stg, reinterpret_cast<uint8_t*>(P.out[w.o]) + at, pitch, w.rows, bytes, lane);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      store_3d(&P.out_map[w.o], stg, c, w.row, w.mat);
+      bulk_commit();
+    }
   }
 }
 
@@ -964,6 +973,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS, TURNED>::THREADS, 1) fp8_gemm_ker
       Fp8Place w;
       w.o = P.mode == FP8_DENSE ? u.g : P.mode == FP8_CONTRACT ? u.bi : 0;
       w.off = u.out_off;
+      w.mat = P.mode == FP8_CONTRACT ? u.g % P.per : 0;
       w.col = u.nt * C::BN + static_cast<int32_t>(part) * C::COLS;
       const int32_t tile_row = static_cast<int32_t>(quarter) * 32;
       const int32_t tile = u.tile + static_cast<int32_t>(crank);
@@ -993,6 +1003,8 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS, TURNED>::THREADS, 1) fp8_gemm_ker
       } else if (w.rows > 0) {
         if (partial) {
           float* to = part_at(P, static_cast<int32_t>(blockIdx.x), u.q0 == 0) + tile_row * 128 + part * C::COLS;
+          if (lane == 0) bulk_wait_read_all();  // of the tile before
+          __syncwarp();
           drain_f32<C::COLS>(to, 128, C::COLS, w.rows, acc, stg, lane, [] {});
         } else if constexpr (QUANT) {
           drain_fp8<C::COLS>(P, w, acc, stg, lane, red[CTAS == 1 ? quarter : 0], part, 2 + quarter, released);
@@ -1002,6 +1014,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS, TURNED>::THREADS, 1) fp8_gemm_ker
       }
       if (CTAS == 1) begun();
     }
+    if (!QUANT && !TURNED && lane == 0) bulk_wait_all();
   }
 
   tc_fence_before();
