@@ -10,7 +10,7 @@
 // belongs to a row without a slot is zero in a training step, where such rows
 // are contracted over, and otherwise not written, and never read for a token.
 //
-// The gather of the tokens' rows is part of their packing, GeLU and the
+// The tokens' rows go to those of their slots as they are packed, GeLU and the
 // activation's packing of the first product's epilogue, and the weighted sum
 // one kernel (combine_kernel), which adds a token's rows in fp32 in the order
 // of its choices, so that results do not depend on the order of execution.
@@ -21,6 +21,7 @@
 #include <cstring>
 
 #include "fp8.h"
+#include "fp8_pack.cuh"
 #include "vec_util.cuh"
 
 using namespace tpf;
@@ -30,6 +31,7 @@ namespace {
 constexpr int kMaxExperts = TP_ROUTE_MAX_EXPERTS, kMaxK = 32;
 constexpr int kDispatchThreads = 1024;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
+constexpr int32_t kFewSlots = 512;  // dispatched and packed by one kernel
 
 // ------------------------------------------------------------------ plan
 
@@ -37,6 +39,7 @@ struct DispatchParams {
   const int32_t* experts;  // [S]
   int32_t *tiles, *pairs, *first, *expert, *pair, *slot, *row;
   int32_t S, E, tile_rows, aligned;
+  TokenPack pack;  // of few slots
 };
 
 __device__ __forceinline__ int32_t tiles_of(int32_t n, int32_t tile_rows) { return (n + tile_rows - 1) / tile_rows; }
@@ -48,6 +51,52 @@ __device__ __forceinline__ int4 four_slots(const DispatchParams& P, int32_t i) {
                    i + 3 < P.S ? P.experts[i + 3] : -1);
 }
 
+// Where there are few slots, blocks behind the experts' pack the tokens, a
+// warp 512 columns, and find their slots' rows by themselves: a launch less
+// before the products (one token: ... us, ... with two kernels).
+__device__ __forceinline__ void pack_few(const DispatchParams& P, int32_t* count) {
+  const TokenPack& K = P.pack;
+  __shared__ int32_t slots[kFewSlots], first[kMaxExperts], warp_sum[kMaxExperts / 32];
+  const int32_t tid = static_cast<int32_t>(threadIdx.x);
+  const uint32_t lane = tid & 31, warp = tid >> 5;
+  for (int32_t e = tid; e < P.E; e += kDispatchThreads) count[e] = 0;
+  __syncthreads();
+  if (tid < P.S) {
+    const int32_t e = P.experts[tid];
+    slots[tid] = e;
+    if (e >= 0 && e < P.E) atomicAdd(count + e, 1);
+  }
+  __syncthreads();
+  int32_t n = 0, sum = 0;
+  if (tid < kMaxExperts) {
+    n = sum = tid < P.E ? tiles_of(count[tid], P.tile_rows) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t u = __shfl_up_sync(kAll, sum, o);
+      if (static_cast<int32_t>(lane) >= o) sum += u;
+    }
+    if (lane == 31) warp_sum[warp] = sum;
+  }
+  __syncthreads();
+  if (tid < kMaxExperts) {
+    const int32_t other = lane < kMaxExperts / 32 ? warp_sum[lane] : 0;
+    first[tid] = (sum - n + __reduce_add_sync(kAll, lane < warp ? other : 0)) * P.tile_rows;
+  }
+  __syncthreads();
+  const uint32_t fours = static_cast<uint32_t>(K.e_block / 512);
+  const int64_t unit = static_cast<int64_t>(blockIdx.x - P.E) * (kDispatchThreads / 32) + warp, t = unit / fours;
+  if (t >= K.tokens) return;
+  int32_t row = -1;
+  for (int32_t j = 0; j < K.k; ++j) {
+    const int32_t slot = static_cast<int32_t>(t) * K.k + j, e = slots[slot];
+    int32_t before = 0;  // slots of the same expert
+    for (int32_t i = static_cast<int32_t>(lane); i < slot; i += 32) before += slots[i] == e;
+    before = __reduce_add_sync(kAll, before);
+    if (static_cast<int32_t>(lane) == j && e >= 0 && e < P.E) row = first[e] + before;
+  }
+  pack_token(K, t, static_cast<uint32_t>(unit % fours), row, lane);
+}
+
 // A thread block an expert.  Each counts all experts' slots, so that no
 // kernel has to run before it, and keeps the first 32768 in registers for the
 // second pass, which gives its own their rows, in their order.
@@ -57,6 +106,10 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const __grid
   __shared__ int32_t warp_sum[2][kDispatchThreads / 32], begin, total, pair_begin, pair_total;
   griddep_wait();
   griddep_launch_dependents();
+  if (static_cast<int32_t>(blockIdx.x) >= P.E) {
+    pack_few(P, count);
+    return;
+  }
   const int32_t me = static_cast<int32_t>(blockIdx.x), tid = static_cast<int32_t>(threadIdx.x);
   const uint32_t lane = tid & 31, warp = tid >> 5;
   for (int32_t e = tid; e < P.E; e += kDispatchThreads) count[e] = 0;
@@ -309,7 +362,6 @@ Fp8Plan plan_at(const Sizes& s, int32_t* at, PlanArrays* a) {
   plan.first = a->first;
   plan.expert = a->expert;
   plan.slot = a->slot;
-  plan.row = a->row;
   return plan;
 }
 
@@ -492,15 +544,21 @@ extern "C" tp_status tp_experts_fwd_fp8(const void* x, const void* experts, cons
   D.E = static_cast<int32_t>(E);
   D.tile_rows = static_cast<int32_t>(s.tile_rows);
   D.aligned = aligned16(experts);
-  TP_TRY(launch_dependent(dispatch_kernel, dim3(static_cast<unsigned>(E)), kDispatchThreads, 0, stream, D));
-  Fp8Pack pack;
-  pack.x = &x;
-  pack.q = &A.xq;
-  pack.rows = s.rows;
-  pack.cols = h;
-  pack.plan = &plan;
-  pack.tokens = T;
-  TP_TRY(fp8_pack(pack, stream));
+  TokenPack& K = D.pack;
+  K.row = at.row;
+  K.x = static_cast<const __nv_bfloat16*>(x);
+  K.q = static_cast<uint8_t*>(A.xq.q);
+  K.e = static_cast<uint8_t*>(A.xq.e);
+  K.tokens = T;
+  K.cols = h;
+  K.ldq = fp8_pitch(h);
+  K.e_block = cdiv(h, 512) * 512;
+  K.k = static_cast<int32_t>(k);
+  K.tile_rows = D.tile_rows;
+  const bool few = s.S <= kFewSlots;
+  const int64_t packs = few ? cdiv(T * (K.e_block / 512), kDispatchThreads / 32) : 0;
+  TP_TRY(launch_dependent(dispatch_kernel, dim3(static_cast<unsigned>(E + packs)), kDispatchThreads, 0, stream, D));
+  if (!few) TP_TRY(fp8_pack_tokens(K, stream));
   uint32_t* status = static_cast<uint32_t*>(ws);
   void* preact = train ? saved->preact : nullptr;
   void* out = train ? saved->out : A.out;

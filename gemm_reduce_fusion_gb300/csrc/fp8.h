@@ -27,7 +27,6 @@ struct Fp8Plan {
   const int32_t* expert;  // expert << 9 | rows of a tile
   const int32_t* first;   // first tile of an expert, E + 1
   const int32_t* slot;    // token * k + choice of a row, or -1
-  const int32_t* row;     // of token * k + choice, or -1
   int64_t max_tiles, tile_rows;
   int E, k;
   bool paired;            // products on CTA pairs
@@ -80,9 +79,11 @@ struct Fp8Pack {
   const Fp8Plan* plan = nullptr;   // rows of x[0] by the plan's slots, rows = those of the plan
   const float* weights = nullptr;  // a factor for each slot
   bool gather = true;              // false: x[0] has the plan's rows
-  int64_t tokens = 0;              // q alone, without weights: x[0]'s tokens, each packed once; rows without a slot stay as they are
 };
 tp_status fp8_pack(const Fp8Pack& p, cudaStream_t stream);
+// Tokens into the rows of their slots (fp8_pack.cuh).
+struct TokenPack;
+tp_status fp8_pack_tokens(const TokenPack& p, cudaStream_t stream);
 
 size_t fp8_linear_workspace(tp_op op, int p, int64_t M, int64_t N, int64_t K);
 

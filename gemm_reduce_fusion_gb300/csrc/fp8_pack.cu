@@ -19,6 +19,7 @@
 
 #include "fp8.h"
 #include "fp8_device.cuh"
+#include "fp8_pack.cuh"
 #include "gelu.cuh"
 #include "vec_util.cuh"
 
@@ -39,8 +40,6 @@ struct PackParams {
   uint32_t batch, strips;      // matrices a tensor; strips of 128 rows of a matrix
   int32_t tiles, gelu;
   const int32_t *plan_tiles, *slot;  // or null
-  const int32_t* row;                // of a slot, or -1: packing by tokens
-  int64_t tokens;
   const float* weights;              // of the slots, or null
   int32_t gather, k, tile_rows;
 };
@@ -58,11 +57,6 @@ __device__ __forceinline__ const __nv_bfloat16* source(const PackParams& P, cons
 
 // What becomes of an element before it is packed.
 enum Source : int { PLAIN = 0, GELU = 1, WEIGHTED = 2 };
-
-// The largest magnitude of bf16 pairs, as 15-bit integers (an infinity or NaN
-// is at least 0x7F80, and the magnitudes are then looked at one by one).
-__device__ __forceinline__ uint32_t max_abs(uint32_t a, uint32_t b) { return __vmaxu2(a, b & 0x7FFF7FFFu); }
-constexpr uint32_t kInfinite = 0x7F80u;
 
 // Two neighbours of a row, as they are packed.
 template <int SRC>
@@ -293,7 +287,7 @@ __global__ void __launch_bounds__(kThreads) fp8_pack_rows_kernel(const __grid_co
 // slots: read and packed once.  (Gathered by the rows, each of six slots packed
 // for itself, 4096 tokens of 4096 took 60 us, so 23 us.)  Rows without a slot are
 // not written.
-__global__ void __launch_bounds__(kThreads) fp8_pack_tokens_kernel(const __grid_constant__ PackParams P) {
+__global__ void __launch_bounds__(kThreads) fp8_pack_tokens_kernel(const __grid_constant__ TokenPack P) {
   griddep_wait();
   griddep_launch_dependents();
   const uint32_t fours = static_cast<uint32_t>(P.e_block / 512), lane = threadIdx.x & 31;
@@ -301,49 +295,7 @@ __global__ void __launch_bounds__(kThreads) fp8_pack_tokens_kernel(const __grid_
   if (t >= P.tokens) return;
   const uint32_t four = static_cast<uint32_t>(unit % fours);
   const int32_t my_row = static_cast<int32_t>(lane) < P.k ? __ldcg(P.row + t * P.k + lane) : -1;  // k <= 32
-  const int64_t c = static_cast<int64_t>(four) * 512 + lane * 16;
-  const __nv_bfloat16* x = P.x[0] + t * P.cols;
-  const uint4 a = c < P.cols ? *reinterpret_cast<const uint4*>(x + c) : make_uint4(0, 0, 0, 0);
-  const uint4 b = c + 8 < P.cols ? *reinterpret_cast<const uint4*>(x + c + 8) : make_uint4(0, 0, 0, 0);
-  const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  float f[16];
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    m = max_abs(m, u[i]);
-    f[2 * i] = bf_lo(u[i]);
-    f[2 * i + 1] = bf_hi(u[i]);
-  }
-  m = max(m & 0xFFFFu, m >> 16);
-#pragma unroll
-  for (int o = 4; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));  // of 128 columns
-  float top = __uint_as_float(m << 16);
-  const bool finite = __all_sync(0xFFFFFFFFu, m < kInfinite);
-  if (!finite) {
-    top = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) top = fmaxf(top, finite_abs(f[i]));
-#pragma unroll
-    for (int o = 4; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-  }
-  const uint32_t e = fp8_exponent(top);
-  const float inv = fp8_inverse(e);
-  uint32_t q[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    q[i] = finite ? fp8_pack4_finite(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3], inv)
-                  : fp8_pack4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3], inv);
-  uint32_t es = 0;  // the four blocks' exponents, which lie side by side
-#pragma unroll
-  for (int i = 0; i < 4; ++i) es |= __shfl_sync(0xFFFFFFFFu, e, i * 8) << (i * 8);
-  for (int32_t j = 0; j < P.k; ++j) {
-    const int64_t r = __shfl_sync(0xFFFFFFFFu, my_row, j);
-    if (r < 0) continue;
-    if (c < P.ldq) *reinterpret_cast<uint4*>(P.q[0] + r * P.ldq + c) = make_uint4(q[0], q[1], q[2], q[3]);
-    const int64_t block = r / P.tile_rows;
-    if (lane == 0)
-      *reinterpret_cast<uint32_t*>(P.e[0] + block * P.e_block + four * 512 + fp8_e_at(static_cast<uint32_t>(r - block * P.tile_rows), 0)) = es;
-  }
+  pack_token(P, t, four, my_row, lane);
 }
 
 template <int SRC>
@@ -426,19 +378,12 @@ tp_status fp8_pack(const Fp8Pack& d, cudaStream_t stream) {
   P.gelu = d.gelu;
   P.tile_rows = 128;
   if (d.plan) {
-    P.row = d.plan->row;
     P.plan_tiles = d.plan->tiles;
     P.slot = d.plan->slot;
     P.weights = d.weights;
     P.gather = d.gather;
     P.k = d.plan->k;
     P.tile_rows = static_cast<int32_t>(d.plan->tile_rows);
-  }
-  if (d.plan && d.tokens > 0) {
-    P.tokens = d.tokens;
-    const int64_t blocks = cdiv(d.tokens * (P.e_block / 512), kThreads / 32);
-    if (blocks > 0x7FFFFFFFll) return TP_ERR_UNSUPPORTED_SHAPE;
-    return launch_dependent(fp8_pack_tokens_kernel, dim3(static_cast<unsigned>(blocks)), kThreads, 0, stream, P);
   }
   // A block of 128 rows for each 128 columns fills the GPU's 152 SMs from some
   // 256 rows on.
@@ -453,6 +398,12 @@ tp_status fp8_pack(const Fp8Pack& d, cudaStream_t stream) {
   if (d.gelu) return launch_pack<GELU>(d, grid, P, stream);
   if (d.weights) return launch_pack<WEIGHTED>(d, grid, P, stream);
   return launch_pack<PLAIN>(d, grid, P, stream);
+}
+
+tp_status fp8_pack_tokens(const TokenPack& P, cudaStream_t stream) {
+  const int64_t blocks = cdiv(P.tokens * (P.e_block / 512), kThreads / 32);
+  if (blocks > 0x7FFFFFFFll) return TP_ERR_UNSUPPORTED_SHAPE;
+  return launch_dependent(fp8_pack_tokens_kernel, dim3(static_cast<unsigned>(blocks)), kThreads, 0, stream, P);
 }
 
 }  // namespace tpf
