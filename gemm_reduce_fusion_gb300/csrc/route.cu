@@ -629,12 +629,20 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const __grid_con
       scores<PER>(P, l, s);
       sc = pick<PER>(s, mine);
     }
-    if (P.renorm) {  // w = s / sum s
-      const float total = fmaxf(warp_sum(sc), FLT_MIN), all = warp_sum(g * sc) / total;
-      g = mine == kNone ? 0.f : (g - all) / total;
+    // w = s / sum s depends on the chosen logits alone: the logit's gradient is
+    // (ds/dl / total) (g - sum_j w_j g_j), and the bracket sum_j w_j (g - g_j),
+    // which keeps its digits where one w is nearly 1 and is 0 for a single
+    // choice.  ds/dl / total is at most 1 (softmax: w), whatever the total.
+    if (P.renorm) {
+      const float sum = warp_sum(sc), total = fmaxf(sum, FLT_MIN), w = __fdiv_rn(sc, total);
+      float rest = 0.f;
+      for (int32_t j = 0; j < P.k; ++j) rest = fmaf(__shfl_sync(kAll, w, j), g - __shfl_sync(kAll, g, j), rest);
+      if (sum < FLT_MIN) rest = g - warp_sum(g * w);  // the weights do not add up to 1
+      g = mine == kNone ? 0.f : rest * (P.sigmoid ? slope / total : w);
+    } else if (P.sigmoid) {
+      g *= slope;
     }
-    if (P.sigmoid) g *= slope;
-    // the gradient of each expert's score (sigmoid: logit)
+    // the gradient of each expert's score, or logit
     float d[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) d[i] = 0.f;
@@ -647,7 +655,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const __grid_con
           if (e % PER == i) d[i] += v;
       }
     }
-    if (!P.sigmoid) {
+    if (!P.sigmoid && !P.renorm) {
       float dot = 0.f;
 #pragma unroll
       for (int i = 0; i < PER; ++i) dot += d[i] * s[i];

@@ -242,3 +242,44 @@ def test_captured_and_replayed(tp):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((e, w, n, d), want))
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_gradient_of_weights_that_add_up_to_one(tp, sigmoid):
+    T, E, k = 64, 40, 4
+    g = torch.Generator().manual_seed(9)
+    l, dw = torch.randn(T, E, generator=g), torch.randn(T, k, generator=g)
+    how = dict(score=int(sigmoid), renorm=True)
+
+    def call(l, k, bias=None):
+        T, E = l.shape
+        e, w, d = (torch.empty((T, k), dtype=torch.int32, device="cuda"), torch.empty((T, k), device="cuda"),
+                   torch.full((T, E), float("nan"), device="cuda"))
+        tp.tp_route_fwd(l.cuda(), e, w, bias=bias, **how)
+        tp.tp_route_bwd(l.cuda(), e, dw[:T, :k].contiguous().cuda(), d, **how)
+        return e, w, d
+
+    # a single choice: its weight is the scale, whatever the logits
+    assert bool((call(l, 1)[2] == 0).all())
+    alone = torch.full_like(l, -math.inf)
+    alone[:, 7] = l[:, 7]
+    assert bool((call(alone, k)[2] == 0).all())
+    # one score far above (softmax), or all others far below: the small differences keep their digits
+    l[:, 3] = 12.0
+    l[:, :3] -= 9.0
+    l[:, 4:] -= 9.0
+    e, w, d = call(l, k)
+    want = gradient(l, e.cpu(), dw, sigmoid, True, 1.0)
+    share, v = route(l, k, None, sigmoid, 1, 1, 1, True, 1.0)[1], dw.to(D)
+    # d_i = w_i c_i sum_j w_j (v_i - v_j), c_i <= 1: fewer than 64 roundings of each weight and of c_i, one or two of the rest
+    size = share * (share[:, None, :] * (v[:, :, None] - v[:, None, :]).abs()).sum(2)
+    slack = torch.zeros(T, E, dtype=D).scatter_(1, e.cpu().long(), 160 * 2.0 ** -24 * size)
+    # (the definition itself leaves 2^-50 of the terms where the sum is 0)
+    assert bool(((d.cpu().to(D) - want).abs() <= slack + 2.0 ** -50).all())
+    # scores that leave the range of fp32, chosen for their bias
+    low = torch.full((4, E), -120.0)
+    low[:, 0] = 100.0
+    bias = torch.zeros(E, device="cuda")
+    bias[1:] = 10.0
+    e, w, d = call(low, k, bias)
+    assert bool((e > 0).all()) and bool(torch.isfinite(w).all()) and bool(torch.isfinite(d).all())
