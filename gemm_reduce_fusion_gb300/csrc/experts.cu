@@ -214,7 +214,7 @@ struct CombineParams {
 
 // Eight columns of a token a thread.  Bound by HBM: 4096 tokens of 4096, six
 // rows each, 46 us, 0.75 of the copy rate.
-__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ CombineParams P) {
+__global__ void __launch_bounds__(256, 4) combine_kernel(const __grid_constant__ CombineParams P) {
   griddep_wait();
   griddep_launch_dependents();
   const int64_t per_row = P.N / 8, unit = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, t = unit / per_row;
