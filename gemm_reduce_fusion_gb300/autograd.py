@@ -471,7 +471,7 @@ class _ExpertsFn(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, p, x, experts, weights, *wb):
-        x = _bf16(x, "x")
+        x, experts, weights = _bf16(x, "x"), experts.contiguous(), weights.contiguous()
         w1 = [_bf16(a, "FC1 weights of the experts") for a in wb[:p]]
         w2 = [_bf16(a, "FC2 weights of the experts") for a in wb[p:]]
         (T, h), (per, _, f), k = x.shape, w1[0].shape, experts.shape[1]

@@ -277,26 +277,27 @@ tp_status backward(bool row, const tp_fp8* xt, const tp_fp8* w, const tp_fp8* dy
   TP_TRY(check_sizes(p, M, N, K, 0, TP_BF16));
   if (static_cast<int64_t>(p) * N > (int64_t(1) << 31) - 1) return TP_ERR_UNSUPPORTED_SHAPE;
   const int nx = row ? p : 1, ny = row ? 1 : p;
-  const bool work = M > 0 && N > 0 && K > 0;
+  // an empty contraction has zeros for its product, and operands without bytes
+  const bool for_x = dx != nullptr && M > 0 && K > 0, for_w = dw != nullptr && N > 0 && K > 0;
   if (dx == nullptr && dw == nullptr) return TP_ERR_INVALID_ARG;
-  TP_TRY(check_fp8(w, p, work && dx != nullptr));
-  TP_TRY(check_fp8(dy, ny, work && dx != nullptr));
-  TP_TRY(check_ptrs(in(dx), nx, work && dx != nullptr));
-  TP_TRY(check_ptrs(preact, nx, work && dx != nullptr && preact != nullptr));
-  TP_TRY(check_fp8(xt, nx, work && dw != nullptr));
-  TP_TRY(check_fp8(dyt, ny, work && dw != nullptr));
-  TP_TRY(check_ptrs(in(dw), p, work && dw != nullptr));
+  TP_TRY(check_fp8(w, p, for_x && N > 0));
+  TP_TRY(check_fp8(dy, ny, for_x && N > 0));
+  TP_TRY(check_ptrs(in(dx), nx, for_x));
+  TP_TRY(check_ptrs(preact, nx, for_x && preact != nullptr));
+  TP_TRY(check_fp8(xt, nx, for_w && M > 0));
+  TP_TRY(check_fp8(dyt, ny, for_w && M > 0));
+  TP_TRY(check_ptrs(in(dw), p, for_w));
   TP_TRY(check_ws(ws, ws_bytes, fp8_linear_workspace(row ? TP_OP_ROW_BWD_FP8 : TP_OP_COL_BWD_FP8, p, M, N, K)));
-  if (!work) return TP_OK;
+  if (!for_x && !for_w) return TP_OK;
   {
     RangeList ins, outs;
-    if (dx) {
+    if (for_x) {
       add_fp8(&ins, w, p, K, N);
       add_fp8(&ins, dy, ny, M, N);
       add_ranges(&ins, preact, nx, static_cast<size_t>(M * K) * 2);
       add_ranges(&outs, in(dx), nx, static_cast<size_t>(M * K) * 2);
     }
-    if (dw) {
+    if (for_w) {
       add_fp8(&ins, xt, nx, K, M);
       add_fp8(&ins, dyt, ny, N, M);
       add_ranges(&outs, in(dw), p, static_cast<size_t>(K * N) * 2);
@@ -306,7 +307,7 @@ tp_status backward(bool row, const tp_fp8* xt, const tp_fp8* w, const tp_fp8* dy
   }
   DevInfo di;
   TP_TRY(device_info(&di));
-  if (dx) {
+  if (for_x) {
     Fp8Product d;
     d.a = dy;
     d.na = ny;
@@ -322,7 +323,7 @@ tp_status backward(bool row, const tp_fp8* xt, const tp_fp8* w, const tp_fp8* dy
     d.aux = const_cast<void* const*>(preact);
     TP_TRY(fp8_product(d, fp8_plan(FP8_DENSE, M, K, N, d.groups, d.segs), parts_of(ws), static_cast<uint32_t*>(ws), stream));
   }
-  if (dw) {
+  if (for_w) {
     Fp8Product d;
     d.a = xt;
     d.na = nx;

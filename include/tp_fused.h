@@ -447,7 +447,8 @@ tp_status tp_row_linear_fwd_fp8(const tp_fp8* x, const tp_fp8* w, const void* bi
  *   w[k]: operand [K, N] of A_k (q of A_k); dy: operands [M, N] and
  *   dyt: operands [N, M] of the output gradients and their transposes;
  *   xt: operands [K, M] of the transposed inputs.  dx (from w, dy) or dw
- *   (from xt, dyt) may be NULL, not both; all bf16.                          */
+ *   (from xt, dyt) may be NULL, not both; all bf16.  Without tokens dw is
+ *   zero, with N == 0 dx is.                                                 */
 tp_status tp_col_linear_bwd_fp8(const tp_fp8* xt, const tp_fp8* w, const tp_fp8* dy, const tp_fp8* dyt, void* dx,
                                 void* const* dw, int p, int64_t M, int64_t N, int64_t K, void* ws, size_t ws_bytes,
                                 cudaStream_t stream);

@@ -169,3 +169,21 @@ def test_rows_behind_the_backward_limit_are_refused(tp):
     with pytest.raises(tp.TPError):
         tp.tp_experts_fwd_fp8(meta(T, h), meta(T, k, dtype=torch.int32).fill_(-1), meta(T, k, dtype=torch.float32), P.o1, P.o2, meta(T, h), ws,
                               saved=tp.experts_saved(E, T, k, h, f))
+
+
+@pytest.mark.parametrize("p,E,T,k,h,f", [(1, 4, 20, 2, 1160, 264), (2, 4, 900, 1, 1160, 520)])
+def test_a_wait_that_runs_out_is_reported(tp, p, E, T, k, h, f):
+    """Single CTAs and pairs: a stage that is never handed over ends the call with a status, and the next call is right."""
+    P = Problem(tp, p, E, T, k, h, f, 3)
+    ws, y = tp.experts_workspace(p, E, T, k, h, f), torch.empty_like(P.x)
+    try:
+        assert tp.tp_debug_set(tp.TP_DEBUG_TIMEOUT_MS, 50) == tp.TP_OK and tp.tp_debug_set(tp.TP_DEBUG_DROP_LOAD, 2) == tp.TP_OK
+        tp.tp_experts_fwd_fp8(P.x, P.experts, P.weights, P.o1, P.o2, y, ws)
+        assert tp.tp_get_device_status(ws) == tp.TP_ERR_DEVICE_TIMEOUT
+    finally:
+        tp.tp_debug_set(tp.TP_DEBUG_TIMEOUT_MS, 0)
+        tp.tp_debug_set(tp.TP_DEBUG_DROP_LOAD, -1)
+    tp.tp_experts_fwd_fp8(P.x, P.experts, P.weights, P.o1, P.o2, y, ws)
+    assert tp.tp_get_device_status(ws) == tp.TP_OK
+    want, slack, _ = forward_reference(P)
+    assert_within(y, want, slack, "y")

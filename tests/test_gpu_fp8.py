@@ -339,3 +339,24 @@ def test_a_wait_that_runs_out_is_reported(tp):
         tp.tp_row_linear_fwd_fp8(x, w, y, ws)
         assert tp.tp_get_device_status(ws) == tp.TP_OK
         assert bool((y == K).all())
+
+
+@pytest.mark.parametrize("p,K,N", [(2, 136, 264), (4, 1032, 2056)])
+def test_gradients_of_empty_contractions_are_zero(tp, p, K, N):
+    """Without tokens the weights' gradients are zero, without outputs the inputs'."""
+    ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    nan = lambda *s: torch.full(s, float("nan"), dtype=BF, device="cuda")  # noqa: E731
+    dw, dx = [nan(K, N) for _ in range(p)], nan(0, K)
+    weights = [tp.fp8_empty(K, N) for _ in range(p)]
+    tp.tp_col_linear_bwd_fp8(tp.fp8_empty(K, 0), weights, [tp.fp8_empty(0, N) for _ in range(p)], [tp.fp8_empty(N, 0) for _ in range(p)], dx, dw, ws)
+    assert all(bool((t == 0).all()) for t in dw)
+    dw = [nan(K, N) for _ in range(p)]
+    tp.tp_row_linear_bwd_fp8([tp.fp8_empty(K, 0) for _ in range(p)], weights, tp.fp8_empty(0, N), tp.fp8_empty(N, 0),
+                             [nan(0, K) for _ in range(p)], dw, ws)
+    assert all(bool((t == 0).all()) for t in dw)
+    M = 300
+    dx, dw = nan(M, K), [nan(K, 0) for _ in range(p)]
+    tp.tp_col_linear_bwd_fp8(tp.fp8_empty(K, M), [tp.fp8_empty(K, 0) for _ in range(p)], [tp.fp8_empty(M, 0) for _ in range(p)],
+                             [tp.fp8_empty(0, M) for _ in range(p)], dx, dw, ws)
+    assert bool((dx == 0).all())
+    assert tp.tp_get_device_status(ws) == tp.TP_OK

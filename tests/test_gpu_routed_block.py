@@ -197,3 +197,29 @@ def test_refusals(blk):
         y = blk.parallel_mlp_fp8(n, [rnd(gen(2), 64, 64)], [rnd(gen(3), 64, 64)])
         g, = torch.autograd.grad(y.float().square().sum(), n, create_graph=True)
         g.float().sum().backward()
+
+
+def test_no_token_and_strided_inputs():
+    from gemm_reduce_fusion_gb300.autograd import parallel_mlp_fp8, route, routed_experts
+    h, f, E, p, k = 64, 128, 4, 2, 2
+    g = torch.Generator(device="cuda").manual_seed(8)
+    mk = lambda *s: (torch.randn(s, generator=g, device="cuda") * 0.1).to(torch.bfloat16).requires_grad_()  # noqa: E731
+    x = torch.empty((0, h), dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    shards = [mk(h, f) for _ in range(p)], [mk(f, h) for _ in range(p)]
+    parallel_mlp_fp8(x, *shards).sum().backward()
+    experts = [mk(E // p, h, f) for _ in range(p)], [mk(E // p, f, h) for _ in range(p)]
+    logits = torch.empty((0, E), device="cuda", requires_grad=True)
+    w, e, counts = route(logits, k, renorm=True)
+    routed_experts(x, e, w, *experts).sum().backward()
+    assert all(bool((t.grad == 0).all()) for t in (*shards[0], *shards[1], *experts[0], *experts[1]))
+    assert x.grad.shape == x.shape and logits.grad.shape == logits.shape and int(counts.abs().sum()) == 0
+    # views that are not contiguous give what their copies give
+    x, l = mk(40, 2 * h).detach(), torch.randn((E, 40), generator=g, device="cuda")
+    got = []
+    for copy in (False, True):
+        xs, ls = (t.contiguous().requires_grad_() if copy else t.requires_grad_() for t in (x.clone()[:, ::2], l.clone().t()))
+        w, e, _ = route(ls, k)
+        y = routed_experts(xs, e if copy else e.t().contiguous().t(), w if copy else w.t().contiguous().t(), *experts)
+        y.float().square().sum().backward()
+        got.append((y, xs.grad, ls.grad))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
