@@ -19,7 +19,7 @@
 // lowest lane with a value has the lowest expert.  A largest value is found by
 // one reduction over the warp of its bits in an order-preserving form, and the
 // lane that has it looks which expert it is.  Bound by instructions (8192
-// tokens, 8 of 256 experts from 4 of 8 groups, with counts and gradient: 28 us,
+// tokens, 8 of 256 experts from 4 of 8 groups, with counts and gradient: 25 us,
 // where the bytes take 2): each choice is a reduction over the warp and a few
 // dependent steps.  One token is the launch.
 #include <cuda_bf16.h>
@@ -603,6 +603,73 @@ __global__ void __launch_bounds__(kCountThreads) route_count_kernel(const __grid
     if (hist[e]) atomicAdd(P.counts + e, hist[e]);
 }
 
+// A lane's choice of a row (kNone: none) and scale * the gradient of its weight.
+__device__ __forceinline__ float chosen(const RouteParams& P, int64_t row, uint32_t lane, uint32_t& mine) {
+  mine = kNone;
+  if (static_cast<int32_t>(lane) >= P.k) return 0.f;
+  const int32_t e = P.experts[row * P.k + lane];
+  if (e < 0 || e >= P.E) return 0.f;
+  mine = static_cast<uint32_t>(e);
+  return P.scale * P.dweights[row * P.k + lane];
+}
+
+// w = s / sum s depends on the chosen logits alone: the gradient of a logit is
+// (ds/dl / total) (g - sum_j w_j g_j), and the bracket sum_j w_j (g - g_j),
+// which keeps its digits where one w is nearly 1 and is 0 for a single choice.
+// slope, ds/dl, is at most s, so that slope / total is at most 1.  (A total
+// below the range is a constant: the weights do not add up to 1 then.)
+__device__ __forceinline__ float through_sum(const RouteParams& P, float g, float sc, float slope) {
+  const float sum = warp_sum(sc), total = fmaxf(sum, FLT_MIN), w = __fdiv_rn(sc, total);
+  float rest = 0.f;
+  for (int32_t j = 0; j < P.k; ++j) rest = fmaf(__shfl_sync(kAll, w, j), g - __shfl_sync(kAll, g, j), rest);
+  return (sum < FLT_MIN ? g : rest) * __fdiv_rn(slope, total);
+}
+
+// Sigmoid: only the chosen logits have a gradient, s (1 - s) without the
+// difference, and only they are read; the row is zeros but for them.  (By whole
+// rows, as for the softmax, 8192 x 256 took 7.1 us, so 4.5.)
+__global__ void __launch_bounds__(kWarps * 32) route_bwd_sigmoid_kernel(const __grid_constant__ RouteParams P) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const uint32_t lane = threadIdx.x & 31;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); row < P.T; row += static_cast<int64_t>(gridDim.x) * kWarps) {
+    const int64_t at = row * P.E;
+    uint32_t mine;
+    float g = chosen(P, row, lane, mine), x = -INFINITY;
+    if (mine != kNone) x = P.f32 ? static_cast<const float*>(P.logits)[at + mine] : __bfloat162float(static_cast<const __nv_bfloat16*>(P.logits)[at + mine]);
+    if (P.vector) {
+      const int32_t n = P.E * (P.f32 ? 4 : 2) / 16;
+      uint4* to = reinterpret_cast<uint4*>(static_cast<uint8_t*>(P.dlogits) + at * (P.f32 ? 4 : 2));
+      for (int32_t i = static_cast<int32_t>(lane); i < n; i += 32) to[i] = make_uint4(0, 0, 0, 0);
+    } else {
+      for (int32_t i = static_cast<int32_t>(lane); i < P.E; i += 32) {
+        if (P.f32) static_cast<float*>(P.dlogits)[at + i] = 0.f;
+        else static_cast<__nv_bfloat16*>(P.dlogits)[at + i] = __float2bfloat16_rn(0.f);
+      }
+    }
+    const float t = expf(-fabsf(x)), u = inverse(1.f + t);
+    const bool open = x > -INFINITY;  // and not NaN
+    const float sc = open ? (x >= 0.f ? u : t * u) : 0.f, slope = open ? t * u * u : 0.f;
+    g = P.renorm ? through_sum(P, g, sc, slope) : g * slope;
+    // a number that comes more than once: its first slot has the sum
+    const uint32_t same = __match_any_sync(kAll, mine);
+    if (__any_sync(kAll, mine != kNone && (same & (same - 1)) != 0)) {
+      float sum = 0.f;
+      for (int32_t j = 0; j < P.k; ++j) {
+        const float v = __shfl_sync(kAll, g, j);
+        if (same >> j & 1) sum += v;
+      }
+      g = sum;
+    }
+    __syncwarp();  // the zeros come first
+    if (mine != kNone && static_cast<int32_t>(lane) == __ffs(same) - 1) {
+      if (P.f32) static_cast<float*>(P.dlogits)[at + mine] = g;
+      else static_cast<__nv_bfloat16*>(P.dlogits)[at + mine] = __float2bfloat16_rn(g);
+    }
+  }
+}
+
+// Softmax.
 template <int PER>
 __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const __grid_constant__ RouteParams P) {
   griddep_wait();
@@ -611,41 +678,14 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const __grid_con
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); row < P.T; row += static_cast<int64_t>(gridDim.x) * kWarps) {
     float l[PER], s[PER];
     load_row<PER>(P, row, lane, l);
-    uint32_t mine = kNone;
-    float g = 0.f;
-    if (static_cast<int32_t>(lane) < P.k) {
-      const int32_t e = P.experts[row * P.k + lane];
-      if (e >= 0 && e < P.E) {
-        mine = static_cast<uint32_t>(e);
-        g = P.scale * P.dweights[row * P.k + lane];
-      }
-    }
-    // the chosen scores: sigmoid's from their own logits, and its gradient
-    // s (1 - s) without the difference
-    float sc, slope = 0.f;
-    if (P.sigmoid) {
-      const float x = pick<PER>(l, mine), t = expf(-fabsf(x)), u = inverse(1.f + t);
-      const bool open = mine != kNone && x > -INFINITY;
-      sc = open ? (x >= 0.f ? u : t * u) : 0.f;
-      slope = open ? t * u * u : 0.f;
-    } else {
-      scores<PER>(P, l, s);
-      sc = pick<PER>(s, mine);
-    }
-    // w = s / sum s depends on the chosen logits alone: the logit's gradient is
-    // (ds/dl / total) (g - sum_j w_j g_j), and the bracket sum_j w_j (g - g_j),
-    // which keeps its digits where one w is nearly 1 and is 0 for a single
-    // choice.  ds/dl / total is at most 1 (softmax: w), whatever the total.
+    uint32_t mine;
+    float g = chosen(P, row, lane, mine);
+    scores<PER>(P, l, s);
     if (P.renorm) {
-      const float sum = warp_sum(sc), total = fmaxf(sum, FLT_MIN), w = __fdiv_rn(sc, total);
-      float rest = 0.f;
-      for (int32_t j = 0; j < P.k; ++j) rest = fmaf(__shfl_sync(kAll, w, j), g - __shfl_sync(kAll, g, j), rest);
-      if (sum < FLT_MIN) rest = g - warp_sum(g * w);  // the weights do not add up to 1
-      g = mine == kNone ? 0.f : rest * (P.sigmoid ? slope / total : w);
-    } else if (P.sigmoid) {
-      g *= slope;
+      const float sc = pick<PER>(s, mine);
+      g = through_sum(P, g, sc, sc);
     }
-    // the gradient of each expert's score, or logit
+    // the gradient of each expert's score (renorm: logit)
     float d[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) d[i] = 0.f;
@@ -658,7 +698,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const __grid_con
           if (e % PER == i) d[i] += v;
       }
     }
-    if (!P.sigmoid && !P.renorm) {
+    if (!P.renorm) {
       float dot = 0.f;
 #pragma unroll
       for (int i = 0; i < PER; ++i) dot += d[i] * s[i];
@@ -743,6 +783,10 @@ tp_status run(bool fwd, RouteParams& P, cudaStream_t stream) {
 }
 
 tp_status run(bool fwd, RouteParams& P, cudaStream_t stream) {
+  if (!fwd && P.sigmoid) {
+    P.vector = P.E * (P.f32 ? 4 : 2) % 16 == 0 && reinterpret_cast<uintptr_t>(P.dlogits) % 16 == 0;
+    return launch_dependent(route_bwd_sigmoid_kernel, dim3(grid_of(P.T)), kWarps * 32, 0, stream, P);
+  }
   if (P.E <= 64) return run<2>(fwd, P, stream);
   if (P.E <= 128) return run<4>(fwd, P, stream);
   if (P.E <= 256) return run<8>(fwd, P, stream);

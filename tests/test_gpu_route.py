@@ -283,3 +283,21 @@ def test_gradient_of_weights_that_add_up_to_one(tp, sigmoid):
     bias[1:] = 10.0
     e, w, d = call(low, k, bias)
     assert bool((e > 0).all()) and bool(torch.isfinite(w).all()) and bool(torch.isfinite(d).all())
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("E,f32", [(40, True), (37, False), (256, False)])
+def test_backward_adds_up_a_number_that_comes_twice(tp, sigmoid, renorm, E, f32):
+    T, k = 9, 5
+    g = torch.Generator().manual_seed(E)
+    l, dw = torch.randn(T, E, generator=g).to(F32 if f32 else BF), torch.randn(T, k, generator=g)
+    e = torch.tensor([[3, 0, 3, -1, 3], [1, 1, 2, 2, E]] + [[0, E - 1, 5, E - 1, 7]] * (T - 2), dtype=torch.int32)
+    flat = torch.full((T * E + 1,), float("nan"), dtype=l.dtype, device="cuda")
+    d = flat[1:].view(T, E)  # rows that begin at any element
+    tp.tp_route_bwd(l.cuda(), e.cuda(), dw.cuda(), d, score=int(sigmoid), renorm=renorm)
+    want = gradient(l, e, dw, sigmoid, renorm, 1.0)
+    # at most a dozen terms below 2 |dw|, each within 64 roundings of 2^-24, and the result's own
+    slack = 12 * 2 * float(dw.abs().max()) * 64 * 2.0 ** -24
+    assert bool(((d.cpu().to(D) - want).abs() <= (2.0 ** -24 if f32 else 2.0 ** -8) * want.abs() + slack).all())
+    assert bool(torch.isnan(flat[0]))
