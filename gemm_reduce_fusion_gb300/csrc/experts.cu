@@ -6,9 +6,9 @@
 // The slots (t, j) of an expert become rows, in the order of t, in tiles of
 // `tile_rows` rows of one expert each (dispatch_kernel).  The products walk
 // the tiles in use (fp8_gemm.cuh, FP8_ROWS), or contract over an expert's
-// rows (FP8_CONTRACT); how many tiles there are stays on the device.  What
-// belongs to a row without a slot is zero in a training step, where such rows
-// are contracted over, and otherwise not written, and never read for a token.
+// rows (FP8_CONTRACT); how many tiles there are stays on the device.  Rows
+// without a slot are packed as zeros where they are contracted over, and are
+// otherwise neither written nor read for a token.
 //
 // The tokens' rows go to those of their slots as they are packed, GeLU and the
 // activation's packing of the first product's epilogue, and the weighted sum
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(256, 4) combine_kernel(const __grid_constant__
         for (int i = 0; i < 8; ++i) sum[i] = fmaf(w[j], f[i], sum[i]);
       }
     } else {
-float4 v[8][2];
+      float4 v[8][2];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float4* from = reinterpret_cast<const float4*>(P.rows32 + r[j] * P.N + c);

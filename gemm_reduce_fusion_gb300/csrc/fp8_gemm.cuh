@@ -489,26 +489,22 @@ __device__ __forceinline__ void drain_fp8(const Fp8GemmParams& P, const Fp8Place
     P.ze[w.o][w.eblock * P.ze_ld + (block >> 2) * 512 + fp8_e_at(static_cast<uint32_t>(w.erow) + lane, block & 3)] = static_cast<uint8_t>(e);
 }
 
-// fp32 results: COLS columns from `to` on, of which `cols` are there.
-template <int COLS, typename Released>
-__device__ __forceinline__ void drain_f32(float* to, int64_t pitch, int32_t cols, int32_t rows, const FromTmem& load, uint32_t stg,
-                                          uint32_t lane, Released released) {
+// fp32 sums of a tile that several runs share: COLS columns of [rows][128].
+template <int COLS>
+__device__ __forceinline__ void drain_sums(float* to, int32_t rows, const FromTmem& load, uint32_t stg, uint32_t lane) {
 #pragma unroll 1
   for (int j = 0; j < COLS / 32; ++j) {
     float v[32];
     load(j, v);
-    if (j == COLS / 32 - 1) released();
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const int32_t c = j * 32 + half * 16;
-      if (c >= cols) continue;
 #pragma unroll
       for (uint32_t i = 0; i < 4; ++i) {
         const int n = half * 16 + i * 4;
         st_shared_v4(stg_at(stg, lane, i), make_uint4(__float_as_uint(v[n]), __float_as_uint(v[n + 1]), __float_as_uint(v[n + 2]),
                                                       __float_as_uint(v[n + 3])));
       }
-      stg_out(stg, reinterpret_cast<uint8_t*>(to + c), pitch * 4, rows, min(cols - c, 16) * 4, lane);
+      stg_out(stg, reinterpret_cast<uint8_t*>(to + j * 32 + half * 16), 128 * 4, rows, 64, lane);
     }
   }
 }
@@ -1017,7 +1013,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CTAS, TURNED>::THREADS, 1) fp8_gemm_ker
           float* to = part_at(P, static_cast<int32_t>(blockIdx.x), u.q0 == 0) + tile_row * 128 + part * C::COLS;
           if (lane == 0) bulk_wait_read_all();  // of the tile before
           __syncwarp();
-          drain_f32<C::COLS>(to, 128, C::COLS, w.rows, acc, stg, lane, [] {});
+          drain_sums<C::COLS>(to, w.rows, acc, stg, lane);
         } else if constexpr (QUANT) {
           drain_fp8<C::COLS>(P, w, acc, stg, lane, red[CTAS == 1 ? quarter : 0], part, 2 + quarter, released);
         } else {

@@ -512,7 +512,8 @@ tp_status tp_route_bwd(const void* logits, const void* experts, const void* dwei
  * saved: NULL, or what the backward call reads: the slots of each expert as
  * rows in tiles of 128 (plan, tp_experts_plan_size bytes), the
  * pre-activations (preact, bf16 [tp_experts_rows, f]) and the experts'
- * outputs (out, bf16 [tp_experts_rows, h]).  A call runs the same products
+ * outputs (out, bf16 [tp_experts_rows, h]); rows without a slot are not
+ * written.  More than 2^23 - 128 rows are refused.  A call runs the same products
  * with and without it, on other tiles.                                      */
 typedef struct {
   void *plan, *preact, *out;
