@@ -37,10 +37,10 @@ from . import (TP_EPI_GELU, TP_NORM_LAYER, TP_NORM_NONE, TP_NORM_RMS, TP_OP_AG_M
                TP_OP_BLOCK_NORM_BWD, TP_OP_COL_BWD_CKPT, TP_OP_COL_FWD, TP_OP_COL_W4, TP_OP_ROW_AR, TP_OP_ROW_BWD_CKPT,
                TP_OP_ROW_RS, TP_OP_ROW_RS_BWD_CKPT, TP_OP_ROW_W4, TP_W4_MAX_M, ckpt_shapes, tp_ag_matmul,
                tp_ag_matmul_bwd_ckpt, tp_block_norm_bwd, tp_block_norm_fwd, tp_ckpt_pack, tp_col_linear_bwd_ckpt,
-               tp_col_linear_fwd, tp_col_linear_fwd_w4, tp_experts_fwd_fp8, tp_experts_workspace_size, tp_row_linear_bwd_ckpt, tp_row_linear_bwd_reducescatter_ckpt,
-               tp_row_linear_fwd_allreduce, tp_row_linear_fwd_reducescatter, tp_row_linear_fwd_w4, tp_w4_pack, tp_w4_unpack,
-               w4_shapes)
-from .autograd import (_bf16, _empty, _grad, _operands, _params, _shards, _workspace, column_parallel_linear, parallel_mlp_fp8, route,
+               tp_col_linear_fwd, tp_col_linear_fwd_w4, tp_experts_fwd_fp8, tp_experts_workspace_size, tp_route_fwd,
+               tp_row_linear_bwd_ckpt, tp_row_linear_bwd_reducescatter_ckpt, tp_row_linear_fwd_allreduce,
+               tp_row_linear_fwd_reducescatter, tp_row_linear_fwd_w4, tp_w4_pack, tp_w4_unpack, w4_shapes)
+from .autograd import (SCORES, _bf16, _empty, _grad, _operands, _params, _shards, _workspace, column_parallel_linear, parallel_mlp_fp8, route,
                        routed_experts)
 
 NORMS = {"none": TP_NORM_NONE, "rms": TP_NORM_RMS, "layer": TP_NORM_LAYER}
@@ -307,6 +307,8 @@ class RoutedMLPBlock(torch.nn.Module):
         E, h, f = w1.shape
         if tuple(router.shape) != (h, E) or tuple(w2.shape) != (E, f, h):
             raise ValueError(f"router [h, E], w1 [E, h, f], w2 [E, f, h]: got {tuple(router.shape)}, {tuple(w1.shape)}, {tuple(w2.shape)}")
+        if score not in SCORES:
+            raise ValueError(f"score is one of {sorted(SCORES)}, got {score!r}")
         self.p, self.k = p, k
         self.routing = dict(score=score, groups=groups, top_groups=top_groups, group_best=group_best, renorm=renorm, scale=scale)
         self.router = torch.nn.Parameter(router.contiguous())
@@ -334,7 +336,7 @@ class ServedRoutedMLPBlock:
     several rows serves multiples of them only."""
 
     def __init__(self, block: RoutedMLPBlock):
-        self.p, self.k, self.routing = block.p, block.k, dict(block.routing)
+        self.p, self.k, self.routing = block.p, block.k, {**block.routing, "score": SCORES[block.routing["score"]]}
         with torch.no_grad():
             copy = lambda v: v.detach().clone() if torch.is_tensor(v) else v  # noqa: E731
             self.how = {k: copy(v) for k, v in _boundary_of(block).items()}
@@ -350,7 +352,9 @@ class ServedRoutedMLPBlock:
         ws = _workspace(n.device, [(TP_OP_COL_FWD, 1, T, E, h)], tp_experts_workspace_size(p, E, T, self.k, h, f))
         logits, z = _empty((T, E), n), _empty((T, h), n)
         tp_col_linear_fwd(n, [self.router], [logits], ws)
-        weights, experts, _ = route(logits, self.k, bias=self.bias, **self.routing)
+        experts = torch.empty((T, self.k), dtype=torch.int32, device=n.device)
+        weights = torch.empty((T, self.k), dtype=torch.float32, device=n.device)
+        tp_route_fwd(logits, experts, weights, bias=self.bias, **self.routing)
         tp_experts_fwd_fp8(n, experts, weights, self.w1, self.w2, z, ws)
         out = _empty((T, h), n) if self.how["pre"] else None
         tp_block_norm_fwd([x], [z], [x], [out] if out is not None else None, **self.how)
