@@ -307,9 +307,13 @@ __device__ __forceinline__ bool choose(const RouteParams& P, int64_t row, uint32
 }
 
 // Whether a lane's group is among the best; score: the group's, `lanes` lanes
-// each.  near: the last that is and the first that is not are within `band`.
+// each.  near: the last that is and the first that is not are within what the
+// scores may be off by, which goes by `size`, the largest magnitude that a
+// group adds up (a sum near 1 of 64.5 and -63.5 has the roundings of those):
+// four values and two sums, of which band_of() covers two values and more
+// (sigmoid: 4 x 2.3 and 2 x 1 units, so 11.2 of twice 6).
 template <typename T>
-__device__ __forceinline__ bool among_best(const RouteParams& P, T score, int32_t group, int32_t lanes, float band, bool& near) {
+__device__ __forceinline__ bool among_best(const RouteParams& P, T score, float size, int32_t group, int32_t lanes, float band, bool& near) {
   int32_t rank = 0;
 #pragma unroll 1
   for (int32_t g = 0; g < P.groups; ++g) {
@@ -321,12 +325,20 @@ __device__ __forceinline__ bool among_best(const RouteParams& P, T score, int32_
     if (band > 0.f && P.tops < P.groups) {
       const bool real = group < P.groups;
       const float last = unordered(warp_max(real && rank == P.tops - 1 ? ordered(score) : 0u)),
-                  first = unordered(warp_max(real && rank == P.tops ? ordered(score) : 0u));
-      near = first > -INFINITY && last - first <= 2.f * band * fmaxf(1.f, fabsf(last));
+                  first = unordered(warp_max(real && rank == P.tops ? ordered(score) : 0u)),
+                  most = __uint_as_float(warp_max(real ? __float_as_uint(size) : 0u));
+      near = first > -INFINITY && last - first <= 2.f * band * fmaxf(1.f, most);
     }
   }
   return group < P.groups && rank < P.tops && open(score);
 }
+
+// The larger magnitude of what a group adds up: its largest value a and, where
+// there is one, b.
+__device__ __forceinline__ float size_of(const RouteParams& P, float a, float b) {
+  return fmaxf(open(a) ? fabsf(a) : 0.f, P.best == 2 && open(b) ? fabsf(b) : 0.f);
+}
+__device__ __forceinline__ float size_of(const RouteParams&, Df, Df) { return 0.f; }  // exact: never near
 
 // Closes the experts (v: -infinity) of groups that are not among the best;
 // false if that is within `band`.
@@ -348,13 +360,14 @@ __device__ __forceinline__ bool keep_groups(const RouteParams& P, T (&v)[PER], f
       a = larger(a, c);
     }
     const T score = P.best == 2 && open(b) ? add(a, b) : a;
-    if (!among_best<T>(P, score, static_cast<int32_t>(lane) / P.group_lanes, P.group_lanes, band, near)) {
+    if (!among_best<T>(P, score, size_of(P, a, b), static_cast<int32_t>(lane) / P.group_lanes, P.group_lanes, band, near)) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) v[i] = shut;
     }
     return !near;
   }
   T score = shut;  // of group `lane`
+  float size_here = 0.f;
   for (int32_t g = 0; g < P.groups; ++g) {
     T a = shut, b = shut;
 #pragma unroll
@@ -371,9 +384,12 @@ __device__ __forceinline__ bool keep_groups(const RouteParams& P, T (&v)[PER], f
       b = larger(smaller(a, c), larger(b, d));
       a = larger(a, c);
     }
-    if (static_cast<int32_t>(lane) == g) score = P.best == 2 && open(b) ? add(a, b) : a;
+    if (static_cast<int32_t>(lane) == g) {
+      score = P.best == 2 && open(b) ? add(a, b) : a;
+      size_here = size_of(P, a, b);
+    }
   }
-  const uint32_t kept = __ballot_sync(kAll, among_best<T>(P, score, static_cast<int32_t>(lane), 1, band, near));
+  const uint32_t kept = __ballot_sync(kAll, among_best<T>(P, score, size_here, static_cast<int32_t>(lane), 1, band, near));
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int32_t e = static_cast<int32_t>(lane) * PER + i;

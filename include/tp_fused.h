@@ -467,8 +467,9 @@ tp_status tp_row_linear_bwd_fp8(const tp_fp8* xt, const tp_fp8* w, const tp_fp8*
  *   weights[t, j] = scale * s of that expert, renorm: divided by the sum of
  *     the chosen s (by 2^-126 where that is less).
  * The choice is that of exact arithmetic on the given logits and biases
- * (values are told apart down to 2^-43, and with a bias a score below 2^-115
- * counts as 0), whatever E, T and the other rows are.
+ * (values are told apart down to 2^-43, with biases beyond 32 to 2^-48 of
+ * them or 2^-24 of the scores, whichever is less; and with a bias a score
+ * below 2^-115 counts as 0), whatever E, T and the other rows are.
  * An expert whose logit is -infinity or NaN is closed: s = 0, and it is not
  * chosen.  A slot without an open expert has experts = -1, weights = 0; a row
  * that is closed throughout has only those.  A logit of +infinity counts as

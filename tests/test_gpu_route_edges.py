@@ -1,0 +1,85 @@
+"""Routing where fp32 scores say nothing: large biases that cancel in a group's
+sum.  The choice is compared with decimal
+arithmetic of 120 digits."""
+import decimal
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+F32, D = torch.float32, torch.float64
+
+
+@pytest.fixture(scope="module")
+def tp():
+    import gemm_reduce_fusion_gb300 as tp
+    return tp
+
+
+def choose(l, bias, k, sigmoid, groups, tops, best):
+    """(experts, gap) of one row in decimals.  gap: the smallest difference that the choice turns on, in units of the larger
+    of 1 and what was added up (2^20 at most), or without a bias of the values (inf: none but exact ties)."""
+    with decimal.localcontext(decimal.Context(prec=120)):
+        one, dec = decimal.Decimal(1), [decimal.Decimal(float(x)) if x > -math.inf else None for x in l.tolist()]
+        top = max((x for x in dec if x is not None), default=None)
+        if sigmoid:
+            s = [None if x is None else one / (one + (-x).exp()) for x in dec]
+        else:
+            e = [None if x is None else (x - top).exp() for x in dec]
+            total = sum((x for x in e if x is not None), decimal.Decimal(0))
+            s = [None if x is None else x / total for x in e]
+        b = [decimal.Decimal(0)] * len(dec) if bias is None else [decimal.Decimal(float(x)) for x in bias.tolist()]
+        v = [None if x is None else x + y for x, y in zip(s, b)]
+        size = len(dec) // groups
+        gaps = []
+
+        def gap(x, y, parts):
+            if x != y:
+                gaps.append((x - y) / (x if bias is None else max(one, *(min(abs(t), decimal.Decimal(2 ** 20)) for t in parts))))
+        kept = set(range(groups))
+        if groups > 1:
+            sums = []
+            for g in range(groups):
+                mine = sorted((x for x in v[g * size:(g + 1) * size] if x is not None), reverse=True)[:best]
+                if mine:
+                    sums.append((-sum(mine), g, mine))
+            sums.sort(key=lambda t: t[:2])
+            if len(sums) > tops:
+                gap(-sums[tops - 1][0], -sums[tops][0], sums[tops - 1][2] + sums[tops][2])
+            kept = {g for _, g, _ in sums[:tops]}
+        order = sorted((e for e in range(len(dec)) if v[e] is not None and e // size in kept), key=lambda e: (-v[e], e))
+        if bias is not None:  # without one the logits tell them apart
+            for x, y in zip(order[:k], order[1:]):
+                gap(v[x], v[y], [v[x], v[y]])
+        return order[:k] + [-1] * (k - len(order)), float(min(gaps, default=decimal.Decimal("inf")))
+
+
+def check(tp, l, bias, k, sigmoid, groups, tops, best):
+    rows = [choose(r, bias, k, sigmoid, groups, tops, best) for r in l]
+    sure = torch.tensor([gap > 2.0 ** -40 for _, gap in rows])  # some times what is documented to be told apart
+    assert int(sure.sum()) >= 0.97 * len(rows)
+    want, l = torch.tensor([e for e, _ in rows], dtype=torch.int32)[sure], l[sure]
+    e, w = torch.empty((l.shape[0], k), dtype=torch.int32, device="cuda"), torch.empty((l.shape[0], k), device="cuda")
+    tp.tp_route_fwd(l.cuda(), e, w, bias=None if bias is None else bias.cuda(), score=int(sigmoid), groups=groups, top_groups=tops, group_best=best)
+    assert torch.equal(e.cpu(), want)
+
+
+def opposite(size, m, sigmoid, seed, T):
+    """Eight groups with biases of +m and -m (a third expert is closed) whose two scores add up to nearly the same."""
+    g = torch.Generator().manual_seed(seed)
+    l, bias = torch.full((T, 8, size), -math.inf, dtype=D), torch.zeros(8, size)
+    l[:, :, 0] = torch.rand(T, 8, generator=g, dtype=D) * 1.5 - 1
+    l[:, :, 1] = -l[:, :, 0] if sigmoid else torch.log(2.5 - l[:, :, 0].exp())
+    l[:, :, 1] += torch.randn(T, 8, generator=g, dtype=D) * (2e-6 if sigmoid else 1e-5)
+    bias[:, 0], bias[:, 1] = m, -m
+    bias[::2, :2] = bias[::2, :2].flip(1)
+    return l.view(T, -1).to(F32), bias.view(-1)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("size", [2, 3])  # groups that end between lanes, and groups that do not
+@pytest.mark.parametrize("m", [16.0, 64.0])
+def test_sums_of_large_biases(tp, m, size, sigmoid):
+    """Each value carries the rounding of a number of m, their sum is near 1: fp32 would take the wrong group."""
+    check(tp, *opposite(size, m, sigmoid, 5, 2500), 4, sigmoid, 8, 4, 2)
