@@ -310,8 +310,8 @@ __device__ __forceinline__ bool choose(const RouteParams& P, int64_t row, uint32
 // each.  near: the last that is and the first that is not are within what the
 // scores may be off by, which goes by `size`, the largest magnitude that a
 // group adds up (a sum near 1 of 64.5 and -63.5 has the roundings of those):
-// four values and two sums, of which band_of() covers two values and more
-// (sigmoid: 4 x 2.3 and 2 x 1 units, so 11.2 of twice 6).
+// for halves of sums (score_of) half of four values' and two sums' roundings,
+// which band_of() covers (sigmoid: 4 x 2.3 and 2 x 1 units, half of 11.2).
 template <typename T>
 __device__ __forceinline__ bool among_best(const RouteParams& P, T score, float size, int32_t group, int32_t lanes, float band, bool& near) {
   int32_t rank = 0;
@@ -327,7 +327,7 @@ __device__ __forceinline__ bool among_best(const RouteParams& P, T score, float 
       const float last = unordered(warp_max(real && rank == P.tops - 1 ? ordered(score) : 0u)),
                   first = unordered(warp_max(real && rank == P.tops ? ordered(score) : 0u)),
                   most = __uint_as_float(warp_max(real ? __float_as_uint(size) : 0u));
-      near = first > -INFINITY && last - first <= 2.f * band * fmaxf(1.f, most);
+      near = first > -INFINITY && last - first <= band * fmaxf(1.f, most);
     }
   }
   return group < P.groups && rank < P.tops && open(score);
@@ -339,6 +339,17 @@ __device__ __forceinline__ float size_of(const RouteParams& P, float a, float b)
   return fmaxf(open(a) ? fabsf(a) : 0.f, P.best == 2 && open(b) ? fabsf(b) : 0.f);
 }
 __device__ __forceinline__ float size_of(const RouteParams&, Df, Df) { return 0.f; }  // exact: never near
+
+// What a group is ranked by, with sums as their halves: two values of the type's
+// lowest do not overflow, and halves are exact (but for values below 2^-125,
+// which fp32 does not decide).
+__device__ __forceinline__ float half_of(float v) { return 0.5f * v; }
+__device__ __forceinline__ Df half_of(Df v) { return {0.5f * v.hi, 0.5f * v.lo}; }
+template <typename T>
+__device__ __forceinline__ T score_of(const RouteParams& P, T a, T b) {
+  if (P.best == 1) return a;
+  return open(b) ? add(half_of(a), half_of(b)) : half_of(a);
+}
 
 // Closes the experts (v: -infinity) of groups that are not among the best;
 // false if that is within `band`.
@@ -359,7 +370,7 @@ __device__ __forceinline__ bool keep_groups(const RouteParams& P, T (&v)[PER], f
       b = larger(smaller(a, c), larger(b, d));
       a = larger(a, c);
     }
-    const T score = P.best == 2 && open(b) ? add(a, b) : a;
+    const T score = score_of(P, a, b);
     if (!among_best<T>(P, score, size_of(P, a, b), static_cast<int32_t>(lane) / P.group_lanes, P.group_lanes, band, near)) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) v[i] = shut;
@@ -385,7 +396,7 @@ __device__ __forceinline__ bool keep_groups(const RouteParams& P, T (&v)[PER], f
       a = larger(a, c);
     }
     if (static_cast<int32_t>(lane) == g) {
-      score = P.best == 2 && open(b) ? add(a, b) : a;
+      score = score_of(P, a, b);
       size_here = size_of(P, a, b);
     }
   }

@@ -1,5 +1,5 @@
 """Routing where fp32 scores say nothing: large biases that cancel in a group's
-sum.  The choice is compared with decimal
+sum, biases of the type's lowest value.  The choice is compared with decimal
 arithmetic of 120 digits."""
 import decimal
 import math
@@ -9,6 +9,7 @@ import torch
 
 pytestmark = pytest.mark.gpu
 F32, D = torch.float32, torch.float64
+LOWEST = float(torch.finfo(F32).min)
 
 
 @pytest.fixture(scope="module")
@@ -83,3 +84,16 @@ def opposite(size, m, sigmoid, seed, T):
 def test_sums_of_large_biases(tp, m, size, sigmoid):
     """Each value carries the rounding of a number of m, their sum is near 1: fp32 would take the wrong group."""
     check(tp, *opposite(size, m, sigmoid, 5, 2500), 4, sigmoid, 8, 4, 2)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("size", [2, 3])
+@pytest.mark.parametrize("best", [1, 2])
+@pytest.mark.parametrize("some", [False, True])
+def test_biases_of_the_lowest_value(tp, some, best, size, sigmoid):
+    """Experts put last by the lowest bias that there is: still open, and two of them do not add up to -infinity."""
+    g = torch.Generator().manual_seed(6)
+    l, bias = torch.randn(40, 4, size, generator=g), torch.full((4, size), LOWEST)
+    if some:
+        bias[2] = 0.25
+    check(tp, l.view(40, -1), bias.view(-1), 2 * size, sigmoid, 4, 2, best)
