@@ -28,6 +28,7 @@
 #include <cfloat>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "host_util.h"
 #include "vec_util.cuh"
@@ -306,6 +307,36 @@ __device__ __forceinline__ bool choose(const RouteParams& P, int64_t row, uint32
   return clear;
 }
 
+// Without a bias, the sum of the scores of a and b (-infinity: none) as
+// e^m r, 1/2 <= r <= 2, which holds scores of any size.  Softmax, but for what
+// all groups have in common: e^a (1 + e^(b - a)).  Sigmoid: of x it is
+// e^min(x, 0) / (1 + e^-|x|).
+struct LogSum {
+  float m;
+  Df r;
+};
+__device__ __forceinline__ bool open(const LogSum& v) { return v.m > -INFINITY; }
+__device__ __forceinline__ LogSum shfl(const LogSum& v, int lane) { return {__shfl_sync(kAll, v.m, lane), shfl(v.r, lane)}; }
+__device__ __forceinline__ Df exp_of_difference(float x, float y) {  // e^(x - y), x <= y
+  return exp_df(x - y < -100.f ? Df{-100.f, 0.f} : two_sum(x, -y));
+}
+__device__ __forceinline__ bool greater(const LogSum& x, const LogSum& y) {
+  if (!open(x) || !open(y)) return open(x) && !open(y);
+  if (x.m >= y.m) return greater(x.r, mul(exp_of_difference(y.m, x.m), y.r));
+  return greater(mul(exp_of_difference(x.m, y.m), x.r), y.r);
+}
+__device__ __noinline__ LogSum log_sum(bool sigmoid, float a, float b) {
+  LogSum v = {sigmoid ? fminf(a, 0.f) : a, {1.f, 0.f}};
+  if (!open(v)) return v;
+  if (sigmoid) v.r = inverse(add(Df{1.f, 0.f}, exp_df(Df{-fminf(fabsf(a), 100.f), 0.f})));
+  if (b > -INFINITY) {
+    Df w = exp_of_difference(sigmoid ? fminf(b, 0.f) : b, v.m);
+    if (sigmoid) w = mul(w, inverse(add(Df{1.f, 0.f}, exp_df(Df{-fminf(fabsf(b), 100.f), 0.f}))));
+    v.r = add(v.r, w);
+  }
+  return v;
+}
+
 // Whether a lane's group is among the best; score: the group's, `lanes` lanes
 // each.  near: the last that is and the first that is not are within what the
 // scores may be off by, which goes by `size`, the largest magnitude that a
@@ -321,7 +352,7 @@ __device__ __forceinline__ bool among_best(const RouteParams& P, T score, float 
     if (greater(other, score) || (!greater(score, other) && g < group)) ++rank;
   }
   near = false;
-  if constexpr (sizeof(T) == 4) {
+  if constexpr (std::is_same_v<T, float>) {
     if (band > 0.f && P.tops < P.groups) {
       const bool real = group < P.groups;
       const float last = unordered(warp_max(real && rank == P.tops - 1 ? ordered(score) : 0u)),
@@ -345,15 +376,16 @@ __device__ __forceinline__ float size_of(const RouteParams&, Df, Df) { return 0.
 // which fp32 does not decide).
 __device__ __forceinline__ float half_of(float v) { return 0.5f * v; }
 __device__ __forceinline__ Df half_of(Df v) { return {0.5f * v.hi, 0.5f * v.lo}; }
-template <typename T>
-__device__ __forceinline__ T score_of(const RouteParams& P, T a, T b) {
-  if (P.best == 1) return a;
-  return open(b) ? add(half_of(a), half_of(b)) : half_of(a);
+template <typename S, typename T>
+__device__ __forceinline__ S score_of(const RouteParams& P, T a, T b) {
+  if constexpr (std::is_same_v<S, LogSum>) return log_sum(P.sigmoid, a, b);
+  else return P.best == 1 ? a : open(b) ? add(half_of(a), half_of(b)) : half_of(a);
 }
 
 // Closes the experts (v: -infinity) of groups that are not among the best;
-// false if that is within `band`.
-template <typename T, int PER>
+// false if that is within `band`.  S: what the groups are ranked by (LogSum: v
+// are logits).
+template <typename S, typename T, int PER>
 __device__ __forceinline__ bool keep_groups(const RouteParams& P, T (&v)[PER], float band, uint32_t lane) {
   const T shut = of<T>(-INFINITY);
   const int32_t size = P.E / P.groups;
@@ -370,14 +402,14 @@ __device__ __forceinline__ bool keep_groups(const RouteParams& P, T (&v)[PER], f
       b = larger(smaller(a, c), larger(b, d));
       a = larger(a, c);
     }
-    const T score = score_of(P, a, b);
-    if (!among_best<T>(P, score, size_of(P, a, b), static_cast<int32_t>(lane) / P.group_lanes, P.group_lanes, band, near)) {
+    const S score = score_of<S>(P, a, b);
+    if (!among_best<S>(P, score, size_of(P, a, b), static_cast<int32_t>(lane) / P.group_lanes, P.group_lanes, band, near)) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) v[i] = shut;
     }
     return !near;
   }
-  T score = shut;  // of group `lane`
+  S score = {};  // of group `lane`
   float size_here = 0.f;
   for (int32_t g = 0; g < P.groups; ++g) {
     T a = shut, b = shut;
@@ -396,11 +428,11 @@ __device__ __forceinline__ bool keep_groups(const RouteParams& P, T (&v)[PER], f
       a = larger(a, c);
     }
     if (static_cast<int32_t>(lane) == g) {
-      score = score_of(P, a, b);
+      score = score_of<S>(P, a, b);
       size_here = size_of(P, a, b);
     }
   }
-  const uint32_t kept = __ballot_sync(kAll, among_best<T>(P, score, size_here, static_cast<int32_t>(lane), 1, band, near));
+  const uint32_t kept = __ballot_sync(kAll, among_best<S>(P, score, size_here, static_cast<int32_t>(lane), 1, band, near));
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int32_t e = static_cast<int32_t>(lane) * PER + i;
@@ -425,12 +457,9 @@ __device__ __forceinline__ Df sigmoid_df(float l) {
   return l >= 0.f ? u : mul(t, u);
 }
 
-// The choice by scores as pairs, for rows that need it.
+// The values of the choice as pairs; -infinity where it cannot go.
 template <int PER>
-__device__ __noinline__ uint32_t choose_exactly(const RouteParams& P, int64_t row, uint32_t lane) {
-  float l[PER];
-  Df v[PER];
-  load_row<PER>(P, row, lane, l);
+__device__ __forceinline__ void exact_values(const RouteParams& P, const float (&l)[PER], uint32_t lane, Df (&v)[PER]) {
   if (P.sigmoid) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) v[i] = sigmoid_df(l[i]);
@@ -452,14 +481,25 @@ __device__ __noinline__ uint32_t choose_exactly(const RouteParams& P, int64_t ro
     for (int i = 0; i < PER; ++i) v[i] = mul(v[i], r);
   }
   values<Df, PER>(P, l, v, lane, v);
-  if (P.groups > 1) keep_groups<Df, PER>(P, v, 0.f, lane);
-  // without a bias what is left is told apart by its logits
+  if (P.groups > 1) keep_groups<Df, Df, PER>(P, v, 0.f, lane);
+}
+
+// The choice by scores as pairs, for rows that need it.
+template <int PER>
+__device__ __noinline__ uint32_t choose_exactly(const RouteParams& P, int64_t row, uint32_t lane) {
+  float l[PER];
+  load_row<PER>(P, row, lane, l);
+  Df v[PER];
+  if (P.bias) {
+    exact_values<PER>(P, l, lane, v);
+  } else {  // groups by sums of two; what is left is told apart by its logits
+    keep_groups<LogSum, float, PER>(P, l, 0.f, lane);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) v[i] = Df{l[i], 0.f};
+  }
   uint64_t key[PER];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const Df x = P.bias ? v[i] : Df{l[i], 0.f};
-    key[i] = open(v[i]) ? static_cast<uint64_t>(ordered(x.hi)) << 32 | ordered(x.lo + 0.f) : 0u;
-  }
+  for (int i = 0; i < PER; ++i) key[i] = open(v[i]) ? static_cast<uint64_t>(ordered(v[i].hi)) << 32 | ordered(v[i].lo + 0.f) : 0u;
   uint32_t mine = kNone;
   for (int32_t j = 0; j < P.k; ++j) {
     uint64_t best = 0;
@@ -496,7 +536,7 @@ __device__ __noinline__ uint32_t choose_among_few(const RouteParams& P, int64_t 
   load_row<PER>(P, row, lane, l);
   scores<PER>(P, l, s);
   values<float, PER>(P, l, s, lane, v);
-  if (P.groups > 1) keep_groups<float, PER>(P, v, 0.f, lane);
+  if (P.groups > 1) keep_groups<float, float, PER>(P, v, 0.f, lane);
   uint32_t n = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
@@ -541,7 +581,7 @@ __device__ __forceinline__ uint32_t select(const RouteParams& P, int64_t row, Fe
   uint32_t key[PER], mine;
   float lowest = 0.f;
   if (by_logit) {
-    if (P.groups > 1) keep_groups<float, PER>(P, l, 0.f, lane);
+    if (P.groups > 1) keep_groups<float, float, PER>(P, l, 0.f, lane);
 #pragma unroll
     for (int i = 0; i < PER; ++i) key[i] = ordered(l[i]);
     choose<PER>(P, row, key, 0.f, lane, mine, lowest);
@@ -550,7 +590,7 @@ __device__ __forceinline__ uint32_t select(const RouteParams& P, int64_t row, Fe
   const float band = band_of(PER, P.sigmoid);
   float v[PER];
   values<float, PER>(P, l, s, lane, v);
-  const bool clear = P.groups == 1 || keep_groups<float, PER>(P, v, band, lane);
+  const bool clear = P.groups == 1 || keep_groups<float, float, PER>(P, v, band, lane);
 #pragma unroll
   for (int i = 0; i < PER; ++i) key[i] = open(v[i]) ? ordered(P.bias ? v[i] : l[i]) : 0u;
   if (clear) {

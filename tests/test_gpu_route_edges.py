@@ -1,5 +1,5 @@
 """Routing where fp32 scores say nothing: large biases that cancel in a group's
-sum, biases of the type's lowest value.  The choice is compared with decimal
+sum, biases of the type's lowest value, scores far below one.  The choice is compared with decimal
 arithmetic of 120 digits."""
 import decimal
 import math
@@ -97,3 +97,15 @@ def test_biases_of_the_lowest_value(tp, some, best, size, sigmoid):
     if some:
         bias[2] = 0.25
     check(tp, l.view(40, -1), bias.view(-1), 2 * size, sigmoid, 4, 2, best)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("size", [4, 5])
+@pytest.mark.parametrize("low", [60.0, 90.0, 150.0, 2000.0])
+def test_sums_of_scores_far_below_one(tp, low, size, sigmoid):
+    """Without a bias, groups of scores below what fp32 holds are told apart."""
+    g = torch.Generator().manual_seed(7)
+    l = torch.randn(200, 8, size, generator=g) * 3 - low
+    l[:100, 5, 1] = 1.0  # one group far above, or all of them down there
+    l[::7, 3, 1:] = -math.inf  # a sum of one
+    check(tp, l.view(200, -1), None, 6, sigmoid, 8, 3, 2)
