@@ -635,7 +635,12 @@ __global__ void __launch_bounds__(kWarps * 32) route_fwd_kernel(const __grid_con
     float sc = 0.f;
     if (mine != kNone) {
       const float l = logit(P, row, mine);
-      sc = P.sigmoid ? inverse(1.f + expf(-l)) : expf(l - norm.top) * norm.r;
+      if (P.sigmoid) {  // below 2^-126 too: their shares of a sum need not be small
+        const float t = expf(-fabsf(l)), u = inverse(1.f + t);
+        sc = l >= 0.f ? u : t * u;
+      } else {
+        sc = expf(l - norm.top) * norm.r;
+      }
     }
     const float total = P.renorm ? fmaxf(warp_sum(sc), FLT_MIN) : 1.f;
     if (static_cast<int32_t>(lane) < P.k) {

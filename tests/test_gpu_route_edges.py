@@ -7,6 +7,8 @@ import math
 import pytest
 import torch
 
+from test_gpu_route import route
+
 pytestmark = pytest.mark.gpu
 F32, D = torch.float32, torch.float64
 LOWEST = float(torch.finfo(F32).min)
@@ -109,3 +111,16 @@ def test_sums_of_scores_far_below_one(tp, low, size, sigmoid):
     l[:100, 5, 1] = 1.0  # one group far above, or all of them down there
     l[::7, 3, 1:] = -math.inf  # a sum of one
     check(tp, l.view(200, -1), None, 6, sigmoid, 8, 3, 2)
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+def test_sigmoid_weights_below_the_normal_range(tp, renorm):
+    T, E, k = 64, 8, 4
+    l = -86 - 17 * torch.rand(T, E, generator=torch.Generator().manual_seed(8))
+    experts, want, _ = route(l, k, None, True, 1, 1, 1, renorm, 1.0)
+    e, w = torch.empty((T, k), dtype=torch.int32, device="cuda"), torch.empty((T, k), device="cuda")
+    tp.tp_route_fwd(l.cuda(), e, w, score=tp.TP_ROUTE_SIGMOID, renorm=renorm)
+    assert torch.equal(e.cpu(), experts)
+    # 64 roundings, and where numbers are that small steps of 2^-149 (of each of k scores, over a sum of 2^-126 or more)
+    step = 2.0 ** -149 * (2 * k / 2.0 ** -126 if renorm else 2)
+    assert bool(((w.cpu().to(D) - want).abs() <= 64 * 2.0 ** -24 * want + step).all())
