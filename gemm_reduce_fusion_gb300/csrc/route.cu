@@ -697,6 +697,43 @@ __device__ __forceinline__ float through_sum(const RouteParams& P, float g, floa
   return (sum < FLT_MIN ? g : rest) * __fdiv_rn(slope, total);
 }
 
+// A number that comes more than once: its first choice gets the sum of their
+// gradients, the others none.
+__device__ __forceinline__ void add_repeated(const RouteParams& P, uint32_t lane, float& g, uint32_t& mine) {
+  const uint32_t same = __match_any_sync(kAll, mine);
+  if (!__any_sync(kAll, mine != kNone && (same & (same - 1)) != 0)) return;
+  float sum = 0.f;
+  for (int32_t j = 0; j < P.k; ++j) {
+    const float v = __shfl_sync(kAll, g, j);
+    if (same >> j & 1) sum += v;
+  }
+  const bool first = mine != kNone && static_cast<int32_t>(lane) == __ffs(same) - 1;
+  g = first ? sum : 0.f;
+  mine = first ? mine : kNone;
+}
+
+// Softmax: the gradient of a chosen logit, s (g - sum_j s_j g_j).  As the scores
+// add up to 1 the bracket is g times the others' scores and
+// sum_j s_j (g - g_j), which keeps its digits where one score is nearly 1.
+// Numbers are there once; in: the lane's experts among them, dot: sum_j s_j g_j.
+template <int PER>
+__device__ __forceinline__ float through_softmax(const RouteParams& P, const float (&s)[PER], float g, uint32_t mine, uint32_t lane,
+                                                 uint32_t& in, float& dot) {
+  in = 0;
+  for (int32_t j = 0; j < P.k; ++j) {
+    const uint32_t e = __shfl_sync(kAll, mine, j);
+    if (e / PER == lane) in |= 1u << e % PER;
+  }
+  float others = 0.f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) others += in >> i & 1 ? 0.f : s[i];
+  const float sc = pick<PER>(s, mine);
+  float rest = g * warp_sum(others);
+  dot = warp_sum(sc * g);
+  for (int32_t j = 0; j < P.k; ++j) rest = fmaf(__shfl_sync(kAll, sc, j), g - __shfl_sync(kAll, g, j), rest);
+  return sc * rest;
+}
+
 // Sigmoid: only the chosen logits have a gradient, s (1 - s) without the
 // difference, and only they are read; the row is zeros but for them.  (By whole
 // rows, as for the softmax, 8192 x 256 took 7.1 us, so 4.5.)
@@ -723,18 +760,9 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_sigmoid_kernel(const __
     const bool open = x > -INFINITY;  // and not NaN
     const float sc = open ? (x >= 0.f ? u : t * u) : 0.f, slope = open ? t * u * u : 0.f;
     g = P.renorm ? through_sum(P, g, sc, slope) : g * slope;
-    // a number that comes more than once: its first slot has the sum
-    const uint32_t same = __match_any_sync(kAll, mine);
-    if (__any_sync(kAll, mine != kNone && (same & (same - 1)) != 0)) {
-      float sum = 0.f;
-      for (int32_t j = 0; j < P.k; ++j) {
-        const float v = __shfl_sync(kAll, g, j);
-        if (same >> j & 1) sum += v;
-      }
-      g = sum;
-    }
+    add_repeated(P, lane, g, mine);
     __syncwarp();  // the zeros come first
-    if (mine != kNone && static_cast<int32_t>(lane) == __ffs(same) - 1) {
+    if (mine != kNone) {
       if (P.f32) static_cast<float*>(P.dlogits)[at + mine] = g;
       else static_cast<__nv_bfloat16*>(P.dlogits)[at + mine] = __float2bfloat16_rn(g);
     }
@@ -753,11 +781,15 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const __grid_con
     uint32_t mine;
     float g = chosen(P, row, lane, mine);
     scores<PER>(P, l, s);
+    uint32_t in = 0;  // the lane's experts that are chosen
+    float dot = 0.f;
     if (P.renorm) {
       const float sc = pick<PER>(s, mine);
       g = through_sum(P, g, sc, sc);
+    } else {
+      add_repeated(P, lane, g, mine);
+      g = through_softmax<PER>(P, s, g, mine, lane, in, dot);
     }
-    // the gradient of each expert's score (renorm: logit)
     float d[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) d[i] = 0.f;
@@ -771,12 +803,9 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const __grid_con
       }
     }
     if (!P.renorm) {
-      float dot = 0.f;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) dot += d[i] * s[i];
-      dot = warp_sum(dot);
-#pragma unroll
-      for (int i = 0; i < PER; ++i) d[i] = s[i] * (d[i] - dot);
+      for (int i = 0; i < PER; ++i)
+        if (!(in >> i & 1)) d[i] = -s[i] * dot;
     }
     const int32_t e0 = static_cast<int32_t>(lane) * PER;
     const int64_t at = row * P.E + e0;

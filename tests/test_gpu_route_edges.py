@@ -1,5 +1,6 @@
 """Routing where fp32 scores say nothing: large biases that cancel in a group's
-sum, biases of the type's lowest value, scores far below one.  The choice is compared with decimal
+sum, biases of the type's lowest value, scores far below one, choices that
+leave next to nothing for the others.  The choice is compared with decimal
 arithmetic of 120 digits."""
 import decimal
 import math
@@ -7,10 +8,10 @@ import math
 import pytest
 import torch
 
-from test_gpu_route import route
+from test_gpu_route import gradient, route
 
 pytestmark = pytest.mark.gpu
-F32, D = torch.float32, torch.float64
+BF, F32, D = torch.bfloat16, torch.float32, torch.float64
 LOWEST = float(torch.finfo(F32).min)
 
 
@@ -124,3 +125,28 @@ def test_sigmoid_weights_below_the_normal_range(tp, renorm):
     # 64 roundings, and where numbers are that small steps of 2^-149 (of each of k scores, over a sum of 2^-126 or more)
     step = 2.0 ** -149 * (2 * k / 2.0 ** -126 if renorm else 2)
     assert bool(((w.cpu().to(D) - want).abs() <= 64 * 2.0 ** -24 * want + step).all())
+
+
+@pytest.mark.parametrize("E,k,f32", [(64, 1, True), (64, 1, False), (60, 3, True), (200, 8, True), (512, 32, True)])
+def test_softmax_gradient_of_a_score_near_one(tp, E, k, f32):
+    """The largest score is 1 but for what its logit leads by: its gradient keeps its digits."""
+    lead = torch.tensor([8.0, 10.0, 12.0, 14.0, 17.0, 20.0]).repeat_interleave(16)
+    T = lead.numel()
+    g = torch.Generator().manual_seed(E + k)
+    l, dw = torch.randn(T, E, generator=g), torch.randn(T, k, generator=g)
+    l[torch.arange(T), torch.randint(0, E, (T,), generator=g)] = l.amax(1) + lead
+    l = l.to(F32 if f32 else BF)
+    e, w, d = (torch.empty((T, k), dtype=torch.int32, device="cuda"), torch.empty((T, k), device="cuda"),
+               torch.full((T, E), float("nan"), dtype=l.dtype, device="cuda"))
+    tp.tp_route_fwd(l.cuda(), e, w, scale=1.5)
+    tp.tp_route_bwd(l.cuda(), e, dw.cuda(), d, scale=1.5)
+    want = gradient(l, e.cpu(), dw, False, False, 1.5)
+    s, v, at = torch.softmax(l.to(D), 1), 1.5 * dw.to(D), e.cpu().long()
+    sc = s.gather(1, at)
+    rest = s.clone().scatter_(1, at, 0.0).sum(1, keepdim=True)
+    # s_i (v_i rest + sum_j s_j (v_i - v_j)) of the chosen, -s_i sum_j s_j v_j of the others.  A score is within 64 roundings
+    # of 2^-24: up to 23 in its exponent's difference (of at most 26: half a step is 2^-20), exp, the sum, a division and a product.
+    terms = s * (sc * v.abs()).sum(1, keepdim=True)
+    terms.scatter_(1, at, sc * (v.abs() * rest + (sc[:, None, :] * (v[:, :, None] - v[:, None, :]).abs()).sum(2)))
+    slack = 160 * 2.0 ** -24 * terms + 2.0 ** -50 * v.abs().sum(1, keepdim=True)  # (the second: the definition's own in 64 bits)
+    assert bool(((d.cpu().to(D) - want).abs() <= (2.0 ** -24 if f32 else 2.0 ** -8) * want.abs() + slack).all())
