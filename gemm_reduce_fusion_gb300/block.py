@@ -288,6 +288,11 @@ class W4MLPBlock:
         return x, out
 
 
+def _whole_eights(router: torch.Tensor) -> torch.Tensor:
+    """A router [h, E] with columns of zeros up to a multiple of 8, as the column layer takes them."""
+    return torch.nn.functional.pad(router, (0, -router.shape[1] % 8)) if router.shape[1] % 8 else router
+
+
 class RoutedMLPBlock(torch.nn.Module):
     """A trained block with experts in the MLP's place: ``y, n = block(x, n)``.
 
@@ -318,8 +323,8 @@ class RoutedMLPBlock(torch.nn.Module):
         _boundary_params(self, h, w1.device, post, pre, gate, alpha, eps)
 
     def forward(self, x, n):
-        logits, = column_parallel_linear(n, [self.router])
-        weights, experts, self.counts = route(logits, self.k, bias=self.bias, **self.routing)
+        logits, = column_parallel_linear(n, [_whole_eights(self.router)])
+        weights, experts, self.counts = route(logits[:, :self.router.shape[1]], self.k, bias=self.bias, **self.routing)
         z = routed_experts(n, experts, weights, list(self.w1), list(self.w2))
         ys, ns = block_boundary([x], [z], **_boundary_of(self))
         return ys[0], (ns[0] if ns else None)
@@ -340,7 +345,7 @@ class ServedRoutedMLPBlock:
         with torch.no_grad():
             copy = lambda v: v.detach().clone() if torch.is_tensor(v) else v  # noqa: E731
             self.how = {k: copy(v) for k, v in _boundary_of(block).items()}
-            self.router, self.bias = copy(block.router), copy(block.bias)
+            self.router, self.bias = copy(_whole_eights(block.router)), copy(block.bias)
             _, self.w1 = _operands([w.detach() for w in block.w1], False, True, tiles=True)
             _, self.w2 = _operands([w.detach() for w in block.w2], False, True, tiles=True)
         self.how.update(post=_kind(self.how["post"]), pre=_kind(self.how["pre"]))
@@ -348,10 +353,11 @@ class ServedRoutedMLPBlock:
     @torch.no_grad()
     def __call__(self, x: torch.Tensor, n: torch.Tensor) -> tuple:
         p, (T, h), (per, f) = self.p, n.shape, self.w1[0].q.shape[:2]
-        E = p * per
-        ws = _workspace(n.device, [(TP_OP_COL_FWD, 1, T, E, h)], tp_experts_workspace_size(p, E, T, self.k, h, f))
-        logits, z = _empty((T, E), n), _empty((T, h), n)
+        E, wide = p * per, self.router.shape[1]
+        ws = _workspace(n.device, [(TP_OP_COL_FWD, 1, T, wide, h)], tp_experts_workspace_size(p, E, T, self.k, h, f))
+        logits, z = _empty((T, wide), n), _empty((T, h), n)
         tp_col_linear_fwd(n, [self.router], [logits], ws)
+        logits = logits[:, :E].contiguous()
         experts = torch.empty((T, self.k), dtype=torch.int32, device=n.device)
         weights = torch.empty((T, self.k), dtype=torch.float32, device=n.device)
         tp_route_fwd(logits, experts, weights, bias=self.bias, **self.routing)

@@ -1,0 +1,49 @@
+"""The routed block with any number of experts."""
+import pytest
+import torch
+
+from test_gpu_routed_block import BF, D, GRAD, OUT, ROUTING, blk, gen, leaf, norm, off, reference, rnd  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("routing", [ROUTING[0], dict(score="sigmoid", renorm=True, scale=2.5)])
+@pytest.mark.parametrize("p,E,T,k,h,f", [(4, 60, 300, 4, 264, 136), (2, 4, 33, 2, 136, 264), (1, 1, 5, 1, 64, 128), (3, 9, 1, 3, 64, 72)])
+def test_any_number_of_experts(blk, p, E, T, k, h, f, routing):  # noqa: F811
+    """Numbers of experts that are not multiples of 8: trained, served, captured."""
+    from gemm_reduce_fusion_gb300.autograd import column_parallel_linear, route
+    g = gen(E + T)
+    router, w1, w2 = rnd(g, h, E, scale=h ** -0.5), rnd(g, E, h, f, scale=h ** -0.5), rnd(g, E, f, h, scale=f ** -0.5)
+    b = blk.RoutedMLPBlock(router, w1, w2, p, k, alpha=0.5, **routing)
+    b.bias.copy_(0.05 * torch.randn(E, generator=g, device="cuda"))
+    x0, n0, dy, dn = (rnd(g, T, h) for _ in range(4))
+    x, n = x0.clone().requires_grad_(), n0.clone().requires_grad_()
+    y, m = b(x, n)
+    torch.autograd.backward([y, m], [dy, dn])
+    assert b.router.grad.shape == (h, E)
+    # the logits of a router with columns of zeros behind its own are those of its own
+    wide = torch.zeros((h, E + 7), dtype=BF, device="cuda")[:, :(E + 7) // 8 * 8].contiguous()
+    wide[:, :E] = router
+    _, experts, counts = route(column_parallel_linear(n0, [wide])[0][:, :E], k, bias=b.bias, **routing)
+    assert torch.equal(counts, b.counts) and int(counts.sum()) == T * k
+    xr, nr, rr, r1, r2 = leaf(x0), leaf(n0), leaf(router), leaf(w1), leaf(w2)
+    yr = xr + 0.5 * norm(reference(nr, rr, r1, r2, experts.long(), routing), 1.0)
+    mr = norm(yr, 1.0)
+    torch.autograd.backward([yr, mr], [dy.to(D), dn.to(D)])
+    assert off(y, yr) < OUT and off(m, mr) < OUT
+    assert off(x.grad, xr.grad) < GRAD and off(n.grad, nr.grad) < GRAD
+    assert off(torch.cat([t.grad for t in b.w1]), r1.grad) < GRAD
+    assert off(torch.cat([t.grad for t in b.w2]), r2.grad) < GRAD
+    if T > 30:
+        assert off(b.router.grad, rr.grad) < GRAD
+    served, xs = b.serve(), x0.clone()
+    ys, ms = served(xs, n0)
+    assert off(ys, y.detach().to(D)) < 2.0 ** -7 and off(ms, m.detach().to(D)) < 2.0 ** -7
+    graph, out = torch.cuda.CUDAGraph(), x0.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        yc, mc = served(out, n0)
+    out.copy_(x0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(yc, ys) and torch.equal(mc, ms)
