@@ -312,6 +312,9 @@ class RoutedMLPBlock(torch.nn.Module):
         E, h, f = w1.shape
         if tuple(router.shape) != (h, E) or tuple(w2.shape) != (E, f, h):
             raise ValueError(f"router [h, E], w1 [E, h, f], w2 [E, f, h]: got {tuple(router.shape)}, {tuple(w1.shape)}, {tuple(w2.shape)}")
+        for name, t in (("router", router), ("w1", w1), ("w2", w2)):
+            if t.dtype != torch.bfloat16:
+                raise TypeError(f"{name}: expected bfloat16, got {t.dtype}")
         if score not in SCORES:
             raise ValueError(f"score is one of {sorted(SCORES)}, got {score!r}")
         self.p, self.k = p, k
