@@ -284,7 +284,7 @@ struct Fp8Block {
 __device__ __forceinline__ Fp8Block fp8_block(const Fp8GemmParams& P, const Fp8Unit& u, int32_t q) {
   Fp8Block b;
   if (P.mode == FP8_DENSE) {
-    const int32_t s = P.segs == 1 ? 0 : q / P.kb;
+    const int32_t s = P.segs == 1 || P.kb == 0 ? 0 : q / P.kb;  // no k-block: an empty contraction
     b.k = q - s * P.kb;
     b.ai = P.a_by_g * u.g + P.a_by_s * s;
     b.bi = P.b_by_g * u.g + P.b_by_s * s;
