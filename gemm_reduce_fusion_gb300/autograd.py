@@ -390,15 +390,16 @@ class _Fp8MLPFn(torch.autograd.Function):
     Backward: dH_k = (dY A2_k^T) GeLU'(H_k), dX = sum_k dH_k A1_k^T,
     dA2_k = GeLU(H_k)^T dY, dA1_k = X^T dH_k, each on operands of its factors.
     Saves H in bf16, and X and the weights as the operands that the backward
-    products take."""
+    products take; without ``grad`` (the mode of the call: inside it is always
+    off) nothing is saved or packed for them."""
 
     @staticmethod
-    def forward(ctx, p, x, *wb):
+    def forward(ctx, p, grad, x, *wb):
         x = _bf16(x, "x")
         w1 = [_bf16(a, "FC1 weight shard") for a in wb[:p]]
         w2 = [_bf16(a, "FC2 weight shard") for a in wb[p:]]
         (M, h), nk = x.shape, w1[0].shape[1]
-        train = any(ctx.needs_input_grad)
+        train = grad and any(ctx.needs_input_grad)
         ws = _workspace(x.device, [(TP_OP_COL_FP8, p, M, nk, h), (TP_OP_ROW_FP8, p, M, h, nk)])
         back1, fwd1 = _operands(w1, train, True, tiles=True)
         back2, fwd2 = _operands(w2, train, True, tiles=True)
@@ -431,7 +432,7 @@ class _Fp8MLPFn(torch.autograd.Function):
         dhq, dht = _operands(dh, True, True)
         dx = _empty((M, h), dy)
         tp_col_linear_bwd_fp8(xt, back1, dhq, dht, dx, dw1, ws)
-        return (None, dx, *dw1, *dw2)
+        return (None, None, dx, *dw1, *dw2)
 
 
 class _RouteFn(torch.autograd.Function):
@@ -467,15 +468,16 @@ class _RouteFn(torch.autograd.Function):
 class _ExpertsFn(torch.autograd.Function):
     """y[t] = sum_j weights[t, j] GeLU(x[t] W1_e) W2_e on 8-bit operands; the
     p shards hold E/p experts each.  Saves x, dispatched slots, pre-activations
-    and the experts' outputs, and the weights as operands."""
+    and the experts' outputs, and the weights as operands; nothing without
+    ``grad``, the mode of the call, and a few tokens then take smaller tiles."""
 
     @staticmethod
-    def forward(ctx, p, x, experts, weights, *wb):
+    def forward(ctx, p, grad, x, experts, weights, *wb):
         x, experts, weights = _bf16(x, "x"), experts.contiguous(), weights.contiguous()
         w1 = [_bf16(a, "FC1 weights of the experts") for a in wb[:p]]
         w2 = [_bf16(a, "FC2 weights of the experts") for a in wb[p:]]
         (T, h), (per, _, f), k = x.shape, w1[0].shape, experts.shape[1]
-        train = any(ctx.needs_input_grad)
+        train = grad and any(ctx.needs_input_grad)
         ws = _workspace(x.device, [], tp_experts_workspace_size(p, p * per, T, k, h, f, train))
         back1, fwd1 = _operands(w1, train, True, tiles=True)
         back2, fwd2 = _operands(w2, train, True, tiles=True)
@@ -497,12 +499,12 @@ class _ExpertsFn(torch.autograd.Function):
         dy = _grad(dy, x)
         ws = _workspace(x.device, [], tp_experts_workspace_size(p, p * per, T, k, h, f, True))
         need = ctx.needs_input_grad
-        dx = _empty((T, h), x) if need[1] else None
-        dw = _empty((T, k), x) if need[3] else None
-        dw1 = [_empty((per, h, f), x) for _ in range(p)] if any(need[4:4 + p]) else None
-        dw2 = [_empty((per, f, h), x) for _ in range(p)] if any(need[4 + p:]) else None
+        dx = _empty((T, h), x) if need[2] else None
+        dw = _empty((T, k), x) if need[4] else None
+        dw1 = [_empty((per, h, f), x) for _ in range(p)] if any(need[5:5 + p]) else None
+        dw2 = [_empty((per, f, h), x) for _ in range(p)] if any(need[5 + p:]) else None
         tp_experts_bwd_fp8(x, weights, dy, back1, back2, dx, dw, dw1, dw2, saved, ws)
-        return (None, dx, None, dw.float() if dw is not None else None, *(dw1 or [None] * p), *(dw2 or [None] * p))
+        return (None, None, dx, None, dw.float() if dw is not None else None, *(dw1 or [None] * p), *(dw2 or [None] * p))
 
 
 # ------------------------------------------------------------------ functional API
@@ -563,7 +565,7 @@ def parallel_mlp_fp8(x: torch.Tensor, w1: Sequence[torch.Tensor], w2: Sequence[t
     """Y = sum_k GeLU(X A1_k) A2_k, every product on 8-bit operands (see _Fp8MLPFn)."""
     if len(w1) != len(w2):
         raise ValueError("FC1 and FC2 need the same number of shards")
-    return _Fp8MLPFn.apply(len(w1), x, *w1, *w2)
+    return _Fp8MLPFn.apply(len(w1), torch.is_grad_enabled(), x, *w1, *w2)
 
 
 SCORES = {"softmax": TP_ROUTE_SOFTMAX, "sigmoid": TP_ROUTE_SIGMOID}
@@ -585,7 +587,7 @@ def routed_experts(x: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor
     w2 [E/p, f, h] holds E/p experts.  Differentiable in x, the weights and every shard."""
     if len(w1) != len(w2):
         raise ValueError("FC1 and FC2 need the same number of shards")
-    return _ExpertsFn.apply(len(w1), x, experts, weights, *w1, *w2)
+    return _ExpertsFn.apply(len(w1), torch.is_grad_enabled(), x, experts, weights, *w1, *w2)
 
 
 # ------------------------------------------------------------------ modules

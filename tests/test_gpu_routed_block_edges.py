@@ -1,4 +1,5 @@
-"""The routed block with any number of experts."""
+"""The routed block with any number of experts, and blocks on 8-bit operands
+where no gradient is recorded."""
 import pytest
 import torch
 
@@ -47,3 +48,31 @@ def test_any_number_of_experts(blk, p, E, T, k, h, f, routing):  # noqa: F811
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(yc, ys) and torch.equal(mc, ms)
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+def test_without_gradients_nothing_is_kept_for_them(blk, mode, monkeypatch):  # noqa: F811
+    """Parameters that require gradients, in an evaluation pass: one orientation of the weights, no saved rows."""
+    from gemm_reduce_fusion_gb300 import autograd as ag
+    g = gen(1)
+    p, E, T, k, h, f = 2, 8, 5, 2, 264, 392
+    w1, w2 = [rnd(g, h, f, scale=h ** -0.5).requires_grad_() for _ in range(p)], [rnd(g, f, h, scale=f ** -0.5).requires_grad_() for _ in range(p)]
+    e1, e2 = ([rnd(g, E // p, *s, scale=s[0] ** -0.5).requires_grad_() for _ in range(p)] for s in ((h, f), (f, h)))
+    x = rnd(g, T, h)
+    experts = torch.stack([torch.randperm(E, generator=g, device="cuda")[:k] for _ in range(T)]).to(torch.int32)
+    weights = torch.rand((T, k), generator=g, device="cuda")
+    want = ag.parallel_mlp_fp8(x, w1, w2), ag.routed_experts(x, experts, weights, e1, e2)
+    assert all(y.requires_grad for y in want)
+    both, pack = [], ag.tp_fp8_pack
+    monkeypatch.setattr(ag, "tp_fp8_pack", lambda x, q=None, qt=None, **kw: (both.append(q is not None and qt is not None), pack(x, q, qt, **kw)))
+    monkeypatch.setattr(ag, "experts_saved", lambda *a, **kw: pytest.fail("memory for a backward pass"))
+    with mode():
+        y, z = ag.parallel_mlp_fp8(x, w1, w2), ag.routed_experts(x, experts, weights, e1, e2)
+        assert not y.requires_grad and not z.requires_grad
+        direct = torch.empty_like(x)
+        ops = [ag._operands(list(w), False, True, tiles=True)[1] for w in (e1, e2)]
+        ag.tp_experts_fwd_fp8(x, experts, weights, *ops, direct, ag._workspace(x.device, [], ag.tp_experts_workspace_size(p, E, T, k, h, f)))
+    assert both and not any(both)
+    assert torch.equal(y, want[0])
+    assert torch.equal(z, direct)  # tiles by the tokens that there are
+    assert off(z, want[1].to(D)) < 2.0 ** -7  # the experts' outputs in fp32 instead of bf16
