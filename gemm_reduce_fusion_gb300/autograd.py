@@ -562,7 +562,9 @@ def sequence_parallel_mlp(xs: Sequence[torch.Tensor], w1: Sequence[torch.Tensor]
 
 
 def parallel_mlp_fp8(x: torch.Tensor, w1: Sequence[torch.Tensor], w2: Sequence[torch.Tensor]) -> torch.Tensor:
-    """Y = sum_k GeLU(X A1_k) A2_k, every product on 8-bit operands (see _Fp8MLPFn)."""
+    """Y = sum_k GeLU(X A1_k) A2_k, every product on 8-bit operands (see _Fp8MLPFn).
+
+    Each call packs the weights, for a backward pass in both orientations."""
     if len(w1) != len(w2):
         raise ValueError("FC1 and FC2 need the same number of shards")
     return _Fp8MLPFn.apply(len(w1), torch.is_grad_enabled(), x, *w1, *w2)
@@ -584,7 +586,10 @@ def route(logits: torch.Tensor, k: int, *, score: str = "softmax", bias=None, gr
 def routed_experts(x: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, w1: Sequence[torch.Tensor],
                    w2: Sequence[torch.Tensor]) -> torch.Tensor:
     """y[t] = sum_j weights[t, j] GeLU(x[t] W1_e) W2_e with e = experts[t, j]; shard r of w1 [E/p, h, f] and
-    w2 [E/p, f, h] holds E/p experts.  Differentiable in x, the weights and every shard."""
+    w2 [E/p, f, h] holds E/p experts.  Differentiable in x, the weights and every shard.
+
+    Each call packs the experts' weights, for a backward pass in both orientations.  Where no gradient is recorded the
+    outputs of few tokens' experts stay fp32 until they are added up, instead of bfloat16."""
     if len(w1) != len(w2):
         raise ValueError("FC1 and FC2 need the same number of shards")
     return _ExpertsFn.apply(len(w1), torch.is_grad_enabled(), x, experts, weights, *w1, *w2)

@@ -299,7 +299,9 @@ class RoutedMLPBlock(torch.nn.Module):
         z[t] = sum_j weights[t, j] GeLU(n[t] W1_e) W2_e,  e = experts[t, j]
 
     router [h, E], w1 [E, h, f] and w2 [E, f, h] bfloat16, the experts split
-    into p shards.  ``k`` experts a token; ``score``, ``groups``,
+    into p shards (h and f multiples of 8).  The logits are bfloat16, as every
+    column layer's outputs here; the choice is that of exact arithmetic on
+    them, and equal ones go to the lower expert.  ``k`` experts a token; ``score``, ``groups``,
     ``top_groups``, ``group_best``, ``renorm`` and ``scale`` as in ``route``.
     ``bias`` (float32 [E], zeros at first, no parameter) moves the choice only:
     a program balances the load by it, from ``counts``, how often each expert

@@ -104,7 +104,12 @@ Fp8Launch fp8_plan(int32_t mode, int64_t rows, int64_t cols, int64_t depth, int 
   // kernel and the parts (64 KiB at 128 rows, written and read, at each end of
   // a run) take as long as some 48 k-blocks of 0.13 us (whole tiles against
   // runs: 384 tiles 12288 deep 113.8 / 115.8 us; 32 tiles 16384 deep, with the
-  // 128 of 4096 before them, 57.5 / 52.4).
+  // 128 of 4096 before them, 57.5 / 52.4.  128 rows, weights from HBM, tiles x
+  // k-blocks, in front the k-blocks that idle SMs would have done: 8, 20 x 8
+  // 5.3 / 9.1; 7, 240 x 16 15.4 / 25.3; 30, 160 x 32 25.0 / 30.2; 30, 80 x 64
+  // 22.0 / 29.0; 54, 480 x 64 95.5 / 103.6; 56, 20 x 64 18.5 / 16.3; 61, 160 x
+  // 64 44.7 / 44.8; 111, 20 x 128 33.2 / 19.3; 121, 160 x 128 86.9 / 74.3.  16
+  // rows change sides at the same place.)
   const int64_t tile_rows = tile_rows_of(mode, rows, plan);
   const int64_t tiles = (mode == FP8_ROWS ? plan->max_tiles : groups * cdiv(rows, 128)) * cdiv(cols, 128);
   if (cdiv(tiles, kSMs) * kb <= tiles * kb / kSMs + 48 || tiles * kb > (int64_t(1) << 30)) return l;

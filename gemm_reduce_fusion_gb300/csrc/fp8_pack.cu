@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kThreads) fp8_pack_kernel(const __grid_constan
       if (all_finite) put_columns<true, SRC>(raw, keep, ilo, ihi, to, P.ldqt);
       else put_columns<false, SRC>(raw, keep, ilo, ihi, to, P.ldqt);
     }
-    if (quarter == 0) {  // columns past the matrix: exponent 0
+    if (quarter == 0) {  // of columns past the matrix too, where no product uses them
       uint8_t* e = P.et[t] + mat * P.et_mat + b * P.et_block + static_cast<int64_t>(strip >> 2) * 512;
       e[fp8_e_at(pair * 2, strip & 3)] = static_cast<uint8_t>(elo);
       e[fp8_e_at(pair * 2 + 1, strip & 3)] = static_cast<uint8_t>(ehi);

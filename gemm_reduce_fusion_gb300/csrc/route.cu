@@ -19,7 +19,7 @@
 // lowest lane with a value has the lowest expert.  A largest value is found by
 // one reduction over the warp of its bits in an order-preserving form, and the
 // lane that has it looks which expert it is.  Bound by instructions (8192
-// tokens, 8 of 256 experts from 4 of 8 groups, with counts and gradient: 25 us,
+// tokens, 8 of 256 experts from 4 of 8 groups, with counts and gradient: 24 us,
 // where the bytes take 2): each choice is a reduction over the warp and a few
 // dependent steps.  One token is the launch.
 #include <cuda_bf16.h>

@@ -532,7 +532,8 @@ tp_status tp_experts_fwd_fp8(const void* x, const void* experts, const void* wei
  *   to bf16;  dx[t] = sum_j dH_r . W1_e^T;  dweights[t, j] = dy[t] . out_r
  *   dW1_e = sum_r x[t]^T . dH_r;  dW2_e = sum_r GeLU(H_r)^T . dO_r
  * every product on operands of its factors, blocks of 128 rows of an expert
- * where they are contracted over.
+ * where they are contracted over; every gradient is rounded to bf16 once, from
+ * an fp32 sum (dx from the sum of its rows, which are bf16).
  *   w1t[r]: E/p operands [h, f] of W1_e; w2t[r]: E/p operands [f, h] of W2_e;
  *   dx: bf16 [T, h]; dweights: bf16 [T, k]; dw1[r]: bf16 [E/p, h, f]; dw2[r]:
  *   bf16 [E/p, f, h], zero for an expert without rows.  Each may be NULL, not
