@@ -1,5 +1,5 @@
-"""The routed block with any number of experts, and blocks on 8-bit operands
-where no gradient is recorded."""
+"""The routed block with any number of experts, blocks on 8-bit operands where no
+gradient is recorded, and their captured training steps."""
 import pytest
 import torch
 
@@ -76,3 +76,41 @@ def test_without_gradients_nothing_is_kept_for_them(blk, mode, monkeypatch):  # 
     assert torch.equal(y, want[0])
     assert torch.equal(z, direct)  # tiles by the tokens that there are
     assert off(z, want[1].to(D)) < 2.0 ** -7  # the experts' outputs in fp32 instead of bf16
+
+
+@pytest.mark.parametrize("E", [None, 16, 60])
+def test_a_captured_training_step_replays(blk, E):  # noqa: F811
+    """Forward and backward in one graph, replayed on other tokens with another routing; None: the MLP block."""
+    g = gen(2)
+    p, T, h, f = 2, 700, 264, 528
+    if E is None:
+        b = blk.MLPBlock(rnd(g, h, f, scale=h ** -0.5), rnd(g, f, h, scale=f ** -0.5), p, fp8=True)
+    else:
+        b = blk.RoutedMLPBlock(rnd(g, h, E, scale=h ** -0.5), rnd(g, E, h, f, scale=h ** -0.5), rnd(g, E, f, h, scale=f ** -0.5), p, 2)
+    xs, gy, gm = [rnd(g, T, h) for _ in range(3)], rnd(g, T, h), rnd(g, T, h)
+    x = xs[0].clone().requires_grad_()
+
+    def step():
+        y, m = b(x, blk.pre_norm([x])[0])
+        return [y, m, *torch.autograd.grad([y, m], [x, *b.parameters()], [gy, gm])]
+
+    def put(t):
+        with torch.no_grad():
+            x.copy_(t)
+    side, want = torch.cuda.Stream(), []
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for t in xs:
+            put(t)
+            want.append([r.clone() for r in step()])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = step()
+    for i in (1, 0, 2):
+        put(xs[i])
+        for t in got:
+            t.detach().fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(s, t) for s, t in zip(got, want[i]))
