@@ -975,7 +975,7 @@ def tp_row_linear_bwd_fp8(xt, w, dy, dyt, dx, dw, ws, preact=None, stream=None) 
         _fp8s(W, "xt", xt if need_w else None, p, K, M, dev), _fp8s(W, "w", w if need_x else None, p, K, N, dev),
         _fp8s(W, "dy", (dy,) if need_x else None, 1, M, N, dev), _fp8s(W, "dyt", (dyt,) if need_w else None, 1, N, M, dev),
         _list(W, "dx", dx, p, (M, K), bf, dev), _list(W, "dw", dw, p, (K, N), bf, dev),
-        _list(W, "preact", preact, p, (M, K), bf, dev), p, M, N, K, wp, wb, _on(stream, dev)), W)
+        _list(W, "preact", preact if need_x else None, p, (M, K), bf, dev), p, M, N, K, wp, wb, _on(stream, dev)), W)
 
 
 # ------------------------------------------------------------------ routing to experts
