@@ -338,11 +338,11 @@ __device__ __noinline__ LogSum log_sum(bool sigmoid, float a, float b) {
 }
 
 // Whether a lane's group is among the best; score: the group's, `lanes` lanes
-// each.  near: the last that is and the first that is not are within what the
-// scores may be off by, which goes by `size`, the largest magnitude that a
-// group adds up (a sum near 1 of 64.5 and -63.5 has the roundings of those):
-// for halves of sums (score_of) half of four values' and two sums' roundings,
-// which band_of() covers (sigmoid: 4 x 2.3 and 2 x 1 units, half of 11.2).
+// each.  near: one that is and one that is not are within what their scores may
+// be off by, which goes by `size`, the largest magnitude that a group adds up (a
+// sum near 1 of 64.5 and -63.5 has the roundings of those): for the half of a
+// sum (score_of) half of two values' and the sum's roundings, which half of
+// band_of() covers (sigmoid: 2 x 2.3 and 1/2 units, half of 5.1, against 3).
 template <typename T>
 __device__ __forceinline__ bool among_best(const RouteParams& P, T score, float size, int32_t group, int32_t lanes, float band, bool& near) {
   int32_t rank = 0;
@@ -354,11 +354,11 @@ __device__ __forceinline__ bool among_best(const RouteParams& P, T score, float 
   near = false;
   if constexpr (std::is_same_v<T, float>) {
     if (band > 0.f && P.tops < P.groups) {
-      const bool real = group < P.groups;
-      const float last = unordered(warp_max(real && rank == P.tops - 1 ? ordered(score) : 0u)),
-                  first = unordered(warp_max(real && rank == P.tops ? ordered(score) : 0u)),
-                  most = __uint_as_float(warp_max(real ? __float_as_uint(size) : 0u));
-      near = first > -INFINITY && last - first <= band * fmaxf(1.f, most);
+      const bool real = group < P.groups, kept = rank < P.tops;
+      const float off = 0.5f * band * fmaxf(1.f, size);
+      const float least = unordered(~warp_max(real && kept ? ~ordered(score - off) : 0u)),
+                  most = unordered(warp_max(real && !kept ? ordered(score + off) : 0u));
+      near = most > -INFINITY && most >= least;
     }
   }
   return group < P.groups && rank < P.tops && open(score);
