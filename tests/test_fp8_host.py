@@ -42,12 +42,6 @@ def test_the_documented_shapes_pass(lib):  # noqa: F811
     assert len(lib.calls) == 11
 
 
-def test_weights_alone_take_no_preactivation(lib):  # noqa: F811
-    """H is read for the inputs' gradients: with the weights' alone it may be given and is not looked at."""
-    tp.tp_row_linear_bwd_fp8(ops(p, K, M), None, None, op(N, M), None, zs(p, K, N), WS, preact=zs(p, M, K), stream=0)
-    assert len(lib.calls) == 1
-
-
 WRONG = {
     "pack rows": lambda: tp.tp_fp8_pack(zs(p, M, 200), ops(p, M + 1, 200), stream=0),
     "pack columns": lambda: tp.tp_fp8_pack(zs(p, M, 200), ops(p, M, 264), stream=0),
